@@ -42,7 +42,7 @@ def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cxx = shutil.which("g++") or "g++"
     objs = []
-    for name in ("svdq_kernels", "svdq_probe"):
+    for name in ("svdq_kernels", "svdq_probe", "svdq_kv_rows", "svdq_kv_attn"):
         obj = os.path.join(BUILD, name + ".o")
         _run([HIPCC] + HIP_FLAGS + ["-c", os.path.join(CSRC, name + ".hip"), "-o", obj])
         objs.append(obj)

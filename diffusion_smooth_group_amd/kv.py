@@ -1,0 +1,334 @@
+"""ctypes binding of the 4-bit key/value cache operators (include/svdq_kv.h).
+
+Argument marshalling only, like ``svdq.py``: torch tensors in and out, the
+work is done by the library's kernels on the current (or the given) stream.
+What runs between a QKV projection and the attention output:
+
+    step = plan(past, fresh, table, free_pages, free_count, page_size, tokens)
+    q = cache.append(k, v, step.slots, q=q, cos=cos, sin=sin, wq=wq, wk=wk, norm=True,
+                     positions=step.positions)
+    out = attention(q, cache, step.block_table, step.q_start, step.kv_len, max_q, max_kv)
+
+Tensors of heads are [tokens, heads, D] with unit stride in D (views of a
+fused QKV row are taken as they are).  A wrong argument raises ValueError
+here or SvdqError with the library's status.
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import svdq as S
+from .svdq import FMT_INT4_G64, FMT_MXFP4_G32, SvdqError  # noqa: F401  (part of this module's interface)
+
+QK_NORM, QK_ROPE, QK_ROPE_HALVES = 1, 2, 4
+ATTN_CAUSAL = 1
+MAX_REQUESTS = 8192
+GROUP = {FMT_MXFP4_G32: 32, FMT_INT4_G64: 64}
+SCALE_DTYPE = {FMT_MXFP4_G32: torch.uint8, FMT_INT4_G64: torch.float16}
+
+_DTYPES = {torch.float16: S.F16, torch.bfloat16: S.BF16}
+_P, _I64, _I32, _U, _F, _SZ = C.c_void_p, C.c_int64, C.c_int32, C.c_uint, C.c_float, C.c_size_t
+
+
+class svdq_heads(C.Structure):
+    _fields_ = [("data", _P), ("token_stride", _I64), ("head_stride", _I64), ("heads", _I32)]
+
+
+class svdq_qk_desc(C.Structure):
+    _fields_ = [("tokens", _I64), ("head_dim", _I32), ("dtype", _I32), ("flags", _U), ("eps", _F), ("wq", _P),
+                ("wk", _P), ("cos", _P), ("sin", _P), ("n_positions", _I64), ("positions", _P)]
+
+
+class svdq_kv_cache(C.Structure):
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("n_pages", _I64),
+                ("page_size", _I32), ("heads", _I32), ("head_dim", _I32), ("fmt", _I32)]
+
+
+class svdq_attn_desc(C.Structure):
+    _fields_ = [("requests", _I64), ("tokens", _I64), ("q_heads", _I32), ("dtype", _I32), ("max_q", _I32),
+                ("max_kv", _I32), ("window", _I32), ("flags", _U), ("scale", _F), ("q_start", _P), ("kv_len", _P),
+                ("block_table", _P), ("table_stride", _I64)]
+
+
+_HP, _QP, _CP, _AP = C.POINTER(svdq_heads), C.POINTER(svdq_qk_desc), C.POINTER(svdq_kv_cache), C.POINTER(svdq_attn_desc)
+_SIGS = {
+    "svdq_qk_norm_rope": [_QP, _HP, _HP, _HP, _HP, _P],
+    "svdq_qk_backward_workspace": [_QP, _I32, _I32, C.POINTER(_SZ)],
+    "svdq_qk_norm_rope_backward": [_QP, _HP, _HP, _HP, _HP, _HP, _HP, _P, _P, _P, _SZ, _P],
+    "svdq_kv_cache_size": [_I64, _I32, _I32, _I32, C.c_int, C.POINTER(_SZ), C.POINTER(_SZ)],
+    "svdq_kv_append": [_QP, _HP, _HP, _HP, _HP, _CP, _P, _P],
+    "svdq_kv_read": [_CP, _P, _I64, C.c_int, _HP, _HP, _P],
+    "svdq_kv_plan": [_P, _P, _I64, _I32, _I64, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P],
+    "svdq_kv_release": [_P, _I64, _I32, _P, _I64, _P, _P, _P, _I64, _P],
+    "svdq_kv_attention_workspace": [_AP, _CP, C.POINTER(_SZ)],
+    "svdq_kv_attention": [_AP, _HP, _CP, _HP, _P, _P, _SZ, _P],
+}
+_FN = {}
+
+
+def _call(name, *args):
+    fn = _FN.get(name)
+    if fn is None:
+        fn = getattr(S.lib_handle(), name)
+        fn.argtypes, fn.restype = _SIGS[name], C.c_int
+        _FN[name] = fn
+    rc = fn(*args)
+    if rc != 0:
+        raise SvdqError(name, rc)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _heads(t, name, tokens, dim, dtype):
+    _need(t.is_cuda and t.dim() == 3 and t.dtype == dtype, f"{name}: a {dtype} GPU tensor [tokens, heads, D] is needed")
+    n, h, d = t.shape
+    _need(n == tokens and d == dim, f"{name}: shape {tuple(t.shape)} does not fit {tokens} tokens of heads of {dim}")
+    s0, s1, s2 = t.stride()
+    _need(s2 == 1 or d == 1, f"{name}: D must have unit stride")
+    return svdq_heads(t.data_ptr(), s0 if n > 1 else 0, s1 if h > 1 else 0, h)
+
+
+def _int32(t, name, n=None):
+    _need(t.is_cuda and t.dtype == torch.int32 and t.is_contiguous(), f"{name}: a contiguous int32 GPU tensor is needed")
+    _need(n is None or t.numel() == n, f"{name}: {n} entries are needed, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions):
+    _need(dtype in _DTYPES, f"float16 or bfloat16 rows are needed, got {dtype}")
+    d = svdq_qk_desc(tokens, dim, _DTYPES[dtype])
+    flags = QK_NORM if norm else 0
+    d.eps = eps
+    if norm:
+        for field, w in (("wq", wq), ("wk", wk)):
+            if w is not None:
+                _need(w.is_cuda and w.dtype == dtype and w.is_contiguous() and w.numel() == dim,
+                      f"{field}: a contiguous {dtype} GPU tensor of {dim} is needed")
+                setattr(d, field, w.data_ptr())
+    _need((cos is None) == (sin is None), "cos and sin go together")
+    if cos is not None:
+        flags |= QK_ROPE | (QK_ROPE_HALVES if halves else 0)
+        for t in (cos, sin):
+            _need(t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 2 and t.shape[1] * 2 == dim
+                  and t.shape[0] == cos.shape[0], "cos, sin: contiguous float32 GPU tables [positions, D / 2] are needed")
+        d.cos, d.sin, d.n_positions = cos.data_ptr(), sin.data_ptr(), cos.shape[0]
+        if positions is not None:
+            d.positions = _int32(positions, "positions", tokens)
+    d.flags = flags
+    return d
+
+
+# ------------------------------------------------------------ norm and rotation
+def qk_norm_rope(q, k, cos=None, sin=None, wq=None, wk=None, eps: float = 1e-6, norm: bool = True, halves: bool = False,
+                 positions=None, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q and k (``norm``; weights wq, wk [D], None for
+    ones) and rotation by the tables cos, sin [positions, D / 2] (None: no
+    rotation), at positions [tokens] (int32, None: 0, 1, ...).  halves: pairs
+    (i, i + D/2), else (2i, 2i + 1).  Returns (q_out, k_out); q_out=q, k_out=k
+    work in place."""
+    tokens, _, dim = q.shape
+    d = _desc(tokens, dim, q.dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    _call("svdq_qk_norm_rope", d, _heads(q, "q", tokens, dim, q.dtype), _heads(k, "k", tokens, dim, q.dtype),
+          _heads(q_out, "q_out", tokens, dim, q.dtype), _heads(k_out, "k_out", tokens, dim, q.dtype), S._stream(stream))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(gq, gk, q, k, cos=None, sin=None, wq=None, wk=None, eps: float = 1e-6, norm: bool = True,
+                          halves: bool = False, positions=None, dq=None, dk=None, ws=None, stream=None):
+    """Gradient of ``qk_norm_rope`` from gq, gk (with respect to its outputs)
+    and its inputs.  Returns (dq, dk, dwq, dwk), the weight gradients fp32 [D]
+    (zero without ``norm``)."""
+    tokens, _, dim = q.shape
+    d = _desc(tokens, dim, q.dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    dw = torch.empty((2, dim), dtype=torch.float32, device=q.device)
+    if ws is None:
+        need = _SZ(0)
+        _call("svdq_qk_backward_workspace", d, q.shape[1], k.shape[1], need)
+        ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+    h = [_heads(t, n, tokens, dim, q.dtype) for t, n in ((q, "q"), (k, "k"), (gq, "gq"), (gk, "gk"), (dq, "dq"), (dk, "dk"))]
+    _call("svdq_qk_norm_rope_backward", d, *h, dw.data_ptr(), dw.data_ptr() + 4 * dim, ws.data_ptr(), ws.numel(),
+          S._stream(stream))
+    return dq, dk, dw[0], dw[1]
+
+
+class _QKNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, cos, sin, eps, halves, positions):
+        ctx.save_for_backward(q, k, wq, wk, cos, sin, positions)
+        ctx.how = eps, halves
+        return qk_norm_rope(q, k, cos, sin, wq, wk, eps, True, halves, positions)
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
+        eps, halves = ctx.how
+        unit = (lambda g: g if g.stride(-1) == 1 and all(s % 8 == 0 for s in g.stride()[:2]) and g.data_ptr() % 16 == 0
+                else g.contiguous())
+        dq, dk, dwq, dwk = qk_norm_rope_backward(unit(gq), unit(gk), q, k, cos, sin, wq, wk, eps, True, halves, positions)
+        return dq, dk, None if wq is None else dwq.to(wq.dtype), None if wk is None else dwk.to(wk.dtype), *[None] * 5
+
+
+def qk_norm_rope_autograd(q, k, wq, wk, cos, sin, eps: float = 1e-6, halves: bool = False, positions=None):
+    """``qk_norm_rope`` under torch.autograd: gradients of q, k, wq and wk."""
+    return _QKNormRope.apply(q, k, wq, wk, cos, sin, eps, halves, positions)
+
+
+# ----------------------------------------------------------------------- cache
+class KVCache:
+    """The paged 4-bit cache of one layer: codes [pages, heads, page_size, D / 2]
+    and scales [pages, heads, page_size, D / G] of K and of V."""
+
+    def __init__(self, n_pages: int, page_size: int, heads: int, head_dim: int, fmt: int, device="cuda"):
+        code, scale = _SZ(0), _SZ(0)
+        _call("svdq_kv_cache_size", n_pages, page_size, heads, head_dim, fmt, code, scale)
+        shape = (n_pages, heads, page_size)
+        codes = [torch.zeros((*shape, head_dim // 2), dtype=torch.uint8, device=device) for _ in "kv"]
+        scales = [torch.zeros((*shape, head_dim // GROUP[fmt]), dtype=SCALE_DTYPE[fmt], device=device) for _ in "kv"]
+        self._hold(codes[0], scales[0], codes[1], scales[1], fmt)
+
+    @classmethod
+    def wrap(cls, k_codes, k_scales, v_codes, v_scales, fmt):
+        """A cache in buffers that the caller has.  fmt: FMT_MXFP4_G32,
+        FMT_INT4_G64, or "mxfp4_g32", "int4_g64"."""
+        fmt = S.FMT_CODES.get(fmt, fmt)
+        _need(fmt in GROUP, f"cache format {fmt!r}")
+        _need(k_codes.dim() == 4, "codes: [pages, heads, page_size, D / 2] is needed")
+        shape, dim = k_codes.shape[:3], 2 * k_codes.shape[3]
+        for t, kind, last in ((k_codes, torch.uint8, dim // 2), (v_codes, torch.uint8, dim // 2),
+                              (k_scales, SCALE_DTYPE[fmt], dim // GROUP[fmt]), (v_scales, SCALE_DTYPE[fmt], dim // GROUP[fmt])):
+            _need(t.is_cuda and t.is_contiguous() and t.dtype == kind and t.shape == (*shape, last),
+                  f"a contiguous {kind} GPU tensor {(*shape, last)} is needed, got {t.dtype} {tuple(t.shape)}")
+        self = cls.__new__(cls)
+        self._hold(k_codes, k_scales, v_codes, v_scales, fmt)
+        return self
+
+    def _hold(self, k_codes, k_scales, v_codes, v_scales, fmt):
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.fmt = k_codes, k_scales, v_codes, v_scales, fmt
+        self.n_pages, self.heads, self.page_size = k_codes.shape[:3]
+        self.head_dim = 2 * k_codes.shape[3]
+        self.device = k_codes.device
+        self.c = svdq_kv_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                               self.n_pages, self.page_size, self.heads, self.head_dim, fmt)
+
+    def append(self, k, v, slots, q=None, cos=None, sin=None, wq=None, wk=None, eps: float = 1e-6, norm: bool = False,
+               halves: bool = False, positions=None, q_out=None, stream=None):
+        """Quantizes k and v [tokens, heads, D] into slots [tokens] (int32, a
+        negative one is skipped).  With norm and / or cos, sin: k is normed and
+        rotated on the way (and q into q_out, which is returned)."""
+        tokens, _, dim = k.shape
+        d = _desc(tokens, dim, k.dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+        hq = ho = None
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            hq, ho = _heads(q, "q", tokens, dim, k.dtype), _heads(q_out, "q_out", tokens, dim, k.dtype)
+        _call("svdq_kv_append", d, hq, _heads(k, "k", tokens, dim, k.dtype), _heads(v, "v", tokens, dim, k.dtype), ho, self.c,
+              _int32(slots, "slots", tokens), S._stream(stream))
+        return q_out
+
+    def read(self, slots, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+        """(k, v) [len(slots), heads, D]: the cached values of the slots, zero
+        for slots outside the cache."""
+        n = slots.numel()
+        shape = (n, self.heads, self.head_dim)
+        _need(dtype in _DTYPES, f"float16 or bfloat16 is needed, got {dtype}")
+        k_out = torch.empty(shape, dtype=dtype, device=self.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=self.device) if v_out is None else v_out
+        _call("svdq_kv_read", self.c, _int32(slots, "slots"), n, _DTYPES[dtype], _heads(k_out, "k_out", n, self.head_dim, dtype),
+              _heads(v_out, "v_out", n, self.head_dim, dtype), S._stream(stream))
+        return k_out, v_out
+
+
+# ------------------------------------------------------------------- step tables
+class Plan(NamedTuple):
+    block_table: torch.Tensor   # [requests, pages], the caller's, new pages entered
+    q_start: torch.Tensor       # [requests + 1]
+    kv_len: torch.Tensor        # [requests]
+    slots: torch.Tensor         # [tokens]
+    positions: torch.Tensor     # [tokens]
+    free_count: torch.Tensor    # [1] pages left
+    missing: torch.Tensor       # [1] pages that were wanted and not there
+
+
+def plan(past, fresh, block_table, free_pages, free_count, page_size: int, tokens: int, stream=None) -> Plan:
+    """Block tables, slots and positions of a step: past [requests] cached
+    tokens, fresh [requests] new ones, pages from the end of free_pages
+    (free_count [1] of them are free).  tokens: length of the slot map, at
+    least the sum of fresh (the rest is -1)."""
+    b = past.numel()
+    _need(block_table.dim() == 2 and block_table.shape[0] == b, "block_table: [requests, pages] is needed")
+    out = torch.empty(2 * b + 3 + 2 * tokens, dtype=torch.int32, device=past.device)
+    at = out.data_ptr()
+    cuts = (b + 1, b, tokens, tokens, 1, 1)
+    q_start, kv_len, slots, positions, left, missing = out.split(cuts)
+    p, ptr = [], at
+    for n in cuts:
+        p.append(ptr)
+        ptr += 4 * n
+    _call("svdq_kv_plan", _int32(past, "past"), _int32(fresh, "fresh", b), b, page_size, tokens, _int32(free_pages, "free_pages"),
+          _int32(free_count, "free_count", 1), free_pages.numel(), _int32(block_table, "block_table"), block_table.shape[1], *p,
+          S._stream(stream))
+    return Plan(block_table, q_start, kv_len, slots, positions, left, missing)
+
+
+def release(done, block_table, kv_len, free_pages, free_count, page_size: int, stream=None):
+    """Gives the pages of the requests with done != 0 back to free_pages (in
+    place: free_pages, free_count, block_table and kv_len)."""
+    b = done.numel()
+    _need(block_table.dim() == 2 and block_table.shape[0] == b, "block_table: [requests, pages] is needed")
+    _call("svdq_kv_release", _int32(done, "done"), b, page_size, _int32(block_table, "block_table"), block_table.shape[1],
+          _int32(kv_len, "kv_len", b), _int32(free_pages, "free_pages"), _int32(free_count, "free_count", 1), free_pages.numel(),
+          S._stream(stream))
+
+
+# --------------------------------------------------------------------- attention
+def attention_workspace(requests: int, tokens: int, q_heads: int, cache: KVCache, max_q: int, max_kv: int,
+                        device="cuda") -> torch.Tensor:
+    """A workspace for ``attention`` calls of these bounds."""
+    d = svdq_attn_desc(requests, tokens, q_heads, S.BF16, max_q, max_kv, 0, ATTN_CAUSAL, 1.0)
+    need = _SZ(0)
+    _call("svdq_kv_attention_workspace", d, cache.c, need)
+    return torch.empty(need.value, dtype=torch.uint8, device=device)
+
+
+def attention(q, cache: KVCache, block_table, q_start, kv_len, max_q: int, max_kv: int, causal: bool = True, window: int = 0,
+              scale: Optional[float] = None, out=None, ws=None, return_lse: bool = False, stream=None):
+    """softmax(scale q k^T) v over the cached tokens, request by request: rows
+    q_start[r] .. q_start[r + 1] of q [tokens, q_heads, D] are request r's, the
+    last of them at position kv_len[r] - 1.  causal: keys up to the row's
+    position; window > 0: only the last `window` of them.  max_q, max_kv bound
+    the rows and cached tokens of a request.  scale: 1 / sqrt(D) by default.
+    A row that sees nothing gives zeros.  Returns out, or (out, lse)."""
+    tokens, hq, dim = q.shape
+    _need(dim == cache.head_dim, f"q: heads of {dim} over a cache of heads of {cache.head_dim}")
+    _need(q.dtype in _DTYPES, f"float16 or bfloat16 rows are needed, got {q.dtype}")
+    b = kv_len.numel()
+    _need(block_table.dim() == 2 and block_table.shape[0] == b, "block_table: [requests, pages] is needed")
+    if out is None:
+        out = torch.empty((tokens, hq, dim), dtype=q.dtype, device=q.device)
+    lse = torch.empty((tokens, hq), dtype=torch.float32, device=q.device) if return_lse else None
+    d = svdq_attn_desc(b, tokens, hq, _DTYPES[q.dtype], max_q, max_kv, window, ATTN_CAUSAL if causal else 0,
+                       1.0 / math.sqrt(dim) if scale is None else scale, _int32(q_start, "q_start", b + 1),
+                       _int32(kv_len, "kv_len"), _int32(block_table, "block_table"), block_table.shape[1])
+    if ws is None:
+        need = _SZ(0)
+        _call("svdq_kv_attention_workspace", d, cache.c, need)
+        ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+    _call("svdq_kv_attention", d, _heads(q, "q", tokens, dim, q.dtype), cache.c, _heads(out, "out", tokens, dim, q.dtype),
+          None if lse is None else lse.data_ptr(), ws.data_ptr() if ws.numel() else None, ws.numel(), S._stream(stream))
+    return (out, lse) if return_lse else out
