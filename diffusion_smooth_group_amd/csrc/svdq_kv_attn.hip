@@ -21,13 +21,13 @@ struct AttnParams {
   const uint16_t* q;
   uint16_t* out;
   float* lse;
-  float* part;              // [item][split][16][D] partial sums, then [item][split][16][2] reference and sum
+  float* part;              // [row slot][split][D] partial sums, then [row slot][split][2] reference and sum
   const uint8_t *kc, *ks, *vc, *vs;
   const int32_t *q_start, *kv_len, *table;
   int64_t qt, qh, ot, oh, tokens, table_stride, n_pages;
   int32_t requests, q_heads, heads, group;      // group = q_heads / heads
   int32_t max_q, max_kv, window, causal, page_shift;
-  int32_t row_tiles, splits, chunk;             // row tiles a request has at most; key chunks
+  int32_t row_tiles, row_slots, splits, chunk;  // row tiles and rows a request and head has at most; key chunks
   float c;                  // scale log2(e)
 };
 
@@ -73,14 +73,22 @@ __device__ __forceinline__ float mx_scale(unsigned e) {
 template <int DT, int FMT>
 constexpr float value_gain() { return DT == SVDQ_F16 && FMT == SVDQ_FMT_MXFP4_G32 ? 8.0f : 1.0f; }
 
-// f16 probabilities are held at 2^6 of their size: the f16 subnormals start
-// far lower than any probability that counts, and 2^(6 + 8) still fits.  The
-// factor is in the row's reference, so it drops out of the quotient.
+// A row's reference is raised only when its maximum has passed it by 2^SLACK;
+// between that no accumulator is touched.  f16: probabilities are held at 2^6
+// of their size, so that f16's subnormals start far below any that counts, and
+// 2^(6 + 8) still fits.  INT4 with f16: what is rounded is p times a value
+// scale, so the reference is raised to the maximum of logit + exponent of the
+// tile's largest value scale.  All of this is part of the reference and drops
+// out of the quotient.
 template <int DT>
 constexpr float p_shift() { return DT == SVDQ_F16 ? 6.0f : 0.0f; }
-// The reference is raised only when a row's maximum has passed it by 2^8;
-// between that the sums stay in range and no accumulator is touched.
 constexpr float SLACK = 8.0f;
+template <int DT, int FMT>
+constexpr bool scaled_reference() { return DT == SVDQ_F16 && FMT == SVDQ_FMT_INT4_G64; }
+// exponent of a value scale as f16 has it (2^e <= s), -24 for zero
+__device__ __forceinline__ float scale_exponent(float s) {
+  return s == 0.0f ? -24.0f : float(int(__float_as_uint(s) >> 23) - 127);
+}
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -100,6 +108,11 @@ __device__ __forceinline__ float quad_sum(float x) {
   const unsigned v = __float_as_uint(m);
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// natural logarithm of a row's sum of exponentials
+__device__ __forceinline__ float row_lse(float base, float sum) {
+  return sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0.69314718055994531f;
 }
 
 // A request's rows and the keys they see.
@@ -235,6 +248,9 @@ __device__ __forceinline__ u32x4 key_frag(unsigned w, float scale) {
 __device__ __forceinline__ unsigned low_halves(unsigned x0, unsigned x1) { return __builtin_amdgcn_perm(x1, x0, 0x05040100u); }
 __device__ __forceinline__ unsigned high_halves(unsigned x0, unsigned x1) { return __builtin_amdgcn_perm(x1, x0, 0x07060302u); }
 
+// (by value: a bit cast of a vector's element in place reads element 0)
+__device__ __forceinline__ f16x2 two_halves(unsigned u) { return __builtin_bit_cast(f16x2, u); }
+
 template <int FMT>
 __device__ __forceinline__ u32x4 query_order(u32x4 q) {
   if constexpr (FMT == SVDQ_FMT_MXFP4_G32) return q;
@@ -264,35 +280,28 @@ __device__ __forceinline__ void value_pair_mx(const unsigned* v, const float* s,
   }
 }
 
-// the same for INT4, from fp8 words: c s rounded to 16 bits once (fp32 product
-// for bf16, f16 product for f16)
+// the same for INT4, from fp8 words: the integers themselves
 template <int DT, bool HI>
-__device__ __forceinline__ void value_pair_int4(const unsigned* v8, const float* s, u32x4* f0, u32x4* f1) {
+__device__ __forceinline__ void value_pair_int4(const unsigned* v8, u32x4* f0, u32x4* f1) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (DT == SVDQ_BF16) {
-      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v8[2 * i], 512.0f, HI);
-      const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v8[2 * i + 1], 512.0f, HI);
-      (*f0)[i] = pack2<DT>(a[0] * s[2 * i], b[0] * s[2 * i + 1]);
-      (*f1)[i] = pack2<DT>(a[1] * s[2 * i], b[1] * s[2 * i + 1]);
-    } else {
-      const _Float16 s0 = (_Float16)s[2 * i], s1 = (_Float16)s[2 * i + 1];
-      const f16x2 a = __builtin_bit_cast(f16x2, cvt_int4<DT, HI>(v8[2 * i])) * f16x2{s0, s0};
-      const f16x2 b = __builtin_bit_cast(f16x2, cvt_int4<DT, HI>(v8[2 * i + 1])) * f16x2{s1, s1};
-      const unsigned x0 = __builtin_bit_cast(unsigned, a), x1 = __builtin_bit_cast(unsigned, b);
-      (*f0)[i] = low_halves(x0, x1);
-      (*f1)[i] = high_halves(x0, x1);
-    }
+    const unsigned x0 = cvt_int4<DT, HI>(v8[2 * i]), x1 = cvt_int4<DT, HI>(v8[2 * i + 1]);
+    (*f0)[i] = low_halves(x0, x1);
+    (*f1)[i] = high_halves(x0, x1);
   }
 }
 
-// column of the result that lane row n of value tile x stands for
+// column of the result that lane row n of value tile x stands for.  MXFP4:
+// the lane's elements in order.  INT4: tile x holds one scale group's columns
+// only (D = 128: tiles 0-3 the first, 4-7 the second), nibbles 0 2 1 3 of the
+// 16 bits of the group that Rows16::step gives the lane.
 template <int FMT, int D>
 __device__ __forceinline__ constexpr int value_col(int n, int x) {
-  // MXFP4: tiles are the lane's elements in order; INT4: nibbles 0 2 4 6 1 3 5 7
   constexpr int PER = D / 16;
   if (FMT == SVDQ_FMT_MXFP4_G32) return PER * n + x;
-  return PER * n + (PER == 8 ? (x < 4 ? 2 * x : 2 * (x - 4) + 1) : (x < 2 ? 2 * x : 2 * (x - 2) + 1));
+  constexpr int ORDER[4] = {0, 2, 1, 3};
+  if (D == 64) return 4 * n + ORDER[x];
+  return 64 * (x / 4) + 8 * (n & 7) + 4 * (n >> 3) + ORDER[x % 4];
 }
 
 template <int DT, int FMT, int D>
@@ -349,6 +358,25 @@ struct Rows16 {
       }
     }
     float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
+    const int m = lane & 15;
+    float vs[FMT == SVDQ_FMT_INT4_G64 ? D / 64 : 1][8];
+    if constexpr (FMT == SVDQ_FMT_INT4_G64) {
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float c = value_scale<DT, FMT, D>(t.vsc, i, g);
+          vs[g][i] = all || (there && token + 8 * b + i < len) ? c : 0.0f;   // a key that is not there may hold a NaN
+        }
+    }
+    if constexpr (scaled_reference<DT, FMT>()) {
+      float most = vs[0][0];
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = fmaxf(most, vs[g][i]);
+      top += scale_exponent(most);
+    }
     top = quad_max(top) - p_shift<DT>();
     if (__any(top > base + SLACK)) {
       const float next = fmaxf(base, top), alpha = exp2_hw(base - next);
@@ -357,32 +385,28 @@ struct Rows16 {
 #pragma unroll
       for (int x = 0; x < NX; ++x) o[x] *= alpha;
     }
-    u32x4 pf;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p0 = exp2_hw(s[2 * i] - base), p1 = exp2_hw(s[2 * i + 1] - base);
-      sum += p0 + p1;
-      pf[i] = pack2<DT>(p0, p1);
-    }
-    // values: keys past the end or on a missing page hold anything, a NaN
-    // included, and must be zero, not only weighted with zero
-    float sc[8];
-    const int m = lane & 15;
-    const int g = FMT == SVDQ_FMT_MXFP4_G32 ? (D == 128 ? m >> 2 : m >> 3) : (D == 128 ? m >> 3 : 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sc[i] = value_scale<DT, FMT, D>(t.vsc, i, g);
-      if (DT == SVDQ_F16 && FMT == SVDQ_FMT_INT4_G64) sc[i] = fminf(sc[i], 9352.0f);   // 7 x 9352 is the last that f16 holds
-    }
-    if (!all) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sc[i] = there && token + 8 * b + i < len ? sc[i] : 0.0f;
-    }
-    unsigned v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = D == 128 ? t.v[i] : t.v[i] >> (16 * (m & 1));
-    u32x4 f0, f1;
     if constexpr (FMT == SVDQ_FMT_MXFP4_G32) {
+      u32x4 pf;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p0 = exp2_hw(s[2 * i] - base), p1 = exp2_hw(s[2 * i + 1] - base);
+        sum += p0 + p1;
+        pf[i] = pack2<DT>(p0, p1);
+      }
+      // keys past the end or on a missing page hold anything, a NaN included:
+      // their values must be zero, not only weighted with zero
+      float sc[8];
+      const int g = D == 128 ? m >> 2 : m >> 3;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sc[i] = value_scale<DT, FMT, D>(t.vsc, i, g);
+      if (!all) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sc[i] = there && token + 8 * b + i < len ? sc[i] : 0.0f;
+      }
+      unsigned v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = D == 128 ? t.v[i] : t.v[i] >> (16 * (m & 1));
+      u32x4 f0, f1;
       value_pair_mx<DT, 0>(v, sc, &f0, &f1);
       o[0] = mfma16<DT>(f0, pf, o[0]);
       o[1] = mfma16<DT>(f1, pf, o[1]);
@@ -398,27 +422,51 @@ struct Rows16 {
         o[7] = mfma16<DT>(f1, pf, o[7]);
       }
     } else {
-      constexpr int H = D == 128 ? 4 : 2;       // tiles of even nibbles
-      unsigned w[8];
+      // The value scales are on the probabilities, one operand per scale
+      // group: the integers are exact, and p s is rounded where p was.
+      float pr[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = int4_even(v[i]);
-      value_pair_int4<DT, false>(w, sc, &f0, &f1);
-      o[0] = mfma16<DT>(f0, pf, o[0]);
-      o[1] = mfma16<DT>(f1, pf, o[1]);
-      if constexpr (D == 128) {
-        value_pair_int4<DT, true>(w, sc, &f0, &f1);
-        o[2] = mfma16<DT>(f0, pf, o[2]);
-        o[3] = mfma16<DT>(f1, pf, o[3]);
+      for (int i = 0; i < 8; ++i) pr[i] = exp2_hw(s[i] - base);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) sum += pr[i] + pr[i + 1];
+      u32x4 pf[D / 64];
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g) {
+        float ps[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ps[i] = pr[i] * vs[g][i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf[g][i] = pack2<DT>(ps[2 * i], ps[2 * i + 1]);
       }
+      unsigned ev[8], od[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = int4_odd(v[i]);
-      value_pair_int4<DT, false>(w, sc, &f0, &f1);
-      o[H] = mfma16<DT>(f0, pf, o[H]);
-      o[H + 1] = mfma16<DT>(f1, pf, o[H + 1]);
+      for (int i = 0; i < 8; ++i) {
+        unsigned w;
+        if constexpr (D == 128) {
+          // lanes n and n + 8 hold eight columns of either group: each takes
+          // four of both, the first group's in the low half
+          const unsigned u = unsigned(__builtin_amdgcn_update_dpp(0, int(t.v[i]), 0x128, 0xF, 0xF, false));   // row_ror:8
+          w = __builtin_amdgcn_perm(t.v[i], u, m < 8 ? 0x01000504u : 0x07060302u);
+        } else {
+          w = t.v[i] >> (16 * (m & 1));
+        }
+        ev[i] = int4_even(w);
+        od[i] = int4_odd(w);
+      }
+      u32x4 f0, f1;
+      value_pair_int4<DT, false>(ev, &f0, &f1);
+      o[0] = mfma16<DT>(f0, pf[0], o[0]);
+      o[1] = mfma16<DT>(f1, pf[0], o[1]);
+      value_pair_int4<DT, false>(od, &f0, &f1);
+      o[2] = mfma16<DT>(f0, pf[0], o[2]);
+      o[3] = mfma16<DT>(f1, pf[0], o[3]);
       if constexpr (D == 128) {
-        value_pair_int4<DT, true>(w, sc, &f0, &f1);
-        o[6] = mfma16<DT>(f0, pf, o[6]);
-        o[7] = mfma16<DT>(f1, pf, o[7]);
+        value_pair_int4<DT, true>(ev, &f0, &f1);
+        o[4] = mfma16<DT>(f0, pf[1], o[4]);
+        o[5] = mfma16<DT>(f1, pf[1], o[5]);
+        value_pair_int4<DT, true>(od, &f0, &f1);
+        o[6] = mfma16<DT>(f0, pf[1], o[6]);
+        o[7] = mfma16<DT>(f1, pf[1], o[7]);
       }
     }
   }
@@ -465,7 +513,6 @@ __global__ __launch_bounds__(256, 2) void k_attn16(AttnParams p) {
   // workgroup -> (request, head, row tile, chunk), chunk fastest
   unsigned id = blockIdx.x;
   const int split = int(id % unsigned(p.splits));
-  const int64_t item = int64_t(id / unsigned(p.splits));
   id /= unsigned(p.splits);
   const int rt = int(id % unsigned(p.row_tiles));
   id /= unsigned(p.row_tiles);
@@ -529,12 +576,12 @@ __global__ __launch_bounds__(256, 2) void k_attn16(AttnParams p) {
   const int row_o = rt * 16 + orow;
   if (row_o >= rows) return;
   if (range.n > 1) {
-    const int64_t at = (item * p.splits + split) * 16 + orow;
+    const int64_t at = ((int64_t(req) * p.heads + h) * p.row_slots + row_o) * p.splits + split;
     float* y = p.part + at * D + d;
 #pragma unroll
     for (int i = 0; i < PER; i += 4) *reinterpret_cast<f32x4*>(y + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
     if ((int(threadIdx.x) & 15) == 0) {
-      float* bs = p.part + int64_t(gridDim.x) * 16 * D + at * 2;
+      float* bs = p.part + int64_t(p.requests) * p.heads * p.row_slots * p.splits * D + at * 2;
       bs[0] = base;
       bs[1] = sum;
     }
@@ -547,50 +594,405 @@ __global__ __launch_bounds__(256, 2) void k_attn16(AttnParams p) {
   for (int i = 0; i < PER; ++i) f[i] *= inv;
   store_row<DT, D>(p, tok, head, d, f);
   if (p.lse && (int(threadIdx.x) & 15) == 0)
-    p.lse[tok * p.q_heads + head] = sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0.69314718055994531f;
+    p.lse[tok * p.q_heads + head] = row_lse(base, sum);
 }
 
-// Joins the chunks of an item, in chunk order.
-template <int DT, int FMT, int D>
-__global__ __launch_bounds__(256) void k_attn_join(AttnParams p) {
-  constexpr int PER = D / 16;
+// --------------------------------------------------- wide row tiles (prompts)
+// 32 query rows a wave on 32x32x16, NW waves that share each stage of KT keys:
+// the workgroup turns a stage's codes into 16-bit operands once, in LDS, in the
+// order in which the matrix core reads them (16 bytes a lane, no conflicts):
+//   K  [chunk of 8 elements][key]   key rows dealt out so that a lane's S^T
+//      registers are 8 neighbouring keys at a time, the operand of O^T = V^T P^T
+//   V  [8 keys][column]             column slots dealt out so that a tile of 32
+//      holds one INT4 scale group and a lane's results are 4 neighbours
+// Stages are double-buffered: stage i + 1 is written and stage i + 2 requested
+// while stage i is multiplied, with one barrier a stage.
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (DT == SVDQ_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ float half_max(float x) {      // over lanes l, l ^ 32
+  const unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+template <int FMT, int D, int NW>
+struct Stage {
+  static constexpr int KT = 64 * NW * 32 / D;     // keys a stage: one 32-element piece of K a thread
+  static constexpr int PAGES = KT / 16;           // page lookups a stage
+  u32x4 k;                  // 32 codes of one key
+  unsigned ke;              // its e8m0, or the key's fp16 scales (thread < KT)
+  unsigned v[8];            // 4 codes of 8 keys
+  u32x4 vsc[FMT == SVDQ_FMT_MXFP4_G32 ? (D == 128 ? 2 : 1) : 1];   // MXFP4: the 8 keys' scales; INT4: [0][0] scales of key `thread`
+};
+
+template <int DT, int FMT, int D, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
+  using St = Stage<FMT, D, NW>;
+  constexpr int KT = St::KT, NC = D / 8, NB = D / 32, NS = D / 16, NX = D / 32, NG = D / 64, PAGES = St::PAGES;
+  constexpr bool MX = FMT == SVDQ_FMT_MXFP4_G32;
+  __shared__ u32x4 sk[2][NC * KT];
+  __shared__ u32x4 sv[2][KT / 8 * D];
+  __shared__ __attribute__((aligned(16))) unsigned sks[2][MX ? 1 : KT], svs[2][MX ? 1 : KT];
+  __shared__ float sve[2][KT / 64];     // exponent of the largest value scale of 64 keys
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  // workgroup -> (row tile, request, head, chunk), chunk fastest; the last row
+  // tiles, which see most keys, first; one head's tiles keep to one XCD where
+  // the number of heads allows it
   unsigned id = blockIdx.x;
-  const int64_t item = id;
-  const int rt = int(id % unsigned(p.row_tiles));
-  id /= unsigned(p.row_tiles);
-  const int h = int(id % unsigned(p.heads)), req = int(id / unsigned(p.heads));
+  const int split = int(id % unsigned(p.splits));
+  id /= unsigned(p.splits);
+  const int h = int(id % unsigned(p.heads));
+  id /= unsigned(p.heads);
+  const int req = int(id % unsigned(p.requests));
+  const int rt = p.row_tiles - 1 - int(id / unsigned(p.requests));
+  constexpr int ROWS = 32 * NW;
   const Request r(p, req);
   const int rows = r.rows * p.group;
-  const int row = rt * 16 + (int(threadIdx.x) >> 4), d = (int(threadIdx.x) & 15) * PER;
-  if (row >= rows) return;
-  const TileRange range(p, r, rt, 16);
-  if (range.n <= 1) return;
-  const int64_t at = item * p.splits * 16 + (int(threadIdx.x) >> 4);
-  const float* bs = p.part + int64_t(gridDim.x) * p.splits * 16 * D;
-  float base = LOWEST;
-  for (int s = 0; s < range.n; ++s) base = fmaxf(base, bs[(at + s * 16) * 2]);
-  float sum = 0.0f, f[PER];
+  if (rt * ROWS >= rows) return;
+  const TileRange range(p, r, rt, ROWS);
+  if (split >= max(range.n, 1)) return;
+  const int m = lane & 31, hb = lane >> 5;
+  const int row = rt * ROWS + 32 * wave + m;
+  const int qi = min(row / p.group, r.rows - 1), qh = h * p.group + row % p.group;
+  const int low = r.low(p, qi), high = row < rows ? r.high(p, qi) : 0;
+  // this wave's rows
+  const int wrow = rt * ROWS + 32 * wave, wq0 = min(wrow / p.group, r.rows - 1), wq1 = min((wrow + 31) / p.group, r.rows - 1);
+  const int wfrom = r.low(p, wq0), wto = wrow < rows ? r.high(p, wq1) : 0, wall_low = r.low(p, wq1), wall_high = r.high(p, wq0);
+  u32x4 q[NS];
+  {
+    const uint16_t* src = p.q + (r.first + qi) * p.qt + int64_t(qh) * p.qh + 8 * hb;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) f[i] = 0.0f;
-  for (int s = 0; s < range.n; ++s) {
-    const float a = exp2_hw(bs[(at + s * 16) * 2] - base);
-    sum += a * bs[(at + s * 16) * 2 + 1];
-    const float* y = p.part + (at + s * 16) * D + d;
+    for (int s = 0; s < NS; ++s) q[s] = query_order<FMT>(*reinterpret_cast<const u32x4*>(src + 16 * s));
+    if (p.c < 0.0f) {       // the sign of the scale goes to the query: the largest product is the largest logit
 #pragma unroll
-    for (int i = 0; i < PER; i += 4) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(y + i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[i + e] += a * v[e];
+      for (int s = 0; s < NS; ++s) q[s] ^= 0x80008000u;
     }
   }
+  const float c = fabsf(p.c);
+  f32x16 o[NX];
+#pragma unroll
+  for (int x = 0; x < NX; ++x)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[x][i] = 0.0f;
+  float base = LOWEST, sum = 0.0f;
+
+  const int from = range.from + split * p.chunk, to = min(range.to, from + p.chunk);
+  const int32_t* table = p.table + int64_t(req) * p.table_stride;
+  const int last_col = (r.len - 1) >> p.page_shift, in_page = (1 << p.page_shift) - 1;
+  const int kkey = tid / NB, kb = tid % NB;                   // K piece: key of the stage, 32-element block
+  const int vkeys = tid / (D / 4) * 8, vn = tid % (D / 4);    // V block: first of 8 keys, columns 4 vn ..
+  // a lane's page of the stage at `token`; every wave looks all of them up
+  auto look_up = [&](int token) {
+    const int t = token + 16 * (lane % PAGES);
+    return table[min(t >> p.page_shift, last_col)];
+  };
+  auto bad_pages = [&](int page) { return unsigned(__ballot(page < 0 || page >= p.n_pages)); };   // bit i: keys 16 i ..
+  auto request = [&](St& st, int token, int page) {
+    const int good = page < 0 || page >= p.n_pages ? 0 : page;
+    const int kp = __shfl(good, kkey / 16), vp = __shfl(good, vkeys / 16);
+    const int64_t krow = ((int64_t(kp) * p.heads + h) << p.page_shift) + ((token + kkey) & in_page);
+    const int64_t vrow = ((int64_t(vp) * p.heads + h) << p.page_shift) + ((token + vkeys) & in_page);
+    st.k = *reinterpret_cast<const u32x4*>(p.kc + krow * (D / 2) + 16 * kb);
+    const uint8_t* vc = p.vc + vrow * (D / 2) + 2 * vn;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st.v[i] = *reinterpret_cast<const uint16_t*>(vc + i * (D / 2));
+    if constexpr (MX) {
+      st.ke = p.ks[krow * NB + kb];
+      const u32x4* vs = reinterpret_cast<const u32x4*>(p.vs + vrow * NB);
+      st.vsc[0] = vs[0];
+      if constexpr (D == 128) st.vsc[1] = vs[1];
+    } else {
+      // thread t < KT brings key t's scales
+      const int sp = __shfl(good, (tid % KT) / 16);
+      if (tid < KT) {
+        const int64_t srow = ((int64_t(sp) * p.heads + h) << p.page_shift) + ((token + tid) & in_page);
+        if constexpr (D == 128) {
+          st.ke = reinterpret_cast<const unsigned*>(p.ks)[srow];
+          st.vsc[0][0] = reinterpret_cast<const unsigned*>(p.vs)[srow];
+        } else {
+          st.ke = reinterpret_cast<const uint16_t*>(p.ks)[srow];
+          st.vsc[0][0] = reinterpret_cast<const uint16_t*>(p.vs)[srow];
+        }
+      }
+    }
+  };
+  auto write = [&](const St& st, int buf, int token, unsigned bad) {
+    // K: key row with bits 2 and 3 exchanged, and an exchange of neighbours by
+    // block that spreads the writes over the banks
+    const int krow = ((kkey & ~12) | ((kkey & 4) << 1) | ((kkey & 8) >> 1)) ^ (kb << 1);
+    const float ks = MX ? mx_scale<DT>(st.ke) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sk[buf][(4 * kb + j) * KT + krow] = key_frag<DT, FMT>(st.k[j], ks);
+    const int slot = 64 * (vn / 16) + vn % 16;                 // column 4 vn + j: slot + 16 j
+    u32x4* v = &sv[buf][vkeys / 8 * D + slot];
+    u32x4 f0, f1;
+    if constexpr (MX) {
+      // keys past the end or on a missing page may hold a NaN: zero
+      const bool gone = (bad >> (vkeys / 16)) & 1u;
+      float sc[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sc[i] = value_scale<DT, FMT, D>(st.vsc, i, D == 128 ? vn >> 3 : vn >> 3);
+      if (gone || token + vkeys + 8 > r.len) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sc[i] = gone || token + vkeys + i >= r.len ? 0.0f : sc[i];
+      }
+      value_pair_mx<DT, 0>(st.v, sc, &f0, &f1);
+      v[0] = f0;
+      v[16] = f1;
+      value_pair_mx<DT, 1>(st.v, sc, &f0, &f1);
+      v[32] = f0;
+      v[48] = f1;
+    } else {
+      unsigned w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = int4_even(st.v[i]);
+      value_pair_int4<DT, false>(w, &f0, &f1);
+      v[0] = f0;
+      v[32] = f1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = int4_odd(st.v[i]);
+      value_pair_int4<DT, false>(w, &f0, &f1);
+      v[16] = f0;
+      v[48] = f1;
+      if (tid < KT) {
+        sks[buf][tid] = st.ke;
+        const bool gone = ((bad >> (tid / 16)) & 1u) || token + tid >= r.len;
+        const unsigned w = gone ? 0u : st.vsc[0][0];
+        svs[buf][tid] = w;
+        if constexpr (scaled_reference<DT, FMT>()) {
+          const f16x2 f = two_halves(w);
+          float most = fmaxf(float(f[0]), float(f[1]));
+#pragma unroll
+          for (int x = 1; x < 64; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
+          if (lane == 0) sve[buf][wave] = scale_exponent(most);
+        }
+      }
+    }
+  };
+  // 64 keys of stage `buf` from key `at` of the stage on
+  auto step = [&](int buf, int token, int at, unsigned bad) {
+    const int t0 = token + at;
+    if (t0 >= wto || t0 + 64 <= wfrom) return;
+    float s[32];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      f32x16 acc[NG];
+#pragma unroll
+      for (int g = 0; g < (MX ? 1 : NG); ++g)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[g][i] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < NS; ++e) {
+        const int chunk = 2 * e + hb;
+        const u32x4 a = sk[buf][chunk * KT + ((at + 32 * kt + m) ^ ((e / 2) << 1))];
+        acc[MX ? 0 : e / 4] = mfma32<DT>(a, q[e], acc[MX ? 0 : e / 4]);
+      }
+      if constexpr (MX) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[16 * kt + i] = acc[0][i];
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {     // keys 16 (x / 2) + 8 hb + 4 (x % 2) ..
+          const u32x4 w = *reinterpret_cast<const u32x4*>(&sks[buf][at + 32 * kt + 16 * (x / 2) + 8 * hb + 4 * (x % 2)]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f16x2 f = two_halves(w[i]);
+            float d = acc[0][4 * x + i] * float(f[0]);
+            if constexpr (NG == 2) d = __builtin_fmaf(acc[1][4 * x + i], float(f[1]), d);
+            s[16 * kt + 4 * x + i] = d;
+          }
+        }
+      }
+    }
+    const unsigned gone = (bad >> (at / 16)) & 15u;
+    if (!(t0 >= wall_low && t0 + 64 <= wall_high && gone == 0u)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int k = 32 * (i / 16) + 16 * ((i % 16) / 8) + 8 * hb + i % 8;
+        const bool see = t0 + k >= low && t0 + k < high && ((gone >> (i / 8)) & 1u) == 0u;
+        s[i] = see ? s[i] : -__builtin_inff();
+      }
+    }
+    float top = s[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i]);
+    top = half_max(top) * c - p_shift<DT>();
+    if constexpr (scaled_reference<DT, FMT>()) top += sve[buf][at / 64];
+    if (__any(top > base + SLACK)) {
+      const float next = fmaxf(base, top), alpha = exp2_hw(base - next);
+      base = next;
+      sum *= alpha;
+#pragma unroll
+      for (int x = 0; x < NX; ++x) o[x] *= alpha;
+    }
+    float part = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      s[i] = exp2_hw(__builtin_fmaf(s[i], c, -base));
+      part += s[i];
+    }
+    sum += part;
+    u32x4 pf[MX ? 1 : NG][4];
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pf[0][i / 4][i % 4] = pack2<DT>(s[2 * i], s[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {       // keys 16 (x / 2) + 8 hb + 4 (x % 2) ..
+        const u32x4 w = *reinterpret_cast<const u32x4*>(&svs[buf][at + 16 * (x / 2) + 8 * hb + 4 * (x % 2)]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[i] = s[4 * x + i] * float(two_halves(w[i])[g]);
+          }
+          pf[g][x / 2][2 * (x % 2)] = pack2<DT>(f[0], f[1]);
+          pf[g][x / 2][2 * (x % 2) + 1] = pack2<DT>(f[2], f[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const u32x4 a = sv[buf][(at / 8 + 2 * j + hb) * D + 32 * x + m];
+        o[x] = mfma32<DT>(a, pf[MX ? 0 : x / 2][j], o[x]);
+      }
+    }
+  };
+
+  if (from < to) {
+    St st;
+    int page = look_up(from);
+    unsigned bad = bad_pages(page), bad1 = 0;
+    request(st, from, page);
+    page = look_up(from + KT);
+    write(st, 0, from, bad);
+    if (from + KT < to) {
+      bad1 = bad_pages(page);
+      request(st, from + KT, page);
+      page = look_up(from + 2 * KT);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int token = from; token < to; token += KT) {
+      const unsigned here = bad;
+      if (token + KT < to) {
+        write(st, buf ^ 1, token + KT, bad1);
+        bad = bad1;
+        if (token + 2 * KT < to) {
+          bad1 = bad_pages(page);
+          request(st, token + 2 * KT, page);
+          page = look_up(token + 3 * KT);
+        }
+      }
+#pragma unroll 1
+      for (int at = 0; at < KT && token + at < to; at += 64) step(buf, token, at, here);
+      __syncthreads();
+      buf ^= 1;
+    }
+  }
+  sum = half_sum(sum);
+  if (row >= rows) return;
+  const bool whole = range.n <= 1;
+  const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
+  const int64_t tok = r.first + row / p.group;
+  const int head = h * p.group + row % p.group;
+  const int64_t slot = ((int64_t(req) * p.heads + h) * p.row_slots + row) * p.splits + split;
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int d = 64 * g + 4 * (8 * (i / 4) + 4 * hb + i % 4);
+      const f32x4 f = {o[2 * g][i] * inv, o[2 * g][i + 8] * inv, o[2 * g + 1][i] * inv, o[2 * g + 1][i + 8] * inv};
+      if (whole) *reinterpret_cast<u32x2*>(p.out + tok * p.ot + head * p.oh + d) = u32x2{pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3])};
+      else *reinterpret_cast<f32x4*>(p.part + slot * D + d) = f;
+    }
+  if (hb != 0) return;
+  if (!whole) {
+    float* bs = p.part + int64_t(p.requests) * p.heads * p.row_slots * p.splits * D + slot * 2;
+    bs[0] = base;
+    bs[1] = sum;
+  } else if (p.lse) {
+    p.lse[tok * p.q_heads + head] = row_lse(base, sum);
+  }
+}
+
+// Joins the chunks of a row: a workgroup per row.  Its threads fetch all
+// references at once, then 1024 / D groups of D / 4 threads walk the chunks and
+// meet in LDS in a fixed order.
+template <int DT, int FMT, int D, int ROWS>
+__global__ __launch_bounds__(256) void k_attn_join(AttnParams p) {
+  constexpr int L = D / 4, G = 256 / L;
+  __shared__ float sw[256];             // weights of 256 chunks
+  __shared__ float red[G][D];
+  __shared__ float wave_v[4], wave_s[4];
+  const int tid = int(threadIdx.x);
+  unsigned id = blockIdx.x;
+  const int row = int(id % unsigned(p.row_slots));
+  id /= unsigned(p.row_slots);
+  const int h = int(id % unsigned(p.heads)), req = int(id / unsigned(p.heads));
+  const Request r(p, req);
+  if (row >= r.rows * p.group) return;
+  const TileRange range(p, r, row / ROWS, ROWS);
+  if (range.n <= 1) return;
+  const int64_t at = int64_t(blockIdx.x) * p.splits;
+  const f32x2* bs = reinterpret_cast<const f32x2*>(p.part + int64_t(gridDim.x) * p.splits * D) + at;
+  float base = LOWEST;
+  for (int s = tid; s < range.n; s += 256) base = fmaxf(base, bs[s][0]);
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) base = fmaxf(base, __shfl_xor(base, m));
+  if ((tid & 63) == 0) wave_v[tid / 64] = base;
+  __syncthreads();
+  base = fmaxf(fmaxf(wave_v[0], wave_v[1]), fmaxf(wave_v[2], wave_v[3]));
+  float sum = 0.0f;
+  f32x4 f = {0, 0, 0, 0};
+  const int grp = tid / L, d = (tid % L) * 4;
+  for (int s0 = 0; s0 < range.n; s0 += 256) {
+    const int n = min(256, range.n - s0);
+    if (tid < n) {
+      const f32x2 v = bs[s0 + tid];
+      const float a = exp2_hw(v[0] - base);
+      sw[tid] = a;
+      sum += a * v[1];
+    }
+    __syncthreads();
+    const float* y = p.part + (at + s0) * D + d;
+#pragma unroll 4
+    for (int s = grp; s < n; s += G) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(y + int64_t(s) * D);
+      const float a = sw[s];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] += a * v[e];
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
+  if ((tid & 63) == 0) wave_s[tid / 64] = sum;
+  *reinterpret_cast<f32x4*>(&red[grp][d]) = f;
+  __syncthreads();
+  sum = (wave_s[0] + wave_s[1]) + (wave_s[2] + wave_s[3]);
+  if (tid >= D / 2) return;
+  float f0 = 0.0f, f1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < G; ++i) { f0 += red[i][2 * tid]; f1 += red[i][2 * tid + 1]; }
   const int64_t tok = r.first + row / p.group;
   const int head = h * p.group + row % p.group;
   const float inv = sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) f[i] *= inv;
-  store_row<DT, D>(p, tok, head, d, f);
-  if (p.lse && (int(threadIdx.x) & 15) == 0)
-    p.lse[tok * p.q_heads + head] = sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0.69314718055994531f;
+  *reinterpret_cast<unsigned*>(p.out + tok * p.ot + head * p.oh + 2 * tid) = pack2<DT>(f0 * inv, f1 * inv);
+  if (p.lse && tid == 0) p.lse[tok * p.q_heads + head] = row_lse(base, sum);
 }
 
 // ---------------------------------------------------------------- host side
@@ -610,7 +1012,9 @@ int device_cus() {
 // bounds the chunks of any call with these requests, rows and lengths, whatever
 // its window, so that one workspace serves them all.
 struct Cut {
-  int64_t items;
+  int64_t items;            // requests x heads x row tiles
+  int64_t row_slots;        // rows of a request and head
+  int rows;                 // rows of a tile: 16 (k_attn16), 128 or 256 (k_attn_rows)
   int row_tiles, splits, chunk, most;
 };
 
@@ -628,35 +1032,47 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   Cut t;
   const int64_t group = d->q_heads / c->heads;
   const int64_t max_q = d->max_q < d->tokens ? d->max_q : d->tokens;
-  const int64_t tiles = ceil_div(max_q * group, 16);
+  t.row_slots = max_q * group;
+  t.rows = t.row_slots <= 64 ? 16 : 128;
+  if (t.rows == 128 && d->requests * c->heads * ceil_div(t.row_slots, 256) >= int64_t(device_cus())) t.rows = 256;
+  const int64_t tiles = ceil_div(t.row_slots, t.rows);
   t.items = d->requests * c->heads * tiles;
   int64_t span = d->max_kv;
   const bool causal = (d->flags & SVDQ_ATTN_CAUSAL) != 0u;   // else a row sees up to the end, whatever its window
   if (causal && d->window > 0 && int64_t(d->window) + max_q < span) span = int64_t(d->window) + max_q;
   if (d->window > 0) span += 31;        // the first tile is rounded down to 32
-  // Chunks of at least 128 keys (a tile for each wave), as many as fill the
-  // chip about four workgroups deep.
-  const int64_t want = ceil_div(int64_t(device_cus()) * 4, t.items > 0 ? t.items : 1);
-  const int64_t all = ceil_div(int64_t(d->max_kv) + 31, 128), here = ceil_div(span, 128);
-  const int64_t n = want < here ? want : here > 0 ? here : 1;
+  // Chunks of at least 128 keys (a tile for each wave of k_attn16) or 512, as
+  // many as fill the chip about four workgroups deep (two of the wide ones).
+  const int64_t least = t.rows == 16 ? 128 : 512;
+  const int64_t want = ceil_div(int64_t(device_cus()) * (t.rows == 16 ? 4 : 2), t.items > 0 ? t.items : 1);
+  const int64_t all = ceil_div(int64_t(d->max_kv) + 31, least), here = ceil_div(span, least);
+  const int64_t n = t.rows == 256 ? 1 : want < here ? want : here > 0 ? here : 1;
   const int64_t chunk = ceil_div(ceil_div(span > 0 ? span : 1, n), 128) * 128;
   t.splits = int(ceil_div(span > 0 ? span : 1, chunk));
-  t.most = int(want < all ? want : all);
+  t.most = int(t.rows == 256 ? 1 : want < all ? want : all);
   t.chunk = int(chunk);
   t.row_tiles = int(tiles);
-  if (t.items * t.most >= (int64_t(1) << 31)) return SVDQ_ERR_UNSUPPORTED;
+  if (t.items * t.most >= (int64_t(1) << 31) || d->requests * c->heads * t.row_slots >= (int64_t(1) << 31)) return SVDQ_ERR_UNSUPPORTED;
   *out = t;
   return SVDQ_OK;
 }
 
-size_t part_bytes(const Cut& t, int splits, int D) {
-  return splits > 1 ? size_t(t.items) * size_t(splits) * 16 * size_t(D + 2) * 4 : 0;
+size_t part_bytes(const svdq_attn_desc* d, const svdq_kv_cache* c, const Cut& t, int splits) {
+  return splits > 1 ? size_t(d->requests) * size_t(c->heads) * size_t(t.row_slots) * size_t(splits) * size_t(c->head_dim + 2) * 4 : 0;
 }
 
 template <int DT, int FMT, int D>
 void launch_attn(const AttnParams& p, const Cut& t, hipStream_t st) {
-  k_attn16<DT, FMT, D><<<dim3(unsigned(t.items * t.splits)), 256, 0, st>>>(p);
-  if (t.splits > 1) k_attn_join<DT, FMT, D><<<dim3(unsigned(t.items)), 256, 0, st>>>(p);
+  const dim3 grid(unsigned(t.items * t.splits)), joins(unsigned(int64_t(p.requests) * p.heads * t.row_slots));
+  if (t.rows == 16) {
+    k_attn16<DT, FMT, D><<<grid, 256, 0, st>>>(p);
+    if (t.splits > 1) k_attn_join<DT, FMT, D, 16><<<joins, 256, 0, st>>>(p);
+  } else if (t.rows == 128) {
+    k_attn_rows<DT, FMT, D, 4><<<grid, 256, 0, st>>>(p);
+    if (t.splits > 1) k_attn_join<DT, FMT, D, 128><<<joins, 256, 0, st>>>(p);
+  } else {
+    k_attn_rows<DT, FMT, D, 8><<<grid, 512, 0, st>>>(p);
+  }
 }
 
 template <int DT, int FMT>
@@ -675,7 +1091,7 @@ extern "C" svdq_status svdq_kv_attention_workspace(const svdq_attn_desc* d, cons
   if (d->requests == 0 || d->tokens == 0 || d->max_q == 0) return SVDQ_OK;
   Cut t;
   if ((st = cut_of(d, c, &t)) != SVDQ_OK) return st;
-  *bytes = part_bytes(t, t.most, c->head_dim);
+  *bytes = part_bytes(d, c, t, t.most);
   return SVDQ_OK;
 }
 
@@ -690,7 +1106,7 @@ extern "C" svdq_status svdq_kv_attention(const svdq_attn_desc* d, const svdq_hea
   if (!d->q_start || !d->kv_len || (d->table_stride > 0 && !d->block_table)) return SVDQ_ERR_INVALID_ARG;
   Cut t;
   if ((st = cut_of(d, c, &t)) != SVDQ_OK) return st;
-  const size_t need = part_bytes(t, t.splits, c->head_dim);
+  const size_t need = part_bytes(d, c, t, t.splits);
   if (need > 0) {
     if (!ws) return SVDQ_ERR_INVALID_ARG;
     if (ws_bytes < need) return SVDQ_ERR_CAPACITY;
@@ -713,9 +1129,10 @@ extern "C" svdq_status svdq_kv_attention(const svdq_attn_desc* d, const svdq_hea
   p.max_q = d->max_q; p.max_kv = d->max_kv; p.window = d->window;
   p.causal = (d->flags & SVDQ_ATTN_CAUSAL) != 0u;
   p.page_shift = page_shift(c->page_size);
-  p.row_tiles = t.row_tiles; p.splits = t.splits; p.chunk = t.chunk;
+  p.row_tiles = t.row_tiles; p.row_slots = int32_t(t.row_slots); p.splits = t.splits; p.chunk = t.chunk;
   const bool mx = c->fmt == SVDQ_FMT_MXFP4_G32, bf = d->dtype == SVDQ_BF16;
   p.c = d->scale * 1.44269504088896341f * (mx && !bf ? 8.0f : 1.0f);
+  if (p.c == 0.0f) p.c = 1.2e-38f;      // every logit is zero to fp32, and a masked -infinity stays one
   if (bf) {
     if (mx) launch_attn<SVDQ_BF16, SVDQ_FMT_MXFP4_G32>(p, t, c->head_dim, stream);
     else launch_attn<SVDQ_BF16, SVDQ_FMT_INT4_G64>(p, t, c->head_dim, stream);

@@ -357,25 +357,34 @@ __global__ __launch_bounds__(256) void k_rows_grad(RowParams p) {
   }
 }
 
-// weight gradient = sum of the partial rows, in a fixed order: 16 rows of
-// lanes walk the partials, then meet in LDS
-__global__ __launch_bounds__(256) void k_rows_grad_sum(const float* pq, const float* pk, float* dq, float* dk, int parts, int D) {
+// Weight gradient = sum of the partial rows, in a fixed order: 64 groups of 4
+// lanes (16 columns) walk the partials, four loads in flight each, then meet in
+// LDS.
+__global__ __launch_bounds__(1024) void k_rows_grad_sum(const float* pq, const float* pk, float* dq, float* dk, int parts, int D) {
   const float* part = blockIdx.y == 0 ? pq : pk;
   float* out = blockIdx.y == 0 ? dq : dk;
   if (out == nullptr) return;
-  const int col = int(blockIdx.x) * 16 + int(threadIdx.x) % 16, lane = int(threadIdx.x) / 16;
-  float s = 0.0f;
-  if (part != nullptr)
-    for (int i = lane; i < parts; i += 16) s += part[int64_t(i) * D + col];
-  __shared__ float red[16][17];
-  red[lane][int(threadIdx.x) % 16] = s;
-  __syncthreads();
-  if (lane == 0) {
-    float v = 0.0f;
+  const int lane = int(threadIdx.x) % 16, grp = int(threadIdx.x) / 16, col = int(blockIdx.x) * 16 + lane;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (part != nullptr) {
+    int i = grp;
+    for (; i + 192 < parts; i += 256) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += red[i][int(threadIdx.x)];
-    out[col] = v;
+      for (int u = 0; u < 4; ++u) s[u] += part[int64_t(i + 64 * u) * D + col];
+    }
+    for (; i < parts; i += 64) s[0] += part[int64_t(i) * D + col];
   }
+  __shared__ float red[64][17];
+  red[grp][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (threadIdx.x >= 256) return;
+  float v = (red[grp][lane] + red[grp + 16][lane]) + (red[grp + 32][lane] + red[grp + 48][lane]);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  __shared__ float last[4][16];
+  if ((int(threadIdx.x) & 63) < 16) last[int(threadIdx.x) / 64][lane] = v;
+  __syncthreads();
+  if (threadIdx.x < 16) out[col] = (last[0][lane] + last[1][lane]) + (last[2][lane] + last[3][lane]);
 }
 
 struct ReadParams {
@@ -755,7 +764,7 @@ extern "C" svdq_status svdq_qk_norm_rope_backward(const svdq_qk_desc* d, const s
     if (d->dtype == SVDQ_BF16) launch_grad<SVDQ_BF16>(p, lanes, blocks, ops, stream);
     else launch_grad<SVDQ_F16>(p, lanes, blocks, ops, stream);
   }
-  if (dwq || dwk) k_rows_grad_sum<<<dim3(unsigned(D / 16), 2), 256, 0, stream>>>(p.part[0], p.part[1], dwq, dwk, blocks, D);
+  if (dwq || dwk) k_rows_grad_sum<<<dim3(unsigned(D / 16), 2), 1024, 0, stream>>>(p.part[0], p.part[1], dwq, dwk, blocks, D);
   return launch_ok();
 }
 

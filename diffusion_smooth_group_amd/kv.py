@@ -30,6 +30,7 @@ MAX_REQUESTS = 8192
 GROUP = {FMT_MXFP4_G32: 32, FMT_INT4_G64: 64}
 SCALE_DTYPE = {FMT_MXFP4_G32: torch.uint8, FMT_INT4_G64: torch.float16}
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, without building a Stream
 _DTYPES = {torch.float16: S.F16, torch.bfloat16: S.BF16}
 _P, _I64, _I32, _U, _F, _SZ = C.c_void_p, C.c_int64, C.c_int32, C.c_uint, C.c_float, C.c_size_t
 
@@ -81,48 +82,65 @@ def _call(name, *args):
         raise SvdqError(name, rc)
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
 def _heads(t, name, tokens, dim, dtype):
-    _need(t.is_cuda and t.dim() == 3 and t.dtype == dtype, f"{name}: a {dtype} GPU tensor [tokens, heads, D] is needed")
     n, h, d = t.shape
-    _need(n == tokens and d == dim, f"{name}: shape {tuple(t.shape)} does not fit {tokens} tokens of heads of {dim}")
     s0, s1, s2 = t.stride()
-    _need(s2 == 1 or d == 1, f"{name}: D must have unit stride")
+    if n != tokens or d != dim or s2 != 1 or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{name}: a {dtype} GPU tensor [{tokens}, heads, {dim}] with unit stride in the last dimension is needed, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return svdq_heads(t.data_ptr(), s0 if n > 1 else 0, s1 if h > 1 else 0, h)
 
 
-def _int32(t, name, n=None):
-    _need(t.is_cuda and t.dtype == torch.int32 and t.is_contiguous(), f"{name}: a contiguous int32 GPU tensor is needed")
-    _need(n is None or t.numel() == n, f"{name}: {n} entries are needed, got {t.numel()}")
+def _int32(t, name, n):
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: a contiguous int32 GPU tensor of {n} entries is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
+def _table(t, b):
+    if t.dim() != 2 or t.shape[0] != b:
+        raise ValueError(f"block_table: [{b}, pages] is needed, got {tuple(t.shape)}")
+    return _int32(t, "block_table", t.numel())
+
+
+def _weight(w, name, dim, dtype):
+    if w is None:
+        return None
+    if w.dtype is not dtype or w.numel() != dim or not w.is_contiguous() or not w.is_cuda:
+        raise ValueError(f"{name}: a contiguous {dtype} GPU tensor of {dim} is needed")
+    return w.data_ptr()
+
+
+def _code(dtype):
+    c = _DTYPES.get(dtype)
+    if c is None:
+        raise ValueError(f"float16 or bfloat16 rows are needed, got {dtype}")
+    return c
+
+
+def _stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return _raw_stream(t.get_device())
+
+
 def _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions):
-    _need(dtype in _DTYPES, f"float16 or bfloat16 rows are needed, got {dtype}")
-    d = svdq_qk_desc(tokens, dim, _DTYPES[dtype])
-    flags = QK_NORM if norm else 0
-    d.eps = eps
+    flags = pq = pk = pc = ps = pp = n = 0
     if norm:
-        for field, w in (("wq", wq), ("wk", wk)):
-            if w is not None:
-                _need(w.is_cuda and w.dtype == dtype and w.is_contiguous() and w.numel() == dim,
-                      f"{field}: a contiguous {dtype} GPU tensor of {dim} is needed")
-                setattr(d, field, w.data_ptr())
-    _need((cos is None) == (sin is None), "cos and sin go together")
+        flags, pq, pk = QK_NORM, _weight(wq, "wq", dim, dtype), _weight(wk, "wk", dim, dtype)
     if cos is not None:
-        flags |= QK_ROPE | (QK_ROPE_HALVES if halves else 0)
+        flags |= QK_ROPE | QK_ROPE_HALVES if halves else QK_ROPE
+        n = cos.shape[0]
         for t in (cos, sin):
-            _need(t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 2 and t.shape[1] * 2 == dim
-                  and t.shape[0] == cos.shape[0], "cos, sin: contiguous float32 GPU tables [positions, D / 2] are needed")
-        d.cos, d.sin, d.n_positions = cos.data_ptr(), sin.data_ptr(), cos.shape[0]
+            if t is None or t.dtype is not torch.float32 or t.dim() != 2 or t.shape[0] != n or t.shape[1] * 2 != dim \
+                    or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"cos, sin: contiguous float32 GPU tables [positions, {dim} / 2] are needed")
+        pc, ps = cos.data_ptr(), sin.data_ptr()
         if positions is not None:
-            d.positions = _int32(positions, "positions", tokens)
-    d.flags = flags
-    return d
+            pp = _int32(positions, "positions", tokens)
+    elif sin is not None:
+        raise ValueError("cos and sin go together")
+    return svdq_qk_desc(tokens, dim, _code(dtype), flags, eps, pq, pk, pc, ps, n, pp)
 
 
 # ------------------------------------------------------------ norm and rotation
@@ -140,7 +158,7 @@ def qk_norm_rope(q, k, cos=None, sin=None, wq=None, wk=None, eps: float = 1e-6, 
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
     _call("svdq_qk_norm_rope", d, _heads(q, "q", tokens, dim, q.dtype), _heads(k, "k", tokens, dim, q.dtype),
-          _heads(q_out, "q_out", tokens, dim, q.dtype), _heads(k_out, "k_out", tokens, dim, q.dtype), S._stream(stream))
+          _heads(q_out, "q_out", tokens, dim, q.dtype), _heads(k_out, "k_out", tokens, dim, q.dtype), _stream(stream, q))
     return q_out, k_out
 
 
@@ -162,7 +180,7 @@ def qk_norm_rope_backward(gq, gk, q, k, cos=None, sin=None, wq=None, wk=None, ep
         ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
     h = [_heads(t, n, tokens, dim, q.dtype) for t, n in ((q, "q"), (k, "k"), (gq, "gq"), (gk, "gk"), (dq, "dq"), (dk, "dk"))]
     _call("svdq_qk_norm_rope_backward", d, *h, dw.data_ptr(), dw.data_ptr() + 4 * dim, ws.data_ptr(), ws.numel(),
-          S._stream(stream))
+          _stream(stream, q))
     return dq, dk, dw[0], dw[1]
 
 
@@ -206,13 +224,13 @@ class KVCache:
         """A cache in buffers that the caller has.  fmt: FMT_MXFP4_G32,
         FMT_INT4_G64, or "mxfp4_g32", "int4_g64"."""
         fmt = S.FMT_CODES.get(fmt, fmt)
-        _need(fmt in GROUP, f"cache format {fmt!r}")
-        _need(k_codes.dim() == 4, "codes: [pages, heads, page_size, D / 2] is needed")
+        if fmt not in GROUP or k_codes.dim() != 4:
+            raise ValueError(f"codes [pages, heads, page_size, D / 2] of a 4-bit format are needed, got {fmt!r} {tuple(k_codes.shape)}")
         shape, dim = k_codes.shape[:3], 2 * k_codes.shape[3]
         for t, kind, last in ((k_codes, torch.uint8, dim // 2), (v_codes, torch.uint8, dim // 2),
                               (k_scales, SCALE_DTYPE[fmt], dim // GROUP[fmt]), (v_scales, SCALE_DTYPE[fmt], dim // GROUP[fmt])):
-            _need(t.is_cuda and t.is_contiguous() and t.dtype == kind and t.shape == (*shape, last),
-                  f"a contiguous {kind} GPU tensor {(*shape, last)} is needed, got {t.dtype} {tuple(t.shape)}")
+            if not t.is_cuda or not t.is_contiguous() or t.dtype is not kind or t.shape != (*shape, last):
+                raise ValueError(f"a contiguous {kind} GPU tensor {(*shape, last)} is needed, got {t.dtype} {tuple(t.shape)}")
         self = cls.__new__(cls)
         self._hold(k_codes, k_scales, v_codes, v_scales, fmt)
         return self
@@ -238,7 +256,7 @@ class KVCache:
                 q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             hq, ho = _heads(q, "q", tokens, dim, k.dtype), _heads(q_out, "q_out", tokens, dim, k.dtype)
         _call("svdq_kv_append", d, hq, _heads(k, "k", tokens, dim, k.dtype), _heads(v, "v", tokens, dim, k.dtype), ho, self.c,
-              _int32(slots, "slots", tokens), S._stream(stream))
+              _int32(slots, "slots", tokens), _stream(stream, k))
         return q_out
 
     def read(self, slots, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
@@ -246,11 +264,11 @@ class KVCache:
         for slots outside the cache."""
         n = slots.numel()
         shape = (n, self.heads, self.head_dim)
-        _need(dtype in _DTYPES, f"float16 or bfloat16 is needed, got {dtype}")
+        code = _code(dtype)
         k_out = torch.empty(shape, dtype=dtype, device=self.device) if k_out is None else k_out
         v_out = torch.empty(shape, dtype=dtype, device=self.device) if v_out is None else v_out
-        _call("svdq_kv_read", self.c, _int32(slots, "slots"), n, _DTYPES[dtype], _heads(k_out, "k_out", n, self.head_dim, dtype),
-              _heads(v_out, "v_out", n, self.head_dim, dtype), S._stream(stream))
+        _call("svdq_kv_read", self.c, _int32(slots, "slots", n), n, code, _heads(k_out, "k_out", n, self.head_dim, dtype),
+              _heads(v_out, "v_out", n, self.head_dim, dtype), _stream(stream, k_out))
         return k_out, v_out
 
 
@@ -271,7 +289,6 @@ def plan(past, fresh, block_table, free_pages, free_count, page_size: int, token
     (free_count [1] of them are free).  tokens: length of the slot map, at
     least the sum of fresh (the rest is -1)."""
     b = past.numel()
-    _need(block_table.dim() == 2 and block_table.shape[0] == b, "block_table: [requests, pages] is needed")
     out = torch.empty(2 * b + 3 + 2 * tokens, dtype=torch.int32, device=past.device)
     at = out.data_ptr()
     cuts = (b + 1, b, tokens, tokens, 1, 1)
@@ -280,9 +297,9 @@ def plan(past, fresh, block_table, free_pages, free_count, page_size: int, token
     for n in cuts:
         p.append(ptr)
         ptr += 4 * n
-    _call("svdq_kv_plan", _int32(past, "past"), _int32(fresh, "fresh", b), b, page_size, tokens, _int32(free_pages, "free_pages"),
-          _int32(free_count, "free_count", 1), free_pages.numel(), _int32(block_table, "block_table"), block_table.shape[1], *p,
-          S._stream(stream))
+    _call("svdq_kv_plan", _int32(past, "past", b), _int32(fresh, "fresh", b), b, page_size, tokens, _int32(free_pages, "free_pages", free_pages.numel()),
+          _int32(free_count, "free_count", 1), free_pages.numel(), _table(block_table, b), block_table.shape[1], *p,
+          _stream(stream, past))
     return Plan(block_table, q_start, kv_len, slots, positions, left, missing)
 
 
@@ -290,10 +307,9 @@ def release(done, block_table, kv_len, free_pages, free_count, page_size: int, s
     """Gives the pages of the requests with done != 0 back to free_pages (in
     place: free_pages, free_count, block_table and kv_len)."""
     b = done.numel()
-    _need(block_table.dim() == 2 and block_table.shape[0] == b, "block_table: [requests, pages] is needed")
-    _call("svdq_kv_release", _int32(done, "done"), b, page_size, _int32(block_table, "block_table"), block_table.shape[1],
-          _int32(kv_len, "kv_len", b), _int32(free_pages, "free_pages"), _int32(free_count, "free_count", 1), free_pages.numel(),
-          S._stream(stream))
+    _call("svdq_kv_release", _int32(done, "done", b), b, page_size, _table(block_table, b), block_table.shape[1],
+          _int32(kv_len, "kv_len", b), _int32(free_pages, "free_pages", free_pages.numel()), _int32(free_count, "free_count", 1), free_pages.numel(),
+          _stream(stream, done))
 
 
 # --------------------------------------------------------------------- attention
@@ -315,20 +331,19 @@ def attention(q, cache: KVCache, block_table, q_start, kv_len, max_q: int, max_k
     the rows and cached tokens of a request.  scale: 1 / sqrt(D) by default.
     A row that sees nothing gives zeros.  Returns out, or (out, lse)."""
     tokens, hq, dim = q.shape
-    _need(dim == cache.head_dim, f"q: heads of {dim} over a cache of heads of {cache.head_dim}")
-    _need(q.dtype in _DTYPES, f"float16 or bfloat16 rows are needed, got {q.dtype}")
+    if dim != cache.head_dim:
+        raise ValueError(f"q: heads of {dim} over a cache of heads of {cache.head_dim}")
     b = kv_len.numel()
-    _need(block_table.dim() == 2 and block_table.shape[0] == b, "block_table: [requests, pages] is needed")
     if out is None:
         out = torch.empty((tokens, hq, dim), dtype=q.dtype, device=q.device)
     lse = torch.empty((tokens, hq), dtype=torch.float32, device=q.device) if return_lse else None
-    d = svdq_attn_desc(b, tokens, hq, _DTYPES[q.dtype], max_q, max_kv, window, ATTN_CAUSAL if causal else 0,
+    d = svdq_attn_desc(b, tokens, hq, _code(q.dtype), max_q, max_kv, window, ATTN_CAUSAL if causal else 0,
                        1.0 / math.sqrt(dim) if scale is None else scale, _int32(q_start, "q_start", b + 1),
-                       _int32(kv_len, "kv_len"), _int32(block_table, "block_table"), block_table.shape[1])
+                       _int32(kv_len, "kv_len", b), _table(block_table, b), block_table.shape[1])
     if ws is None:
         need = _SZ(0)
         _call("svdq_kv_attention_workspace", d, cache.c, need)
         ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
     _call("svdq_kv_attention", d, _heads(q, "q", tokens, dim, q.dtype), cache.c, _heads(out, "out", tokens, dim, q.dtype),
-          None if lse is None else lse.data_ptr(), ws.data_ptr() if ws.numel() else None, ws.numel(), S._stream(stream))
+          None if lse is None else lse.data_ptr(), ws.data_ptr() if ws.numel() else None, ws.numel(), _stream(stream, q))
     return (out, lse) if return_lse else out

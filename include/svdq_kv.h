@@ -172,8 +172,9 @@ typedef struct {
  * outside the cache are not seen.  lse: NULL or fp32 [tokens][q_heads], the
  * natural logarithm of the sum of exponentials.  Products are on the 16-bit
  * matrix cores with fp32 accumulation, softmax statistics are fp32, the
- * probabilities are rounded to 16 bits for the second product.  With f16,
- * cached values above 65504 count as 65504.  ws: >= svdq_kv_attention_workspace
+ * probabilities (INT4: times the value scale) are rounded to 16 bits for the
+ * second product.  With f16, MXFP4 scales above 2^15 count as 2^15 and ones
+ * below 2^-124 as 2^-124.  ws: >= svdq_kv_attention_workspace
  * bytes, 256-byte aligned (may be NULL where that is 0); its content need
  * not be kept between calls.  The size goes by requests, tokens, q_heads,
  * max_q, max_kv and the cache's shape alone. */
