@@ -143,20 +143,6 @@ struct Request {
   }
 };
 
-// Cache rows of 16 neighbouring tokens of one head, and whether their page is there.
-struct HalfTile {
-  int64_t row;
-  bool ok;
-};
-__device__ __forceinline__ HalfTile half_tile(const AttnParams& p, const int32_t* table, int token, int last_col, int h) {
-  const int col = min(token >> p.page_shift, last_col);
-  const int page = __builtin_amdgcn_readfirstlane(table[col]);
-  HalfTile t;
-  t.ok = page >= 0 && page < p.n_pages;
-  t.row = ((int64_t(t.ok ? page : 0) * p.heads + h) << p.page_shift) + (token & ((1 << p.page_shift) - 1));
-  return t;
-}
-
 // ----------------------------------------------------- 16 rows and one wave
 // S^T = K Q^T on 16x16x32: keys are rows of the result, query rows its
 // columns, so that a lane holds the probabilities of one query row for the
@@ -176,46 +162,59 @@ struct Tile32 {
   u32x4 vsc[NS];            // scales of these keys
   bool ok0, ok1;            // the pages of the tile's halves are there
 
-  __device__ __forceinline__ void load(const AttnParams& p, const HalfTile& h0, const HalfTile& h1, int lane) {
+  // page0, page1: the pages of the tile's two halves, the same for all lanes.
+  // Where a page holds the whole tile every address is a scalar base plus the
+  // lane's fixed offset; pages of 16 give the lanes of either half their own.
+  __device__ __forceinline__ void load(const AttnParams& p, int token, int page0, int page1, int h, int lane) {
+    ok0 = page0 >= 0 && page0 < p.n_pages;
+    ok1 = page1 >= 0 && page1 < p.n_pages;
+    const int64_t row0 = ((int64_t(ok0 ? page0 : 0) * p.heads + h) << p.page_shift) + (token & ((1 << p.page_shift) - 1));
+    if (p.page_shift > 4) {
+      load_rows(p, row0, 0, lane);
+    } else {
+      const int64_t row1 = (int64_t(ok1 ? page1 : 0) * p.heads + h) << 4;
+      load_rows(p, row0, row1 - 16 - row0, lane);
+    }
+  }
+  // shift: distance of the second half's rows from where they would follow
+  __device__ __forceinline__ void load_rows(const AttnParams& p, int64_t row0, int64_t shift, int lane) {
     const int m = lane & 15, b = lane >> 4;
-    ok0 = h0.ok;
-    ok1 = h1.ok;
+    constexpr int SB = D / 32;                  // scale bytes of a row
+    const uint8_t *kc = p.kc + row0 * (D / 2), *ks = p.ks + row0 * SB, *vc = p.vc + row0 * (D / 2), *vs = p.vs + row0 * SB;
+    const int64_t kshift = m >= 8 ? shift : 0, vshift = b >= 2 ? shift : 0;
+    const uint8_t *kc1 = kc + kshift * (D / 2), *ks1 = ks + kshift * SB, *vc1 = vc + vshift * (D / 2), *vs1 = vs + vshift * SB;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      const int lt = 8 * (m >> 2) + 4 * a + (m & 3);
-      const int64_t row = (m >= 8 ? h1.row - 16 : h0.row) + lt;
-      const uint8_t* c = p.kc + row * (D / 2);
+      const unsigned lt = unsigned(8 * (m >> 2) + 4 * a + (m & 3));
       if constexpr (FMT == SVDQ_FMT_MXFP4_G32) {
         if constexpr (D == 128) {
-          const u32x4 w = *reinterpret_cast<const u32x4*>(c + 16 * b);
+          const u32x4 w = *reinterpret_cast<const u32x4*>(kc1 + (lt * 64u + 16u * b));
           k[a][0] = w[0]; k[a][1] = w[1]; k[a][2] = w[2]; k[a][3] = w[3];
-          ke[a] = p.ks[row * 4 + b];
+          ke[a] = ks1[lt * 4u + b];
         } else {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(c + 8 * b);
+          const u32x2 w = *reinterpret_cast<const u32x2*>(kc1 + (lt * 32u + 8u * b));
           k[a][0] = w[0]; k[a][1] = w[1];
-          ke[a] = p.ks[row * 2 + (b >> 1)];
+          ke[a] = ks1[lt * 2u + (b >> 1)];
         }
       } else {
 #pragma unroll
         for (int g = 0; g < D / 64; ++g) {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(c + 32 * g + 8 * b);
+          const u32x2 w = *reinterpret_cast<const u32x2*>(kc1 + (lt * unsigned(D / 2) + 32u * g + 8u * b));
           k[a][2 * g] = w[0];
           k[a][2 * g + 1] = w[1];
         }
       }
     }
-    const int64_t row = (b >= 2 ? h1.row - 16 : h0.row) + 8 * b;
-    const uint8_t* c = p.vc + row * (D / 2) + (D == 128 ? 4 * m : 4 * (m >> 1));
+    const unsigned vo = unsigned(8 * b * (D / 2) + (D == 128 ? 4 * m : 4 * (m >> 1)));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const unsigned*>(c + i * (D / 2));
-    constexpr int SB = FMT == SVDQ_FMT_MXFP4_G32 ? D / 32 : D / 32;   // scale bytes of a row
-    const u32x4* sv = reinterpret_cast<const u32x4*>(p.vs + row * SB);
+    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const unsigned*>(vc1 + (vo + unsigned(i * (D / 2))));
 #pragma unroll
-    for (int i = 0; i < NS; ++i) vsc[i] = sv[i];
+    for (int i = 0; i < NS; ++i) vsc[i] = *reinterpret_cast<const u32x4*>(vs1 + (8u * b * SB + 16u * i));
     if constexpr (FMT == SVDQ_FMT_INT4_G64) {
-      const u32x4* sk = reinterpret_cast<const u32x4*>(p.ks + row * SB);
+      // the lane's rows of S^T are the keys of its V block
+      const uint8_t* kss = ks + vshift * SB;
 #pragma unroll
-      for (int i = 0; i < NS; ++i) ksc[i] = sk[i];
+      for (int i = 0; i < NS; ++i) ksc[i] = *reinterpret_cast<const u32x4*>(kss + (8u * b * SB + 16u * i));
     }
   }
 };
@@ -250,6 +249,17 @@ __device__ __forceinline__ unsigned high_halves(unsigned x0, unsigned x1) { retu
 
 // (by value: a bit cast of a vector's element in place reads element 0)
 __device__ __forceinline__ f16x2 two_halves(unsigned u) { return __builtin_bit_cast(f16x2, u); }
+
+// a * (half H of h) + c in one mixed-precision instruction.  With c a zero that
+// the compiler does not know for one, the plain product takes one too (a
+// constant zero is folded into a conversion and a product).
+template <int H>
+__device__ __forceinline__ float fma_half(float a, unsigned h, float c) { return __builtin_fmaf(a, float(two_halves(h)[H]), c); }
+__device__ __forceinline__ float hidden_zero() {
+  float z = 0.0f;
+  asm("" : "+v"(z));
+  return z;
+}
 
 template <int FMT>
 __device__ __forceinline__ u32x4 query_order(u32x4 q) {
@@ -537,18 +547,32 @@ __global__ __launch_bounds__(256, 2) void k_attn16(AttnParams p) {
   const int from = range.from + split * p.chunk, to = min(range.to, from + p.chunk);
   const int32_t* table = p.table + int64_t(req) * p.table_stride;
   const int last_col = (r.len - 1) >> p.page_shift;
-  int token = from + 32 * wave;
-  Tile32<FMT, D> cur, next;
-  if (token < to) {
-    cur.load(p, half_tile(p, table, token, last_col, h), half_tile(p, table, token + 16, last_col, h), lane);
-    for (;;) {
-      const int after = token + 128;
-      if (after < to) next.load(p, half_tile(p, table, after, last_col, h), half_tile(p, table, after + 16, last_col, h), lane);
-      const bool all = token >= range.all_low && token + 32 <= range.all_high && cur.ok0 && cur.ok1;
-      w.step(p, cur, token, r.len, all, lane);
-      if (after >= to) break;
-      cur = next;
-      token = after;
+  // This wave's tiles: from + 32 (wave + 4 i).  Their pages are fetched 64
+  // tiles at a time, one a lane, so that no tile waits for a table entry.
+  const int first = from + 32 * __builtin_amdgcn_readfirstlane(wave), tiles = first < to ? (to - first + 127) / 128 : 0;
+  int pages0 = 0, pages1 = 0;
+  auto fetch = [&](Tile32<FMT, D>& t, int i) {
+    if ((i & 63) == 0) {
+      const int at = first + 128 * (i + lane);
+      pages0 = table[min(at >> p.page_shift, last_col)];
+      pages1 = p.page_shift > 4 ? pages0 : table[min((at + 16) >> p.page_shift, last_col)];
+    }
+    t.load(p, first + 128 * i, __builtin_amdgcn_readlane(pages0, i & 63), __builtin_amdgcn_readlane(pages1, i & 63), h, lane);
+  };
+  auto multiply = [&](const Tile32<FMT, D>& t, int i) {
+    const int token = first + 128 * i;
+    w.step(p, t, token, r.len, token >= range.all_low && token + 32 <= range.all_high && t.ok0 && t.ok1, lane);
+  };
+  if (tiles > 0) {
+    Tile32<FMT, D> t0, t1;
+    fetch(t0, 0);
+    for (int i = 0;;) {
+      if (i + 1 < tiles) fetch(t1, i + 1);
+      multiply(t0, i);
+      if (++i >= tiles) break;
+      if (i + 1 < tiles) fetch(t0, i + 1);
+      multiply(t1, i);
+      if (++i >= tiles) break;
     }
   }
   // rows of lane (m, b), tile x, register i: column value_col(4 b + i, x)
@@ -625,6 +649,20 @@ __device__ __forceinline__ float half_sum(float x) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+// N matrix instructions that take an operand from LDS each: four reads go ahead
+// of the first, then one behind each (left alone, the compiler waits for nearly
+// every read right where it is used).
+template <int N>
+__device__ __forceinline__ void reads_ahead() {
+  __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+  for (int i = 0; i < N - 4; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+}
+
 template <int FMT, int D, int NW>
 struct Stage {
   static constexpr int KT = 64 * NW * 32 / D;     // keys a stage: one 32-element piece of K a thread
@@ -640,6 +678,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   using St = Stage<FMT, D, NW>;
   constexpr int KT = St::KT, NC = D / 8, NB = D / 32, NS = D / 16, NX = D / 32, NG = D / 64, PAGES = St::PAGES;
   constexpr bool MX = FMT == SVDQ_FMT_MXFP4_G32;
+  constexpr int NA = MX ? 1 : NG;       // accumulators of a logit (INT4: one a scale group)
   __shared__ u32x4 sk[2][NC * KT];
   __shared__ u32x4 sv[2][KT / 8 * D];
   __shared__ __attribute__((aligned(16))) unsigned sks[2][MX ? 1 : KT], svs[2][MX ? 1 : KT];
@@ -662,20 +701,20 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   const TileRange range(p, r, rt, ROWS);
   if (split >= max(range.n, 1)) return;
   const int m = lane & 31, hb = lane >> 5;
-  const int row = rt * ROWS + 32 * wave + m;
+  // this wave's rows
+  const int wrow = rt * ROWS + 32 * wave, wq0 = min(wrow / p.group, r.rows - 1), wq1 = min((wrow + 32 - 1) / p.group, r.rows - 1);
+  const int wfrom = r.low(p, wq0), wto = wrow < rows ? r.high(p, wq1) : 0, wall_low = r.low(p, wq1), wall_high = r.high(p, wq0);
+  const int row = wrow + m;
   const int qi = min(row / p.group, r.rows - 1), qh = h * p.group + row % p.group;
   const int low = r.low(p, qi), high = row < rows ? r.high(p, qi) : 0;
-  // this wave's rows
-  const int wrow = rt * ROWS + 32 * wave, wq0 = min(wrow / p.group, r.rows - 1), wq1 = min((wrow + 31) / p.group, r.rows - 1);
-  const int wfrom = r.low(p, wq0), wto = wrow < rows ? r.high(p, wq1) : 0, wall_low = r.low(p, wq1), wall_high = r.high(p, wq0);
   u32x4 q[NS];
   {
     const uint16_t* src = p.q + (r.first + qi) * p.qt + int64_t(qh) * p.qh + 8 * hb;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) q[s] = query_order<FMT>(*reinterpret_cast<const u32x4*>(src + 16 * s));
+    for (int e = 0; e < NS; ++e) q[e] = query_order<FMT>(*reinterpret_cast<const u32x4*>(src + 16 * e));
     if (p.c < 0.0f) {       // the sign of the scale goes to the query: the largest product is the largest logit
 #pragma unroll
-      for (int s = 0; s < NS; ++s) q[s] ^= 0x80008000u;
+      for (int e = 0; e < NS; ++e) q[e] ^= 0x80008000u;
     }
   }
   const float c = fabsf(p.c);
@@ -685,6 +724,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[x][i] = 0.0f;
   float base = LOWEST, sum = 0.0f;
+  const float zero = hidden_zero();
 
   const int from = range.from + split * p.chunk, to = min(range.to, from + p.chunk);
   const int32_t* table = p.table + int64_t(req) * p.table_stride;
@@ -726,7 +766,24 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       }
     }
   };
-  auto write = [&](const St& st, int buf, int token, unsigned bad) {
+  // Keys past the end or on a missing page may hold a NaN: their value scales
+  // become zero (MXFP4: the smallest), before the stage is turned into operands.
+  auto mend = [&](St& st, int token, unsigned bad) {
+    if (bad == 0u && token + KT <= r.len) return;       // the same for all threads
+    if constexpr (MX) {
+      const bool gone = (bad >> (vkeys / 16)) & 1u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool zero = gone || token + vkeys + i >= r.len;
+        if constexpr (D == 128) st.vsc[i / 4][i % 4] = zero ? 0u : st.vsc[i / 4][i % 4];
+        else st.vsc[0][i / 2] = zero ? st.vsc[0][i / 2] & (i % 2 ? 0x0000FFFFu : 0xFFFF0000u) : st.vsc[0][i / 2];
+      }
+    } else {
+      const bool gone = ((bad >> ((tid % KT) / 16)) & 1u) || token + tid >= r.len;
+      st.vsc[0][0] = gone ? 0u : st.vsc[0][0];
+    }
+  };
+  auto write = [&](const St& st, int buf) {
     // K: key row with bits 2 and 3 exchanged, and an exchange of neighbours by
     // block that spreads the writes over the banks
     const int krow = ((kkey & ~12) | ((kkey & 4) << 1) | ((kkey & 8) >> 1)) ^ (kb << 1);
@@ -737,15 +794,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     u32x4* v = &sv[buf][vkeys / 8 * D + slot];
     u32x4 f0, f1;
     if constexpr (MX) {
-      // keys past the end or on a missing page may hold a NaN: zero
-      const bool gone = (bad >> (vkeys / 16)) & 1u;
       float sc[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sc[i] = value_scale<DT, FMT, D>(st.vsc, i, D == 128 ? vn >> 3 : vn >> 3);
-      if (gone || token + vkeys + 8 > r.len) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sc[i] = gone || token + vkeys + i >= r.len ? 0.0f : sc[i];
-      }
+      for (int i = 0; i < 8; ++i) sc[i] = value_scale<DT, FMT, D>(st.vsc, i, vn >> 3);
       value_pair_mx<DT, 0>(st.v, sc, &f0, &f1);
       v[0] = f0;
       v[16] = f1;
@@ -764,39 +815,36 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       value_pair_int4<DT, false>(w, &f0, &f1);
       v[16] = f0;
       v[48] = f1;
-      if (tid < KT) {
-        sks[buf][tid] = st.ke;
-        const bool gone = ((bad >> (tid / 16)) & 1u) || token + tid >= r.len;
-        const unsigned w = gone ? 0u : st.vsc[0][0];
-        svs[buf][tid] = w;
-        if constexpr (scaled_reference<DT, FMT>()) {
-          const f16x2 f = two_halves(w);
-          float most = fmaxf(float(f[0]), float(f[1]));
-#pragma unroll
-          for (int x = 1; x < 64; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
-          if (lane == 0) sve[buf][wave] = scale_exponent(most);
-        }
-      }
     }
   };
-  // 64 keys of stage `buf` from key `at` of the stage on
-  auto step = [&](int buf, int token, int at, unsigned bad) {
-    const int t0 = token + at;
-    if (t0 >= wto || t0 + 64 <= wfrom) return;
-    float s[32];
+  auto write_scales = [&](const St& st, int buf) {             // INT4
+    if (MX || tid >= KT) return;
+    sks[buf][tid] = st.ke;
+    svs[buf][tid] = st.vsc[0][0];
+    if constexpr (scaled_reference<DT, FMT>()) {
+      const f16x2 f = two_halves(st.vsc[0][0]);
+      float most = fmaxf(float(f[0]), float(f[1]));
+#pragma unroll
+      for (int x = 1; x < 64; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
+      if (lane == 0) sve[buf][wave] = scale_exponent(most);
+    }
+  };
+
+  // Logits of 64 keys of stage `buf` from key `at` of it on.
+  auto logits = [&](int buf, int at, float* s) {
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
-      f32x16 acc[NG];
+      f32x16 acc[NA];
 #pragma unroll
-      for (int g = 0; g < (MX ? 1 : NG); ++g)
+      for (int g = 0; g < NA; ++g)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[g][i] = 0.0f;
 #pragma unroll
       for (int e = 0; e < NS; ++e) {
-        const int chunk = 2 * e + hb;
-        const u32x4 a = sk[buf][chunk * KT + ((at + 32 * kt + m) ^ ((e / 2) << 1))];
+        const u32x4 a = sk[buf][(2 * e + hb) * KT + ((at + 32 * kt + m) ^ ((e / 2) << 1))];
         acc[MX ? 0 : e / 4] = mfma32<DT>(a, q[e], acc[MX ? 0 : e / 4]);
       }
+      reads_ahead<NS>();
       if constexpr (MX) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[16 * kt + i] = acc[0][i];
@@ -806,14 +854,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
           const u32x4 w = *reinterpret_cast<const u32x4*>(&sks[buf][at + 32 * kt + 16 * (x / 2) + 8 * hb + 4 * (x % 2)]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const f16x2 f = two_halves(w[i]);
-            float d = acc[0][4 * x + i] * float(f[0]);
-            if constexpr (NG == 2) d = __builtin_fmaf(acc[1][4 * x + i], float(f[1]), d);
+            float d = fma_half<0>(acc[0][4 * x + i], w[i], zero);
+            if constexpr (NG == 2) d = fma_half<1>(acc[NA - 1][4 * x + i], w[i], d);
             s[16 * kt + 4 * x + i] = d;
           }
         }
       }
     }
+  };
+  // Masks them and raises the rows' references where they need it.
+  auto refer = [&](int buf, int token, int at, unsigned bad, float* s) {
+    const int t0 = token + at;
     const unsigned gone = (bad >> (at / 16)) & 15u;
     if (!(t0 >= wall_low && t0 + 64 <= wall_high && gone == 0u)) {
 #pragma unroll
@@ -835,6 +886,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
 #pragma unroll
       for (int x = 0; x < NX; ++x) o[x] *= alpha;
     }
+  };
+  // Probabilities of these keys as operands.
+  auto weigh = [&](int buf, int at, float* s, u32x4 (*pf)[4]) {
     float part = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
@@ -842,7 +896,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       part += s[i];
     }
     sum += part;
-    u32x4 pf[MX ? 1 : NG][4];
     if constexpr (MX) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) pf[0][i / 4][i % 4] = pack2<DT>(s[2 * i], s[2 * i + 1]);
@@ -851,17 +904,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       for (int x = 0; x < 8; ++x) {       // keys 16 (x / 2) + 8 hb + 4 (x % 2) ..
         const u32x4 w = *reinterpret_cast<const u32x4*>(&svs[buf][at + 16 * (x / 2) + 8 * hb + 4 * (x % 2)]);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float f[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[i] = s[4 * x + i] * float(two_halves(w[i])[g]);
-          }
-          pf[g][x / 2][2 * (x % 2)] = pack2<DT>(f[0], f[1]);
-          pf[g][x / 2][2 * (x % 2) + 1] = pack2<DT>(f[2], f[3]);
+        for (int i = 0; i < 4; i += 2) {
+          const float p0 = s[4 * x + i], p1 = s[4 * x + i + 1];
+          pf[0][x / 2][2 * (x % 2) + i / 2] = pack2<DT>(fma_half<0>(p0, w[i], zero), fma_half<0>(p1, w[i + 1], zero));
+          if constexpr (NG == 2)
+            pf[NA - 1][x / 2][2 * (x % 2) + i / 2] = pack2<DT>(fma_half<1>(p0, w[i], zero), fma_half<1>(p1, w[i + 1], zero));
         }
       }
     }
+  };
+  auto add_values = [&](int buf, int at, const u32x4 (*pf)[4]) {
 #pragma unroll
     for (int x = 0; x < NX; ++x) {
 #pragma unroll
@@ -870,6 +922,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
         o[x] = mfma32<DT>(a, pf[MX ? 0 : x / 2][j], o[x]);
       }
     }
+    reads_ahead<4 * NX>();
   };
 
   if (from < to) {
@@ -878,18 +931,23 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     unsigned bad = bad_pages(page), bad1 = 0;
     request(st, from, page);
     page = look_up(from + KT);
-    write(st, 0, from, bad);
+    mend(st, from, bad);
+    write(st, 0);
+    write_scales(st, 0);
     if (from + KT < to) {
       bad1 = bad_pages(page);
       request(st, from + KT, page);
       page = look_up(from + 2 * KT);
     }
     __syncthreads();
+    auto used = [&](int t) { return t < wto && t + 64 > wfrom && t < to; };
     int buf = 0;
     for (int token = from; token < to; token += KT) {
       const unsigned here = bad;
       if (token + KT < to) {
-        write(st, buf ^ 1, token + KT, bad1);
+        mend(st, token + KT, bad1);
+        write_scales(st, buf ^ 1);
+        write(st, buf ^ 1);
         bad = bad1;
         if (token + 2 * KT < to) {
           bad1 = bad_pages(page);
@@ -897,8 +955,22 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
           page = look_up(token + 3 * KT);
         }
       }
-#pragma unroll 1
-      for (int at = 0; at < KT && token + at < to; at += 64) step(buf, token, at, here);
+#pragma unroll 2
+      for (int at = 0; at < KT; at += 64) {
+        if (!used(token + at)) continue;
+        float s[32];
+        u32x4 pf[NA][4];
+        // the wave that multiplies issues before the one beside it that does
+        // not, which keeps the two apart
+        __builtin_amdgcn_s_setprio(1);
+        logits(buf, at, s);
+        __builtin_amdgcn_s_setprio(0);
+        refer(buf, token, at, here, s);
+        weigh(buf, at, s, pf);
+        __builtin_amdgcn_s_setprio(1);
+        add_values(buf, at, pf);
+        __builtin_amdgcn_s_setprio(0);
+      }
       __syncthreads();
       buf ^= 1;
     }
@@ -1042,9 +1114,11 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   if (causal && d->window > 0 && int64_t(d->window) + max_q < span) span = int64_t(d->window) + max_q;
   if (d->window > 0) span += 31;        // the first tile is rounded down to 32
   // Chunks of at least 128 keys (a tile for each wave of k_attn16) or 512, as
-  // many as fill the chip about four workgroups deep (two of the wide ones).
+  // many as fill the chip about eight workgroups deep (two of the wide ones):
+  // 48 requests of up to 16384 tokens, 8 heads: 140 us at four, 129 at eight,
+  // 138 at twelve.
   const int64_t least = t.rows == 16 ? 128 : 512;
-  const int64_t want = ceil_div(int64_t(device_cus()) * (t.rows == 16 ? 4 : 2), t.items > 0 ? t.items : 1);
+  const int64_t want = ceil_div(int64_t(device_cus()) * (t.rows == 16 ? 8 : 2), t.items > 0 ? t.items : 1);
   const int64_t all = ceil_div(int64_t(d->max_kv) + 31, least), here = ceil_div(span, least);
   const int64_t n = t.rows == 256 ? 1 : want < here ? want : here > 0 ? here : 1;
   const int64_t chunk = ceil_div(ceil_div(span > 0 ? span : 1, n), 128) * 128;
