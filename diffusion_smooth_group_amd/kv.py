@@ -91,6 +91,14 @@ def _heads(t, name, tokens, dim, dtype):
     return svdq_heads(t.data_ptr(), s0 if n > 1 else 0, s1 if h > 1 else 0, h)
 
 
+def _new(like):
+    """An output of like's shape and type, and its view for the call."""
+    t = torch.empty_like(like)
+    s0, s1, _ = t.stride()
+    n, h, _ = t.shape
+    return t, svdq_heads(t.data_ptr(), s0 if n > 1 else 0, s1 if h > 1 else 0, h)
+
+
 def _int32(t, name, n):
     if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: a contiguous int32 GPU tensor of {n} entries is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -131,10 +139,10 @@ def _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions):
     if cos is not None:
         flags |= QK_ROPE | QK_ROPE_HALVES if halves else QK_ROPE
         n = cos.shape[0]
-        for t in (cos, sin):
-            if t is None or t.dtype is not torch.float32 or t.dim() != 2 or t.shape[0] != n or t.shape[1] * 2 != dim \
-                    or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError(f"cos, sin: contiguous float32 GPU tables [positions, {dim} / 2] are needed")
+        f32, shape = torch.float32, (n, dim // 2)
+        if sin is None or cos.dtype is not f32 or sin.dtype is not f32 or cos.shape != shape or sin.shape != shape \
+                or not (cos.is_contiguous() and sin.is_contiguous() and cos.is_cuda and sin.is_cuda):
+            raise ValueError(f"cos, sin: contiguous float32 GPU tables [positions, {dim} / 2] are needed")
         pc, ps = cos.data_ptr(), sin.data_ptr()
         if positions is not None:
             pp = _int32(positions, "positions", tokens)
@@ -152,13 +160,18 @@ def qk_norm_rope(q, k, cos=None, sin=None, wq=None, wk=None, eps: float = 1e-6, 
     (i, i + D/2), else (2i, 2i + 1).  Returns (q_out, k_out); q_out=q, k_out=k
     work in place."""
     tokens, _, dim = q.shape
-    d = _desc(tokens, dim, q.dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+    dtype = q.dtype
+    d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+    hq, hk = _heads(q, "q", tokens, dim, dtype), _heads(k, "k", tokens, dim, dtype)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out, hqo = _new(q)
+    else:
+        hqo = _heads(q_out, "q_out", tokens, dim, dtype)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    _call("svdq_qk_norm_rope", d, _heads(q, "q", tokens, dim, q.dtype), _heads(k, "k", tokens, dim, q.dtype),
-          _heads(q_out, "q_out", tokens, dim, q.dtype), _heads(k_out, "k_out", tokens, dim, q.dtype), _stream(stream, q))
+        k_out, hko = _new(k)
+    else:
+        hko = _heads(k_out, "k_out", tokens, dim, dtype)
+    _call("svdq_qk_norm_rope", d, hq, hk, hqo, hko, _stream(stream, q))
     return q_out, k_out
 
 
@@ -168,20 +181,20 @@ def qk_norm_rope_backward(gq, gk, q, k, cos=None, sin=None, wq=None, wk=None, ep
     and its inputs.  Returns (dq, dk, dwq, dwk), the weight gradients fp32 [D]
     (zero without ``norm``)."""
     tokens, _, dim = q.shape
-    d = _desc(tokens, dim, q.dtype, cos, sin, wq, wk, eps, norm, halves, positions)
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if dk is None:
-        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    dw = torch.empty((2, dim), dtype=torch.float32, device=q.device)
+    dtype = q.dtype
+    d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+    h = [_heads(t, n, tokens, dim, dtype) for t, n in ((q, "q"), (k, "k"), (gq, "gq"), (gk, "gk"))]
+    for t, like, n in ((dq, q, "dq"), (dk, k, "dk")):
+        h.append(_new(like) if t is None else (t, _heads(t, n, tokens, dim, dtype)))
+    (dq, hdq), (dk, hdk) = h[4:]
+    dwq, dwk = dw = q.new_empty((2, dim), dtype=torch.float32).unbind()
     if ws is None:
         need = _SZ(0)
         _call("svdq_qk_backward_workspace", d, q.shape[1], k.shape[1], need)
-        ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-    h = [_heads(t, n, tokens, dim, q.dtype) for t, n in ((q, "q"), (k, "k"), (gq, "gq"), (gk, "gk"), (dq, "dq"), (dk, "dk"))]
-    _call("svdq_qk_norm_rope_backward", d, *h, dw.data_ptr(), dw.data_ptr() + 4 * dim, ws.data_ptr(), ws.numel(),
+        ws = q.new_empty(need.value, dtype=torch.uint8)
+    _call("svdq_qk_norm_rope_backward", d, *h[:4], hdq, hdk, dwq.data_ptr(), dwk.data_ptr(), ws.data_ptr(), ws.numel(),
           _stream(stream, q))
-    return dq, dk, dw[0], dw[1]
+    return dq, dk, *dw
 
 
 class _QKNormRope(torch.autograd.Function):
@@ -252,9 +265,11 @@ class KVCache:
         d = _desc(tokens, dim, k.dtype, cos, sin, wq, wk, eps, norm, halves, positions)
         hq = ho = None
         if q is not None:
+            hq = _heads(q, "q", tokens, dim, k.dtype)
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            hq, ho = _heads(q, "q", tokens, dim, k.dtype), _heads(q_out, "q_out", tokens, dim, k.dtype)
+                q_out, ho = _new(q)
+            else:
+                ho = _heads(q_out, "q_out", tokens, dim, k.dtype)
         _call("svdq_kv_append", d, hq, _heads(k, "k", tokens, dim, k.dtype), _heads(v, "v", tokens, dim, k.dtype), ho, self.c,
               _int32(slots, "slots", tokens), _stream(stream, k))
         return q_out
@@ -263,12 +278,13 @@ class KVCache:
         """(k, v) [len(slots), heads, D]: the cached values of the slots, zero
         for slots outside the cache."""
         n = slots.numel()
-        shape = (n, self.heads, self.head_dim)
-        code = _code(dtype)
-        k_out = torch.empty(shape, dtype=dtype, device=self.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=self.device) if v_out is None else v_out
-        _call("svdq_kv_read", self.c, _int32(slots, "slots", n), n, code, _heads(k_out, "k_out", n, self.head_dim, dtype),
-              _heads(v_out, "v_out", n, self.head_dim, dtype), _stream(stream, k_out))
+        code, at, hd = _code(dtype), _int32(slots, "slots", n), self.head_dim
+        if k_out is None:
+            k_out = self.k_codes.new_empty((n, self.heads, hd), dtype=dtype)
+        if v_out is None:
+            v_out = self.k_codes.new_empty((n, self.heads, hd), dtype=dtype)
+        _call("svdq_kv_read", self.c, at, n, code, _heads(k_out, "k_out", n, hd, dtype), _heads(v_out, "v_out", n, hd, dtype),
+              _stream(stream, slots))
         return k_out, v_out
 
 
@@ -289,7 +305,7 @@ def plan(past, fresh, block_table, free_pages, free_count, page_size: int, token
     (free_count [1] of them are free).  tokens: length of the slot map, at
     least the sum of fresh (the rest is -1)."""
     b = past.numel()
-    out = torch.empty(2 * b + 3 + 2 * tokens, dtype=torch.int32, device=past.device)
+    out = past.new_empty(2 * b + 3 + 2 * tokens)
     at = out.data_ptr()
     cuts = (b + 1, b, tokens, tokens, 1, 1)
     q_start, kv_len, slots, positions, left, missing = out.split(cuts)
@@ -334,16 +350,19 @@ def attention(q, cache: KVCache, block_table, q_start, kv_len, max_q: int, max_k
     if dim != cache.head_dim:
         raise ValueError(f"q: heads of {dim} over a cache of heads of {cache.head_dim}")
     b = kv_len.numel()
+    hin = _heads(q, "q", tokens, dim, q.dtype)
     if out is None:
-        out = torch.empty((tokens, hq, dim), dtype=q.dtype, device=q.device)
-    lse = torch.empty((tokens, hq), dtype=torch.float32, device=q.device) if return_lse else None
+        out, hout = _new(q)
+    else:
+        hout = _heads(out, "out", tokens, dim, q.dtype)
+    lse = q.new_empty((tokens, hq), dtype=torch.float32) if return_lse else None
     d = svdq_attn_desc(b, tokens, hq, _code(q.dtype), max_q, max_kv, window, ATTN_CAUSAL if causal else 0,
                        1.0 / math.sqrt(dim) if scale is None else scale, _int32(q_start, "q_start", b + 1),
                        _int32(kv_len, "kv_len", b), _table(block_table, b), block_table.shape[1])
     if ws is None:
         need = _SZ(0)
         _call("svdq_kv_attention_workspace", d, cache.c, need)
-        ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-    _call("svdq_kv_attention", d, _heads(q, "q", tokens, dim, q.dtype), cache.c, _heads(out, "out", tokens, dim, q.dtype),
+        ws = q.new_empty(need.value, dtype=torch.uint8)
+    _call("svdq_kv_attention", d, hin, cache.c, hout,
           None if lse is None else lse.data_ptr(), ws.data_ptr() if ws.numel() else None, ws.numel(), _stream(stream, q))
     return (out, lse) if return_lse else out
