@@ -1001,9 +1001,48 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   }
 }
 
-// Joins the chunks of a row: a workgroup per row.  Its threads fetch all
-// references at once, then 1024 / D groups of D / 4 threads walk the chunks and
-// meet in LDS in a fixed order.
+// Joins the chunks of a row.  Few chunks: D / 4 lanes a row, several rows a
+// workgroup.
+template <int DT, int FMT, int D, int ROWS>
+__global__ __launch_bounds__(256) void k_attn_join_few(AttnParams p) {
+  constexpr int L = D / 4, G = 256 / L;
+  const int64_t slot = int64_t(blockIdx.x) * G + int(threadIdx.x) / L, slots = int64_t(p.requests) * p.heads * p.row_slots;
+  if (slot >= slots) return;
+  unsigned id = unsigned(slot);
+  const int row = int(id % unsigned(p.row_slots));
+  id /= unsigned(p.row_slots);
+  const int h = int(id % unsigned(p.heads)), req = int(id / unsigned(p.heads));
+  const Request r(p, req);
+  if (row >= r.rows * p.group) return;
+  const TileRange range(p, r, row / ROWS, ROWS);
+  if (range.n <= 1) return;
+  const int d = int(threadIdx.x) % L * 4;
+  const int64_t at = slot * p.splits;
+  const f32x2* bs = reinterpret_cast<const f32x2*>(p.part + slots * p.splits * D) + at;
+  const float* y = p.part + at * D + d;
+  float base = LOWEST, sum = 0.0f;
+  f32x4 f = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < range.n; ++s) base = fmaxf(base, bs[s][0]);
+#pragma unroll 4
+  for (int s = 0; s < range.n; ++s) {
+    const f32x2 v = bs[s];
+    const f32x4 u = *reinterpret_cast<const f32x4*>(y + int64_t(s) * D);
+    const float a = exp2_hw(v[0] - base);
+    sum += a * v[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] += a * u[e];
+  }
+  const int64_t tok = r.first + row / p.group;
+  const int head = h * p.group + row % p.group;
+  const float inv = sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
+  *reinterpret_cast<u32x2*>(p.out + tok * p.ot + head * p.oh + d) = u32x2{pack2<DT>(f[0] * inv, f[1] * inv), pack2<DT>(f[2] * inv, f[3] * inv)};
+  if (p.lse && d == 0) p.lse[tok * p.q_heads + head] = row_lse(base, sum);
+}
+
+// Many chunks: a workgroup a row.  Its threads fetch all references at once,
+// then 1024 / D groups of D / 4 threads walk the chunks and meet in LDS in a
+// fixed order.
 template <int DT, int FMT, int D, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnParams p) {
   constexpr int L = D / 4, G = 256 / L;
@@ -1105,8 +1144,14 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   const int64_t group = d->q_heads / c->heads;
   const int64_t max_q = d->max_q < d->tokens ? d->max_q : d->tokens;
   t.row_slots = max_q * group;
-  t.rows = t.row_slots <= 64 ? 16 : 128;
-  if (t.rows == 128 && d->requests * c->heads * ceil_div(t.row_slots, 256) >= int64_t(device_cus())) t.rows = 256;
+  // Up to 80 rows, tiles of 16 that read the cache once each (8 requests of
+  // 4000 tokens, 8 heads: 40 rows 25 us against 29 with a tile of 128, 72 rows
+  // 31 against 31; one request of 8000 tokens, 65 rows: 15 against 23).  Above
+  // that the wide tiles, 256 rows where they give half the compute units work:
+  // 4 requests of 2048 rows, 2 heads in pairs: 108 us against 121 with 128 rows,
+  // but 2 requests of 300 rows, 24 heads: 54 against 47.
+  t.rows = t.row_slots <= 80 ? 16 : 128;
+  if (t.rows == 128 && d->requests * c->heads * ceil_div(t.row_slots, 256) * 2 >= int64_t(device_cus())) t.rows = 256;
   const int64_t tiles = ceil_div(t.row_slots, t.rows);
   t.items = d->requests * c->heads * tiles;
   int64_t span = d->max_kv;
@@ -1114,11 +1159,11 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   if (causal && d->window > 0 && int64_t(d->window) + max_q < span) span = int64_t(d->window) + max_q;
   if (d->window > 0) span += 31;        // the first tile is rounded down to 32
   // Chunks of at least 128 keys (a tile for each wave of k_attn16) or 512, as
-  // many as fill the chip about eight workgroups deep (two of the wide ones):
-  // 48 requests of up to 16384 tokens, 8 heads: 140 us at four, 129 at eight,
-  // 138 at twelve.
+  // many as eight workgroups (two of the wide ones) a compute unit, and none
+  // where that many are there: 48 requests of up to 16384 tokens, 8 heads: 140 us
+  // at four, 129 at eight, 138 at twelve.
   const int64_t least = t.rows == 16 ? 128 : 512;
-  const int64_t want = ceil_div(int64_t(device_cus()) * (t.rows == 16 ? 8 : 2), t.items > 0 ? t.items : 1);
+  const int64_t fit = int64_t(device_cus()) * (t.rows == 16 ? 8 : 2) / (t.items > 0 ? t.items : 1), want = fit < 1 ? 1 : fit;
   const int64_t all = ceil_div(int64_t(d->max_kv) + 31, least), here = ceil_div(span, least);
   const int64_t n = t.rows == 256 ? 1 : want < here ? want : here > 0 ? here : 1;
   const int64_t chunk = ceil_div(ceil_div(span > 0 ? span : 1, n), 128) * 128;
@@ -1135,15 +1180,22 @@ size_t part_bytes(const svdq_attn_desc* d, const svdq_kv_cache* c, const Cut& t,
   return splits > 1 ? size_t(d->requests) * size_t(c->heads) * size_t(t.row_slots) * size_t(splits) * size_t(c->head_dim + 2) * 4 : 0;
 }
 
+template <int DT, int FMT, int D, int ROWS>
+void launch_join(const AttnParams& p, const Cut& t, hipStream_t st) {
+  const int64_t slots = int64_t(p.requests) * p.heads * t.row_slots;
+  if (t.splits <= 16) k_attn_join_few<DT, FMT, D, ROWS><<<dim3(unsigned(ceil_div(slots, 1024 / D))), 256, 0, st>>>(p);
+  else k_attn_join<DT, FMT, D, ROWS><<<dim3(unsigned(slots)), 256, 0, st>>>(p);
+}
+
 template <int DT, int FMT, int D>
 void launch_attn(const AttnParams& p, const Cut& t, hipStream_t st) {
-  const dim3 grid(unsigned(t.items * t.splits)), joins(unsigned(int64_t(p.requests) * p.heads * t.row_slots));
+  const dim3 grid(unsigned(t.items * t.splits));
   if (t.rows == 16) {
     k_attn16<DT, FMT, D><<<grid, 256, 0, st>>>(p);
-    if (t.splits > 1) k_attn_join<DT, FMT, D, 16><<<joins, 256, 0, st>>>(p);
+    if (t.splits > 1) launch_join<DT, FMT, D, 16>(p, t, st);
   } else if (t.rows == 128) {
     k_attn_rows<DT, FMT, D, 4><<<grid, 256, 0, st>>>(p);
-    if (t.splits > 1) k_attn_join<DT, FMT, D, 128><<<joins, 256, 0, st>>>(p);
+    if (t.splits > 1) launch_join<DT, FMT, D, 128>(p, t, st);
   } else {
     k_attn_rows<DT, FMT, D, 8><<<grid, 512, 0, st>>>(p);
   }
