@@ -76,8 +76,7 @@ __device__ __forceinline__ float lane_max(float v) {
 // cos and sin of the lane's 8 pairs.  Halves: pair i = (i, i + D/2), the
 // lane's pairs are [8j, 8j + 8).  Else pairs are neighbours: [4j, 4j + 4) in
 // the first piece, [D/4 + 4j, ..) in the second.
-__device__ __forceinline__ void load_angles(const RowParams& p, int64_t t, int j, bool halves, float* c, float* s) {
-  const int64_t pos = p.positions ? int64_t(p.positions[t]) : t;
+__device__ __forceinline__ void load_angles(const RowParams& p, int64_t pos, int j, bool halves, float* c, float* s) {
   if (pos < 0 || pos >= p.n_positions) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = s[i] = __builtin_nanf("");
@@ -92,26 +91,32 @@ __device__ __forceinline__ void load_angles(const RowParams& p, int64_t t, int j
   for (int i = 0; i < 4; ++i) { c[i] = c0[i]; c[4 + i] = c1[i]; s[i] = s0[i]; s[4 + i] = s1[i]; }
 }
 
-// rotation of the lane's 8 pairs by +angle (sign = 1) or -angle (sign = -1)
-__device__ __forceinline__ void rotate(float* a, float* b, const float* c, const float* s, bool halves, float sign) {
+// (u, v) turned by the angle of cos c, sin n; BACK: by its negative
+template <bool BACK>
+__device__ __forceinline__ void turn(float* u, float* v, float c, float n) {
+  const float x = *u, y = *v;
+  *u = BACK ? __builtin_fmaf(y, n, x * c) : __builtin_fmaf(-y, n, x * c);
+  *v = BACK ? __builtin_fmaf(-x, n, y * c) : __builtin_fmaf(x, n, y * c);
+}
+template <bool BACK>
+__device__ __forceinline__ void rotate(float* a, float* b, const float* c, const float* s, bool halves) {
   if (halves) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float u = a[i], v = b[i], n = sign * s[i];
-      a[i] = u * c[i] - v * n;
-      b[i] = u * n + v * c[i];
-    }
+    for (int i = 0; i < 8; ++i) turn<BACK>(&a[i], &b[i], c[i], s[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float u = a[2 * i], v = a[2 * i + 1], n = sign * s[i];
-      a[2 * i] = u * c[i] - v * n;
-      a[2 * i + 1] = u * n + v * c[i];
-      const float u1 = b[2 * i], v1 = b[2 * i + 1], n1 = sign * s[4 + i];
-      b[2 * i] = u1 * c[4 + i] - v1 * n1;
-      b[2 * i + 1] = u1 * n1 + v1 * c[4 + i];
+      turn<BACK>(&a[2 * i], &a[2 * i + 1], c[i], s[i]);
+      turn<BACK>(&b[2 * i], &b[2 * i + 1], c[4 + i], s[4 + i]);
     }
   }
+}
+// sum over i of a[i] x[i] + b[i] y[i], two chains
+__device__ __forceinline__ float dot16(const float* a, const float* x, const float* b, const float* y) {
+  float s = a[0] * x[0], t = b[0] * y[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) { s = __builtin_fmaf(a[i], x[i], s); t = __builtin_fmaf(b[i], y[i], t); }
+  return s + t;
 }
 
 // 8 nibbles of the MXFP4 piece f under the group's e8m0 exponent e: the
@@ -222,10 +227,7 @@ __global__ __launch_bounds__(256) void k_rows(RowParams p) {
   unpack8<DT>(va, a);
   unpack8<DT>(vb, b);
   if (o.norm) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += a[i] * a[i] + b[i] * b[i];
-    s = row_sum<L>(s);
+    const float s = row_sum<L>(dot16(a, a, b, b));
     const float r = 1.0f / sqrtf(s / float(p.D) + p.eps);
 #pragma unroll
     for (int i = 0; i < 8; ++i) { a[i] *= r; b[i] *= r; }
@@ -239,14 +241,14 @@ __global__ __launch_bounds__(256) void k_rows(RowParams p) {
   }
   if (o.rope && on) {
     float c[8], s[8];
-    load_angles(p, t, j, halves, c, s);
-    rotate(a, b, c, s, halves, 1.0f);
+    load_angles(p, p.positions ? int64_t(p.positions[t]) : t, j, halves, c, s);
+    rotate<false>(a, b, c, s, halves);
   }
   if (FMT < 0 || which == 0) {
     if (on) {
       uint16_t* y = o.y + t * o.yt + h * o.yh + 8 * j;
-      *reinterpret_cast<u32x4*>(y) = pack8<DT>(a);
-      *reinterpret_cast<u32x4*>(y + half) = pack8<DT>(b);
+      __builtin_nontemporal_store(pack8<DT>(a), reinterpret_cast<u32x4*>(y));
+      __builtin_nontemporal_store(pack8<DT>(b), reinterpret_cast<u32x4*>(y + half));
     }
   } else {
     if constexpr (FMT >= 0 && (L == 4 || L == 8)) {
@@ -280,61 +282,74 @@ __global__ __launch_bounds__(256) void k_rows_grad(RowParams p) {
     unpack8<DT>(*reinterpret_cast<const u32x4*>(o.w + half + 8 * j), wb);
   }
   const float inv_d = 1.0f / float(p.D);
-  for (int64_t base = int64_t(blockIdx.x) * RPB; base < rows; base += int64_t(gridDim.x) * RPB) {
+  // The next row's values and position are requested before this row's work.
+  struct Row {
+    u32x4 va, vb, ua, ub;
+    int64_t t, pos;
+    int h;
+    bool on;
+  } next;
+  auto request = [&](int64_t base) {
     const int64_t row = base + grp;
-    const bool on = row < rows && lane_on;
+    next.on = row < rows && lane_on;
     const unsigned r32 = unsigned(row < rows ? row : 0);
-    const int64_t t = int64_t(r32 / unsigned(o.heads));
-    const int h = int(r32 % unsigned(o.heads));
-    float a[8], b[8], ga[8], gb[8];
-    u32x4 va = {0, 0, 0, 0}, vb = va, ua = va, ub = va;
-    if (on) {
-      const uint16_t* g = o.g + t * o.gt + h * o.gh + 8 * j;
-      ua = *reinterpret_cast<const u32x4*>(g);
-      ub = *reinterpret_cast<const u32x4*>(g + half);
+    next.t = int64_t(r32 / unsigned(o.heads));
+    next.h = int(r32 % unsigned(o.heads));
+    next.va = next.vb = next.ua = next.ub = u32x4{0, 0, 0, 0};
+    next.pos = next.t;
+    if (next.on) {
+      const uint16_t* g = o.g + next.t * o.gt + next.h * o.gh + 8 * j;
+      next.ua = *reinterpret_cast<const u32x4*>(g);
+      next.ub = *reinterpret_cast<const u32x4*>(g + half);
       if (o.norm) {
-        const uint16_t* x = o.x + t * o.xt + h * o.xh + 8 * j;
-        va = *reinterpret_cast<const u32x4*>(x);
-        vb = *reinterpret_cast<const u32x4*>(x + half);
+        const uint16_t* x = o.x + next.t * o.xt + next.h * o.xh + 8 * j;
+        next.va = *reinterpret_cast<const u32x4*>(x);
+        next.vb = *reinterpret_cast<const u32x4*>(x + half);
       }
+      if (p.positions) next.pos = p.positions[next.t];
     }
+  };
+  const int64_t step = int64_t(gridDim.x) * RPB;
+  int64_t base = int64_t(blockIdx.x) * RPB;
+  if (base < rows) request(base);
+  for (; base < rows; base += step) {
+    const u32x4 va = next.va, vb = next.vb, ua = next.ua, ub = next.ub;
+    const int64_t t = next.t, pos = next.pos;
+    const int h = next.h;
+    const bool on = next.on;
+    float c[8], sn[8];
+    if (o.rope && on) load_angles(p, pos, j, halves, c, sn);
+    if (base + step < rows) request(base + step);
+    float a[8], b[8], ga[8], gb[8];
     unpack8<DT>(ua, ga);
     unpack8<DT>(ub, gb);
-    if (o.rope && on) {
-      float c[8], s[8];
-      load_angles(p, t, j, halves, c, s);
-      rotate(ga, gb, c, s, halves, -1.0f);
-    }
+    if (o.rope && on) rotate<true>(ga, gb, c, sn, halves);
     if (o.norm) {
       unpack8<DT>(va, a);
       unpack8<DT>(vb, b);
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += a[i] * a[i] + b[i] * b[i];
-      s = row_sum<L>(s);
+      const float s = row_sum<L>(dot16(a, a, b, b));
       const float r = 1.0f / sqrtf(s / float(p.D) + p.eps);
-      float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         a[i] *= r;                       // x r, the unit row
         b[i] *= r;
-        da[i] += ga[i] * a[i];
-        db[i] += gb[i] * b[i];
+        da[i] = __builtin_fmaf(ga[i], a[i], da[i]);
+        db[i] = __builtin_fmaf(gb[i], b[i], db[i]);
         ga[i] *= wa[i];
         gb[i] *= wb[i];
-        dot += ga[i] * a[i] + gb[i] * b[i];
       }
-      dot = row_sum<L>(dot) * inv_d;
+      // dx = r u - x r (r mean(u x r))
+      const float back = r * (row_sum<L>(dot16(ga, a, gb, b)) * inv_d);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        ga[i] = r * (ga[i] - a[i] * dot);
-        gb[i] = r * (gb[i] - b[i] * dot);
+        ga[i] = __builtin_fmaf(-a[i], back, r * ga[i]);
+        gb[i] = __builtin_fmaf(-b[i], back, r * gb[i]);
       }
     }
     if (on) {
       uint16_t* y = o.y + t * o.yt + h * o.yh + 8 * j;
-      *reinterpret_cast<u32x4*>(y) = pack8<DT>(ga);
-      *reinterpret_cast<u32x4*>(y + half) = pack8<DT>(gb);
+      __builtin_nontemporal_store(pack8<DT>(ga), reinterpret_cast<u32x4*>(y));
+      __builtin_nontemporal_store(pack8<DT>(gb), reinterpret_cast<u32x4*>(y + half));
     }
   }
   if (!o.norm || p.part[which] == nullptr) return;
@@ -436,8 +451,8 @@ __global__ __launch_bounds__(256) void k_read(ReadParams p) {
     hi = pack8<DT>(f + 8);
   }
   uint16_t* y = p.y[which] + t * p.yt[which] + h * p.yh[which] + 16 * j;
-  *reinterpret_cast<u32x4*>(y) = lo;
-  *reinterpret_cast<u32x4*>(y + 8) = hi;
+  __builtin_nontemporal_store(lo, reinterpret_cast<u32x4*>(y));
+  __builtin_nontemporal_store(hi, reinterpret_cast<u32x4*>(y + 8));
 }
 
 // ------------------------------------------------------------ step tables
@@ -647,9 +662,14 @@ void launch_append(const RowParams& p, int lanes, int64_t rows, int ops, hipStre
   else k_rows<DT, 8, FMT><<<grid, 256, 0, st>>>(p);
 }
 
+// Workgroups an operand: q's and k's together are three a compute unit, as many
+// as the registers hold at once (4607 tokens, 24 heads of 128: 43 us; 512
+// blocks, a second round, 50; 1024 47).  The weight gradients' partial rows, and
+// with them the workspace, go by this number.
+constexpr int64_t GRAD_BLOCKS = 384;
 int grad_blocks(int64_t rows, int lanes) {
   const int64_t blocks = ceil_div(rows, 256 / lanes);
-  return int(blocks < 1 ? 1 : blocks > 1024 ? 1024 : blocks);
+  return int(blocks < 1 ? 1 : blocks > GRAD_BLOCKS ? GRAD_BLOCKS : blocks);
 }
 
 template <int DT>
