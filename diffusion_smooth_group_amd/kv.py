@@ -329,13 +329,19 @@ def release(done, block_table, kv_len, free_pages, free_count, page_size: int, s
 
 
 # --------------------------------------------------------------------- attention
-def attention_workspace(requests: int, tokens: int, q_heads: int, cache: KVCache, max_q: int, max_kv: int,
-                        device="cuda") -> torch.Tensor:
-    """A workspace for ``attention`` calls of these bounds."""
+def attention_workspace_size(requests: int, tokens: int, q_heads: int, cache: KVCache, max_q: int, max_kv: int) -> int:
+    """Bytes of workspace that ``attention`` calls of these bounds need."""
     d = svdq_attn_desc(requests, tokens, q_heads, S.BF16, max_q, max_kv, 0, ATTN_CAUSAL, 1.0)
     need = _SZ(0)
     _call("svdq_kv_attention_workspace", d, cache.c, need)
-    return torch.empty(need.value, dtype=torch.uint8, device=device)
+    return need.value
+
+
+def attention_workspace(requests: int, tokens: int, q_heads: int, cache: KVCache, max_q: int, max_kv: int,
+                        device="cuda") -> torch.Tensor:
+    """A workspace for ``attention`` calls of these bounds.  One stream at a
+    time may use it."""
+    return torch.empty(attention_workspace_size(requests, tokens, q_heads, cache, max_q, max_kv), dtype=torch.uint8, device=device)
 
 
 def attention(q, cache: KVCache, block_table, q_start, kv_len, max_q: int, max_kv: int, causal: bool = True, window: int = 0,

@@ -151,6 +151,21 @@ def test_prompts(fmt, dtype, dim, page, hk, group, fresh, lens, causal, window):
     _run(fmt, dtype, dim, page, hk, group, fresh, lens, causal, window)
 
 
+@pytest.mark.parametrize("fmt,dtype,dim", FORMS)
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 50)])
+def test_many_requests_of_wide_tiles(fmt, dtype, dim, causal, window):
+    """Tiles of 256 rows: enough requests and heads for half the compute units."""
+    fresh = [81 + r % 3 * 40 for r in range(22)]
+    _run(fmt, dtype, dim, 32, 3, 2, fresh, [n + 61 * (r % 4) for r, n in enumerate(fresh)], causal, window)
+
+
+@pytest.mark.parametrize("fmt,dtype,dim", FORMS)
+def test_wide_tiles_in_joined_chunks(fmt, dtype, dim):
+    """One request, few heads: a tile of 128 rows over chunks of a long cache."""
+    _run(fmt, dtype, dim, 64, 1, 1, [100], [2500])
+    _run(fmt, dtype, dim, 16, 1, 2, [70], [1800], True, 1100)
+
+
 @pytest.mark.parametrize("fmt,dtype", [("mxfp4_g32", "bf16"), ("int4_g64", "f16")])
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 3), (False, 3)])
 def test_requests_without_rows_tokens_or_visible_keys(fmt, dtype, causal, window):
