@@ -271,8 +271,10 @@ __device__ __forceinline__ u32x4 query_order(u32x4 q) {
 template <int DT, int FMT, int D>
 __device__ __forceinline__ float value_scale(const u32x4* sc, int i, int g) {
   if constexpr (FMT == SVDQ_FMT_MXFP4_G32) {
-    const unsigned w = D == 128 ? sc[i / 4][i % 4] >> (8 * g) : sc[0][i / 2] >> (16 * (i % 2) + 8 * g);
-    return mx_scale<DT>(w & 255u);
+    const unsigned w = D == 128 ? sc[i / 4][i % 4] : sc[0][i / 2];
+    const unsigned b = D == 128 ? 8 * g : 16 * (i % 2) + 8 * g;         // bit of the byte
+    if constexpr (DT == SVDQ_F16) return mx_scale<DT>((w >> b) & 255u);
+    return __uint_as_float(__builtin_amdgcn_alignbit(w, w, b + 9u) & 0x7F800000u);   // rotated to bits 23-30
   } else {
     const unsigned w = D == 128 ? sc[i / 4][i % 4] >> (16 * g) : sc[0][i / 2] >> (16 * (i % 2));
     return h2f<SVDQ_F16>(w & 0xFFFFu);
@@ -296,6 +298,17 @@ __device__ __forceinline__ void value_pair_int4(const unsigned* v8, u32x4* f0, u
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const unsigned x0 = cvt_int4<DT, HI>(v8[2 * i]), x1 = cvt_int4<DT, HI>(v8[2 * i + 1]);
+    (*f0)[i] = low_halves(x0, x1);
+    (*f1)[i] = high_halves(x0, x1);
+  }
+}
+
+// the same from dwords with the codes of two keys each, first key in the low half
+template <int DT>
+__device__ __forceinline__ void value_quad_int4(const unsigned* two, u32x4* f0, u32x4* f1) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned x0 = cvt_int4<DT, false>(two[i]), x1 = cvt_int4<DT, true>(two[i]);
     (*f0)[i] = low_halves(x0, x1);
     (*f1)[i] = high_halves(x0, x1);
   }
@@ -668,9 +681,9 @@ struct Stage {
   static constexpr int KT = 64 * NW * 32 / D;     // keys a stage: one 32-element piece of K a thread
   static constexpr int PAGES = KT / 16;           // page lookups a stage
   u32x4 k;                  // 32 codes of one key
-  unsigned ke;              // its e8m0, or the key's fp16 scales (thread < KT)
+  unsigned ke;              // MXFP4: its e8m0; INT4: a key's fp16 scales (lanes < WH * 16)
   unsigned v[8];            // 4 codes of 8 keys
-  u32x4 vsc[FMT == SVDQ_FMT_MXFP4_G32 ? (D == 128 ? 2 : 1) : 1];   // MXFP4: the 8 keys' scales; INT4: [0][0] scales of key `thread`
+  u32x4 vsc[FMT == SVDQ_FMT_MXFP4_G32 ? (D == 128 ? 2 : 1) : 1];   // MXFP4: the 8 keys' scales; INT4: [0][0] of the lane's key
 };
 
 template <int DT, int FMT, int D, int NW>
@@ -682,7 +695,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   __shared__ u32x4 sk[2][NC * KT];
   __shared__ u32x4 sv[2][KT / 8 * D];
   __shared__ __attribute__((aligned(16))) unsigned sks[2][MX ? 1 : KT], svs[2][MX ? 1 : KT];
-  __shared__ float sve[2][KT / 64];     // exponent of the largest value scale of 64 keys
+  __shared__ float sve[2][NW];          // exponent of the largest value scale of a wave's keys
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
   // workgroup -> (row tile, request, head, chunk), chunk fastest; the last row
   // tiles, which see most keys, first; one head's tiles keep to one XCD where
@@ -729,9 +742,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   const int from = range.from + split * p.chunk, to = min(range.to, from + p.chunk);
   const int32_t* table = p.table + int64_t(req) * p.table_stride;
   const int last_col = (r.len - 1) >> p.page_shift, in_page = (1 << p.page_shift) - 1;
+  // A wave brings the WH x 16 keys [16 WH wave, ..) of a stage, whose pages are
+  // the same for all its lanes: addresses are scalar bases plus lane offsets.
+  constexpr int WH = KT / 16 / NW;
+  const int wv = __builtin_amdgcn_readfirstlane(wave);
   const int kkey = tid / NB, kb = tid % NB;                   // K piece: key of the stage, 32-element block
   const int vkeys = tid / (D / 4) * 8, vn = tid % (D / 4);    // V block: first of 8 keys, columns 4 vn ..
-  // a lane's page of the stage at `token`; every wave looks all of them up
+  // a lane's page of the stage at `token` (lane l: keys 16 (l % PAGES) ..)
   auto look_up = [&](int token) {
     const int t = token + 16 * (lane % PAGES);
     return table[min(t >> p.page_shift, last_col)];
@@ -739,30 +756,34 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   auto bad_pages = [&](int page) { return unsigned(__ballot(page < 0 || page >= p.n_pages)); };   // bit i: keys 16 i ..
   auto request = [&](St& st, int token, int page) {
     const int good = page < 0 || page >= p.n_pages ? 0 : page;
-    const int kp = __shfl(good, kkey / 16), vp = __shfl(good, vkeys / 16);
-    const int64_t krow = ((int64_t(kp) * p.heads + h) << p.page_shift) + ((token + kkey) & in_page);
-    const int64_t vrow = ((int64_t(vp) * p.heads + h) << p.page_shift) + ((token + vkeys) & in_page);
-    st.k = *reinterpret_cast<const u32x4*>(p.kc + krow * (D / 2) + 16 * kb);
-    const uint8_t* vc = p.vc + vrow * (D / 2) + 2 * vn;
+    int64_t row[WH];        // cache row of the first key of each 16
+#pragma unroll
+    for (int i = 0; i < WH; ++i)
+      row[i] = ((int64_t(__builtin_amdgcn_readlane(good, wv * WH + i)) * p.heads + h) << p.page_shift) +
+               ((token + 16 * (wv * WH + i)) & in_page);
+    auto at = [&](const void* base, int key, int row_bytes) {  // key of the wave's
+      const uint8_t* b0 = static_cast<const uint8_t*>(base) + row[0] * row_bytes;
+      if constexpr (WH == 1) return b0 + unsigned(key * row_bytes);
+      const uint8_t* b1 = static_cast<const uint8_t*>(base) + row[WH - 1] * row_bytes;
+      return (key >= 16 ? b1 : b0) + unsigned((key & 15) * row_bytes);
+    };
+    st.k = *reinterpret_cast<const u32x4*>(at(p.kc, lane / NB, D / 2) + 16 * kb);
+    const int vk = lane / (D / 4) * 8;
+    const uint8_t* vc = at(p.vc, vk, D / 2) + 2 * vn;
 #pragma unroll
     for (int i = 0; i < 8; ++i) st.v[i] = *reinterpret_cast<const uint16_t*>(vc + i * (D / 2));
     if constexpr (MX) {
-      st.ke = p.ks[krow * NB + kb];
-      const u32x4* vs = reinterpret_cast<const u32x4*>(p.vs + vrow * NB);
+      st.ke = *(at(p.ks, lane / NB, NB) + kb);
+      const u32x4* vs = reinterpret_cast<const u32x4*>(at(p.vs, vk, NB));
       st.vsc[0] = vs[0];
       if constexpr (D == 128) st.vsc[1] = vs[1];
-    } else {
-      // thread t < KT brings key t's scales
-      const int sp = __shfl(good, (tid % KT) / 16);
-      if (tid < KT) {
-        const int64_t srow = ((int64_t(sp) * p.heads + h) << p.page_shift) + ((token + tid) & in_page);
-        if constexpr (D == 128) {
-          st.ke = reinterpret_cast<const unsigned*>(p.ks)[srow];
-          st.vsc[0][0] = reinterpret_cast<const unsigned*>(p.vs)[srow];
-        } else {
-          st.ke = reinterpret_cast<const uint16_t*>(p.ks)[srow];
-          st.vsc[0][0] = reinterpret_cast<const uint16_t*>(p.vs)[srow];
-        }
+    } else if (lane < 16 * WH) {
+      if constexpr (D == 128) {
+        st.ke = *reinterpret_cast<const unsigned*>(at(p.ks, lane, 4));
+        st.vsc[0][0] = *reinterpret_cast<const unsigned*>(at(p.vs, lane, 4));
+      } else {
+        st.ke = *reinterpret_cast<const uint16_t*>(at(p.ks, lane, 2));
+        st.vsc[0][0] = *reinterpret_cast<const uint16_t*>(at(p.vs, lane, 2));
       }
     }
   };
@@ -779,7 +800,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
         else st.vsc[0][i / 2] = zero ? st.vsc[0][i / 2] & (i % 2 ? 0x0000FFFFu : 0xFFFF0000u) : st.vsc[0][i / 2];
       }
     } else {
-      const bool gone = ((bad >> ((tid % KT) / 16)) & 1u) || token + tid >= r.len;
+      const int key = 16 * WH * wave + lane % (16 * WH);
+      const bool gone = ((bad >> (key / 16)) & 1u) || token + key >= r.len;
       st.vsc[0][0] = gone ? 0u : st.vsc[0][0];
     }
   };
@@ -804,29 +826,34 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       v[32] = f0;
       v[48] = f1;
     } else {
-      unsigned w[8];
+      // two keys' codes in a dword, so that the bits are moved once for both
+      unsigned ev[4], od[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = int4_even(st.v[i]);
-      value_pair_int4<DT, false>(w, &f0, &f1);
+      for (int i = 0; i < 4; ++i) {
+        const unsigned w = st.v[2 * i] | (st.v[2 * i + 1] << 16);
+        ev[i] = int4_even(w);
+        od[i] = int4_odd(w);
+      }
+      value_quad_int4<DT>(ev, &f0, &f1);
       v[0] = f0;
       v[32] = f1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = int4_odd(st.v[i]);
-      value_pair_int4<DT, false>(w, &f0, &f1);
+      value_quad_int4<DT>(od, &f0, &f1);
       v[16] = f0;
       v[48] = f1;
     }
   };
   auto write_scales = [&](const St& st, int buf) {             // INT4
-    if (MX || tid >= KT) return;
-    sks[buf][tid] = st.ke;
-    svs[buf][tid] = st.vsc[0][0];
-    if constexpr (scaled_reference<DT, FMT>()) {
-      const f16x2 f = two_halves(st.vsc[0][0]);
-      float most = fmaxf(float(f[0]), float(f[1]));
+    if constexpr (!MX) {
+      if (lane >= 16 * WH) return;
+      sks[buf][16 * WH * wave + lane] = st.ke;
+      svs[buf][16 * WH * wave + lane] = st.vsc[0][0];
+      if constexpr (scaled_reference<DT, FMT>()) {
+        const f16x2 f = two_halves(st.vsc[0][0]);
+        float most = fmaxf(float(f[0]), float(f[1]));
 #pragma unroll
-      for (int x = 1; x < 64; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
-      if (lane == 0) sve[buf][wave] = scale_exponent(most);
+        for (int x = 1; x < 16 * WH; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
+        if (lane == 0) sve[buf][wave] = scale_exponent(most);
+      }
     }
   };
 
@@ -878,7 +905,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
 #pragma unroll
     for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i]);
     top = half_max(top) * c - p_shift<DT>();
-    if constexpr (scaled_reference<DT, FMT>()) top += sve[buf][at / 64];
+    if constexpr (scaled_reference<DT, FMT>()) {
+      float most = sve[buf][at / (16 * WH)];
+#pragma unroll
+      for (int i = 1; i < 4 / WH; ++i) most = fmaxf(most, sve[buf][at / (16 * WH) + i]);
+      top += most;
+    }
     if (__any(top > base + SLACK)) {
       const float next = fmaxf(base, top), alpha = exp2_hw(base - next);
       base = next;
@@ -1159,16 +1191,16 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   if (causal && d->window > 0 && int64_t(d->window) + max_q < span) span = int64_t(d->window) + max_q;
   if (d->window > 0) span += 31;        // the first tile is rounded down to 32
   // Chunks of at least 128 keys (a tile for each wave of k_attn16) or 512, as
-  // many as eight workgroups (two of the wide ones) a compute unit, and none
+  // many as eight workgroups (two, one of the wide ones) a compute unit, and none
   // where that many are there: 48 requests of up to 16384 tokens, 8 heads: 140 us
   // at four, 129 at eight, 138 at twelve.
   const int64_t least = t.rows == 16 ? 128 : 512;
-  const int64_t fit = int64_t(device_cus()) * (t.rows == 16 ? 8 : 2) / (t.items > 0 ? t.items : 1), want = fit < 1 ? 1 : fit;
+  const int64_t fit = int64_t(device_cus()) * (t.rows == 16 ? 8 : t.rows == 128 ? 2 : 1) / (t.items > 0 ? t.items : 1), want = fit < 1 ? 1 : fit;
   const int64_t all = ceil_div(int64_t(d->max_kv) + 31, least), here = ceil_div(span, least);
-  const int64_t n = t.rows == 256 ? 1 : want < here ? want : here > 0 ? here : 1;
+  const int64_t n = want < here ? want : here > 0 ? here : 1;
   const int64_t chunk = ceil_div(ceil_div(span > 0 ? span : 1, n), 128) * 128;
   t.splits = int(ceil_div(span > 0 ? span : 1, chunk));
-  t.most = int(t.rows == 256 ? 1 : want < all ? want : all);
+  t.most = int(want < all ? want : all);
   t.chunk = int(chunk);
   t.row_tiles = int(tiles);
   if (t.items * t.most >= (int64_t(1) << 31) || d->requests * c->heads * t.row_slots >= (int64_t(1) << 31)) return SVDQ_ERR_UNSUPPORTED;
@@ -1198,6 +1230,7 @@ void launch_attn(const AttnParams& p, const Cut& t, hipStream_t st) {
     if (t.splits > 1) launch_join<DT, FMT, D, 128>(p, t, st);
   } else {
     k_attn_rows<DT, FMT, D, 8><<<grid, 512, 0, st>>>(p);
+    if (t.splits > 1) launch_join<DT, FMT, D, 256>(p, t, st);
   }
 }
 
