@@ -150,7 +150,14 @@ struct Request {
 // O^T = V^T P^T as it stands; the keys of the two K tiles are dealt out for
 // that (tile a, row r: key 8 (r / 4) + 4 a + r % 4).  V^T needs 8 keys of one
 // column in a lane: a lane loads 8 keys' codes of its own columns and pairs
-// neighbouring keys after the conversion.
+// neighbouring keys after the conversion.  The cache's bytes bound it (136 a key
+// and head of 128): the codes go from memory to registers and are turned there,
+// with two tiles in flight a wave and three waves a SIMD.  48 requests of up to
+// 16384 tokens, 8 heads of 128, 4 query heads each: MXFP4 114 us, 4.8 TB/s; INT4
+// 182 us, where the vector unit is the bound (its integers need twice MXFP4's
+// instructions: bits to fp8, conversion, and scales on both sums).  Two row tiles
+// a wave on the same operands were slower for MXFP4 (40 rows: 309 us against 199
+// with three tiles of 16: two waves a SIMD instead of three).
 template <int FMT, int D>
 struct Tile32 {
   static constexpr int NJ = D / 32;
@@ -644,6 +651,14 @@ __global__ __launch_bounds__(256, 2) void k_attn16(AttnParams p) {
 //      holds one INT4 scale group and a lane's results are 4 neighbours
 // Stages are double-buffered: stage i + 1 is written and stage i + 2 requested
 // while stage i is multiplied, with one barrier a stage.
+// The matrix products bound it, and the vector work beside them: a matrix
+// instruction keeps the SIMD from issuing vector ones for half its time.  4608
+// tokens, 24 heads of 128, no mask, MXFP4: 264 us, 990 TFLOP/s (a large bf16
+// matrix product: 1250), of which 16% is the second round of 432 workgroups on
+// 256 compute units.  INT4 has the scales of both sums on top: 5 x 2047 rows
+// behind up to 8191 tokens, 32 heads over 8: 1017 us, 673 TFLOP/s.  Tried and
+// slower: the next products under this softmax (281 us), the two waves of a SIMD
+// one phase apart (306), 64 rows a wave (434), no running maximum (282).
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
   if constexpr (DT == SVDQ_BF16)
@@ -1176,13 +1191,15 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   const int64_t group = d->q_heads / c->heads;
   const int64_t max_q = d->max_q < d->tokens ? d->max_q : d->tokens;
   t.row_slots = max_q * group;
-  // Up to 80 rows, tiles of 16 that read the cache once each (8 requests of
-  // 4000 tokens, 8 heads: 40 rows 25 us against 29 with a tile of 128, 72 rows
-  // 31 against 31; one request of 8000 tokens, 65 rows: 15 against 23).  Above
-  // that the wide tiles, 256 rows where they give half the compute units work:
-  // 4 requests of 2048 rows, 2 heads in pairs: 108 us against 121 with 128 rows,
-  // but 2 requests of 300 rows, 24 heads: 54 against 47.
-  t.rows = t.row_slots <= 80 ? 16 : 128;
+  // Up to 80 rows a request and head, or 1024 in all, tiles of 16 that read the
+  // cache once each (8 requests of 4000 tokens, 8 heads: 40 rows 25 us against 29
+  // with a tile of 128, 72 rows 31 against 31; one request and head: 128 rows 15
+  // against 23, 512 rows 19 against 23; one request, 8 heads: 128 rows 24 against
+  // 24, 256 rows 29 against 26).  Above that the wide tiles, 256 rows where they
+  // give half the compute units work: 4 requests of 2048 rows, 2 heads in pairs:
+  // 103 us against 121 with 128 rows, but 2 requests of 300 rows, 24 heads: 54
+  // against 47.
+  t.rows = t.row_slots <= 80 || d->requests * c->heads * t.row_slots <= 1024 ? 16 : 128;
   if (t.rows == 128 && d->requests * c->heads * ceil_div(t.row_slots, 256) * 2 >= int64_t(device_cus())) t.rows = 256;
   const int64_t tiles = ceil_div(t.row_slots, t.rows);
   t.items = d->requests * c->heads * tiles;

@@ -161,9 +161,11 @@ def test_many_requests_of_wide_tiles(fmt, dtype, dim, causal, window):
 
 @pytest.mark.parametrize("fmt,dtype,dim", FORMS)
 def test_wide_tiles_in_joined_chunks(fmt, dtype, dim):
-    """One request, few heads: a tile of 128 rows over chunks of a long cache."""
+    """Few requests and heads: tiles of 128 rows over chunks of a long cache,
+    and rows just under what they take (tiles of 16)."""
+    _run(fmt, dtype, dim, 64, 3, 4, [90], [2500])
+    _run(fmt, dtype, dim, 16, 9, 2, [70], [1800], True, 1100)
     _run(fmt, dtype, dim, 64, 1, 1, [100], [2500])
-    _run(fmt, dtype, dim, 16, 1, 2, [70], [1800], True, 1100)
 
 
 @pytest.mark.parametrize("fmt,dtype", [("mxfp4_g32", "bf16"), ("int4_g64", "f16")])
