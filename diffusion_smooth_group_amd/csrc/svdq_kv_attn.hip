@@ -1191,6 +1191,8 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   const int64_t group = d->q_heads / c->heads;
   const int64_t max_q = d->max_q < d->tokens ? d->max_q : d->tokens;
   t.row_slots = max_q * group;
+  const int64_t slots = product_below(d->requests, c->heads, t.row_slots, int64_t(1) << 31);
+  if (slots < 0) return SVDQ_ERR_UNSUPPORTED;
   // Up to 80 rows a request and head, or 1024 in all, tiles of 16 that read the
   // cache once each (8 requests of 4000 tokens, 8 heads: 40 rows 25 us against 29
   // with a tile of 128, 72 rows 31 against 31; one request and head: 128 rows 15
@@ -1199,7 +1201,7 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   // give half the compute units work: 4 requests of 2048 rows, 2 heads in pairs:
   // 103 us against 121 with 128 rows, but 2 requests of 300 rows, 24 heads: 54
   // against 47.
-  t.rows = t.row_slots <= 80 || d->requests * c->heads * t.row_slots <= 1024 ? 16 : 128;
+  t.rows = t.row_slots <= 80 || slots <= 1024 ? 16 : 128;
   if (t.rows == 128 && d->requests * c->heads * ceil_div(t.row_slots, 256) * 2 >= int64_t(device_cus())) t.rows = 256;
   const int64_t tiles = ceil_div(t.row_slots, t.rows);
   t.items = d->requests * c->heads * tiles;
@@ -1220,7 +1222,7 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   t.most = int(want < all ? want : all);
   t.chunk = int(chunk);
   t.row_tiles = int(tiles);
-  if (t.items * t.most >= (int64_t(1) << 31) || d->requests * c->heads * t.row_slots >= (int64_t(1) << 31)) return SVDQ_ERR_UNSUPPORTED;
+  if (t.items * t.most >= MAX_THREADS / 512) return SVDQ_ERR_UNSUPPORTED;   // a join has fewer: only calls of few rows are cut
   *out = t;
   return SVDQ_OK;
 }

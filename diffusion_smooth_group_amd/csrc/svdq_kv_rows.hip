@@ -697,8 +697,12 @@ void launch_grad(const RowParams& p, int lanes, int blocks, int ops, hipStream_t
   }
 }
 
+// rows below 2^31, and their lanes within a launch
 svdq_status check_rows(const svdq_qk_desc* d, int64_t heads) {
-  return d->tokens * heads >= (int64_t(1) << 31) ? SVDQ_ERR_UNSUPPORTED : SVDQ_OK;
+  const int lanes = row_lanes(d->head_dim);
+  return product_below(d->tokens, heads, 1, int64_t(1) << 31) < 0 || product_below(d->tokens, heads, lanes, MAX_THREADS - 256 * lanes) < 0
+             ? SVDQ_ERR_UNSUPPORTED
+             : SVDQ_OK;
 }
 
 template <int DT, int FMT>
@@ -751,6 +755,7 @@ extern "C" svdq_status svdq_qk_backward_workspace(const svdq_qk_desc* d, int32_t
   svdq_status st = check_desc(d);
   if (st != SVDQ_OK) return st;
   if (!bytes || q_heads < 1 || k_heads < 0) return SVDQ_ERR_INVALID_ARG;
+  if ((st = check_rows(d, q_heads > k_heads ? q_heads : k_heads)) != SVDQ_OK) return st;
   const int lanes = row_lanes(d->head_dim);
   const int blocks = grad_blocks(d->tokens * (q_heads > k_heads ? q_heads : k_heads), lanes);
   *bytes = size_t(2) * size_t(blocks) * size_t(d->head_dim) * 4;
@@ -857,7 +862,9 @@ extern "C" svdq_status svdq_kv_read(const svdq_kv_cache* cache, const int32_t* s
   }
   if (n == 0 || (!k_out && !v_out)) return SVDQ_OK;
   if (!slots) return SVDQ_ERR_INVALID_ARG;
-  if (n * cache->heads >= (int64_t(1) << 31)) return SVDQ_ERR_UNSUPPORTED;
+  if (product_below(n, cache->heads, 1, int64_t(1) << 31) < 0 ||
+      product_below(n, cache->heads, cache->head_dim / 16, MAX_THREADS - 4096) < 0)
+    return SVDQ_ERR_UNSUPPORTED;
   ReadParams p = {};
   p.codes[0] = static_cast<const uint8_t*>(cache->k_codes);
   p.scales[0] = static_cast<const uint8_t*>(cache->k_scales);

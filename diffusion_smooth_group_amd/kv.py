@@ -351,7 +351,8 @@ def attention(q, cache: KVCache, block_table, q_start, kv_len, max_q: int, max_k
     last of them at position kv_len[r] - 1.  causal: keys up to the row's
     position; window > 0: only the last `window` of them.  max_q, max_kv bound
     the rows and cached tokens of a request.  scale: 1 / sqrt(D) by default.
-    A row that sees nothing gives zeros.  Returns out, or (out, lse)."""
+    A row that sees nothing gives zeros; a row of no request is not written.
+    Returns out, or (out, lse)."""
     tokens, hq, dim = q.shape
     if dim != cache.head_dim:
         raise ValueError(f"q: heads of {dim} over a cache of heads of {cache.head_dim}")

@@ -168,8 +168,8 @@ typedef struct {
 
 /* out = softmax(scale q k^T over the keys a query sees) v, request by
  * request.  Query i of request r has position kv_len[r] - (its rows) + i.
- * A row that sees no key gives zeros (and lse -infinity).  Keys on a page
- * outside the cache are not seen.  lse: NULL or fp32 [tokens][q_heads], the
+ * A row that sees no key gives zeros (and lse -infinity); a row of no request
+ * is left as it was.  Keys on a page outside the cache are not seen.  lse: NULL or fp32 [tokens][q_heads], the
  * natural logarithm of the sum of exponentials.  Products are on the 16-bit
  * matrix cores with fp32 accumulation, softmax statistics are fp32, the
  * probabilities (INT4: times the value scale) are rounded to 16 bits for the

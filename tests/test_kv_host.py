@@ -120,6 +120,19 @@ def test_norm_rope_empty_calls_and_row_limit():
     assert fn("svdq_qk_norm_rope")(None, h, h, h, h, None) == INVALID
 
 
+@pytest.mark.parametrize("tokens", [(1 << 31) // 4, 1 << 40, (1 << 62) + 1, (1 << 63) - 1])
+def test_sizes_past_what_a_launch_holds_are_refused_without_overflow(tokens):
+    h, n = heads(), C.c_size_t()
+    assert fn("svdq_qk_norm_rope")(qk(tokens=tokens), h, h, h, h, None) == UNSUPPORTED
+    assert fn("svdq_qk_backward_workspace")(qk(tokens=tokens), 4, 4, n) == UNSUPPORTED
+    assert fn("svdq_qk_norm_rope_backward")(qk(tokens=tokens), h, h, h, h, h, h, P, P, P, 1 << 30, None) == UNSUPPORTED
+    assert fn("svdq_kv_append")(qk(tokens=tokens), None, h, h, None, cache(), P, None) == UNSUPPORTED
+    assert fn("svdq_kv_read")(cache(), P, tokens, S.F16, h, h, None) == UNSUPPORTED
+    q = heads(8, 1024, 128)
+    for change in (dict(requests=tokens), dict(tokens=tokens, max_q=(1 << 31) - 1, requests=1 << 20)):
+        assert fn("svdq_kv_attention")(attn(**change), q, cache(), q, None, P, 1 << 30, None) == UNSUPPORTED
+
+
 def test_backward_workspace():
     n = C.c_size_t()
     assert fn("svdq_qk_backward_workspace")(qk(), 4, 4, n) == OK and n.value == 2 * 2 * 128 * 4    # 40 rows: two groups of 32
