@@ -310,14 +310,18 @@ __device__ __forceinline__ void value_pair_int4(const unsigned* v8, u32x4* f0, u
   }
 }
 
-// the same from dwords with the codes of two keys each, first key in the low half
-template <int DT>
-__device__ __forceinline__ void value_quad_int4(const unsigned* two, u32x4* f0, u32x4* f1) {
+// The same from dwords with the codes of two keys each, first key in the low
+// half, as f16.  SCALED: times the keys' scales, rounded once; `gain` is 512 for
+// the values themselves.
+template <bool SCALED>
+__device__ __forceinline__ void value_quad_int4(const unsigned* two, const unsigned* scale, float gain, u32x4* f0, u32x4* f1) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const unsigned x0 = cvt_int4<DT, false>(two[i]), x1 = cvt_int4<DT, true>(two[i]);
-    (*f0)[i] = low_halves(x0, x1);
-    (*f1)[i] = high_halves(x0, x1);
+    const unsigned x0 = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(two[i], gain, false));
+    const unsigned x1 = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(two[i], gain, true));
+    const unsigned low = low_halves(x0, x1), high = high_halves(x0, x1);
+    (*f0)[i] = SCALED ? __builtin_bit_cast(unsigned, two_halves(low) * two_halves(scale[i])) : low;
+    (*f1)[i] = SCALED ? __builtin_bit_cast(unsigned, two_halves(high) * two_halves(scale[i])) : high;
   }
 }
 
@@ -651,14 +655,21 @@ __global__ __launch_bounds__(256, 2) void k_attn16(AttnParams p) {
 //      holds one INT4 scale group and a lane's results are 4 neighbours
 // Stages are double-buffered: stage i + 1 is written and stage i + 2 requested
 // while stage i is multiplied, with one barrier a stage.
+// INT4: the integers of K go in exactly, the scales of a key come in with the
+// multiply-add that takes the reference off.  V, for bf16, goes in times its
+// scales as f16, beside f16 probabilities: two roundings to 11 bits instead of
+// one of the probabilities to 8 (relative error 1.7e-3 against 2.3e-3), and 5 x
+// 2047 rows take 902 us instead of 1017 with the scales on the probabilities.
+// For f16 that second rounding costs precision (3.4e-4 against 2.8e-4): there
+// the integers go in and the scales stay on the probabilities.
 // The matrix products bound it, and the vector work beside them: a matrix
 // instruction keeps the SIMD from issuing vector ones for half its time.  4608
-// tokens, 24 heads of 128, no mask, MXFP4: 264 us, 990 TFLOP/s (a large bf16
+// tokens, 24 heads of 128, no mask, MXFP4: 262 us, 995 TFLOP/s (a large bf16
 // matrix product: 1250), of which 16% is the second round of 432 workgroups on
-// 256 compute units.  INT4 has the scales of both sums on top: 5 x 2047 rows
-// behind up to 8191 tokens, 32 heads over 8: 1017 us, 673 TFLOP/s.  Tried and
-// slower: the next products under this softmax (281 us), the two waves of a SIMD
-// one phase apart (306), 64 rows a wave (434), no running maximum (282).
+// 256 compute units.  5 x 2047 rows behind up to 8191 tokens, 32 heads over 8:
+// INT4 856 us, 800 TFLOP/s (f16: 973); MXFP4 701, 977.  Tried and slower: the next products
+// under this softmax (281 us), the two waves of a SIMD one phase apart (306), 64
+// rows a wave (434), no running maximum (282).
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
   if constexpr (DT == SVDQ_BF16)
@@ -698,7 +709,7 @@ struct Stage {
   u32x4 k;                  // 32 codes of one key
   unsigned ke;              // MXFP4: its e8m0; INT4: a key's fp16 scales (lanes < WH * 16)
   unsigned v[8];            // 4 codes of 8 keys
-  u32x4 vsc[FMT == SVDQ_FMT_MXFP4_G32 ? (D == 128 ? 2 : 1) : 1];   // MXFP4: the 8 keys' scales; INT4: [0][0] of the lane's key
+  u32x4 vsc[D == 128 ? 2 : 1];   // the 8 keys' scales (of a key: D / 32 bytes)
 };
 
 template <int DT, int FMT, int D, int NW>
@@ -707,10 +718,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   constexpr int KT = St::KT, NC = D / 8, NB = D / 32, NS = D / 16, NX = D / 32, NG = D / 64, PAGES = St::PAGES;
   constexpr bool MX = FMT == SVDQ_FMT_MXFP4_G32;
   constexpr int NA = MX ? 1 : NG;       // accumulators of a logit (INT4: one a scale group)
+  constexpr int VT = MX ? DT : SVDQ_F16;  // type of the second product's operands
+  constexpr bool PS = scaled_reference<DT, FMT>();   // value scales on the probabilities, not on the values
+  constexpr int NP = PS ? NG : 1;       // probabilities of a logit
   __shared__ u32x4 sk[2][NC * KT];
   __shared__ u32x4 sv[2][KT / 8 * D];
-  __shared__ __attribute__((aligned(16))) unsigned sks[2][MX ? 1 : KT], svs[2][MX ? 1 : KT];
-  __shared__ float sve[2][NW];          // exponent of the largest value scale of a wave's keys
+  __shared__ __attribute__((aligned(16))) float sks[2][MX ? 1 : KT * NG];   // INT4: key scales x c
+  __shared__ __attribute__((aligned(16))) unsigned svs[2][PS ? KT : 1];  // value scales
+  __shared__ float svx[2][MX ? 1 : NW]; // exponents: PS: of the largest value scale of a wave's keys; else what its values were divided by
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
   // workgroup -> (row tile, request, head, chunk), chunk fastest; the last row
   // tiles, which see most keys, first; one head's tiles keep to one XCD where
@@ -730,7 +745,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   if (split >= max(range.n, 1)) return;
   const int m = lane & 31, hb = lane >> 5;
   // this wave's rows
-  const int wrow = rt * ROWS + 32 * wave, wq0 = min(wrow / p.group, r.rows - 1), wq1 = min((wrow + 32 - 1) / p.group, r.rows - 1);
+  const int wv = __builtin_amdgcn_readfirstlane(wave);
+  const int wrow = rt * ROWS + 32 * wv, wq0 = min(wrow / p.group, r.rows - 1), wq1 = min((wrow + 32 - 1) / p.group, r.rows - 1);
   const int wfrom = r.low(p, wq0), wto = wrow < rows ? r.high(p, wq1) : 0, wall_low = r.low(p, wq1), wall_high = r.high(p, wq0);
   const int row = wrow + m;
   const int qi = min(row / p.group, r.rows - 1), qh = h * p.group + row % p.group;
@@ -751,7 +767,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   for (int x = 0; x < NX; ++x)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[x][i] = 0.0f;
-  float base = LOWEST, sum = 0.0f;
+  // A row's reference, and how far above it a logit may be before it is raised
+  // (-infinity until the row has seen a key).
+  float base = 0.0f, limit = -__builtin_inff(), sum = 0.0f;
   const float zero = hidden_zero();
 
   const int from = range.from + split * p.chunk, to = min(range.to, from + p.chunk);
@@ -760,7 +778,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   // A wave brings the WH x 16 keys [16 WH wave, ..) of a stage, whose pages are
   // the same for all its lanes: addresses are scalar bases plus lane offsets.
   constexpr int WH = KT / 16 / NW;
-  const int wv = __builtin_amdgcn_readfirstlane(wave);
   const int kkey = tid / NB, kb = tid % NB;                   // K piece: key of the stage, 32-element block
   const int vkeys = tid / (D / 4) * 8, vn = tid % (D / 4);    // V block: first of 8 keys, columns 4 vn ..
   // a lane's page of the stage at `token` (lane l: keys 16 (l % PAGES) ..)
@@ -787,37 +804,26 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     const uint8_t* vc = at(p.vc, vk, D / 2) + 2 * vn;
 #pragma unroll
     for (int i = 0; i < 8; ++i) st.v[i] = *reinterpret_cast<const uint16_t*>(vc + i * (D / 2));
+    const u32x4* vs = reinterpret_cast<const u32x4*>(at(p.vs, vk, NB));
+    st.vsc[0] = vs[0];
+    if constexpr (D == 128) st.vsc[1] = vs[1];
     if constexpr (MX) {
       st.ke = *(at(p.ks, lane / NB, NB) + kb);
-      const u32x4* vs = reinterpret_cast<const u32x4*>(at(p.vs, vk, NB));
-      st.vsc[0] = vs[0];
-      if constexpr (D == 128) st.vsc[1] = vs[1];
     } else if (lane < 16 * WH) {
-      if constexpr (D == 128) {
-        st.ke = *reinterpret_cast<const unsigned*>(at(p.ks, lane, 4));
-        st.vsc[0][0] = *reinterpret_cast<const unsigned*>(at(p.vs, lane, 4));
-      } else {
-        st.ke = *reinterpret_cast<const uint16_t*>(at(p.ks, lane, 2));
-        st.vsc[0][0] = *reinterpret_cast<const uint16_t*>(at(p.vs, lane, 2));
-      }
+      if constexpr (D == 128) st.ke = *reinterpret_cast<const unsigned*>(at(p.ks, lane, 4));
+      else st.ke = *reinterpret_cast<const uint16_t*>(at(p.ks, lane, 2));
     }
   };
   // Keys past the end or on a missing page may hold a NaN: their value scales
   // become zero (MXFP4: the smallest), before the stage is turned into operands.
   auto mend = [&](St& st, int token, unsigned bad) {
     if (bad == 0u && token + KT <= r.len) return;       // the same for all threads
-    if constexpr (MX) {
-      const bool gone = (bad >> (vkeys / 16)) & 1u;
+    const bool gone = (bad >> (vkeys / 16)) & 1u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool zero = gone || token + vkeys + i >= r.len;
-        if constexpr (D == 128) st.vsc[i / 4][i % 4] = zero ? 0u : st.vsc[i / 4][i % 4];
-        else st.vsc[0][i / 2] = zero ? st.vsc[0][i / 2] & (i % 2 ? 0x0000FFFFu : 0xFFFF0000u) : st.vsc[0][i / 2];
-      }
-    } else {
-      const int key = 16 * WH * wave + lane % (16 * WH);
-      const bool gone = ((bad >> (key / 16)) & 1u) || token + key >= r.len;
-      st.vsc[0][0] = gone ? 0u : st.vsc[0][0];
+    for (int i = 0; i < 8; ++i) {
+      const bool zero = gone || token + vkeys + i >= r.len;
+      if constexpr (D == 128) st.vsc[i / 4][i % 4] = zero ? 0u : st.vsc[i / 4][i % 4];
+      else st.vsc[0][i / 2] = zero ? st.vsc[0][i / 2] & (i % 2 ? 0x0000FFFFu : 0xFFFF0000u) : st.vsc[0][i / 2];
     }
   };
   auto write = [&](const St& st, int buf) {
@@ -842,38 +848,66 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       v[48] = f1;
     } else {
       // two keys' codes in a dword, so that the bits are moved once for both
-      unsigned ev[4], od[4];
+      unsigned ev[4], od[4], sc[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const unsigned w = st.v[2 * i] | (st.v[2 * i + 1] << 16);
         ev[i] = int4_even(w);
         od[i] = int4_odd(w);
       }
-      value_quad_int4<DT>(ev, &f0, &f1);
+      float gain = 512.0f;
+      if constexpr (PS) {
+        f16x2 most = two_halves(st.vsc[0][0]);
+#pragma unroll
+        for (int i = 1; i < D / 16; ++i) most = __builtin_elementwise_max(most, two_halves(st.vsc[i / 4][i % 4]));
+        float x = fmaxf(float(most[0]), float(most[1]));
+        x = D == 128 ? half_max(x) : quad_max(x);
+        if (lane == 0) svx[buf][wave] = scale_exponent(x);
+        if (vn == 0) {
+          u32x4* y = reinterpret_cast<u32x4*>(&svs[buf][vkeys]);
+          if constexpr (D == 128) {
+            y[0] = st.vsc[0];
+            y[1] = st.vsc[1];
+          } else {
+            y[0] = u32x4{st.vsc[0][0], st.vsc[0][0] >> 16, st.vsc[0][1], st.vsc[0][1] >> 16};
+            y[1] = u32x4{st.vsc[0][2], st.vsc[0][2] >> 16, st.vsc[0][3], st.vsc[0][3] >> 16};
+          }
+        }
+      } else {
+        const unsigned pick = vn >= 16 ? 0x07060302u : 0x05040100u;      // D = 128: the half of the columns' group
+        // 7 times a scale from 2^13 on would pass f16: then the wave's values go
+        // in at an eighth, and their probabilities at eight times
+        bool big = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (D == 128) sc[i] = __builtin_amdgcn_perm(st.vsc[i / 2][2 * i % 4 + 1], st.vsc[i / 2][2 * i % 4], pick);
+          else sc[i] = st.vsc[0][i];
+          big |= (sc[i] & 0x7000u) == 0x7000u || (sc[i] & 0x70000000u) == 0x70000000u;
+        }
+        const bool any = __any(big);
+        if (any) gain = 64.0f;
+        if (lane == 0) svx[buf][wave] = any ? 3.0f : 0.0f;
+      }
+      if (lane < 16 * WH) {
+        const f16x2 ks = two_halves(st.ke);
+        if constexpr (NG == 2) *reinterpret_cast<f32x2*>(&sks[buf][2 * (16 * WH * wave + lane)]) = f32x2{float(ks[0]) * c, float(ks[1]) * c};
+        else sks[buf][16 * WH * wave + lane] = float(ks[0]) * c;
+      }
+      value_quad_int4<!PS>(ev, sc, gain, &f0, &f1);
       v[0] = f0;
       v[32] = f1;
-      value_quad_int4<DT>(od, &f0, &f1);
+      value_quad_int4<!PS>(od, sc, gain, &f0, &f1);
       v[16] = f0;
       v[48] = f1;
     }
   };
-  auto write_scales = [&](const St& st, int buf) {             // INT4
-    if constexpr (!MX) {
-      if (lane >= 16 * WH) return;
-      sks[buf][16 * WH * wave + lane] = st.ke;
-      svs[buf][16 * WH * wave + lane] = st.vsc[0][0];
-      if constexpr (scaled_reference<DT, FMT>()) {
-        const f16x2 f = two_halves(st.vsc[0][0]);
-        float most = fmaxf(float(f[0]), float(f[1]));
-#pragma unroll
-        for (int x = 1; x < 16 * WH; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
-        if (lane == 0) sve[buf][wave] = scale_exponent(most);
-      }
-    }
-  };
 
-  // Logits of 64 keys of stage `buf` from key `at` of it on.
-  auto logits = [&](int buf, int at, float* s) {
+  // Logits of 64 keys of stage `buf` from key `at` of it on.  INT4: in powers of
+  // two and less the reference so far, one multiply-add a logit and scale group
+  // (866 us where the reference took one of its own, 905).  MXFP4: as they come
+  // from the product (taken here, before the maximum, the multiply-add that it
+  // needs all the same costs 270 us instead of 262).
+  auto logits = [&](int buf, int at, f32x16* s) {
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
       f32x16 acc[NA];
@@ -888,77 +922,108 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       }
       reads_ahead<NS>();
       if constexpr (MX) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[16 * kt + i] = acc[0][i];
+        s[kt] = acc[0];
       } else {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {     // keys 16 (x / 2) + 8 hb + 4 (x % 2) ..
-          const u32x4 w = *reinterpret_cast<const u32x4*>(&sks[buf][at + 32 * kt + 16 * (x / 2) + 8 * hb + 4 * (x % 2)]);
+          f32x4 w[NG];
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            w[g] = *reinterpret_cast<const f32x4*>(&sks[buf][(at + 32 * kt + 16 * (x / 2) + 8 * hb + 4 * (x % 2)) * NG + 4 * g]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float d = fma_half<0>(acc[0][4 * x + i], w[i], zero);
-            if constexpr (NG == 2) d = fma_half<1>(acc[NA - 1][4 * x + i], w[i], d);
-            s[16 * kt + 4 * x + i] = d;
+            if constexpr (NG == 2)
+              s[kt][4 * x + i] = __builtin_fmaf(acc[NA - 1][4 * x + i], w[i / 2][2 * i % 4 + 1],
+                                                __builtin_fmaf(acc[0][4 * x + i], w[i / 2][2 * i % 4], -base));
+            else
+              s[kt][4 * x + i] = __builtin_fmaf(acc[0][4 * x + i], w[0][i], -base);
           }
         }
+        asm volatile("" : "+v"(s[kt]));    // here, not after the next tile's products: 66 registers of spills
       }
     }
   };
   // Masks them and raises the rows' references where they need it.
-  auto refer = [&](int buf, int token, int at, unsigned bad, float* s) {
+  auto refer = [&](int token, int at, unsigned bad, float most, f32x16* s) {
     const int t0 = token + at;
     const unsigned gone = (bad >> (at / 16)) & 15u;
     if (!(t0 >= wall_low && t0 + 64 <= wall_high && gone == 0u)) {
+      // (in place, as vectors: element by element the compiler copies the
+      // logits on the way round this, too)
+      const unsigned first = unsigned(t0 + 8 * hb - low), wide = unsigned(max(high - low, 0));
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const int k = 32 * (i / 16) + 16 * ((i % 16) / 8) + 8 * hb + i % 8;
-        const bool see = t0 + k >= low && t0 + k < high && ((gone >> (i / 8)) & 1u) == 0u;
-        s[i] = see ? s[i] : -__builtin_inff();
+        const unsigned k = 32 * (i / 16) + 16 * ((i % 16) / 8) + i % 8;
+        s[i / 16][i % 16] = first + k < wide ? s[i / 16][i % 16] : -__builtin_inff();
+      }
+      if (gone != 0u) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          s[i / 16][i % 16] = ((gone >> (i / 8)) & 1u) == 0u ? s[i / 16][i % 16] : -__builtin_inff();
       }
     }
-    float top = s[0];
+    float top = s[0][0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i]);
-    top = half_max(top) * c - p_shift<DT>();
-    if constexpr (scaled_reference<DT, FMT>()) {
-      float most = sve[buf][at / (16 * WH)];
-#pragma unroll
-      for (int i = 1; i < 4 / WH; ++i) most = fmaxf(most, sve[buf][at / (16 * WH) + i]);
-      top += most;
-    }
-    if (__any(top > base + SLACK)) {
-      const float next = fmaxf(base, top), alpha = exp2_hw(base - next);
-      base = next;
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+    top = half_max(top);
+    if constexpr (MX) top = __builtin_fmaf(top, c, -base);
+    else top += most;
+    if (__any(top > limit)) {
+      const bool first_keys = limit < 0.0f, seen = top > -__builtin_inff();
+      const float up = first_keys ? (seen ? top - p_shift<VT>() : 0.0f) : fmaxf(top - p_shift<VT>(), 0.0f);
+      const float alpha = first_keys ? 1.0f : exp2_hw(-up);
+      base += up;
+      limit = first_keys && !seen ? limit : p_shift<VT>() + SLACK;
+      if constexpr (!MX) {
+        s[0] -= up;
+        s[1] -= up;
+      }
       sum *= alpha;
 #pragma unroll
       for (int x = 0; x < NX; ++x) o[x] *= alpha;
     }
   };
   // Probabilities of these keys as operands.
-  auto weigh = [&](int buf, int at, float* s, u32x4 (*pf)[4]) {
+  auto weigh = [&](int buf, int at, float most, f32x16* s, u32x4 (*pf)[4]) {
     float part = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      s[i] = exp2_hw(__builtin_fmaf(s[i], c, -base));
-      part += s[i];
+      s[i / 16][i % 16] = exp2_hw(MX ? __builtin_fmaf(s[i / 16][i % 16], c, -base) : s[i / 16][i % 16]);
+      part += s[i / 16][i % 16];
     }
     sum += part;
-    if constexpr (MX) {
+    if constexpr (!PS) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) pf[0][i / 4][i % 4] = pack2<DT>(s[2 * i], s[2 * i + 1]);
+      for (int i = 0; i < 16; ++i) pf[0][i / 4][i % 4] = pack2<VT>(s[i / 8][2 * i % 16], s[i / 8][2 * i % 16 + 1]);
+      if (!MX && most > 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {       // keys 16 i ..
+          const _Float16 g = svx[buf][(at + 16 * i) / (16 * WH)] > 0.0f ? 8 : 1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pf[0][i][e] = __builtin_bit_cast(unsigned, two_halves(pf[0][i][e]) * f16x2{g, g});
+        }
+      }
     } else {
 #pragma unroll
       for (int x = 0; x < 8; ++x) {       // keys 16 (x / 2) + 8 hb + 4 (x % 2) ..
         const u32x4 w = *reinterpret_cast<const u32x4*>(&svs[buf][at + 16 * (x / 2) + 8 * hb + 4 * (x % 2)]);
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float p0 = s[4 * x + i], p1 = s[4 * x + i + 1];
-          pf[0][x / 2][2 * (x % 2) + i / 2] = pack2<DT>(fma_half<0>(p0, w[i], zero), fma_half<0>(p1, w[i + 1], zero));
-          if constexpr (NG == 2)
-            pf[NA - 1][x / 2][2 * (x % 2) + i / 2] = pack2<DT>(fma_half<1>(p0, w[i], zero), fma_half<1>(p1, w[i + 1], zero));
+          const float p0 = s[x / 4][4 * x % 16 + i], p1 = s[x / 4][4 * x % 16 + i + 1];
+          pf[0][x / 2][2 * (x % 2) + i / 2] = pack2<VT>(fma_half<0>(p0, w[i], zero), fma_half<0>(p1, w[i + 1], zero));
+          if constexpr (NP == 2)
+            pf[NP - 1][x / 2][2 * (x % 2) + i / 2] = pack2<VT>(fma_half<1>(p0, w[i], zero), fma_half<1>(p1, w[i + 1], zero));
         }
       }
     }
+  };
+  // the largest exponent of these keys' values
+  auto exponent = [&](int buf, int at) {
+    if constexpr (MX) return 0.0f;
+    float most = svx[buf][at / (16 * WH)];
+#pragma unroll
+    for (int i = 1; i < 4 / WH; ++i) most = fmaxf(most, svx[buf][at / (16 * WH) + i]);
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
   };
   auto add_values = [&](int buf, int at, const u32x4 (*pf)[4]) {
 #pragma unroll
@@ -966,7 +1031,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const u32x4 a = sv[buf][(at / 8 + 2 * j + hb) * D + 32 * x + m];
-        o[x] = mfma32<DT>(a, pf[MX ? 0 : x / 2][j], o[x]);
+        o[x] = mfma32<VT>(a, pf[NP == 2 ? x / 2 : 0][j], o[x]);
       }
     }
     reads_ahead<4 * NX>();
@@ -980,7 +1045,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     page = look_up(from + KT);
     mend(st, from, bad);
     write(st, 0);
-    write_scales(st, 0);
     if (from + KT < to) {
       bad1 = bad_pages(page);
       request(st, from + KT, page);
@@ -993,7 +1057,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       const unsigned here = bad;
       if (token + KT < to) {
         mend(st, token + KT, bad1);
-        write_scales(st, buf ^ 1);
         write(st, buf ^ 1);
         bad = bad1;
         if (token + 2 * KT < to) {
@@ -1005,15 +1068,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
 #pragma unroll 2
       for (int at = 0; at < KT; at += 64) {
         if (!used(token + at)) continue;
-        float s[32];
-        u32x4 pf[NA][4];
+        f32x16 s[2];
+        u32x4 pf[NP][4];
         // the wave that multiplies issues before the one beside it that does
         // not, which keeps the two apart
         __builtin_amdgcn_s_setprio(1);
         logits(buf, at, s);
         __builtin_amdgcn_s_setprio(0);
-        refer(buf, token, at, here, s);
-        weigh(buf, at, s, pf);
+        const float most = exponent(buf, at);
+        refer(token, at, here, most, s);
+        weigh(buf, at, most, s, pf);
         __builtin_amdgcn_s_setprio(1);
         add_values(buf, at, pf);
         __builtin_amdgcn_s_setprio(0);
@@ -1023,6 +1087,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     }
   }
   sum = half_sum(sum);
+  if (limit < 0.0f) base = LOWEST;
   if (row >= rows) return;
   const bool whole = range.n <= 1;
   const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;

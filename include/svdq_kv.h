@@ -169,11 +169,12 @@ typedef struct {
 /* out = softmax(scale q k^T over the keys a query sees) v, request by
  * request.  Query i of request r has position kv_len[r] - (its rows) + i.
  * A row that sees no key gives zeros (and lse -infinity); a row of no request
- * is left as it was.  Keys on a page outside the cache are not seen.  lse: NULL or fp32 [tokens][q_heads], the
- * natural logarithm of the sum of exponentials.  Products are on the 16-bit
- * matrix cores with fp32 accumulation, softmax statistics are fp32, the
- * probabilities (INT4: times the value scale) are rounded to 16 bits for the
- * second product.  With f16, MXFP4 scales above 2^15 count as 2^15 and ones
+ * is left as it was.  Keys on a page outside the cache are not seen.  lse: NULL
+ * or fp32 [tokens][q_heads], the natural logarithm of the sum of exponentials.
+ * Products are on the 16-bit matrix cores with fp32 accumulation, softmax
+ * statistics are fp32, the probabilities (INT4: times the value scale, or, with
+ * bf16 and many rows, they and the values to f16's 11 bits) are rounded to 16
+ * bits for the second product.  With f16, MXFP4 scales above 2^15 count as 2^15 and ones
  * below 2^-124 as 2^-124.  ws: >= svdq_kv_attention_workspace
  * bytes, 256-byte aligned (may be NULL where that is 0); its content need
  * not be kept between calls.  The size goes by requests, tokens, q_heads,

@@ -184,6 +184,25 @@ def test_scales_of_logits_and_of_values(fmt, dtype, dim):
     _run(fmt, dtype, dim, 16, 1, 2, [1], [300], k_size=2.0 ** -9)
 
 
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("bf16", 128), ("f16", 64), ("f16", 128)])
+@pytest.mark.parametrize("fresh", [[1], [90]])
+def test_value_scales_near_the_end_of_f16(dtype, dim, fresh):
+    """INT4 values past f16's range (7 x 65504) beside ones of ordinary size, in
+    some keys of a tile and in whole tiles."""
+    torch, kv, _ = _mods()
+    cache, table, slots, q, start, length = _setup("int4_g64", dtype, dim, 16, 1, 2, fresh, [300])
+    top = 65504.0 if dtype == "bf16" else 9000.0           # 7 x 9000 is what an f16 result holds
+    s = cache.v_scales.view(-1, dim // 64)
+    at = slots.long()
+    for keys, scale in ((at[37], top), (at[150:155], 8191.0), (at[155:160], 8192.0), (at[192:256], top / 2)):
+        s[keys] = scale
+    assert torch.equal(cache.v_scales.view(-1, dim // 64)[at[37]], torch.full((dim // 64,), top, device="cuda").half())
+    out, lse = kv.attention(q, cache, table, start, length, max(fresh), 300, return_lse=True)
+    k, v = _values64(cache, slots, "int4_g64")
+    assert float(v.abs().max()) > 50000
+    _check(out, lse, _reference(q, k, v, fresh, [300], 2, True, 0, dim ** -0.5), dtype, dim)
+
+
 @pytest.mark.parametrize("fresh", [[1, 1], [30, 4]])
 def test_bounds_pages_outside_the_cache_and_bad_lengths(fresh):
     """Missing pages are not seen; max_q, max_kv and the table's width bound
