@@ -90,16 +90,20 @@ __device__ __forceinline__ float scale_exponent(float s) {
   return s == 0.0f ? -24.0f : float(int(__float_as_uint(s) >> 23) - 127);
 }
 
+// NaN if either is one: one instruction for three, where fmaxf has to quiet its
+// operands first.  A row with a NaN gives NaN by its probabilities.
+__device__ __forceinline__ float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // max / sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48 of a column
 __device__ __forceinline__ float quad_max(float x) {
   const unsigned u = __float_as_uint(x);
   const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const float m = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const float m = maximum(__uint_as_float(a[0]), __uint_as_float(a[1]));
   const unsigned v = __float_as_uint(m);
   const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  return maximum(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float quad_sum(float x) {
   const unsigned u = __float_as_uint(x);
@@ -154,8 +158,9 @@ struct Request {
 // and head of 128): the codes go from memory to registers and are turned there,
 // with two tiles in flight a wave and three waves a SIMD.  48 requests of up to
 // 16384 tokens, 8 heads of 128, 4 query heads each: MXFP4 114 us, 4.8 TB/s; INT4
-// 182 us, where the vector unit is the bound (its integers need twice MXFP4's
-// instructions: bits to fp8, conversion, and scales on both sums).  Two row tiles
+// 129 us (f16 136), where the vector unit is the bound: bits to fp8, conversion,
+// and scales on both sums.  With the converted values paired instead of their
+// codes, and 190 registers, two waves, it took 180.  Two row tiles
 // a wave on the same operands were slower for MXFP4 (40 rows: 309 us against 199
 // with three tiles of 16: two waves a SIMD instead of three).
 template <int FMT, int D>
@@ -274,18 +279,13 @@ __device__ __forceinline__ u32x4 query_order(u32x4 q) {
   return u32x4{low_halves(q[0], q[1]), low_halves(q[2], q[3]), high_halves(q[0], q[1]), high_halves(q[2], q[3])};
 }
 
-// 8 keys' scales of one head row group, fp32 (INT4) or converter scales (MXFP4)
-template <int DT, int FMT, int D>
+// MXFP4: converter scale of key i and group g
+template <int DT, int D>
 __device__ __forceinline__ float value_scale(const u32x4* sc, int i, int g) {
-  if constexpr (FMT == SVDQ_FMT_MXFP4_G32) {
-    const unsigned w = D == 128 ? sc[i / 4][i % 4] : sc[0][i / 2];
-    const unsigned b = D == 128 ? 8 * g : 16 * (i % 2) + 8 * g;         // bit of the byte
-    if constexpr (DT == SVDQ_F16) return mx_scale<DT>((w >> b) & 255u);
-    return __uint_as_float(__builtin_amdgcn_alignbit(w, w, b + 9u) & 0x7F800000u);   // rotated to bits 23-30
-  } else {
-    const unsigned w = D == 128 ? sc[i / 4][i % 4] >> (16 * g) : sc[0][i / 2] >> (16 * (i % 2));
-    return h2f<SVDQ_F16>(w & 0xFFFFu);
-  }
+  const unsigned w = D == 128 ? sc[i / 4][i % 4] : sc[0][i / 2];
+  const unsigned b = D == 128 ? 8 * g : 16 * (i % 2) + 8 * g;         // bit of the byte
+  if constexpr (DT == SVDQ_F16) return mx_scale<DT>((w >> b) & 255u);
+  return __uint_as_float(__builtin_amdgcn_alignbit(w, w, b + 9u) & 0x7F800000u);   // rotated to bits 23-30
 }
 
 // two value fragments (columns x and x + 1 of the pair) of 8 keys, MXFP4
@@ -299,43 +299,57 @@ __device__ __forceinline__ void value_pair_mx(const unsigned* v, const float* s,
   }
 }
 
-// the same for INT4, from fp8 words: the integers themselves
-template <int DT, bool HI>
-__device__ __forceinline__ void value_pair_int4(const unsigned* v8, u32x4* f0, u32x4* f1) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned x0 = cvt_int4<DT, HI>(v8[2 * i]), x1 = cvt_int4<DT, HI>(v8[2 * i + 1]);
-    (*f0)[i] = low_halves(x0, x1);
-    (*f1)[i] = high_halves(x0, x1);
-  }
+// INT4: the codes of four keys are dealt out by columns before they are
+// converted, half as many byte moves as for the converted values.  y[j]: bytes
+// first + j of v[0] .. v[3] (j = 0, 1); `pick` has the bytes of two words.
+__device__ __forceinline__ unsigned byte_pick(int first) { return first == 0 ? 0x05010400u : 0x07030602u; }
+__device__ __forceinline__ void deal(const unsigned* v, unsigned pick, unsigned* y) {
+  const unsigned a = __builtin_amdgcn_perm(v[1], v[0], pick), b = __builtin_amdgcn_perm(v[3], v[2], pick);
+  y[0] = low_halves(a, b);
+  y[1] = high_halves(a, b);
 }
-
-// The same from dwords with the codes of two keys each, first key in the low
-// half, as f16.  SCALED: times the keys' scales, rounded once; `gain` is 512 for
-// the values themselves.
-template <bool SCALED>
-__device__ __forceinline__ void value_quad_int4(const unsigned* two, const unsigned* scale, float gain, u32x4* f0, u32x4* f1) {
+// one column's value fragment from its fp8 words of the keys 0 .. 3 and 4 .. 7
+template <int DT>
+__device__ __forceinline__ u32x4 value_int4(unsigned keys0, unsigned keys4) {
+  return u32x4{cvt_int4<DT, false>(keys0), cvt_int4<DT, true>(keys0), cvt_int4<DT, false>(keys4), cvt_int4<DT, true>(keys4)};
+}
+// The same times the keys' scales (pairs), as f16 rounded once; `gain` is 512
+// for the values themselves.
+__device__ __forceinline__ u32x4 value_int4_scaled(unsigned keys0, unsigned keys4, const unsigned* scale, float gain) {
+  const u32x4 f = {__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(keys0, gain, false)),
+                   __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(keys0, gain, true)),
+                   __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(keys4, gain, false)),
+                   __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(keys4, gain, true))};
+  u32x4 y;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned x0 = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(two[i], gain, false));
-    const unsigned x1 = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(two[i], gain, true));
-    const unsigned low = low_halves(x0, x1), high = high_halves(x0, x1);
-    (*f0)[i] = SCALED ? __builtin_bit_cast(unsigned, two_halves(low) * two_halves(scale[i])) : low;
-    (*f1)[i] = SCALED ? __builtin_bit_cast(unsigned, two_halves(high) * two_halves(scale[i])) : high;
-  }
+  for (int i = 0; i < 4; ++i) y[i] = __builtin_bit_cast(unsigned, two_halves(f[i]) * two_halves(scale[i]));
+  return y;
+}
+// scale of key i and group g in the words of 8 keys, and a times it (see fma_half)
+template <int D>
+__device__ __forceinline__ float fma_scale(float a, const u32x4* sc, int i, int g, float c) {
+  const unsigned w = D == 128 ? sc[i / 4][i % 4] : sc[0][i / 2];
+  return __builtin_fmaf(a, float(two_halves(w)[D == 128 ? g : i % 2]), c);
+}
+// largest of 8 keys' scales
+template <int D>
+__device__ __forceinline__ float most_scale(const u32x4* sc) {
+  f16x2 most = two_halves(sc[0][0]);
+#pragma unroll
+  for (int i = 1; i < D / 16; ++i) most = __builtin_elementwise_max(most, two_halves(sc[i / 4][i % 4]));
+  return fmaxf(float(most[0]), float(most[1]));
 }
 
 // column of the result that lane row n of value tile x stands for.  MXFP4:
 // the lane's elements in order.  INT4: tile x holds one scale group's columns
-// only (D = 128: tiles 0-3 the first, 4-7 the second), nibbles 0 2 1 3 of the
-// 16 bits of the group that Rows16::step gives the lane.
+// only (D = 128: tiles 0-3 the first, 4-7 the second), the nibbles of the 16
+// bits of the group that Rows16::step gives the lane in order.
 template <int FMT, int D>
 __device__ __forceinline__ constexpr int value_col(int n, int x) {
   constexpr int PER = D / 16;
   if (FMT == SVDQ_FMT_MXFP4_G32) return PER * n + x;
-  constexpr int ORDER[4] = {0, 2, 1, 3};
-  if (D == 64) return 4 * n + ORDER[x];
-  return 64 * (x / 4) + 8 * (n & 7) + 4 * (n >> 3) + ORDER[x % 4];
+  if (D == 64) return 4 * n + x;
+  return 64 * (x / 4) + 8 * (n & 7) + 4 * (n >> 3) + x % 4;
 }
 
 template <int DT, int FMT, int D>
@@ -353,10 +367,11 @@ struct Rows16 {
     sum = 0.0f;
   }
 
-  // all: every row sees every key of the tile and both pages are there
-  __device__ __forceinline__ void step(const AttnParams& p, const Tile32<FMT, D>& t, int token, int len, bool all, int lane) {
+  // all: every row sees every key of the tile and both pages are there; c > 0
+  __device__ __forceinline__ void step(const Tile32<FMT, D>& t, int token, int len, bool all, float c, int lane) {
     const int b = lane >> 4;
-    float s[8];
+    const float zero = hidden_zero();
+    f32x4 s[2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       f32x4 acc = {0, 0, 0, 0};
@@ -364,53 +379,44 @@ struct Rows16 {
         const float e = mx_scale<DT>(t.ke[a]);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc = mfma16<DT>(key_frag<DT, FMT>(t.k[a][j], e), q[j], acc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[4 * a + i] = acc[i];
+        s[a] = acc;
       } else {
         acc = mfma16<DT>(key_frag<DT, FMT>(t.k[a][0], 0.0f), q[0], acc);
         acc = mfma16<DT>(key_frag<DT, FMT>(t.k[a][1], 0.0f), q[1], acc);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[4 * a + i] = acc[i] * value_scale<DT, FMT, D>(t.ksc, 4 * a + i, 0);
+        for (int i = 0; i < 4; ++i) s[a][i] = fma_scale<D>(acc[i], t.ksc, 4 * a + i, 0, zero);
         if constexpr (D == 128) {
           acc = f32x4{0, 0, 0, 0};
           acc = mfma16<DT>(key_frag<DT, FMT>(t.k[a][2], 0.0f), q[2], acc);
           acc = mfma16<DT>(key_frag<DT, FMT>(t.k[a][3], 0.0f), q[3], acc);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s[4 * a + i] = __builtin_fmaf(acc[i], value_scale<DT, FMT, D>(t.ksc, 4 * a + i, 1), s[4 * a + i]);
+          for (int i = 0; i < 4; ++i) s[a][i] = fma_scale<D>(acc[i], t.ksc, 4 * a + i, 1, s[a][i]);
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] *= p.c;
     const bool there = b >= 2 ? t.ok1 : t.ok0;
+    const int last = there ? len - (token + 8 * b) : 0;       // keys from here on are not there: they may hold a NaN
+    u32x4 vsc[Tile32<FMT, D>::NS];
+#pragma unroll
+    for (int i = 0; i < Tile32<FMT, D>::NS; ++i) vsc[i] = t.vsc[i];
     if (!all) {
+      const unsigned first = unsigned(token + 8 * b - low), wide = there ? unsigned(max(high - low, 0)) : 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = token + 8 * b + i;
-        s[i] = there && k >= low && k < high ? s[i] : -__builtin_inff();
-      }
-    }
-    float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-    const int m = lane & 15;
-    float vs[FMT == SVDQ_FMT_INT4_G64 ? D / 64 : 1][8];
-    if constexpr (FMT == SVDQ_FMT_INT4_G64) {
-#pragma unroll
-      for (int g = 0; g < D / 64; ++g)
+      for (int i = 0; i < 8; ++i) s[i / 4][i % 4] = first + unsigned(i) < wide ? s[i / 4][i % 4] : -__builtin_inff();
+      if constexpr (FMT == SVDQ_FMT_INT4_G64) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float c = value_scale<DT, FMT, D>(t.vsc, i, g);
-          vs[g][i] = all || (there && token + 8 * b + i < len) ? c : 0.0f;   // a key that is not there may hold a NaN
+          if constexpr (D == 128) vsc[i / 4][i % 4] = i < last ? vsc[i / 4][i % 4] : 0u;
+          else vsc[0][i / 2] = i < last ? vsc[0][i / 2] : vsc[0][i / 2] & (i % 2 ? 0x0000FFFFu : 0xFFFF0000u);
         }
+      }
     }
-    if constexpr (scaled_reference<DT, FMT>()) {
-      float most = vs[0][0];
+    const int m = lane & 15;
+    float top = s[0][0];
 #pragma unroll
-      for (int g = 0; g < D / 64; ++g)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) most = fmaxf(most, vs[g][i]);
-      top += scale_exponent(most);
-    }
+    for (int i = 1; i < 8; ++i) top = maximum(top, s[i / 4][i % 4]);
+    top *= c;
+    if constexpr (scaled_reference<DT, FMT>()) top += scale_exponent(most_scale<D>(vsc));
     top = quad_max(top) - p_shift<DT>();
     if (__any(top > base + SLACK)) {
       const float next = fmaxf(base, top), alpha = exp2_hw(base - next);
@@ -423,7 +429,7 @@ struct Rows16 {
       u32x4 pf;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float p0 = exp2_hw(s[2 * i] - base), p1 = exp2_hw(s[2 * i + 1] - base);
+        const float p0 = exp2_hw(__builtin_fmaf(s[i / 2][2 * i % 4], c, -base)), p1 = exp2_hw(__builtin_fmaf(s[i / 2][2 * i % 4 + 1], c, -base));
         sum += p0 + p1;
         pf[i] = pack2<DT>(p0, p1);
       }
@@ -432,10 +438,10 @@ struct Rows16 {
       float sc[8];
       const int g = D == 128 ? m >> 2 : m >> 3;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sc[i] = value_scale<DT, FMT, D>(t.vsc, i, g);
+      for (int i = 0; i < 8; ++i) sc[i] = value_scale<DT, D>(t.vsc, i, g);
       if (!all) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sc[i] = there && token + 8 * b + i < len ? sc[i] : 0.0f;
+        for (int i = 0; i < 8; ++i) sc[i] = i < last ? sc[i] : 0.0f;
       }
       unsigned v[8];
 #pragma unroll
@@ -460,48 +466,43 @@ struct Rows16 {
       // group: the integers are exact, and p s is rounded where p was.
       float pr[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pr[i] = exp2_hw(s[i] - base);
+      for (int i = 0; i < 8; ++i) pr[i] = exp2_hw(__builtin_fmaf(s[i / 4][i % 4], c, -base));
 #pragma unroll
       for (int i = 0; i < 8; i += 2) sum += pr[i] + pr[i + 1];
       u32x4 pf[D / 64];
 #pragma unroll
-      for (int g = 0; g < D / 64; ++g) {
-        float ps[8];
+      for (int g = 0; g < D / 64; ++g)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ps[i] = pr[i] * vs[g][i];
+        for (int i = 0; i < 4; ++i)
+          pf[g][i] = pack2<DT>(fma_scale<D>(pr[2 * i], vsc, 2 * i, g, zero), fma_scale<D>(pr[2 * i + 1], vsc, 2 * i + 1, g, zero));
+      // D = 128: lanes n and n + 8 hold eight columns of either group: each
+      // takes four of both.  `own` are a lane's own columns of its group,
+      // `other` the four that go to the lane across.
+      constexpr int NG = D / 64;
+      unsigned cols[NG][2][2];            // [group][keys 0 .. 3, 4 .. 7][byte]
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pf[g][i] = pack2<DT>(ps[2 * i], ps[2 * i + 1]);
-      }
-      unsigned ev[8], od[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        unsigned w;
+      for (int k = 0; k < 2; ++k) {
         if constexpr (D == 128) {
-          // lanes n and n + 8 hold eight columns of either group: each takes
-          // four of both, the first group's in the low half
-          const unsigned u = unsigned(__builtin_amdgcn_update_dpp(0, int(t.v[i]), 0x128, 0xF, 0xF, false));   // row_ror:8
-          w = __builtin_amdgcn_perm(t.v[i], u, m < 8 ? 0x01000504u : 0x07060302u);
+          unsigned own[2], other[2];
+          deal(t.v + 4 * k, m < 8 ? byte_pick(0) : byte_pick(2), own);
+          deal(t.v + 4 * k, m < 8 ? byte_pick(2) : byte_pick(0), other);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {   // row_ror:8 into the upper eight lanes, and into the lower ones
+            cols[0][k][j] = unsigned(__builtin_amdgcn_update_dpp(int(own[j]), int(other[j]), 0x128, 0xF, 0xC, false));
+            cols[NG - 1][k][j] = unsigned(__builtin_amdgcn_update_dpp(int(own[j]), int(other[j]), 0x128, 0xF, 0x3, false));
+          }
         } else {
-          w = t.v[i] >> (16 * (m & 1));
+          deal(t.v + 4 * k, m % 2 == 0 ? byte_pick(0) : byte_pick(2), cols[0][k]);
         }
-        ev[i] = int4_even(w);
-        od[i] = int4_odd(w);
       }
-      u32x4 f0, f1;
-      value_pair_int4<DT, false>(ev, &f0, &f1);
-      o[0] = mfma16<DT>(f0, pf[0], o[0]);
-      o[1] = mfma16<DT>(f1, pf[0], o[1]);
-      value_pair_int4<DT, false>(od, &f0, &f1);
-      o[2] = mfma16<DT>(f0, pf[0], o[2]);
-      o[3] = mfma16<DT>(f1, pf[0], o[3]);
-      if constexpr (D == 128) {
-        value_pair_int4<DT, true>(ev, &f0, &f1);
-        o[4] = mfma16<DT>(f0, pf[1], o[4]);
-        o[5] = mfma16<DT>(f1, pf[1], o[5]);
-        value_pair_int4<DT, true>(od, &f0, &f1);
-        o[6] = mfma16<DT>(f0, pf[1], o[6]);
-        o[7] = mfma16<DT>(f1, pf[1], o[7]);
-      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const unsigned w0 = cols[g][0][j], w4 = cols[g][1][j];
+          o[4 * g + 2 * j] = mfma16<DT>(value_int4<DT>(int4_even(w0), int4_even(w4)), pf[g], o[4 * g + 2 * j]);
+          o[4 * g + 2 * j + 1] = mfma16<DT>(value_int4<DT>(int4_odd(w0), int4_odd(w4)), pf[g], o[4 * g + 2 * j + 1]);
+        }
     }
   }
 };
@@ -539,7 +540,7 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int64_t token, in
 // One workgroup: 16 query rows that share a cache head, one chunk of keys, four
 // waves that take its 32-key tiles in turn and meet in LDS at the end.
 template <int DT, int FMT, int D>
-__global__ __launch_bounds__(256, 2) void k_attn16(AttnParams p) {
+__global__ __launch_bounds__(256, 3) void k_attn16(AttnParams p) {
   constexpr int NJ = D / 32, NX = D / 16, PER = D / 16, LD = D + 4;
   __shared__ float so[4][16][LD];
   __shared__ float sb[4][16], ss[4][16];
@@ -567,6 +568,10 @@ __global__ __launch_bounds__(256, 2) void k_attn16(AttnParams p) {
     const uint16_t* q = p.q + (r.first + qi) * p.qt + int64_t(qh) * p.qh;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) w.q[j] = query_order<FMT>(*reinterpret_cast<const u32x4*>(q + frag_dim<FMT, D>(j, b)));
+    if (p.c < 0.0f) {       // the sign of the scale goes to the query: the largest product is the largest logit
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) w.q[j] ^= 0x80008000u;
+    }
   }
   const int from = range.from + split * p.chunk, to = min(range.to, from + p.chunk);
   const int32_t* table = p.table + int64_t(req) * p.table_stride;
@@ -585,7 +590,7 @@ __global__ __launch_bounds__(256, 2) void k_attn16(AttnParams p) {
   };
   auto multiply = [&](const Tile32<FMT, D>& t, int i) {
     const int token = first + 128 * i;
-    w.step(p, t, token, r.len, token >= range.all_low && token + 32 <= range.all_high && t.ok0 && t.ok1, lane);
+    w.step(t, token, r.len, token >= range.all_low && token + 32 <= range.all_high && t.ok0 && t.ok1, fabsf(p.c), lane);
   };
   if (tiles > 0) {
     Tile32<FMT, D> t0, t1;
@@ -835,11 +840,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     for (int j = 0; j < 4; ++j) sk[buf][(4 * kb + j) * KT + krow] = key_frag<DT, FMT>(st.k[j], ks);
     const int slot = 64 * (vn / 16) + vn % 16;                 // column 4 vn + j: slot + 16 j
     u32x4* v = &sv[buf][vkeys / 8 * D + slot];
-    u32x4 f0, f1;
     if constexpr (MX) {
+      u32x4 f0, f1;
       float sc[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sc[i] = value_scale<DT, FMT, D>(st.vsc, i, vn >> 3);
+      for (int i = 0; i < 8; ++i) sc[i] = value_scale<DT, D>(st.vsc, i, vn >> 3);
       value_pair_mx<DT, 0>(st.v, sc, &f0, &f1);
       v[0] = f0;
       v[16] = f1;
@@ -847,20 +852,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       v[32] = f0;
       v[48] = f1;
     } else {
-      // two keys' codes in a dword, so that the bits are moved once for both
-      unsigned ev[4], od[4], sc[4] = {0, 0, 0, 0};
+      unsigned cols[2][2], sc[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const unsigned w = st.v[2 * i] | (st.v[2 * i + 1] << 16);
-        ev[i] = int4_even(w);
-        od[i] = int4_odd(w);
-      }
+      for (int k = 0; k < 2; ++k) deal(st.v + 4 * k, byte_pick(0), cols[k]);
       float gain = 512.0f;
       if constexpr (PS) {
-        f16x2 most = two_halves(st.vsc[0][0]);
-#pragma unroll
-        for (int i = 1; i < D / 16; ++i) most = __builtin_elementwise_max(most, two_halves(st.vsc[i / 4][i % 4]));
-        float x = fmaxf(float(most[0]), float(most[1]));
+        float x = most_scale<D>(st.vsc);
         x = D == 128 ? half_max(x) : quad_max(x);
         if (lane == 0) svx[buf][wave] = scale_exponent(x);
         if (vn == 0) {
@@ -893,12 +890,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
         if constexpr (NG == 2) *reinterpret_cast<f32x2*>(&sks[buf][2 * (16 * WH * wave + lane)]) = f32x2{float(ks[0]) * c, float(ks[1]) * c};
         else sks[buf][16 * WH * wave + lane] = float(ks[0]) * c;
       }
-      value_quad_int4<!PS>(ev, sc, gain, &f0, &f1);
-      v[0] = f0;
-      v[32] = f1;
-      value_quad_int4<!PS>(od, sc, gain, &f0, &f1);
-      v[16] = f0;
-      v[48] = f1;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const unsigned w0 = cols[0][j], w4 = cols[1][j];
+        if constexpr (PS) {
+          v[32 * j] = value_int4<VT>(int4_even(w0), int4_even(w4));
+          v[32 * j + 16] = value_int4<VT>(int4_odd(w0), int4_odd(w4));
+        } else {
+          v[32 * j] = value_int4_scaled(int4_even(w0), int4_even(w4), sc, gain);
+          v[32 * j + 16] = value_int4_scaled(int4_odd(w0), int4_odd(w4), sc, gain);
+        }
+      }
     }
   };
 
@@ -964,7 +966,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     }
     float top = s[0][0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);     // `maximum` was no faster here (INT4 840 us, 834)
     top = half_max(top);
     if constexpr (MX) top = __builtin_fmaf(top, c, -base);
     else top += most;
