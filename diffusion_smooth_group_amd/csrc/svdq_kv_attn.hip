@@ -156,11 +156,13 @@ struct Request {
 // column in a lane: a lane loads 8 keys' codes of its own columns and pairs
 // neighbouring keys after the conversion.  The cache's bytes bound it (136 a key
 // and head of 128): the codes go from memory to registers and are turned there,
-// with two tiles in flight a wave and three waves a SIMD.  48 requests of up to
+// with two tiles in flight a wave and three waves a SIMD (four with D = 64).  48 requests of up to
 // 16384 tokens, 8 heads of 128, 4 query heads each: MXFP4 114 us, 4.8 TB/s; INT4
 // 129 us (f16 136), where the vector unit is the bound: bits to fp8, conversion,
 // and scales on both sums.  With the converted values paired instead of their
-// codes, and 190 registers, two waves, it took 180.  Two row tiles
+// codes, and 190 registers, two waves, it took 180.  20 heads of 64 with a query
+// head each: MXFP4 198 us, INT4 208, 2.9 and 2.8 TB/s, the vector unit again (as
+// many keys a byte twice over, and one row of the 16 in use).  Two row tiles
 // a wave on the same operands were slower for MXFP4 (40 rows: 309 us against 199
 // with three tiles of 16: two waves a SIMD instead of three).
 template <int FMT, int D>
@@ -217,9 +219,12 @@ struct Tile32 {
         }
       }
     }
-    const unsigned vo = unsigned(8 * b * (D / 2) + (D == 128 ? 4 * m : 4 * (m >> 1)));
+    const unsigned vo = unsigned(8 * b * (D / 2) + D / 32 * m);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const unsigned*>(vc1 + (vo + unsigned(i * (D / 2))));
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (D == 128) v[i] = *reinterpret_cast<const unsigned*>(vc1 + (vo + unsigned(i * (D / 2))));
+      else v[i] = *reinterpret_cast<const uint16_t*>(vc1 + (vo + unsigned(i * (D / 2))));
+    }
 #pragma unroll
     for (int i = 0; i < NS; ++i) vsc[i] = *reinterpret_cast<const u32x4*>(vs1 + (8u * b * SB + 16u * i));
     if constexpr (FMT == SVDQ_FMT_INT4_G64) {
@@ -443,21 +448,18 @@ struct Rows16 {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sc[i] = i < last ? sc[i] : 0.0f;
       }
-      unsigned v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = D == 128 ? t.v[i] : t.v[i] >> (16 * (m & 1));
       u32x4 f0, f1;
-      value_pair_mx<DT, 0>(v, sc, &f0, &f1);
+      value_pair_mx<DT, 0>(t.v, sc, &f0, &f1);
       o[0] = mfma16<DT>(f0, pf, o[0]);
       o[1] = mfma16<DT>(f1, pf, o[1]);
-      value_pair_mx<DT, 1>(v, sc, &f0, &f1);
+      value_pair_mx<DT, 1>(t.v, sc, &f0, &f1);
       o[2] = mfma16<DT>(f0, pf, o[2]);
       o[3] = mfma16<DT>(f1, pf, o[3]);
       if constexpr (D == 128) {
-        value_pair_mx<DT, 2>(v, sc, &f0, &f1);
+        value_pair_mx<DT, 2>(t.v, sc, &f0, &f1);
         o[4] = mfma16<DT>(f0, pf, o[4]);
         o[5] = mfma16<DT>(f1, pf, o[5]);
-        value_pair_mx<DT, 3>(v, sc, &f0, &f1);
+        value_pair_mx<DT, 3>(t.v, sc, &f0, &f1);
         o[6] = mfma16<DT>(f0, pf, o[6]);
         o[7] = mfma16<DT>(f1, pf, o[7]);
       }
@@ -492,7 +494,7 @@ struct Rows16 {
             cols[NG - 1][k][j] = unsigned(__builtin_amdgcn_update_dpp(int(own[j]), int(other[j]), 0x128, 0xF, 0x3, false));
           }
         } else {
-          deal(t.v + 4 * k, m % 2 == 0 ? byte_pick(0) : byte_pick(2), cols[0][k]);
+          deal(t.v + 4 * k, byte_pick(0), cols[0][k]);
         }
       }
 #pragma unroll
