@@ -154,15 +154,16 @@ struct Request {
 // O^T = V^T P^T as it stands; the keys of the two K tiles are dealt out for
 // that (tile a, row r: key 8 (r / 4) + 4 a + r % 4).  V^T needs 8 keys of one
 // column in a lane: a lane loads 8 keys' codes of its own columns and pairs
-// neighbouring keys after the conversion.  The cache's bytes bound it (136 a key
-// and head of 128): the codes go from memory to registers and are turned there,
-// with two tiles in flight a wave and three waves a SIMD (four with D = 64).  48 requests of up to
+// neighbouring keys, MXFP4 after the conversion (each key has its own scale),
+// INT4 before it.  The cache's bytes bound it (136 a key and head of 128): the
+// codes go from memory to registers and are turned there, with two tiles in
+// flight a wave and three waves a SIMD (four with D = 64).  48 requests of up to
 // 16384 tokens, 8 heads of 128, 4 query heads each: MXFP4 114 us, 4.8 TB/s; INT4
 // 129 us (f16 136), where the vector unit is the bound: bits to fp8, conversion,
 // and scales on both sums.  With the converted values paired instead of their
 // codes, and 190 registers, two waves, it took 180.  20 heads of 64 with a query
-// head each: MXFP4 198 us, INT4 208, 2.9 and 2.8 TB/s, the vector unit again (as
-// many keys a byte twice over, and one row of the 16 in use).  Two row tiles
+// head each: MXFP4 198 us, INT4 208, 3.4 and 3.3 TB/s, the vector unit again (as
+// many instructions for half the bytes a key).  Two row tiles
 // a wave on the same operands were slower for MXFP4 (40 rows: 309 us against 199
 // with three tiles of 16: two waves a SIMD instead of three).
 template <int FMT, int D>
@@ -1278,17 +1279,30 @@ svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, Cut* out) {
   const bool causal = (d->flags & SVDQ_ATTN_CAUSAL) != 0u;   // else a row sees up to the end, whatever its window
   if (causal && d->window > 0 && int64_t(d->window) + max_q < span) span = int64_t(d->window) + max_q;
   if (d->window > 0) span += 31;        // the first tile is rounded down to 32
-  // Chunks of at least 128 keys (a tile for each wave of k_attn16) or 512, as
-  // many as eight workgroups (two, one of the wide ones) a compute unit, and none
-  // where that many are there: 48 requests of up to 16384 tokens, 8 heads: 140 us
-  // at four, 129 at eight, 138 at twelve.
-  const int64_t least = t.rows == 16 ? 128 : 512;
-  const int64_t fit = int64_t(device_cus()) * (t.rows == 16 ? 8 : t.rows == 128 ? 2 : 1) / (t.items > 0 ? t.items : 1), want = fit < 1 ? 1 : fit;
-  const int64_t all = ceil_div(int64_t(d->max_kv) + 31, least), here = ceil_div(span, least);
-  const int64_t n = want < here ? want : here > 0 ? here : 1;
+  // Chunks.  Wide tiles: of at least 512 keys, two workgroups a compute unit (one
+  // of 256 rows), none where that many are there.  Tiles of 16: none up to 1024
+  // keys, where the second launch costs more than it saves (a request, 8 heads,
+  // 512 keys: 6.7 us on the GPU and 12 a call, against 7.6 and 15 in four; 1024
+  // keys: 9.5 and 12, against 8.1 and 16); above that two workgroups a compute
+  // unit over chunks of at least 256, four where those still have 1024 and eight
+  // where they have 2048, so that what a chunk costs beside its keys stays small
+  // and long ones end together (16 requests of up to 2048, 8 heads: 15 us with 4
+  // chunks, 17 with 8, 20 with 16; of 8192: 33 with 8, 36 with 16; 48 of up to
+  // 16384: 129 at eight workgroups a unit, 140 at four, 138 at twelve).
+  const int64_t per = t.items > 0 ? t.items : 1;
+  auto fit = [&](int64_t groups) { const int64_t f = int64_t(device_cus()) * groups / per; return f < 1 ? int64_t(1) : f; };
+  auto chunks = [&](int64_t keys) {
+    auto least = [&](int64_t most, int64_t n) { return most < n ? most : n < 1 ? int64_t(1) : n; };
+    if (t.rows != 16) return least(fit(t.rows == 128 ? 2 : 1), ceil_div(keys, 512));
+    if (keys <= 1024) return int64_t(1);
+    if (keys >= 2048 * fit(8)) return fit(8);
+    if (keys >= 1024 * fit(4)) return fit(4);
+    return least(fit(2), ceil_div(keys, 256));
+  };
+  const int64_t all = int64_t(d->max_kv) + 31, n = chunks(span);
   const int64_t chunk = ceil_div(ceil_div(span > 0 ? span : 1, n), 128) * 128;
   t.splits = int(ceil_div(span > 0 ? span : 1, chunk));
-  t.most = int(want < all ? want : all);
+  t.most = int(chunks(all));            // more keys are never fewer chunks
   t.chunk = int(chunk);
   t.row_tiles = int(tiles);
   if (t.items * t.most >= MAX_THREADS / 512) return SVDQ_ERR_UNSUPPORTED;   // a join has fewer: only calls of few rows are cut

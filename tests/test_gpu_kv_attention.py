@@ -139,6 +139,18 @@ def test_few_rows(fmt, dtype, dim, page, hk, group, fresh, lens):
 
 
 @pytest.mark.parametrize("fmt,dtype,dim", FORMS)
+@pytest.mark.parametrize("fresh,lens,causal,window", [
+    ([1, 1], [5200, 1025], True, 0),            # more than 16 chunks
+    ([1], [70000], True, 0),                    # more than 256
+    ([2, 1], [1024, 900], True, 0),             # one, of eight tiles a wave
+    ([3, 1], [9000, 6000], True, 5000),
+    ([3, 1], [9000, 100], False, 4200),
+])
+def test_few_rows_in_chunks(fmt, dtype, dim, fresh, lens, causal, window):
+    _run(fmt, dtype, dim, 64, 1, 2, fresh, lens, causal, window)
+
+
+@pytest.mark.parametrize("fmt,dtype,dim", FORMS)
 @pytest.mark.parametrize("page,hk,group,fresh,lens,causal,window", [
     (16, 1, 2, [40], [40], True, 0),
     (64, 2, 1, [129], [129], False, 0),
