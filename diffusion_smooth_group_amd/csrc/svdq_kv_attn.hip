@@ -675,9 +675,9 @@ __global__ __launch_bounds__(256, 3) void k_attn16(AttnParams p) {
 // tokens, 24 heads of 128, no mask, MXFP4: 262 us, 995 TFLOP/s (a large bf16
 // matrix product: 1250), of which 16% is the second round of 432 workgroups on
 // 256 compute units.  5 x 2047 rows behind up to 8191 tokens, 32 heads over 8:
-// INT4 856 us, 800 TFLOP/s (f16: 973); MXFP4 701, 977.  Tried and slower: the next products
-// under this softmax (281 us), the two waves of a SIMD one phase apart (306), 64
-// rows a wave (434), no running maximum (282).
+// INT4 845 us, 809 TFLOP/s (f16: 960); MXFP4 705, 970.  Tried and slower: the
+// next products under this softmax (281 us), the two waves of a SIMD one phase
+// apart (306), 64 rows a wave (434), no running maximum (282).
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
   if constexpr (DT == SVDQ_BF16)
