@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "svdq_kv.h"
+#include "svdq_kv_cut.h"
 
 namespace svdq_kv {
 
@@ -32,20 +33,9 @@ __device__ __forceinline__ unsigned pack2(float a, float b) {
   else return __builtin_bit_cast(unsigned, f16x2{(_Float16)a, (_Float16)b});
 }
 
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 inline bool dtype_ok(int dt) { return dt == SVDQ_F16 || dt == SVDQ_BF16; }
 inline svdq_status launch_ok() { return hipGetLastError() == hipSuccess ? SVDQ_OK : SVDQ_ERR_HIP; }
-
-// a * b * c where all are not negative and the product is below `limit`; -1 otherwise
-inline int64_t product_below(int64_t a, int64_t b, int64_t c, int64_t limit) {
-  const __int128 p = __int128(a) * b;
-  if (p >= limit && c > 0) return -1;
-  const __int128 q = c > 0 ? p * c : 0;
-  return q >= limit ? -1 : int64_t(q);
-}
-// threads of a launch's x dimension
-constexpr int64_t MAX_THREADS = int64_t(1) << 32;
 
 // log2 of a page size the cache takes, -1 otherwise
 inline int page_shift(int page_size) {
