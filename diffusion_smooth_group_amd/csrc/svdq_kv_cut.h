@@ -32,18 +32,19 @@ constexpr int64_t MAX_THREADS = int64_t(1) << 32;
 
 // A request's rows and the keys they see.
 struct Request {
-  int rows, all_rows, len, true_len;
-  int64_t first;
+  int rows, len;
+  int64_t first, before;    // position of row 0 (below 0: rows that stand before the first token)
   template <class P>
   SVDQ_HD Request(const P& p, int r) {
     const int64_t s = p.q_start[r], e = p.q_start[r + 1];
-    all_rows = int(e - s);
     first = s < 0 ? 0 : s;
     int64_t n = e < p.tokens ? e : p.tokens;
     n -= first;
     rows = n < 0 || s < 0 ? 0 : int(n < p.max_q ? n : p.max_q);
-    true_len = p.kv_len[r];
-    const int64_t room = p.table_stride << p.page_shift;
+    const int64_t true_len = p.kv_len[r];
+    before = true_len - (e - s);
+    const int64_t columns = p.table_stride < (int64_t(1) << 27) ? p.table_stride : int64_t(1) << 27;   // of 16 tokens at least
+    const int64_t room = columns << p.page_shift;
     int64_t l = true_len < p.max_kv ? true_len : p.max_kv;
     l = l < room ? l : room;
     len = p.n_pages == 0 || l < 0 ? 0 : int(l);
@@ -51,13 +52,15 @@ struct Request {
   // keys [low, high) that row i sees
   template <class P>
   SVDQ_HD int high(const P& p, int i) const {
-    const int pos = true_len - all_rows + i;
-    return p.causal ? larger(0, smaller(pos + 1, len)) : len;
+    if (!p.causal) return len;
+    const int64_t end = before + i + 1;
+    return end < 0 ? 0 : end < len ? int(end) : len;
   }
   template <class P>
   SVDQ_HD int low(const P& p, int i) const {
-    const int pos = true_len - all_rows + i;
-    return p.window > 0 ? larger(0, pos - p.window + 1) : 0;
+    if (p.window <= 0) return 0;
+    const int64_t begin = before + i + 1 - p.window;
+    return begin < 0 ? 0 : begin < len ? int(begin) : len;
   }
 };
 
@@ -99,7 +102,7 @@ inline svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, int c
   const int64_t group = d->q_heads / c->heads;
   const int64_t max_q = d->max_q < d->tokens ? d->max_q : d->tokens;
   t.row_slots = max_q * group;
-  const int64_t slots = product_below(d->requests, c->heads, t.row_slots, int64_t(1) << 31);
+  const int64_t slots = product_below(d->requests, c->heads, t.row_slots, (int64_t(1) << 31) - 512);   // a tile's last row, too, is an int
   if (slots < 0) return SVDQ_ERR_UNSUPPORTED;
   // Up to 80 rows a request and head, or 1024 in all, tiles of 16 that read the
   // cache once each (8 requests of 4000 tokens, 8 heads: 40 rows 25 us against 29
@@ -113,7 +116,14 @@ inline svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, int c
   if (t.rows == 128 && d->requests * c->heads * ceil_div(t.row_slots, 256) * 2 >= int64_t(cus)) t.rows = 256;
   const int64_t tiles = ceil_div(t.row_slots, t.rows);
   t.items = d->requests * c->heads * tiles;
-  int64_t span = d->max_kv;
+  // No request has more keys than its row of the block table holds, so that a
+  // max_kv of "no bound" is cut as the table's width is.
+  const __int128 room = __int128(d->table_stride) * c->page_size;
+  const int64_t keys = d->max_kv < room ? d->max_kv : int64_t(room);
+  // Key indexes are 32-bit in the kernels: a chunk is no longer than this, and
+  // look-ups run up to 8192 keys ahead.
+  if (keys > SVDQ_KV_MAX_TOKENS) return SVDQ_ERR_UNSUPPORTED;
+  int64_t span = keys;
   const bool causal = (d->flags & SVDQ_ATTN_CAUSAL) != 0u;   // else a row sees up to the end, whatever its window
   if (causal && d->window > 0 && int64_t(d->window) + max_q < span) span = int64_t(d->window) + max_q;
   if (d->window > 0) span += 31;        // the first tile is rounded down to 32

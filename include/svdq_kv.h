@@ -146,6 +146,8 @@ svdq_status svdq_kv_plan(const int32_t* past, const int32_t* fresh, int64_t requ
                          int32_t* block_table, int64_t table_stride, int32_t* q_start, int32_t* kv_len, int32_t* slots,
                          int32_t* positions, int32_t* free_left, int32_t* missing, hipStream_t stream);
 
+#define SVDQ_KV_MAX_TOKENS ((1 << 30) - 16384)
+
 enum {
   SVDQ_ATTN_CAUSAL = 1u     /* a query sees keys up to its own position */
 };
@@ -156,7 +158,9 @@ typedef struct {
   int32_t q_heads;          /* multiple of cache->heads: query head h reads cache head h / (q_heads / heads) */
   int32_t dtype;            /* svdq_dtype of q and out */
   int32_t max_q, max_kv;    /* bounds on a request's query rows and cached tokens; rows or
-                               tokens past them are not computed or seen */
+                               tokens past them are not computed or seen.  max_kv may be
+                               INT32_MAX: the table's width bounds the tokens as well, and
+                               the smaller of both is at most SVDQ_KV_MAX_TOKENS */
   int32_t window;           /* > 0: a query at position p sees keys above p - window; 0: all */
   unsigned flags;           /* SVDQ_ATTN_* */
   float scale;              /* of the logits, commonly 1 / sqrt(D) */
