@@ -12,9 +12,15 @@ What runs between a QKV projection and the attention output:
 Tensors of heads are [tokens, heads, D] with unit stride in D (views of a
 fused QKV row are taken as they are).  A wrong argument raises ValueError
 here or SvdqError with the library's status.
+
+A call runs on the current stream.  With stream= (a torch stream or a raw
+handle) it is as if made under ``torch.cuda.stream(stream)``: outputs and
+workspaces that it allocates belong to that stream, too, so its memory goes to
+nobody else while its kernels run.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 from typing import NamedTuple, Optional
@@ -126,9 +132,20 @@ def _code(dtype):
     return c
 
 
-def _stream(stream, t):
-    if stream is not None:
-        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, t):
+    """The context of a call: `stream` is the current stream in it, for the
+    allocator as for the launch (t: a tensor of the call)."""
+    if stream is None:
+        return _HERE
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device) if stream else torch.cuda.default_stream(t.device)
+    return torch.cuda.stream(stream)
+
+
+def _stream(t):
     return _raw_stream(t.get_device())
 
 
@@ -159,20 +176,21 @@ def qk_norm_rope(q, k, cos=None, sin=None, wq=None, wk=None, eps: float = 1e-6, 
     rotation), at positions [tokens] (int32, None: 0, 1, ...).  halves: pairs
     (i, i + D/2), else (2i, 2i + 1).  Returns (q_out, k_out); q_out=q, k_out=k
     work in place."""
-    tokens, _, dim = q.shape
-    dtype = q.dtype
-    d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions)
-    hq, hk = _heads(q, "q", tokens, dim, dtype), _heads(k, "k", tokens, dim, dtype)
-    if q_out is None:
-        q_out, hqo = _new(q)
-    else:
-        hqo = _heads(q_out, "q_out", tokens, dim, dtype)
-    if k_out is None:
-        k_out, hko = _new(k)
-    else:
-        hko = _heads(k_out, "k_out", tokens, dim, dtype)
-    _call("svdq_qk_norm_rope", d, hq, hk, hqo, hko, _stream(stream, q))
-    return q_out, k_out
+    with _on(stream, q):
+        tokens, _, dim = q.shape
+        dtype = q.dtype
+        d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+        hq, hk = _heads(q, "q", tokens, dim, dtype), _heads(k, "k", tokens, dim, dtype)
+        if q_out is None:
+            q_out, hqo = _new(q)
+        else:
+            hqo = _heads(q_out, "q_out", tokens, dim, dtype)
+        if k_out is None:
+            k_out, hko = _new(k)
+        else:
+            hko = _heads(k_out, "k_out", tokens, dim, dtype)
+        _call("svdq_qk_norm_rope", d, hq, hk, hqo, hko, _stream(q))
+        return q_out, k_out
 
 
 def qk_norm_rope_backward(gq, gk, q, k, cos=None, sin=None, wq=None, wk=None, eps: float = 1e-6, norm: bool = True,
@@ -180,21 +198,22 @@ def qk_norm_rope_backward(gq, gk, q, k, cos=None, sin=None, wq=None, wk=None, ep
     """Gradient of ``qk_norm_rope`` from gq, gk (with respect to its outputs)
     and its inputs.  Returns (dq, dk, dwq, dwk), the weight gradients fp32 [D]
     (zero without ``norm``)."""
-    tokens, _, dim = q.shape
-    dtype = q.dtype
-    d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions)
-    h = [_heads(t, n, tokens, dim, dtype) for t, n in ((q, "q"), (k, "k"), (gq, "gq"), (gk, "gk"))]
-    for t, like, n in ((dq, q, "dq"), (dk, k, "dk")):
-        h.append(_new(like) if t is None else (t, _heads(t, n, tokens, dim, dtype)))
-    (dq, hdq), (dk, hdk) = h[4:]
-    dwq, dwk = dw = q.new_empty((2, dim), dtype=torch.float32).unbind()
-    if ws is None:
-        need = _SZ(0)
-        _call("svdq_qk_backward_workspace", d, q.shape[1], k.shape[1], need)
-        ws = q.new_empty(need.value, dtype=torch.uint8)
-    _call("svdq_qk_norm_rope_backward", d, *h[:4], hdq, hdk, dwq.data_ptr(), dwk.data_ptr(), ws.data_ptr(), ws.numel(),
-          _stream(stream, q))
-    return dq, dk, *dw
+    with _on(stream, q):
+        tokens, _, dim = q.shape
+        dtype = q.dtype
+        d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+        h = [_heads(t, n, tokens, dim, dtype) for t, n in ((q, "q"), (k, "k"), (gq, "gq"), (gk, "gk"))]
+        for t, like, n in ((dq, q, "dq"), (dk, k, "dk")):
+            h.append(_new(like) if t is None else (t, _heads(t, n, tokens, dim, dtype)))
+        (dq, hdq), (dk, hdk) = h[4:]
+        dwq, dwk = dw = q.new_empty((2, dim), dtype=torch.float32).unbind()
+        if ws is None:
+            need = _SZ(0)
+            _call("svdq_qk_backward_workspace", d, q.shape[1], k.shape[1], need)
+            ws = q.new_empty(need.value, dtype=torch.uint8)
+        _call("svdq_qk_norm_rope_backward", d, *h[:4], hdq, hdk, dwq.data_ptr(), dwk.data_ptr(), ws.data_ptr(), ws.numel(),
+              _stream(q))
+        return dq, dk, *dw
 
 
 class _QKNormRope(torch.autograd.Function):
@@ -261,31 +280,33 @@ class KVCache:
         """Quantizes k and v [tokens, heads, D] into slots [tokens] (int32, a
         negative one is skipped).  With norm and / or cos, sin: k is normed and
         rotated on the way (and q into q_out, which is returned)."""
-        tokens, _, dim = k.shape
-        d = _desc(tokens, dim, k.dtype, cos, sin, wq, wk, eps, norm, halves, positions)
-        hq = ho = None
-        if q is not None:
-            hq = _heads(q, "q", tokens, dim, k.dtype)
-            if q_out is None:
-                q_out, ho = _new(q)
-            else:
-                ho = _heads(q_out, "q_out", tokens, dim, k.dtype)
-        _call("svdq_kv_append", d, hq, _heads(k, "k", tokens, dim, k.dtype), _heads(v, "v", tokens, dim, k.dtype), ho, self.c,
-              _int32(slots, "slots", tokens), _stream(stream, k))
-        return q_out
+        with _on(stream, k):
+            tokens, _, dim = k.shape
+            d = _desc(tokens, dim, k.dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+            hq = ho = None
+            if q is not None:
+                hq = _heads(q, "q", tokens, dim, k.dtype)
+                if q_out is None:
+                    q_out, ho = _new(q)
+                else:
+                    ho = _heads(q_out, "q_out", tokens, dim, k.dtype)
+            _call("svdq_kv_append", d, hq, _heads(k, "k", tokens, dim, k.dtype), _heads(v, "v", tokens, dim, k.dtype), ho, self.c,
+                  _int32(slots, "slots", tokens), _stream(k))
+            return q_out
 
     def read(self, slots, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
         """(k, v) [len(slots), heads, D]: the cached values of the slots, zero
         for slots outside the cache."""
-        n = slots.numel()
-        code, at, hd = _code(dtype), _int32(slots, "slots", n), self.head_dim
-        if k_out is None:
-            k_out = self.k_codes.new_empty((n, self.heads, hd), dtype=dtype)
-        if v_out is None:
-            v_out = self.k_codes.new_empty((n, self.heads, hd), dtype=dtype)
-        _call("svdq_kv_read", self.c, at, n, code, _heads(k_out, "k_out", n, hd, dtype), _heads(v_out, "v_out", n, hd, dtype),
-              _stream(stream, slots))
-        return k_out, v_out
+        with _on(stream, slots):
+            n = slots.numel()
+            code, at, hd = _code(dtype), _int32(slots, "slots", n), self.head_dim
+            if k_out is None:
+                k_out = self.k_codes.new_empty((n, self.heads, hd), dtype=dtype)
+            if v_out is None:
+                v_out = self.k_codes.new_empty((n, self.heads, hd), dtype=dtype)
+            _call("svdq_kv_read", self.c, at, n, code, _heads(k_out, "k_out", n, hd, dtype), _heads(v_out, "v_out", n, hd, dtype),
+                  _stream(slots))
+            return k_out, v_out
 
 
 # ------------------------------------------------------------------- step tables
@@ -304,28 +325,30 @@ def plan(past, fresh, block_table, free_pages, free_count, page_size: int, token
     tokens, fresh [requests] new ones, pages from the end of free_pages
     (free_count [1] of them are free).  tokens: length of the slot map, at
     least the sum of fresh (the rest is -1)."""
-    b = past.numel()
-    out = past.new_empty(2 * b + 3 + 2 * tokens)
-    at = out.data_ptr()
-    cuts = (b + 1, b, tokens, tokens, 1, 1)
-    q_start, kv_len, slots, positions, left, missing = out.split(cuts)
-    p, ptr = [], at
-    for n in cuts:
-        p.append(ptr)
-        ptr += 4 * n
-    _call("svdq_kv_plan", _int32(past, "past", b), _int32(fresh, "fresh", b), b, page_size, tokens, _int32(free_pages, "free_pages", free_pages.numel()),
-          _int32(free_count, "free_count", 1), free_pages.numel(), _table(block_table, b), block_table.shape[1], *p,
-          _stream(stream, past))
-    return Plan(block_table, q_start, kv_len, slots, positions, left, missing)
+    with _on(stream, past):
+        b = past.numel()
+        out = past.new_empty(2 * b + 3 + 2 * tokens)
+        at = out.data_ptr()
+        cuts = (b + 1, b, tokens, tokens, 1, 1)
+        q_start, kv_len, slots, positions, left, missing = out.split(cuts)
+        p, ptr = [], at
+        for n in cuts:
+            p.append(ptr)
+            ptr += 4 * n
+        _call("svdq_kv_plan", _int32(past, "past", b), _int32(fresh, "fresh", b), b, page_size, tokens, _int32(free_pages, "free_pages", free_pages.numel()),
+              _int32(free_count, "free_count", 1), free_pages.numel(), _table(block_table, b), block_table.shape[1], *p,
+              _stream(past))
+        return Plan(block_table, q_start, kv_len, slots, positions, left, missing)
 
 
 def release(done, block_table, kv_len, free_pages, free_count, page_size: int, stream=None):
     """Gives the pages of the requests with done != 0 back to free_pages (in
     place: free_pages, free_count, block_table and kv_len)."""
-    b = done.numel()
-    _call("svdq_kv_release", _int32(done, "done", b), b, page_size, _table(block_table, b), block_table.shape[1],
-          _int32(kv_len, "kv_len", b), _int32(free_pages, "free_pages", free_pages.numel()), _int32(free_count, "free_count", 1), free_pages.numel(),
-          _stream(stream, done))
+    with _on(stream, done):
+        b = done.numel()
+        _call("svdq_kv_release", _int32(done, "done", b), b, page_size, _table(block_table, b), block_table.shape[1],
+              _int32(kv_len, "kv_len", b), _int32(free_pages, "free_pages", free_pages.numel()), _int32(free_count, "free_count", 1), free_pages.numel(),
+              _stream(done))
 
 
 # --------------------------------------------------------------------- attention
@@ -353,23 +376,24 @@ def attention(q, cache: KVCache, block_table, q_start, kv_len, max_q: int, max_k
     the rows and cached tokens of a request.  scale: 1 / sqrt(D) by default.
     A row that sees nothing gives zeros; a row of no request is not written.
     Returns out, or (out, lse)."""
-    tokens, hq, dim = q.shape
-    if dim != cache.head_dim:
-        raise ValueError(f"q: heads of {dim} over a cache of heads of {cache.head_dim}")
-    b = kv_len.numel()
-    hin = _heads(q, "q", tokens, dim, q.dtype)
-    if out is None:
-        out, hout = _new(q)
-    else:
-        hout = _heads(out, "out", tokens, dim, q.dtype)
-    lse = q.new_empty((tokens, hq), dtype=torch.float32) if return_lse else None
-    d = svdq_attn_desc(b, tokens, hq, _code(q.dtype), max_q, max_kv, window, ATTN_CAUSAL if causal else 0,
-                       1.0 / math.sqrt(dim) if scale is None else scale, _int32(q_start, "q_start", b + 1),
-                       _int32(kv_len, "kv_len", b), _table(block_table, b), block_table.shape[1])
-    if ws is None:
-        need = _SZ(0)
-        _call("svdq_kv_attention_workspace", d, cache.c, need)
-        ws = q.new_empty(need.value, dtype=torch.uint8)
-    _call("svdq_kv_attention", d, hin, cache.c, hout,
-          None if lse is None else lse.data_ptr(), ws.data_ptr() if ws.numel() else None, ws.numel(), _stream(stream, q))
-    return (out, lse) if return_lse else out
+    with _on(stream, q):
+        tokens, hq, dim = q.shape
+        if dim != cache.head_dim:
+            raise ValueError(f"q: heads of {dim} over a cache of heads of {cache.head_dim}")
+        b = kv_len.numel()
+        hin = _heads(q, "q", tokens, dim, q.dtype)
+        if out is None:
+            out, hout = _new(q)
+        else:
+            hout = _heads(out, "out", tokens, dim, q.dtype)
+        lse = q.new_empty((tokens, hq), dtype=torch.float32) if return_lse else None
+        d = svdq_attn_desc(b, tokens, hq, _code(q.dtype), max_q, max_kv, window, ATTN_CAUSAL if causal else 0,
+                           1.0 / math.sqrt(dim) if scale is None else scale, _int32(q_start, "q_start", b + 1),
+                           _int32(kv_len, "kv_len", b), _table(block_table, b), block_table.shape[1])
+        if ws is None:
+            need = _SZ(0)
+            _call("svdq_kv_attention_workspace", d, cache.c, need)
+            ws = q.new_empty(need.value, dtype=torch.uint8)
+        _call("svdq_kv_attention", d, hin, cache.c, hout,
+              None if lse is None else lse.data_ptr(), ws.data_ptr() if ws.numel() else None, ws.numel(), _stream(q))
+        return (out, lse) if return_lse else out

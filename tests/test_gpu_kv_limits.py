@@ -36,3 +36,67 @@ def test_rows_before_the_first_token_under_the_widest_window():
     cache, table, slots, q, start, length = _setup("mxfp4_g32", "bf16", 64, 16, 1, 1, [9, 120], [4, 50])
     want = kv.attention(q, cache, table, start, length, 120, 50, causal=False)
     assert torch.equal(kv.attention(q, cache, table, start, length, 120, 50, causal=False, window=(1 << 31) - 1), want)
+
+
+def _scratch(monkeypatch, kv, name, at):
+    """Where the calls of `name` had argument `at` (a pointer), in a list."""
+    seen, call = [], kv._call
+
+    def record(fn, *args):
+        if fn == name:
+            seen.append(args[at])
+        return call(fn, *args)
+    monkeypatch.setattr(kv, "_call", record)
+    return seen
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_scratch_and_outputs_belong_to_the_stream_of_the_call(monkeypatch, raw):
+    """A call on another stream leaves no memory that the current stream's
+    next allocations could take while its kernels still run."""
+    torch, kv, _ = _mods()
+    cache, table, slots, q, start, length = _setup("mxfp4_g32", "bf16", 128, 64, 2, 4, [1, 1], [8000, 5000])
+    want, wl = kv.attention(q, cache, table, start, length, 1, 8000, return_lse=True)
+    x, g = torch.randn((700, 6, 128), device="cuda").bfloat16(), torch.randn((700, 6, 128), device="cuda").bfloat16()
+    w = torch.ones(128, device="cuda").bfloat16()
+    grads = kv.qk_norm_rope_backward(g, g, x, x, wq=w, wk=w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    stream = side.cuda_stream if raw else side
+    taken = _scratch(monkeypatch, kv, "svdq_kv_attention", 5), _scratch(monkeypatch, kv, "svdq_qk_norm_rope_backward", 9)
+    got, lse = kv.attention(q, cache, table, start, length, 1, 8000, return_lse=True, stream=stream)
+    back = kv.qk_norm_rope_backward(g, g, x, x, wq=w, wk=w, stream=stream)
+    sizes = (kv.attention_workspace_size(2, 2, 8, cache, 1, 8000), 2 * 132 * 128 * 4)
+    held = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(20)]
+    assert all(len(p) == 1 and p[0] for p in taken) and sizes[0] > 0
+    for t in held:
+        for p in taken:
+            assert not t.data_ptr() <= p[0] < t.data_ptr() + t.numel()
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(lse, wl) and all(torch.equal(a, b) for a, b in zip(back, grads))
+
+
+def test_every_call_takes_a_stream():
+    torch, kv, S = _mods()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    cache = kv.KVCache(4, 16, 2, 64, S.FMT_MXFP4_G32)
+    x = torch.randn((20, 2, 64), device="cuda").bfloat16()
+    past, fresh, table = torch.zeros(1, **i32), torch.full((1,), 20, **i32), torch.full((1, 3), -1, **i32)
+    free, count, done = torch.arange(4, **i32), torch.full((1,), 4, **i32), torch.ones(1, **i32)
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream, 0):
+        table.fill_(-1)
+        torch.cuda.synchronize()
+        p = kv.plan(past, fresh, table, free, count, 16, 20, stream=stream)
+        cache.append(x, x, p.slots, stream=stream)
+        k, v = cache.read(p.slots, stream=stream)
+        out = kv.attention(x, cache, p.block_table, p.q_start, p.kv_len, 20, 20, stream=stream)
+        y, _ = kv.qk_norm_rope(x, x, stream=stream)
+        torch.cuda.synchronize()
+        kv.release(done, p.block_table, p.kv_len, free, p.free_count, 16, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(k, v) and out.isfinite().all() and torch.equal(y, kv.qk_norm_rope(x, x)[0])
+        assert sorted(free.tolist()) == [0, 1, 2, 3] and p.free_count.tolist() == [4] and p.block_table.tolist() == [[-1] * 3]
+        free.copy_(torch.arange(4))
