@@ -16,7 +16,8 @@ here or SvdqError with the library's status.
 A call runs on the current stream.  With stream= (a torch stream or a raw
 handle) it is as if made under ``torch.cuda.stream(stream)``: outputs and
 workspaces that it allocates belong to that stream, too, so its memory goes to
-nobody else while its kernels run.
+nobody else while its kernels run.  All tensors of a call are on one device,
+which need not be the current one.
 """
 from __future__ import annotations
 
@@ -37,6 +38,7 @@ GROUP = {FMT_MXFP4_G32: 32, FMT_INT4_G64: 64}
 SCALE_DTYPE = {FMT_MXFP4_G32: torch.uint8, FMT_INT4_G64: torch.float16}
 
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, without building a Stream
+_current_device = torch._C._cuda_getDevice         # the current device's index
 _DTYPES = {torch.float16: S.F16, torch.bfloat16: S.BF16}
 _P, _I64, _I32, _U, _F, _SZ = C.c_void_p, C.c_int64, C.c_int32, C.c_uint, C.c_float, C.c_size_t
 
@@ -88,11 +90,11 @@ def _call(name, *args):
         raise SvdqError(name, rc)
 
 
-def _heads(t, name, tokens, dim, dtype):
+def _heads(t, name, tokens, dim, dtype, dev):
     n, h, d = t.shape
     s0, s1, s2 = t.stride()
-    if n != tokens or d != dim or s2 != 1 or t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{name}: a {dtype} GPU tensor [{tokens}, heads, {dim}] with unit stride in the last dimension is needed, "
+    if n != tokens or d != dim or s2 != 1 or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: a {dtype} tensor [{tokens}, heads, {dim}] on cuda:{dev} with unit stride in the last dimension is needed, "
                          f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return svdq_heads(t.data_ptr(), s0 if n > 1 else 0, s1 if h > 1 else 0, h)
 
@@ -105,24 +107,32 @@ def _new(like):
     return t, svdq_heads(t.data_ptr(), s0 if n > 1 else 0, s1 if h > 1 else 0, h)
 
 
-def _int32(t, name, n):
-    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: a contiguous int32 GPU tensor of {n} entries is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _int32(t, name, n, dev):
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: a contiguous int32 tensor of {n} entries on cuda:{dev} is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _table(t, b):
+def _table(t, b, dev):
     if t.dim() != 2 or t.shape[0] != b:
         raise ValueError(f"block_table: [{b}, pages] is needed, got {tuple(t.shape)}")
-    return _int32(t, "block_table", t.numel())
+    return _int32(t, "block_table", t.numel(), dev)
 
 
-def _weight(w, name, dim, dtype):
+def _weight(w, name, dim, dtype, dev):
     if w is None:
         return None
-    if w.dtype is not dtype or w.numel() != dim or not w.is_contiguous() or not w.is_cuda:
-        raise ValueError(f"{name}: a contiguous {dtype} GPU tensor of {dim} is needed")
+    if w.dtype is not dtype or w.numel() != dim or not w.is_contiguous() or w.get_device() != dev:
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of {dim} on cuda:{dev} is needed")
     return w.data_ptr()
+
+
+def _scratch(ws, dev):
+    """Address and bytes of a workspace."""
+    if not ws.is_contiguous() or ws.get_device() != dev:
+        raise ValueError(f"ws: a contiguous tensor on cuda:{dev} is needed, got strides {ws.stride()} on {ws.device}")
+    n = ws.numel() * ws.element_size()
+    return ws.data_ptr() if n else None, n
 
 
 def _code(dtype):
@@ -137,9 +147,13 @@ _HERE = contextlib.nullcontext()
 
 def _on(stream, t):
     """The context of a call: `stream` is the current stream in it, for the
-    allocator as for the launch (t: a tensor of the call)."""
+    allocator as for the launch, and the device of t, a tensor of the call, the
+    current device, to which a launch goes."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"GPU tensors are needed, got one on {t.device}")
     if stream is None:
-        return _HERE
+        return _HERE if index == _current_device() else torch.cuda.device(index)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=t.device) if stream else torch.cuda.default_stream(t.device)
     return torch.cuda.stream(stream)
@@ -149,20 +163,20 @@ def _stream(t):
     return _raw_stream(t.get_device())
 
 
-def _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions):
+def _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions, dev):
     flags = pq = pk = pc = ps = pp = n = 0
     if norm:
-        flags, pq, pk = QK_NORM, _weight(wq, "wq", dim, dtype), _weight(wk, "wk", dim, dtype)
+        flags, pq, pk = QK_NORM, _weight(wq, "wq", dim, dtype, dev), _weight(wk, "wk", dim, dtype, dev)
     if cos is not None:
         flags |= QK_ROPE | QK_ROPE_HALVES if halves else QK_ROPE
         n = cos.shape[0]
         f32, shape = torch.float32, (n, dim // 2)
         if sin is None or cos.dtype is not f32 or sin.dtype is not f32 or cos.shape != shape or sin.shape != shape \
-                or not (cos.is_contiguous() and sin.is_contiguous() and cos.is_cuda and sin.is_cuda):
-            raise ValueError(f"cos, sin: contiguous float32 GPU tables [positions, {dim} / 2] are needed")
+                or not (cos.is_contiguous() and sin.is_contiguous() and cos.get_device() == sin.get_device() == dev):
+            raise ValueError(f"cos, sin: contiguous float32 tables [positions, {dim} / 2] on cuda:{dev} are needed")
         pc, ps = cos.data_ptr(), sin.data_ptr()
         if positions is not None:
-            pp = _int32(positions, "positions", tokens)
+            pp = _int32(positions, "positions", tokens, dev)
     elif sin is not None:
         raise ValueError("cos and sin go together")
     return svdq_qk_desc(tokens, dim, _code(dtype), flags, eps, pq, pk, pc, ps, n, pp)
@@ -177,18 +191,19 @@ def qk_norm_rope(q, k, cos=None, sin=None, wq=None, wk=None, eps: float = 1e-6, 
     (i, i + D/2), else (2i, 2i + 1).  Returns (q_out, k_out); q_out=q, k_out=k
     work in place."""
     with _on(stream, q):
+        dev = _current_device()
         tokens, _, dim = q.shape
         dtype = q.dtype
-        d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions)
-        hq, hk = _heads(q, "q", tokens, dim, dtype), _heads(k, "k", tokens, dim, dtype)
+        d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions, dev)
+        hq, hk = _heads(q, "q", tokens, dim, dtype, dev), _heads(k, "k", tokens, dim, dtype, dev)
         if q_out is None:
             q_out, hqo = _new(q)
         else:
-            hqo = _heads(q_out, "q_out", tokens, dim, dtype)
+            hqo = _heads(q_out, "q_out", tokens, dim, dtype, dev)
         if k_out is None:
             k_out, hko = _new(k)
         else:
-            hko = _heads(k_out, "k_out", tokens, dim, dtype)
+            hko = _heads(k_out, "k_out", tokens, dim, dtype, dev)
         _call("svdq_qk_norm_rope", d, hq, hk, hqo, hko, _stream(q))
         return q_out, k_out
 
@@ -199,19 +214,20 @@ def qk_norm_rope_backward(gq, gk, q, k, cos=None, sin=None, wq=None, wk=None, ep
     and its inputs.  Returns (dq, dk, dwq, dwk), the weight gradients fp32 [D]
     (zero without ``norm``)."""
     with _on(stream, q):
+        dev = _current_device()
         tokens, _, dim = q.shape
         dtype = q.dtype
-        d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions)
-        h = [_heads(t, n, tokens, dim, dtype) for t, n in ((q, "q"), (k, "k"), (gq, "gq"), (gk, "gk"))]
+        d = _desc(tokens, dim, dtype, cos, sin, wq, wk, eps, norm, halves, positions, dev)
+        h = [_heads(t, n, tokens, dim, dtype, dev) for t, n in ((q, "q"), (k, "k"), (gq, "gq"), (gk, "gk"))]
         for t, like, n in ((dq, q, "dq"), (dk, k, "dk")):
-            h.append(_new(like) if t is None else (t, _heads(t, n, tokens, dim, dtype)))
+            h.append(_new(like) if t is None else (t, _heads(t, n, tokens, dim, dtype, dev)))
         (dq, hdq), (dk, hdk) = h[4:]
         dwq, dwk = dw = q.new_empty((2, dim), dtype=torch.float32).unbind()
         if ws is None:
             need = _SZ(0)
             _call("svdq_qk_backward_workspace", d, q.shape[1], k.shape[1], need)
             ws = q.new_empty(need.value, dtype=torch.uint8)
-        _call("svdq_qk_norm_rope_backward", d, *h[:4], hdq, hdk, dwq.data_ptr(), dwk.data_ptr(), ws.data_ptr(), ws.numel(),
+        _call("svdq_qk_norm_rope_backward", d, *h[:4], hdq, hdk, dwq.data_ptr(), dwk.data_ptr(), *_scratch(ws, dev),
               _stream(q))
         return dq, dk, *dw
 
@@ -261,8 +277,9 @@ class KVCache:
         shape, dim = k_codes.shape[:3], 2 * k_codes.shape[3]
         for t, kind, last in ((k_codes, torch.uint8, dim // 2), (v_codes, torch.uint8, dim // 2),
                               (k_scales, SCALE_DTYPE[fmt], dim // GROUP[fmt]), (v_scales, SCALE_DTYPE[fmt], dim // GROUP[fmt])):
-            if not t.is_cuda or not t.is_contiguous() or t.dtype is not kind or t.shape != (*shape, last):
-                raise ValueError(f"a contiguous {kind} GPU tensor {(*shape, last)} is needed, got {t.dtype} {tuple(t.shape)}")
+            if not t.is_cuda or t.device != k_codes.device or not t.is_contiguous() or t.dtype is not kind or t.shape != (*shape, last):
+                raise ValueError(f"a contiguous {kind} GPU tensor {(*shape, last)} is needed, all four on one device, "
+                                 f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         self = cls.__new__(cls)
         self._hold(k_codes, k_scales, v_codes, v_scales, fmt)
         return self
@@ -271,9 +288,13 @@ class KVCache:
         self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.fmt = k_codes, k_scales, v_codes, v_scales, fmt
         self.n_pages, self.heads, self.page_size = k_codes.shape[:3]
         self.head_dim = 2 * k_codes.shape[3]
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         self.c = svdq_kv_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
                                self.n_pages, self.page_size, self.heads, self.head_dim, fmt)
+
+    def _here(self, dev):
+        if self.index != dev:
+            raise ValueError(f"the cache is on {self.device}, the call's tensors on cuda:{dev}")
 
     def append(self, k, v, slots, q=None, cos=None, sin=None, wq=None, wk=None, eps: float = 1e-6, norm: bool = False,
                halves: bool = False, positions=None, q_out=None, stream=None):
@@ -281,30 +302,34 @@ class KVCache:
         negative one is skipped).  With norm and / or cos, sin: k is normed and
         rotated on the way (and q into q_out, which is returned)."""
         with _on(stream, k):
+            dev = _current_device()
+            self._here(dev)
             tokens, _, dim = k.shape
-            d = _desc(tokens, dim, k.dtype, cos, sin, wq, wk, eps, norm, halves, positions)
+            d = _desc(tokens, dim, k.dtype, cos, sin, wq, wk, eps, norm, halves, positions, dev)
             hq = ho = None
             if q is not None:
-                hq = _heads(q, "q", tokens, dim, k.dtype)
+                hq = _heads(q, "q", tokens, dim, k.dtype, dev)
                 if q_out is None:
                     q_out, ho = _new(q)
                 else:
-                    ho = _heads(q_out, "q_out", tokens, dim, k.dtype)
-            _call("svdq_kv_append", d, hq, _heads(k, "k", tokens, dim, k.dtype), _heads(v, "v", tokens, dim, k.dtype), ho, self.c,
-                  _int32(slots, "slots", tokens), _stream(k))
+                    ho = _heads(q_out, "q_out", tokens, dim, k.dtype, dev)
+            _call("svdq_kv_append", d, hq, _heads(k, "k", tokens, dim, k.dtype, dev), _heads(v, "v", tokens, dim, k.dtype, dev), ho, self.c,
+                  _int32(slots, "slots", tokens, dev), _stream(k))
             return q_out
 
     def read(self, slots, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
         """(k, v) [len(slots), heads, D]: the cached values of the slots, zero
         for slots outside the cache."""
         with _on(stream, slots):
+            dev = _current_device()
+            self._here(dev)
             n = slots.numel()
-            code, at, hd = _code(dtype), _int32(slots, "slots", n), self.head_dim
+            code, at, hd = _code(dtype), _int32(slots, "slots", n, dev), self.head_dim
             if k_out is None:
                 k_out = self.k_codes.new_empty((n, self.heads, hd), dtype=dtype)
             if v_out is None:
                 v_out = self.k_codes.new_empty((n, self.heads, hd), dtype=dtype)
-            _call("svdq_kv_read", self.c, at, n, code, _heads(k_out, "k_out", n, hd, dtype), _heads(v_out, "v_out", n, hd, dtype),
+            _call("svdq_kv_read", self.c, at, n, code, _heads(k_out, "k_out", n, hd, dtype, dev), _heads(v_out, "v_out", n, hd, dtype, dev),
                   _stream(slots))
             return k_out, v_out
 
@@ -326,6 +351,7 @@ def plan(past, fresh, block_table, free_pages, free_count, page_size: int, token
     (free_count [1] of them are free).  tokens: length of the slot map, at
     least the sum of fresh (the rest is -1)."""
     with _on(stream, past):
+        dev = _current_device()
         b = past.numel()
         out = past.new_empty(2 * b + 3 + 2 * tokens)
         at = out.data_ptr()
@@ -335,9 +361,10 @@ def plan(past, fresh, block_table, free_pages, free_count, page_size: int, token
         for n in cuts:
             p.append(ptr)
             ptr += 4 * n
-        _call("svdq_kv_plan", _int32(past, "past", b), _int32(fresh, "fresh", b), b, page_size, tokens, _int32(free_pages, "free_pages", free_pages.numel()),
-              _int32(free_count, "free_count", 1), free_pages.numel(), _table(block_table, b), block_table.shape[1], *p,
-              _stream(past))
+        room = free_pages.numel()
+        _call("svdq_kv_plan", _int32(past, "past", b, dev), _int32(fresh, "fresh", b, dev), b, page_size, tokens,
+              _int32(free_pages, "free_pages", room, dev), _int32(free_count, "free_count", 1, dev), room, _table(block_table, b, dev),
+              block_table.shape[1], *p, _stream(past))
         return Plan(block_table, q_start, kv_len, slots, positions, left, missing)
 
 
@@ -345,9 +372,11 @@ def release(done, block_table, kv_len, free_pages, free_count, page_size: int, s
     """Gives the pages of the requests with done != 0 back to free_pages (in
     place: free_pages, free_count, block_table and kv_len)."""
     with _on(stream, done):
+        dev = _current_device()
         b = done.numel()
-        _call("svdq_kv_release", _int32(done, "done", b), b, page_size, _table(block_table, b), block_table.shape[1],
-              _int32(kv_len, "kv_len", b), _int32(free_pages, "free_pages", free_pages.numel()), _int32(free_count, "free_count", 1), free_pages.numel(),
+        room = free_pages.numel()
+        _call("svdq_kv_release", _int32(done, "done", b, dev), b, page_size, _table(block_table, b, dev), block_table.shape[1],
+              _int32(kv_len, "kv_len", b, dev), _int32(free_pages, "free_pages", room, dev), _int32(free_count, "free_count", 1, dev), room,
               _stream(done))
 
 
@@ -361,10 +390,11 @@ def attention_workspace_size(requests: int, tokens: int, q_heads: int, cache: KV
 
 
 def attention_workspace(requests: int, tokens: int, q_heads: int, cache: KVCache, max_q: int, max_kv: int,
-                        device="cuda") -> torch.Tensor:
-    """A workspace for ``attention`` calls of these bounds.  One stream at a
-    time may use it."""
-    return torch.empty(attention_workspace_size(requests, tokens, q_heads, cache, max_q, max_kv), dtype=torch.uint8, device=device)
+                        device=None) -> torch.Tensor:
+    """A workspace for ``attention`` calls of these bounds, on the cache's
+    device.  One stream at a time may use it."""
+    return torch.empty(attention_workspace_size(requests, tokens, q_heads, cache, max_q, max_kv), dtype=torch.uint8,
+                       device=cache.device if device is None else device)
 
 
 def attention(q, cache: KVCache, block_table, q_start, kv_len, max_q: int, max_kv: int, causal: bool = True, window: int = 0,
@@ -377,23 +407,25 @@ def attention(q, cache: KVCache, block_table, q_start, kv_len, max_q: int, max_k
     A row that sees nothing gives zeros; a row of no request is not written.
     Returns out, or (out, lse)."""
     with _on(stream, q):
+        dev = _current_device()
+        cache._here(dev)
         tokens, hq, dim = q.shape
         if dim != cache.head_dim:
             raise ValueError(f"q: heads of {dim} over a cache of heads of {cache.head_dim}")
         b = kv_len.numel()
-        hin = _heads(q, "q", tokens, dim, q.dtype)
+        hin = _heads(q, "q", tokens, dim, q.dtype, dev)
         if out is None:
             out, hout = _new(q)
         else:
-            hout = _heads(out, "out", tokens, dim, q.dtype)
+            hout = _heads(out, "out", tokens, dim, q.dtype, dev)
         lse = q.new_empty((tokens, hq), dtype=torch.float32) if return_lse else None
         d = svdq_attn_desc(b, tokens, hq, _code(q.dtype), max_q, max_kv, window, ATTN_CAUSAL if causal else 0,
-                           1.0 / math.sqrt(dim) if scale is None else scale, _int32(q_start, "q_start", b + 1),
-                           _int32(kv_len, "kv_len", b), _table(block_table, b), block_table.shape[1])
+                           1.0 / math.sqrt(dim) if scale is None else scale, _int32(q_start, "q_start", b + 1, dev),
+                           _int32(kv_len, "kv_len", b, dev), _table(block_table, b, dev), block_table.shape[1])
         if ws is None:
             need = _SZ(0)
             _call("svdq_kv_attention_workspace", d, cache.c, need)
             ws = q.new_empty(need.value, dtype=torch.uint8)
         _call("svdq_kv_attention", d, hin, cache.c, hout,
-              None if lse is None else lse.data_ptr(), ws.data_ptr() if ws.numel() else None, ws.numel(), _stream(q))
+              None if lse is None else lse.data_ptr(), *_scratch(ws, dev), _stream(q))
         return (out, lse) if return_lse else out

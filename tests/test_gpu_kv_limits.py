@@ -100,3 +100,17 @@ def test_every_call_takes_a_stream():
         assert torch.equal(k, v) and out.isfinite().all() and torch.equal(y, kv.qk_norm_rope(x, x)[0])
         assert sorted(free.tolist()) == [0, 1, 2, 3] and p.free_count.tolist() == [4] and p.block_table.tolist() == [[-1] * 3]
         free.copy_(torch.arange(4))
+
+
+def test_workspaces_that_are_refused():
+    torch, kv, _ = _mods()
+    cache, table, _, q, start, length = _setup("mxfp4_g32", "bf16", 128, 64, 2, 4, [1], [5000])
+    need = kv.attention_workspace_size(1, 1, 8, cache, 1, 5000)
+    one = torch.empty(1, dtype=torch.uint8, device="cuda")
+    for ws in (one.expand(need), torch.empty(need, dtype=torch.uint8), torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            kv.attention(q, cache, table, start, length, 1, 5000, ws=ws)
+    words = torch.empty(need // 4, dtype=torch.float32, device="cuda")        # bytes count, not elements
+    assert torch.equal(kv.attention(q, cache, table, start, length, 1, 5000, ws=words), kv.attention(q, cache, table, start, length, 1, 5000))
+    with pytest.raises(kv.SvdqError):
+        kv.attention(q, cache, table, start, length, 1, 5000, ws=words[:-1])
