@@ -90,6 +90,13 @@ def _call(name, *args):
         raise SvdqError(name, rc)
 
 
+def _size(v, name, bits=32):
+    """v, if the library's integer holds it (ctypes keeps the low bits of any)."""
+    if -1 << bits - 1 <= v < 1 << bits - 1:
+        return v
+    raise ValueError(f"{name}: {v} is no {bits}-bit integer")
+
+
 def _heads(t, name, tokens, dim, dtype, dev):
     n, h, d = t.shape
     s0, s1, s2 = t.stride()
@@ -261,7 +268,8 @@ class KVCache:
 
     def __init__(self, n_pages: int, page_size: int, heads: int, head_dim: int, fmt: int, device="cuda"):
         code, scale = _SZ(0), _SZ(0)
-        _call("svdq_kv_cache_size", n_pages, page_size, heads, head_dim, fmt, code, scale)
+        _call("svdq_kv_cache_size", _size(n_pages, "n_pages", 64), _size(page_size, "page_size"), _size(heads, "heads"),
+              _size(head_dim, "head_dim"), fmt, code, scale)
         shape = (n_pages, heads, page_size)
         codes = [torch.zeros((*shape, head_dim // 2), dtype=torch.uint8, device=device) for _ in "kv"]
         scales = [torch.zeros((*shape, head_dim // GROUP[fmt]), dtype=SCALE_DTYPE[fmt], device=device) for _ in "kv"]
@@ -362,7 +370,8 @@ def plan(past, fresh, block_table, free_pages, free_count, page_size: int, token
             p.append(ptr)
             ptr += 4 * n
         room = free_pages.numel()
-        _call("svdq_kv_plan", _int32(past, "past", b, dev), _int32(fresh, "fresh", b, dev), b, page_size, tokens,
+        _call("svdq_kv_plan", _int32(past, "past", b, dev), _int32(fresh, "fresh", b, dev), b,
+              _size(page_size, "page_size"), tokens,
               _int32(free_pages, "free_pages", room, dev), _int32(free_count, "free_count", 1, dev), room, _table(block_table, b, dev),
               block_table.shape[1], *p, _stream(past))
         return Plan(block_table, q_start, kv_len, slots, positions, left, missing)
@@ -375,7 +384,7 @@ def release(done, block_table, kv_len, free_pages, free_count, page_size: int, s
         dev = _current_device()
         b = done.numel()
         room = free_pages.numel()
-        _call("svdq_kv_release", _int32(done, "done", b, dev), b, page_size, _table(block_table, b, dev), block_table.shape[1],
+        _call("svdq_kv_release", _int32(done, "done", b, dev), b, _size(page_size, "page_size"), _table(block_table, b, dev), block_table.shape[1],
               _int32(kv_len, "kv_len", b, dev), _int32(free_pages, "free_pages", room, dev), _int32(free_count, "free_count", 1, dev), room,
               _stream(done))
 
@@ -383,7 +392,8 @@ def release(done, block_table, kv_len, free_pages, free_count, page_size: int, s
 # --------------------------------------------------------------------- attention
 def attention_workspace_size(requests: int, tokens: int, q_heads: int, cache: KVCache, max_q: int, max_kv: int) -> int:
     """Bytes of workspace that ``attention`` calls of these bounds need."""
-    d = svdq_attn_desc(requests, tokens, q_heads, S.BF16, max_q, max_kv, 0, ATTN_CAUSAL, 1.0)
+    d = svdq_attn_desc(_size(requests, "requests", 64), _size(tokens, "tokens", 64), _size(q_heads, "q_heads"), S.BF16,
+                       _size(max_q, "max_q"), _size(max_kv, "max_kv"), 0, ATTN_CAUSAL, 1.0)
     need = _SZ(0)
     _call("svdq_kv_attention_workspace", d, cache.c, need)
     return need.value
@@ -419,7 +429,8 @@ def attention(q, cache: KVCache, block_table, q_start, kv_len, max_q: int, max_k
         else:
             hout = _heads(out, "out", tokens, dim, q.dtype, dev)
         lse = q.new_empty((tokens, hq), dtype=torch.float32) if return_lse else None
-        d = svdq_attn_desc(b, tokens, hq, _code(q.dtype), max_q, max_kv, window, ATTN_CAUSAL if causal else 0,
+        d = svdq_attn_desc(b, tokens, hq, _code(q.dtype), _size(max_q, "max_q"), _size(max_kv, "max_kv"), _size(window, "window"),
+                           ATTN_CAUSAL if causal else 0,
                            1.0 / math.sqrt(dim) if scale is None else scale, _int32(q_start, "q_start", b + 1, dev),
                            _int32(kv_len, "kv_len", b, dev), _table(block_table, b, dev), block_table.shape[1])
         if ws is None:

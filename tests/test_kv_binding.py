@@ -31,6 +31,12 @@ class T:
     def is_contiguous(self):
         return True
 
+    def element_size(self):
+        return 4
+
+    def stride(self):
+        return tuple(range(len(self.shape)))
+
     def data_ptr(self):
         return 4096 * (self.index + 2)
 
@@ -95,4 +101,55 @@ def test_tensors_of_two_devices_are_refused(devices, name, device):
 def test_tensors_of_the_host_are_refused(devices):
     with pytest.raises(ValueError):
         kv.release(**tables(-1), page_size=16)
+    assert not devices.launches
+
+
+class Rows(T):
+    dtype = torch.float16
+
+    def stride(self):
+        return self.shape[1] * self.shape[2], self.shape[2], 1
+
+
+def cache(device):
+    c = kv.KVCache.__new__(kv.KVCache)
+    c.heads, c.head_dim, c.index, c.device, c.n_pages, c.page_size, c.c = 2, 64, device, f"cuda:{device}", 4, 16, None
+    return c
+
+
+def attention(**change):
+    q = Rows(0, 6, 4, 64)
+    args = dict(q=q, cache=cache(0), block_table=T(0, 3, 5), q_start=T(0, 4), kv_len=T(0, 3), max_q=2, max_kv=80, out=q, ws=T(0, 1000))
+    return kv.attention(**(args | change))
+
+
+@pytest.mark.parametrize("name", ["max_q", "max_kv", "window"])
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 8, -(1 << 31) - 1, 1 << 70])
+def test_sizes_that_do_not_fit_are_refused(devices, name, value):
+    """ctypes would pass their low 32 bits."""
+    with pytest.raises(ValueError, match=name):
+        attention(**{name: value})
+    assert not devices.launches
+
+
+def test_sizes_that_fit_arrive(devices, monkeypatch):
+    seen = []
+    monkeypatch.setattr(kv, "_call", lambda name, d, *args: seen.append((d.max_q, d.max_kv, d.window)))
+    attention(max_q=(1 << 31) - 1, max_kv=(1 << 31) - 1, window=7)
+    assert seen == [((1 << 31) - 1, (1 << 31) - 1, 7)]
+
+
+@pytest.mark.parametrize("change", [dict(requests=1 << 63), dict(q_heads=(1 << 32) + 4), dict(max_q=(1 << 32) + 1), dict(max_kv=(1 << 32) + 8)])
+def test_workspace_sizes_that_do_not_fit_are_refused(change):
+    args = dict(requests=2, tokens=2, q_heads=4, cache=cache(0), max_q=1, max_kv=80)
+    with pytest.raises(ValueError, match=next(iter(change))):
+        kv.attention_workspace_size(**(args | change))
+
+
+def test_cache_and_page_sizes_that_do_not_fit_are_refused(devices):
+    for change in (dict(n_pages=1 << 64), dict(page_size=(1 << 32) + 16), dict(heads=(1 << 32) + 1), dict(head_dim=(1 << 32) + 64)):
+        with pytest.raises(ValueError, match=next(iter(change))):
+            kv.KVCache(**(dict(n_pages=2, page_size=16, heads=1, head_dim=64, fmt=kv.FMT_MXFP4_G32) | change))
+    with pytest.raises(ValueError, match="page_size"):
+        kv.release(**tables(0), page_size=(1 << 32) + 16)
     assert not devices.launches
