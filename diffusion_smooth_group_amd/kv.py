@@ -239,6 +239,14 @@ def qk_norm_rope_backward(gq, gk, q, k, cos=None, sin=None, wq=None, wk=None, ep
         return dq, dk, *dw
 
 
+def _rows(g):
+    """g as the library takes rows; a gradient that is the same for all heads
+    (stride 0, from a sum over heads) is written out."""
+    t, h, d = g.stride()
+    fits = d == 1 and t >= 0 and t % 8 == 0 and h % 8 == 0 and (h >= g.shape[2] or g.shape[1] == 1) and g.data_ptr() % 16 == 0
+    return g if fits else g.contiguous()
+
+
 class _QKNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, wq, wk, cos, sin, eps, halves, positions):
@@ -250,9 +258,7 @@ class _QKNormRope(torch.autograd.Function):
     def backward(ctx, gq, gk):
         q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
         eps, halves = ctx.how
-        unit = (lambda g: g if g.stride(-1) == 1 and all(s % 8 == 0 for s in g.stride()[:2]) and g.data_ptr() % 16 == 0
-                else g.contiguous())
-        dq, dk, dwq, dwk = qk_norm_rope_backward(unit(gq), unit(gk), q, k, cos, sin, wq, wk, eps, True, halves, positions)
+        dq, dk, dwq, dwk = qk_norm_rope_backward(_rows(gq), _rows(gk), q, k, cos, sin, wq, wk, eps, True, halves, positions)
         return dq, dk, None if wq is None else dwq.to(wq.dtype), None if wk is None else dwk.to(wk.dtype), *[None] * 5
 
 

@@ -114,3 +114,15 @@ def test_workspaces_that_are_refused():
     assert torch.equal(kv.attention(q, cache, table, start, length, 1, 5000, ws=words), kv.attention(q, cache, table, start, length, 1, 5000))
     with pytest.raises(kv.SvdqError):
         kv.attention(q, cache, table, start, length, 1, 5000, ws=words[:-1])
+
+
+def test_autograd_of_a_loss_over_all_heads():
+    """The gradient of a sum over heads arrives with a head stride of 0."""
+    torch, kv, _ = _mods()
+    q, k = (torch.randn((9, h, 64), device="cuda").bfloat16().requires_grad_() for h in (4, 2))
+    w, c = torch.rand(64, device="cuda").bfloat16(), torch.randn((9, 64), device="cuda").bfloat16()
+    yq, yk = kv.qk_norm_rope_autograd(q, k, w, w, None, None)
+    ((yq.sum(1) * c).sum() + (yk.sum(1) * c).sum()).backward()
+    gq, gk = (c[:, None].expand(9, h, 64).contiguous() for h in (4, 2))
+    dq, dk, _, _ = kv.qk_norm_rope_backward(gq, gk, q.detach(), k.detach(), wq=w, wk=w)
+    assert torch.equal(q.grad, dq) and torch.equal(k.grad, dk)

@@ -153,3 +153,41 @@ def test_cache_and_page_sizes_that_do_not_fit_are_refused(devices):
     with pytest.raises(ValueError, match="page_size"):
         kv.release(**tables(0), page_size=(1 << 32) + 16)
     assert not devices.launches
+
+
+# ------------------------------------------------------------------------ autograd
+@pytest.fixture
+def taken(monkeypatch):
+    """The gradients that the library would be given, with a forward pass that
+    doubles (on the CPU: only the wiring is tested)."""
+    seen = []
+
+    def forward(q, k, *_):
+        return 2 * q, 2 * k
+
+    def backward(gq, gk, q, k, cos, sin, wq, wk, *_):
+        seen.extend((gq, gk))
+        return 2 * gq, 2 * gk, torch.ones(q.shape[2]), torch.ones(q.shape[2])
+    monkeypatch.setattr(kv, "qk_norm_rope", forward)
+    monkeypatch.setattr(kv, "qk_norm_rope_backward", backward)
+    return seen
+
+
+LOSSES = {"sum over heads": lambda y, c: (y.sum(1) * c).sum(), "mean over heads": lambda y, c: (y.mean(1) * c).sum(),
+          "sum": lambda y, c: y.sum(), "mean over tokens": lambda y, c: (y.mean(0) * c[0]).sum(), "one head": lambda y, c: (y[:, 1] * c).sum(),
+          "columns first": lambda y, c: (y.transpose(1, 2) * c[:, :, None]).sum(), "heads first": lambda y, c: (y.transpose(0, 1) * c).sum(),
+          "odd columns": lambda y, c: (y[..., 1::2] * c[:, None, 1::2]).sum()}
+
+
+@pytest.mark.parametrize("loss", list(LOSSES))
+@pytest.mark.parametrize("tokens,heads", [(5, 3), (1, 2), (5, 2)])
+def test_every_gradient_arrives_as_rows_that_the_library_takes(taken, loss, tokens, heads):
+    q, k, c = torch.randn(tokens, heads, 64), torch.randn(tokens, 2, 64), torch.randn(tokens, 64)
+    q.requires_grad_(), k.requires_grad_()
+    yq, yk = kv.qk_norm_rope_autograd(q, k, None, None, None, None)
+    (LOSSES[loss](yq, c) + LOSSES[loss](yk, c)).backward()
+    for g, y in zip(taken, (q, k)):
+        t, h, d = g.stride()
+        assert d == 1 and t % 8 == 0 and t >= 0 and h % 8 == 0 and (g.shape[1] == 1 or h >= 64) and g.data_ptr() % 16 == 0
+        want = torch.autograd.grad(LOSSES[loss](y, c), y)[0]
+        assert torch.equal(g, want)
