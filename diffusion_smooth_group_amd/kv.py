@@ -27,6 +27,7 @@ import math
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import svdq as S
 from .svdq import FMT_INT4_G64, FMT_MXFP4_G32, SvdqError  # noqa: F401  (part of this module's interface)
@@ -255,6 +256,7 @@ class _QKNormRope(torch.autograd.Function):
         return qk_norm_rope(q, k, cos, sin, wq, wk, eps, True, halves, positions)
 
     @staticmethod
+    @once_differentiable        # a second derivative raises: without this it would be missing without a word
     def backward(ctx, gq, gk):
         q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
         eps, halves = ctx.how
@@ -263,7 +265,8 @@ class _QKNormRope(torch.autograd.Function):
 
 
 def qk_norm_rope_autograd(q, k, wq, wk, cos, sin, eps: float = 1e-6, halves: bool = False, positions=None):
-    """``qk_norm_rope`` under torch.autograd: gradients of q, k, wq and wk."""
+    """``qk_norm_rope`` under torch.autograd: gradients of q, k, wq and wk.
+    They can not be differentiated again (torch raises an error)."""
     return _QKNormRope.apply(q, k, wq, wk, cos, sin, eps, halves, positions)
 
 

@@ -191,3 +191,12 @@ def test_every_gradient_arrives_as_rows_that_the_library_takes(taken, loss, toke
         assert d == 1 and t % 8 == 0 and t >= 0 and h % 8 == 0 and (g.shape[1] == 1 or h >= 64) and g.data_ptr() % 16 == 0
         want = torch.autograd.grad(LOSSES[loss](y, c), y)[0]
         assert torch.equal(g, want)
+
+
+def test_a_second_derivative_is_refused(taken):
+    """A penalty on the gradient beside another loss: an error, no wrong sum."""
+    q, k = torch.randn(5, 2, 64, requires_grad=True), torch.randn(5, 2, 64, requires_grad=True)
+    yq, yk = kv.qk_norm_rope_autograd(q, k, None, None, None, None)
+    dq, = torch.autograd.grad((yq ** 2).sum() + yk.sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (dq.square().sum() + (yk ** 2).sum()).backward()
