@@ -250,24 +250,25 @@ def _rows(g):
 
 class _QKNormRope(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, wq, wk, cos, sin, eps, halves, positions):
+    def forward(ctx, q, k, wq, wk, cos, sin, eps, halves, positions, norm):
         ctx.save_for_backward(q, k, wq, wk, cos, sin, positions)
-        ctx.how = eps, halves
-        return qk_norm_rope(q, k, cos, sin, wq, wk, eps, True, halves, positions)
+        ctx.how = eps, halves, norm
+        return qk_norm_rope(q, k, cos, sin, wq, wk, eps, norm, halves, positions)
 
     @staticmethod
     @once_differentiable        # a second derivative raises: without this it would be missing without a word
     def backward(ctx, gq, gk):
         q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
-        eps, halves = ctx.how
-        dq, dk, dwq, dwk = qk_norm_rope_backward(_rows(gq), _rows(gk), q, k, cos, sin, wq, wk, eps, True, halves, positions)
-        return dq, dk, None if wq is None else dwq.to(wq.dtype), None if wk is None else dwk.to(wk.dtype), *[None] * 5
+        eps, halves, norm = ctx.how
+        dq, dk, dwq, dwk = qk_norm_rope_backward(_rows(gq), _rows(gk), q, k, cos, sin, wq, wk, eps, norm, halves, positions)
+        return dq, dk, None if wq is None else dwq.to(wq.dtype), None if wk is None else dwk.to(wk.dtype), *[None] * 6
 
 
-def qk_norm_rope_autograd(q, k, wq, wk, cos, sin, eps: float = 1e-6, halves: bool = False, positions=None):
-    """``qk_norm_rope`` under torch.autograd: gradients of q, k, wq and wk.
-    They can not be differentiated again (torch raises an error)."""
-    return _QKNormRope.apply(q, k, wq, wk, cos, sin, eps, halves, positions)
+def qk_norm_rope_autograd(q, k, wq, wk, cos, sin, eps: float = 1e-6, halves: bool = False, positions=None, norm: bool = True):
+    """``qk_norm_rope`` under torch.autograd: gradients of q, k, wq and wk
+    (zero for the weights without ``norm``).  They can not be differentiated
+    again (torch raises an error)."""
+    return _QKNormRope.apply(q, k, wq, wk, cos, sin, eps, halves, positions, norm)
 
 
 # ----------------------------------------------------------------------- cache

@@ -126,3 +126,18 @@ def test_autograd_of_a_loss_over_all_heads():
     gq, gk = (c[:, None].expand(9, h, 64).contiguous() for h in (4, 2))
     dq, dk, _, _ = kv.qk_norm_rope_backward(gq, gk, q.detach(), k.detach(), wq=w, wk=w)
     assert torch.equal(q.grad, dq) and torch.equal(k.grad, dk)
+
+
+@pytest.mark.parametrize("halves", [False, True])
+def test_autograd_of_the_rotation_alone(halves):
+    torch, kv, _ = _mods()
+    q, k, gq = (torch.randn((9, h, 64), device="cuda").half() for h in (4, 2, 4))
+    a = torch.rand((9, 32), device="cuda") * 6
+    cos, sin = a.cos(), a.sin()
+    q.requires_grad_(), k.requires_grad_()
+    yq, yk = kv.qk_norm_rope_autograd(q, k, None, None, cos, sin, halves=halves, norm=False)
+    want = kv.qk_norm_rope(q.detach(), k.detach(), cos, sin, norm=False, halves=halves)
+    assert torch.equal(yq, want[0]) and torch.equal(yk, want[1])
+    ((yq * gq).sum() + yk.sum()).backward()
+    dq, dk, _, _ = kv.qk_norm_rope_backward(gq, torch.ones_like(yk), q.detach(), k.detach(), cos, sin, norm=False, halves=halves)
+    assert torch.equal(q.grad, dq) and torch.equal(k.grad, dk)
