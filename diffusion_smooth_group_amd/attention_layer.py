@@ -49,13 +49,14 @@ class SVDQAttention:
     def forward(self, x, step: kv.Plan, max_q: int, max_kv: int, ws=None):
         """x [tokens, K]: the new tokens of all requests, request after request;
         step: the plan that gave them their slots; max_q, max_kv: bounds on a
-        request's new and cached tokens; ws: the attention's workspace, or None
+        request's new and cached tokens.  Rows past the last request's (a padded
+        step) come out as the projection of zeros.  ws: the attention's workspace, or None
         for one of the call's own."""
         tokens, d, hq, hk = x.shape[0], self.cache.head_dim, self.q_heads, self.cache.heads
         rows = self._linear(self.qkv, x).view(tokens, hq + 2 * hk, d)
         q, k, v = rows[:, :hq], rows[:, hq:hq + hk], rows[:, hq + hk:]
         self.cache.append(k, v, step.slots, q=q, q_out=q, positions=step.positions, **self.how)
-        o = torch.empty((tokens, hq, d), dtype=x.dtype, device=x.device)
+        o = torch.zeros((tokens, hq, d), dtype=x.dtype, device=x.device)
         kv.attention(q, self.cache, step.block_table, step.q_start, step.kv_len, max_q, max_kv, window=self.window, out=o, ws=ws)
         return self._linear(self.out, o.view(tokens, hq * d))
 

@@ -80,3 +80,20 @@ def test_calls_on_two_streams_share_no_workspace(monkeypatch):
     torch.cuda.synchronize()
     assert len(here) == len(used) == 3 and not set(here) & set(used)
     assert torch.equal(first, second)
+
+
+def test_rows_of_no_request_are_the_projection_of_zeros():
+    """A step padded to a fixed number of tokens, in memory that held NaN."""
+    import torch
+
+    from diffusion_smooth_group_amd import kv
+    net = _layer(1)
+    x = torch.randn((70, 256), device="cuda").bfloat16()
+    padded = torch.cat((x, torch.zeros((58, 256), device="cuda").bfloat16()))
+    want = net(x, _step(torch, kv, [0, 0], [40, 30]), 40, 40)
+    zeros = net.out.forward(torch.zeros((58, net.out.K), device="cuda").bfloat16())
+    for _ in range(3):
+        held = [torch.full((128 * n,), float("nan"), device="cuda").bfloat16() for n in (64, 128, 256, 512, 1024)]
+        del held
+        got = net(padded, _step(torch, kv, [0, 0], [40, 30], tokens=128), 40, 40)
+        assert torch.equal(got[:70], want) and torch.equal(got[70:], zeros)
