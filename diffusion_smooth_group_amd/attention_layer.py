@@ -20,7 +20,9 @@ from .svdq import SVDQLinear, workspace_size
 class SVDQAttention:
     """qkv: SVDQLinear K -> (q_heads + 2 k_heads) D, rows q heads, k heads, v
     heads; out: SVDQLinear q_heads D -> N; wq, wk: norm weights [D] or None; cos,
-    sin: rotation tables [positions, D / 2]; cache: this layer's KVCache.
+    sin: rotation tables [positions, D / 2]; cache: this layer's KVCache;
+    causal, window: which keys a token sees (causal=False: all of its request,
+    as in an image transformer, whose request is an image's tokens in one step).
 
     A call keeps nothing.  Its workspaces come from torch's allocator, under the
     current stream (or into the pool of the graph that is being captured), so
@@ -28,14 +30,15 @@ class SVDQAttention:
     do share is the cache; its order is the caller's."""
 
     def __init__(self, qkv: SVDQLinear, out: SVDQLinear, q_heads: int, cache: kv.KVCache, cos, sin, wq=None, wk=None,
-                 eps: float = 1e-6, norm: bool = True, halves: bool = False, window: int = 0):
+                 eps: float = 1e-6, norm: bool = True, halves: bool = False, window: int = 0,
+                 causal: bool = True):
         rows = (q_heads + 2 * cache.heads) * cache.head_dim
         if qkv.N != rows or out.K != q_heads * cache.head_dim:
             raise ValueError(f"{q_heads} query heads of {cache.head_dim} over {cache.heads} cache heads need a projection to {rows} "
                              f"and one from {q_heads * cache.head_dim}, got {qkv.N} and {out.K}")
         self.qkv, self.out, self.q_heads, self.cache = qkv, out, q_heads, cache
         self.how = dict(cos=cos, sin=sin, wq=wq, wk=wk, eps=eps, norm=norm, halves=halves)
-        self.window = window
+        self.window, self.causal = window, causal
 
     def workspace(self, requests: int, tokens: int, max_q: int, max_kv: int):
         """A workspace for the attention of calls of these bounds, for callers
@@ -57,7 +60,8 @@ class SVDQAttention:
         q, k, v = rows[:, :hq], rows[:, hq:hq + hk], rows[:, hq + hk:]
         self.cache.append(k, v, step.slots, q=q, q_out=q, positions=step.positions, **self.how)
         o = torch.zeros((tokens, hq, d), dtype=x.dtype, device=x.device)
-        kv.attention(q, self.cache, step.block_table, step.q_start, step.kv_len, max_q, max_kv, window=self.window, out=o, ws=ws)
+        kv.attention(q, self.cache, step.block_table, step.q_start, step.kv_len, max_q, max_kv, causal=self.causal, window=self.window, out=o,
+                     ws=ws)
         return self._linear(self.out, o.view(tokens, hq * d))
 
     __call__ = forward

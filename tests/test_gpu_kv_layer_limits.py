@@ -97,3 +97,22 @@ def test_rows_of_no_request_are_the_projection_of_zeros():
         del held
         got = net(padded, _step(torch, kv, [0, 0], [40, 30], tokens=128), 40, 40)
         assert torch.equal(got[:70], want) and torch.equal(got[70:], zeros)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 7), (False, 7)])
+def test_masks_of_the_layer_are_those_of_the_attention(causal, window):
+    """The layer against its operators, called one after the other."""
+    import torch
+
+    from diffusion_smooth_group_amd import kv
+    from diffusion_smooth_group_amd.attention_layer import SVDQAttention
+    net = _layer(1)
+    net = SVDQAttention(net.qkv, net.out, 4, net.cache, net.how["cos"], net.how["sin"], net.how["wq"], net.how["wk"], halves=True,
+                        window=window, causal=causal)
+    x = torch.randn((100, 256), device="cuda").bfloat16()
+    step = _step(torch, kv, [0, 0], [60, 40])
+    got = net(x, step, 60, 60)
+    rows = net.qkv.forward(x).view(100, 8, 64)
+    q = net.cache.append(rows[:, 4:6], rows[:, 6:], step.slots, q=rows[:, :4], positions=step.positions, **net.how)
+    o = kv.attention(q, net.cache, step.block_table, step.q_start, step.kv_len, 60, 60, causal=causal, window=window)
+    assert torch.equal(got, net.out.forward(o.contiguous().view(100, 256)))
