@@ -1239,7 +1239,7 @@ extern "C" svdq_status svdq_kv_attention_workspace(const svdq_attn_desc* d, cons
   if (d->requests == 0 || d->tokens == 0 || d->max_q == 0) return SVDQ_OK;
   Cut t;
   if ((st = cut_of(d, c, device_cus(), &t)) != SVDQ_OK) return st;
-  *bytes = part_bytes(d, c, t, t.most);
+  *bytes = part_bytes(c, most_part_rows(d, c, device_cus()));
   return SVDQ_OK;
 }
 
@@ -1254,7 +1254,7 @@ extern "C" svdq_status svdq_kv_attention(const svdq_attn_desc* d, const svdq_hea
   if (!d->q_start || !d->kv_len || (d->table_stride > 0 && !d->block_table)) return SVDQ_ERR_INVALID_ARG;
   Cut t;
   if ((st = cut_of(d, c, device_cus(), &t)) != SVDQ_OK) return st;
-  const size_t need = part_bytes(d, c, t, t.splits);
+  const size_t need = part_bytes(c, part_rows(d, c, t));
   if (need > 0) {
     if (!ws) return SVDQ_ERR_INVALID_ARG;
     if (ws_bytes < need) return SVDQ_ERR_CAPACITY;

@@ -87,14 +87,12 @@ struct TileRange {
   SVDQ_HD int chunk_to(const P& p, int i) const { return smaller(to, chunk_from(p, i) + p.chunk); }
 };
 
-// How a call is cut: row tiles per request and head, and key chunks.  `most`
-// bounds the chunks of any call with these requests, rows and lengths, whatever
-// its window, so that one workspace serves them all.
+// How a call is cut: row tiles per request and head, and key chunks.
 struct Cut {
   int64_t items;            // requests x heads x row tiles
   int64_t row_slots;        // rows of a request and head
   int rows;                 // rows of a tile: 16 (k_attn16), 128 or 256 (k_attn_rows)
-  int row_tiles, splits, chunk, most;
+  int row_tiles, splits, chunk;
 };
 
 inline svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, int cus, Cut* out) {
@@ -147,19 +145,35 @@ inline svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, int c
     if (keys >= 1024 * fit(4)) return fit(4);
     return least(fit(2), ceil_div(keys, 256));
   };
-  const int64_t all = int64_t(d->max_kv) + 31, n = chunks(span);
+  const int64_t n = chunks(span);
   const int64_t chunk = ceil_div(ceil_div(span > 0 ? span : 1, n), 128) * 128;
   t.splits = int(ceil_div(span > 0 ? span : 1, chunk));
-  t.most = int(chunks(all));            // more keys are never fewer chunks
   t.chunk = int(chunk);
   t.row_tiles = int(tiles);
-  if (t.items * t.most >= MAX_THREADS / 512) return SVDQ_ERR_UNSUPPORTED;   // a join has fewer: only calls of few rows are cut
+  if (t.items * t.splits >= MAX_THREADS / 512) return SVDQ_ERR_UNSUPPORTED;   // a join has fewer: only calls of few rows are cut
   *out = t;
   return SVDQ_OK;
 }
 
-inline size_t part_bytes(const svdq_attn_desc* d, const svdq_kv_cache* c, const Cut& t, int splits) {
-  return splits > 1 ? size_t(d->requests) * size_t(c->heads) * size_t(t.row_slots) * size_t(splits) * size_t(c->head_dim + 2) * 4 : 0;
+inline size_t part_bytes(const svdq_kv_cache* c, int64_t rows) { return size_t(rows) * size_t(c->head_dim + 2) * 4; }
+
+// partial rows that a call leaves for its join
+inline int64_t part_rows(const svdq_attn_desc* d, const svdq_kv_cache* c, const Cut& t) {
+  return t.splits > 1 ? d->requests * c->heads * t.row_slots * t.splits : 0;
+}
+
+// Partial rows of any call with at most these requests, tokens, max_q and
+// max_kv: fewer of them are cut into more chunks.  Chunks of a tile x tiles are
+// at most 8 workgroups a compute unit with tiles of 16, of which a tile has
+// row_slots rows at most, 2 with 128 and 1 with 256; and each row has at most
+// as many chunks as there are least ones in its keys.
+inline int64_t most_part_rows(const svdq_attn_desc* d, const svdq_kv_cache* c, int cus) {
+  const int64_t max_q = d->max_q < d->tokens ? d->max_q : d->tokens, row_slots = max_q * (d->q_heads / c->heads);
+  const int64_t slots = d->requests * c->heads * row_slots, keys = int64_t(d->max_kv) + 31;
+  auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+  const int64_t few = keys <= 1024 ? 0 : least(8 * int64_t(cus) * least(16, row_slots), slots * ceil_div(keys, 256));
+  const int64_t wide = keys <= 512 || row_slots <= 80 || slots <= 1024 ? 0 : least(256 * int64_t(cus), slots * ceil_div(keys, 512));
+  return few > wide ? few : wide;
 }
 
 }  // namespace svdq_kv

@@ -401,7 +401,8 @@ def release(done, block_table, kv_len, free_pages, free_count, page_size: int, s
 
 # --------------------------------------------------------------------- attention
 def attention_workspace_size(requests: int, tokens: int, q_heads: int, cache: KVCache, max_q: int, max_kv: int) -> int:
-    """Bytes of workspace that ``attention`` calls of these bounds need."""
+    """Bytes of workspace that ``attention`` calls with at most these requests,
+    tokens, max_q and max_kv need."""
     d = svdq_attn_desc(_size(requests, "requests", 64), _size(tokens, "tokens", 64), _size(q_heads, "q_heads"), S.BF16,
                        _size(max_q, "max_q"), _size(max_kv, "max_kv"), 0, ATTN_CAUSAL, 1.0)
     need = _SZ(0)
@@ -411,7 +412,7 @@ def attention_workspace_size(requests: int, tokens: int, q_heads: int, cache: KV
 
 def attention_workspace(requests: int, tokens: int, q_heads: int, cache: KVCache, max_q: int, max_kv: int,
                         device=None) -> torch.Tensor:
-    """A workspace for ``attention`` calls of these bounds, on the cache's
+    """A workspace for ``attention`` calls of these bounds and smaller ones, on the cache's
     device.  One stream at a time may use it."""
     return torch.empty(attention_workspace_size(requests, tokens, q_heads, cache, max_q, max_kv), dtype=torch.uint8,
                        device=cache.device if device is None else device)

@@ -182,7 +182,8 @@ typedef struct {
  * below 2^-124 as 2^-124.  ws: >= svdq_kv_attention_workspace
  * bytes, 256-byte aligned (may be NULL where that is 0); its content need
  * not be kept between calls.  The size goes by requests, tokens, q_heads,
- * max_q, max_kv and the cache's shape alone. */
+ * max_q, max_kv and the cache's shape alone, and is enough for every call with
+ * as many of them or fewer (same q_heads, same shape). */
 svdq_status svdq_kv_attention_workspace(const svdq_attn_desc* desc, const svdq_kv_cache* cache, size_t* bytes);
 svdq_status svdq_kv_attention(const svdq_attn_desc* desc, const svdq_heads* q, const svdq_kv_cache* cache,
                               const svdq_heads* out, float* lse, void* ws, size_t ws_bytes, hipStream_t stream);

@@ -141,3 +141,14 @@ def test_autograd_of_the_rotation_alone(halves):
     ((yq * gq).sum() + yk.sum()).backward()
     dq, dk, _, _ = kv.qk_norm_rope_backward(gq, torch.ones_like(yk), q.detach(), k.detach(), cos, sin, norm=False, halves=halves)
     assert torch.equal(q.grad, dq) and torch.equal(k.grad, dk)
+
+
+def test_one_workspace_serves_smaller_steps():
+    """Sized once for prompts of many requests, used as they end."""
+    torch, kv, _ = _mods()
+    for requests, rows, length in ((1, 1, 8000), (3, 2, 5000), (1, 90, 2500), (2, 300, 3000)):
+        cache, table, _, q, start, lens = _setup("mxfp4_g32", "bf16", 64, 64, 2, 4, [rows] * requests, [length] * requests)
+        ws = kv.attention_workspace(300, 300 * 2048, 8, cache, 2048, 16384)
+        want, wl = kv.attention(q, cache, table, start, lens, rows, length, return_lse=True)
+        got, gl = kv.attention(q, cache, table, start, lens, rows, length, ws=ws, return_lse=True)
+        assert torch.equal(got, want) and torch.equal(gl, wl)

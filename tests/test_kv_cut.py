@@ -35,7 +35,8 @@ int main() {
     c.n_pages = 1000; c.page_size = 1 << shift; c.heads = int32_t(heads); c.head_dim = int32_t(dim);
     Cut t = {};
     const int st = int(cut_of(&d, &c, int(cus), &t));
-    printf("%d %d %d %d %lld", st, t.rows, t.splits, t.chunk, (long long)(st ? 0 : part_bytes(&d, &c, t, t.most)));
+    printf("%d %d %d %d %lld %lld", st, t.rows, t.splits, t.chunk, (long long)(st ? 0 : part_rows(&d, &c, t)),
+           (long long)(st ? 0 : most_part_rows(&d, &c, int(cus))));
     if (st == 0) {
       const int32_t start[2] = {int32_t(s), int32_t(e)}, length[1] = {int32_t(len)};
       const P p = {start, length, tokens, stride, c.n_pages, d.max_q, d.max_kv, d.window, int32_t(causal), int32_t(shift), int32_t(q_heads / heads), t.chunk};
@@ -87,12 +88,13 @@ def case(**kw):
 
 def check(c, got):
     """Against the definition in Python's integers."""
-    status, tile_rows, splits, chunk, _ = got[:5]
+    status, tile_rows, splits, chunk, part, most = got[:6]
+    assert part <= most, c
     if status:
         return
     n = min(c["end"], c["tokens"]) - c["start"]
     rows = max(0, min(n, c["max_q"]))
-    assert got[5] == rows, c
+    assert got[6] == rows, c
     if rows == 0:
         return
     room = c["stride"] << c["shift"]
@@ -102,10 +104,10 @@ def check(c, got):
     def sees(i):
         pos = last_pos + i
         return (min(length, max(0, pos - c["window"] + 1)) if c["window"] else 0), (max(0, min(pos + 1, length)) if c["causal"] else length)
-    assert got[6:10] == [*sees(0), *sees(rows - 1)], c
+    assert got[7:11] == [*sees(0), *sees(rows - 1)], c
     group = c["q_heads"] // c["heads"]
     tiles = -(-rows * group // tile_rows)
-    at = 10
+    at = 11
     for rt in (0, tiles - 1):
         first, last, begin, end, chunks, f0, t0, f1, t1 = got[at:at + 9]
         at += 9
@@ -171,3 +173,38 @@ def test_random_calls(program):
     for c, g in zip(cases, run(program, cases)):
         assert g[0] == 0, c
         check(c, g)
+
+
+def test_a_workspace_serves_every_smaller_call(program):
+    """Fewer requests, tokens, rows or keys are cut into more chunks."""
+    rng = random.Random(11)
+
+    def some(most):
+        return rng.choice([most, rng.randint(1, most), int(2 ** rng.uniform(0, 31)) % most + 1])
+    cases, of = [], []
+    for _ in range(600):
+        heads, group = rng.choice([1, 2, 5, 8, 24]), rng.choice([1, 2, 4, 5, 8])
+        requests, max_q = int(2 ** rng.uniform(0, 10)), int(2 ** rng.uniform(0, 12))
+        full = case(requests=requests, tokens=rng.choice([requests, requests * max_q]), q_heads=heads * group, heads=heads, max_q=max_q,
+                    max_kv=int(2 ** rng.uniform(0, 17)), stride=100000, cus=rng.choice([256, 256, 64, 304]))
+        at = len(cases)
+        cases.append(full)
+        of.append(at)
+        for _ in range(30):
+            cases.append(full | dict(requests=some(requests), tokens=some(full["tokens"]), max_q=some(max_q), max_kv=some(full["max_kv"]),
+                                     window=rng.choice([0, 0, 1, 300]), causal=rng.randint(0, 1), stride=rng.choice([100000, 3, 700])))
+            of.append(at)
+    got = run(program, cases)
+    for c, g, i in zip(cases, got, of):
+        assert g[0] in (0, UNSUPPORTED)
+        if g[0] == 0 and got[i][0] == 0:
+            assert g[4] <= got[i][5] and g[5] <= got[i][5], (c, cases[i])
+
+
+def test_workspaces_stay_within_what_fills_the_chip(program):
+    """A bound, not a multiple of the largest shape: at most 65536 partial rows
+    with 256 compute units."""
+    cases = [case(requests=r, tokens=r * q, max_q=q, max_kv=1 << 20, stride=1 << 20, q_heads=64, heads=h) for r in (1, 100, 500)
+             for q in (1, 100, 5000) for h in (1, 8, 64)]
+    for c, g in zip(cases, run(program, cases)):
+        assert g[0] == UNSUPPORTED or g[5] <= 65536, c
