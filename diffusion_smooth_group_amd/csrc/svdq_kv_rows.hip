@@ -562,7 +562,8 @@ __global__ __launch_bounds__(256) void k_plan(PlanParams p) {
           pg = k >= 0 && k < count ? p.free_pages[count - 1 - k] : -1;
         }
       }
-      slot = pg < 0 ? -1 : (pg << p.page_shift) + (pos & (page - 1));
+      // a page that no cache has (slots are 31-bit) must not wrap to one that it has
+      slot = pg < 0 || pg > (0x7FFFFFFF >> p.page_shift) ? -1 : (pg << p.page_shift) + (pos & (page - 1));
     }
     p.slots[t] = slot;
     p.positions[t] = pos;

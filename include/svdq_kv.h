@@ -133,7 +133,8 @@ svdq_status svdq_kv_read(const svdq_kv_cache* cache, const int32_t* slots, int64
  *   q_start [requests + 1]   prefix sums of fresh
  *   kv_len [requests]        past + fresh
  *   slots, positions [tokens] of the new tokens, request after request;
- *               slot -1 where there is no page or the table has no column;
+ *               slot -1 where there is no page, the table has no column or
+ *               the page's slots would pass 2^31;
  *               past the sum of fresh: slot -1, position 0
  *   free_left [1]            pages left in the free list
  *   missing [1]              pages that were wanted and not there

@@ -152,3 +152,24 @@ def test_one_workspace_serves_smaller_steps():
         want, wl = kv.attention(q, cache, table, start, lens, rows, length, return_lse=True)
         got, gl = kv.attention(q, cache, table, start, lens, rows, length, ws=ws, return_lse=True)
         assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_page_numbers_past_every_cache_give_no_slot(page):
+    """Their slots would wrap to other requests' pages."""
+    torch, kv, _ = _mods()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    last = (1 << 31) // page - 1                           # its last slot is 2^31 - 1
+    bad = [last + 1, 1 << 28, (1 << 28) + 5, (1 << 31) - 1]
+    free = torch.tensor([*bad, last, 7], **i32)
+    p = kv.plan(torch.zeros(6, **i32), torch.full((6,), 3, **i32), torch.full((6, 2), -1, **i32), free, torch.tensor([6], **i32), page, 18)
+    slots = p.slots.view(6, 3).tolist()
+    assert slots[0] == [7 * page + i for i in range(3)] and slots[1] == [last * page + i for i in range(3)]
+    for row, number in zip(slots[2:], reversed(bad)):
+        assert number > last and row == [-1] * 3
+    held = p.block_table[:, 0].tolist()
+    assert held == list(reversed(free.tolist()))           # the table has what the list had
+    # the same for a page that the table held before
+    table = torch.tensor([[1 << 28, -1]], **i32)
+    p = kv.plan(torch.tensor([2], **i32), torch.tensor([3], **i32), table, free, torch.tensor([6], **i32), page, 3)
+    assert p.slots.tolist() == [-1] * 3
