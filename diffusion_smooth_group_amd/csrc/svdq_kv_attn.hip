@@ -24,8 +24,8 @@ struct AttnParams {
   float* part;              // [row slot][split][D] partial sums, then [row slot][split][2] reference and sum
   const uint8_t *kc, *ks, *vc, *vs;
   const int32_t *q_start, *kv_len, *table;
-  int64_t qt, qh, ot, oh, tokens, table_stride, n_pages;
-  int32_t requests, q_heads, heads, group;      // group = q_heads / heads
+  int64_t qt, qh, ot, oh, table_stride, n_pages;
+  int32_t tokens, requests, q_heads, heads, group;      // group = q_heads / heads
   int32_t max_q, max_kv, window, causal, page_shift;
   int32_t row_tiles, row_slots, splits, chunk;  // row tiles and rows a request and head has at most; key chunks
   float c;                  // scale log2(e)
@@ -523,7 +523,7 @@ __global__ __launch_bounds__(256, 3) void k_attn16(AttnParams p) {
   w.low = r.low(p, qi);
   w.high = row < rows ? r.high(p, qi) : 0;
   {
-    const uint16_t* q = p.q + (r.first + qi) * p.qt + int64_t(qh) * p.qh;
+    const uint16_t* q = p.q + int64_t(r.first + qi) * p.qt + int64_t(qh) * p.qh;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) w.q[j] = query_order<FMT>(*reinterpret_cast<const u32x4*>(q + frag_dim<FMT, D>(j, b)));
     if (p.c < 0.0f) {       // the sign of the scale goes to the query: the largest product is the largest logit
@@ -598,7 +598,7 @@ __global__ __launch_bounds__(256, 3) void k_attn16(AttnParams p) {
     }
     return;
   }
-  const int64_t tok = r.first + row_o / p.group;
+  const int64_t tok = int64_t(r.first) + row_o / p.group;
   const int head = h * p.group + row_o % p.group;
   const float inv = sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
 #pragma unroll
@@ -716,7 +716,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   const int low = r.low(p, qi), high = row < rows ? r.high(p, qi) : 0;
   u32x4 q[NS];
   {
-    const uint16_t* src = p.q + (r.first + qi) * p.qt + int64_t(qh) * p.qh + 8 * hb;
+    const uint16_t* src = p.q + int64_t(r.first + qi) * p.qt + int64_t(qh) * p.qh + 8 * hb;
 #pragma unroll
     for (int e = 0; e < NS; ++e) q[e] = query_order<FMT>(*reinterpret_cast<const u32x4*>(src + 16 * e));
     if (p.c < 0.0f) {       // the sign of the scale goes to the query: the largest product is the largest logit
@@ -1013,6 +1013,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     __syncthreads();
     auto used = [&](int t) { return t < wto && t + 64 > wfrom && t < to; };
     int buf = 0;
+    // Where the loop stands in memory, by what its instructions' fetches make of
+    // it (4608 full, MXFP4, by its offset in 32 bytes: 265 .. 279 us, f16 268 .. 284;
+    // 5 x 2047 rows: MXFP4 705 .. 727, INT4 846 .. 857).
+    constexpr int OFFSET = !MX ? 6 : DT == SVDQ_F16 ? 0 : 2;       // words
+    asm volatile(".p2align 6\n\t.rept %0\n\ts_nop 0\n\t.endr" ::"i"(OFFSET));
     for (int token = from; token < to; token += KT) {
       const unsigned here = bad;
       if (token + KT < to) {
@@ -1051,7 +1056,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   if (row >= rows) return;
   const bool whole = range.n <= 1;
   const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
-  const int64_t tok = r.first + row / p.group;
+  const int64_t tok = int64_t(r.first) + row / p.group;
   const int head = h * p.group + row % p.group;
   const int64_t slot = ((int64_t(req) * p.heads + h) * p.row_slots + row) * p.splits + split;
 #pragma unroll
@@ -1105,7 +1110,7 @@ __global__ __launch_bounds__(256) void k_attn_join_few(AttnParams p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] += a * u[e];
   }
-  const int64_t tok = r.first + row / p.group;
+  const int64_t tok = int64_t(r.first) + row / p.group;
   const int head = h * p.group + row % p.group;
   const float inv = sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
   *reinterpret_cast<u32x2*>(p.out + tok * p.ot + head * p.oh + d) = u32x2{pack2<DT>(f[0] * inv, f[1] * inv), pack2<DT>(f[2] * inv, f[3] * inv)};
@@ -1171,7 +1176,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnParams p) {
   float f0 = 0.0f, f1 = 0.0f;
 #pragma unroll
   for (int i = 0; i < G; ++i) { f0 += red[i][2 * tid]; f1 += red[i][2 * tid + 1]; }
-  const int64_t tok = r.first + row / p.group;
+  const int64_t tok = int64_t(r.first) + row / p.group;
   const int head = h * p.group + row % p.group;
   const float inv = sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
   *reinterpret_cast<unsigned*>(p.out + tok * p.ot + head * p.oh + 2 * tid) = pack2<DT>(f0 * inv, f1 * inv);
@@ -1272,9 +1277,9 @@ extern "C" svdq_status svdq_kv_attention(const svdq_attn_desc* d, const svdq_hea
   p.q_start = d->q_start; p.kv_len = d->kv_len; p.table = d->block_table;
   p.qt = q->token_stride; p.qh = q->head_stride;
   p.ot = out->token_stride; p.oh = out->head_stride;
-  p.tokens = d->tokens; p.table_stride = d->table_stride; p.n_pages = c->n_pages;
+  p.tokens = t.tokens; p.table_stride = d->table_stride; p.n_pages = c->n_pages;
   p.requests = int32_t(d->requests); p.q_heads = d->q_heads; p.heads = c->heads; p.group = d->q_heads / c->heads;
-  p.max_q = d->max_q; p.max_kv = d->max_kv; p.window = d->window;
+  p.max_q = d->max_q; p.max_kv = t.keys; p.window = d->window;
   p.causal = (d->flags & SVDQ_ATTN_CAUSAL) != 0u;
   p.page_shift = page_shift(c->page_size);
   p.row_tiles = t.row_tiles; p.row_slots = int32_t(t.row_slots); p.splits = t.splits; p.chunk = t.chunk;

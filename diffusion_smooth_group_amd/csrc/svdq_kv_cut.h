@@ -30,37 +30,28 @@ inline int64_t product_below(int64_t a, int64_t b, int64_t c, int64_t limit) {
 // threads of a launch's x dimension
 constexpr int64_t MAX_THREADS = int64_t(1) << 32;
 
-// A request's rows and the keys they see.
+// A request's rows and the keys they see.  All in 32 bits, of which the scalar
+// unit has comparisons, and without overflow for any offsets and lengths.
 struct Request {
-  int rows, len;
-  int64_t first, before;    // position of row 0 (below 0: rows that stand before the first token)
+  int rows, len, first;
+  int before;               // position of row 0 (below 0: rows that stand before the first token)
   template <class P>
   SVDQ_HD Request(const P& p, int r) {
-    const int64_t s = p.q_start[r], e = p.q_start[r + 1];
-    first = s < 0 ? 0 : s;
-    int64_t n = e < p.tokens ? e : p.tokens;
-    n -= first;
-    rows = n < 0 || s < 0 ? 0 : int(n < p.max_q ? n : p.max_q);
-    const int64_t true_len = p.kv_len[r];
-    before = true_len - (e - s);
-    const int64_t columns = p.table_stride < (int64_t(1) << 27) ? p.table_stride : int64_t(1) << 27;   // of 16 tokens at least
-    const int64_t room = columns << p.page_shift;
-    int64_t l = true_len < p.max_kv ? true_len : p.max_kv;
-    l = l < room ? l : room;
-    len = p.n_pages == 0 || l < 0 ? 0 : int(l);
+    const int s = p.q_start[r], e = smaller(p.q_start[r + 1], p.tokens), held = larger(p.kv_len[r], 0);
+    first = s;
+    rows = s < 0 || e <= s ? 0 : smaller(e - s, p.max_q);
+    before = rows > 0 ? held - (p.q_start[r + 1] - s) : 0;
+    len = smaller(held, p.max_kv);
   }
   // keys [low, high) that row i sees
   template <class P>
   SVDQ_HD int high(const P& p, int i) const {
-    if (!p.causal) return len;
-    const int64_t end = before + i + 1;
-    return end < 0 ? 0 : end < len ? int(end) : len;
+    return p.causal ? larger(0, smaller(before + i + 1, len)) : len;
   }
   template <class P>
   SVDQ_HD int low(const P& p, int i) const {
-    if (p.window <= 0) return 0;
-    const int64_t begin = before + i + 1 - p.window;
-    return begin < 0 ? 0 : begin < len ? int(begin) : len;
+    const int end = before + i + 1;
+    return p.window > 0 && end > p.window ? smaller(end - p.window, len) : 0;
   }
 };
 
@@ -93,6 +84,7 @@ struct Cut {
   int64_t row_slots;        // rows of a request and head
   int rows;                 // rows of a tile: 16 (k_attn16), 128 or 256 (k_attn_rows)
   int row_tiles, splits, chunk;
+  int keys, tokens;         // most keys of a request, query rows: the arguments within what they can be
 };
 
 inline svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, int cus, Cut* out) {
@@ -149,6 +141,8 @@ inline svdq_status cut_of(const svdq_attn_desc* d, const svdq_kv_cache* c, int c
   const int64_t chunk = ceil_div(ceil_div(span > 0 ? span : 1, n), 128) * 128;
   t.splits = int(ceil_div(span > 0 ? span : 1, chunk));
   t.chunk = int(chunk);
+  t.keys = c->n_pages == 0 ? 0 : int(keys);
+  t.tokens = int(d->tokens < 0x7FFFFFFF ? d->tokens : 0x7FFFFFFF);     // offsets are 32-bit
   t.row_tiles = int(tiles);
   if (t.items * t.splits >= MAX_THREADS / 512) return SVDQ_ERR_UNSUPPORTED;   // a join has fewer: only calls of few rows are cut
   *out = t;

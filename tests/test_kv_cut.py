@@ -21,8 +21,7 @@ SOURCE = r"""
 using namespace svdq_kv;
 struct P {
   const int32_t *q_start, *kv_len;
-  int64_t tokens, table_stride, n_pages;
-  int32_t max_q, max_kv, window, causal, page_shift, group, chunk;
+  int32_t tokens, max_q, max_kv, window, causal, group, chunk;
 };
 int main() {
   long long requests, tokens, q_heads, max_q, max_kv, window, causal, stride, shift, heads, dim, cus, s, e, len;
@@ -39,7 +38,7 @@ int main() {
            (long long)(st ? 0 : most_part_rows(&d, &c, int(cus))));
     if (st == 0) {
       const int32_t start[2] = {int32_t(s), int32_t(e)}, length[1] = {int32_t(len)};
-      const P p = {start, length, tokens, stride, c.n_pages, d.max_q, d.max_kv, d.window, int32_t(causal), int32_t(shift), int32_t(q_heads / heads), t.chunk};
+      const P p = {start, length, t.tokens, d.max_q, t.keys, d.window, int32_t(causal), int32_t(q_heads / heads), t.chunk};
       const Request r(p, 0);
       printf(" %d", r.rows);
       if (r.rows > 0) {
