@@ -61,15 +61,21 @@ __device__ __forceinline__ unsigned cvt_int4(unsigned fp8) {   // bytes 0, 1 (or
   else return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(fp8, 512.0f, HI));
 }
 
-// e8m0 byte in bits 23-30, ready as the converters' scale.  f16: values are
-// held at 2^-3 of their size (so that 6 x 2^15 still fits and 2^-20 x 0.5 is
-// still exact), exponents limited to what f16 can then hold; the missing 2^3
-// is put back on the fp32 sums.
+// e8m0 byte in bits 23-30, ready as the converters' scale.  f16 has 40 binades,
+// the cache's scales 254.  Few rows: Rows16 has bf16 operands for f16, too.  Many
+// rows: values are held at 2^-3 of their size, which is exact for the scales
+// 2^-20 .. 2^15, and the missing 2^3 is put back on the fp32 sums; a workgroup
+// that meets other scales (`off_scale`; a group of zeros has any) does its rows
+// again as Rows16 does.
+__device__ __forceinline__ unsigned f16_scale(unsigned e) { return min(max(e, 107u), 142u); }
+__device__ __forceinline__ unsigned off_scale(unsigned e) { return e ^ f16_scale(e); }   // 0: one that f16 takes
 template <int DT>
 __device__ __forceinline__ float mx_scale(unsigned e) {
-  if constexpr (DT == SVDQ_F16) e = min(max(e, 3u), 142u) - 3u;
+  if constexpr (DT == SVDQ_F16) e = f16_scale(e) - 3u;
   return __uint_as_float(e << 23);
 }
+template <int DT, int FMT>
+constexpr bool checks_scales() { return DT == SVDQ_F16 && FMT == SVDQ_FMT_MXFP4_G32; }
 template <int DT, int FMT>
 constexpr float value_gain() { return DT == SVDQ_F16 && FMT == SVDQ_FMT_MXFP4_G32 ? 8.0f : 1.0f; }
 
@@ -257,12 +263,17 @@ __device__ __forceinline__ u32x4 query_order(u32x4 q) {
   return u32x4{low_halves(q[0], q[1]), low_halves(q[2], q[3]), high_halves(q[0], q[1]), high_halves(q[2], q[3])};
 }
 
-// MXFP4: converter scale of key i and group g
+// MXFP4: exponent and converter scale of key i and group g
+template <int D>
+__device__ __forceinline__ unsigned value_exponent(const u32x4* sc, int i, int g) {
+  const unsigned w = D == 128 ? sc[i / 4][i % 4] : sc[0][i / 2];
+  return (w >> (D == 128 ? 8 * g : 16 * (i % 2) + 8 * g)) & 255u;
+}
 template <int DT, int D>
 __device__ __forceinline__ float value_scale(const u32x4* sc, int i, int g) {
   const unsigned w = D == 128 ? sc[i / 4][i % 4] : sc[0][i / 2];
   const unsigned b = D == 128 ? 8 * g : 16 * (i % 2) + 8 * g;         // bit of the byte
-  if constexpr (DT == SVDQ_F16) return mx_scale<DT>((w >> b) & 255u);
+  if constexpr (DT == SVDQ_F16) return mx_scale<DT>(value_exponent<D>(sc, i, g));
   return __uint_as_float(__builtin_amdgcn_alignbit(w, w, b + 9u) & 0x7F800000u);   // rotated to bits 23-30
 }
 
@@ -330,15 +341,54 @@ __device__ __forceinline__ constexpr int value_col(int n, int x) {
   return 64 * (x / 4) + 8 * (n & 7) + 4 * (n >> 3) + x % 4;
 }
 
+// 16-bit values as two bf16 ones whose sum they are: 8 bits, and the other three
+// of an f16's eleven.
+__device__ __forceinline__ void split_f16(u32x4 x, u32x4* hi, u32x4* lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = h2f<SVDQ_F16>(x[i] & 0xFFFFu), b = h2f<SVDQ_F16>(x[i] >> 16);
+    const unsigned w = pack2<SVDQ_BF16>(a, b);
+    (*hi)[i] = w;
+    (*lo)[i] = pack2<SVDQ_BF16>(a - h2f<SVDQ_BF16>(w & 0xFFFFu), b - __uint_as_float(w & 0xFFFF0000u));
+  }
+}
+
 template <int DT, int FMT, int D>
 struct Rows16 {
   static constexpr int NJ = D / 32, NX = D / 16;
+  // f16 over MXFP4: f16 does not hold all scales of the cache, bf16 does.  The
+  // operands are bf16, of q (exactly) and of the probabilities (to 16 bits) two
+  // each.  48 requests of up to 16384 tokens, 8 heads of 128: 130 us, where f16
+  // operands and scales outside 2^-20 .. 2^15 wrong took 118, and a look at every
+  // scale with a second way for such tiles 131; 20 heads of 64: 223, 201, 266.
+  static constexpr bool TWO = DT == SVDQ_F16 && FMT == SVDQ_FMT_MXFP4_G32;
+  static constexpr int OT = TWO ? SVDQ_BF16 : DT;   // type of the operands
+  static constexpr int LOW = TWO ? NJ * 64 : 1;     // a wave's second terms of q, in LDS
   u32x4 q[NJ];
+  const u32x4* low_q;
   f32x4 o[NX];
   float base, sum;          // reference and this lane's part of the sum
   int low, high;            // keys that this lane's row sees
 
-  __device__ __forceinline__ void clear() {
+  // row: this lane's query row.  negate: the sign of the scale goes to the query,
+  // so that the largest product is the largest logit.
+  // wave_low: LOW pieces of LDS of the wave's own.
+  __device__ __forceinline__ void start(const uint16_t* row, bool negate, int lane, u32x4* wave_low) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) q[j] = query_order<FMT>(*reinterpret_cast<const u32x4*>(row + frag_dim<FMT, D>(j, lane >> 4)));
+    if (negate) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) q[j] ^= 0x80008000u;
+    }
+    if constexpr (TWO) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        u32x4 lo;
+        split_f16(q[j], &q[j], &lo);
+        wave_low[64 * j + lane] = lo;
+      }
+    }
+    low_q = wave_low;
 #pragma unroll
     for (int x = 0; x < NX; ++x) o[x] = f32x4{0, 0, 0, 0};
     base = LOWEST;
@@ -349,15 +399,22 @@ struct Rows16 {
   __device__ __forceinline__ void step(const Tile32<FMT, D>& t, int token, int len, bool all, float c, int lane) {
     const int b = lane >> 4;
     const float zero = hidden_zero();
+    int low_at = lane;
+    if constexpr (TWO) asm volatile("" : "+v"(low_at));     // read here, not kept in registers from tile to tile
     f32x4 s[2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       f32x4 acc = {0, 0, 0, 0};
       if constexpr (FMT == SVDQ_FMT_MXFP4_G32) {
-        const float e = mx_scale<DT>(t.ke[a]);
+        const float e = mx_scale<OT>(t.ke[a]);
+        f32x4 more = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc = mfma16<DT>(key_frag<DT, FMT>(t.k[a][j], e), q[j], acc);
-        s[a] = acc;
+        for (int j = 0; j < NJ; ++j) {
+          const u32x4 f = key_frag<OT, FMT>(t.k[a][j], e);
+          acc = mfma16<OT>(f, q[j], acc);
+          if constexpr (TWO) more = mfma16<OT>(f, low_q[64 * j + low_at], more);
+        }
+        s[a] = TWO ? acc + more : acc;
       } else {
         acc = mfma16<DT>(key_frag<DT, FMT>(t.k[a][0], 0.0f), q[0], acc);
         acc = mfma16<DT>(key_frag<DT, FMT>(t.k[a][1], 0.0f), q[1], acc);
@@ -395,7 +452,7 @@ struct Rows16 {
     for (int i = 1; i < 8; ++i) top = maximum(top, s[i / 4][i % 4]);
     top *= c;
     if constexpr (scaled_reference<DT, FMT>()) top += scale_exponent(most_scale<D>(vsc));
-    top = quad_max(top) - p_shift<DT>();
+    top = quad_max(top) - p_shift<OT>();
     if (__any(top > base + SLACK)) {
       const float next = fmaxf(base, top), alpha = exp2_hw(base - next);
       base = next;
@@ -404,37 +461,46 @@ struct Rows16 {
       for (int x = 0; x < NX; ++x) o[x] *= alpha;
     }
     if constexpr (FMT == SVDQ_FMT_MXFP4_G32) {
-      u32x4 pf;
+      // bf16: the probabilities are rounded to 8 bits, as usual for attention in
+      // bf16: relative error 2.1e-3, of which the result's own rounding is 1.7e-3.
+      // A second term for the rest leaves 1.7e-3 and costs 123 us instead of 118
+      // (heads of 64: 211, 197).
+      u32x4 pf, pl = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p0 = exp2_hw(__builtin_fmaf(s[i / 2][2 * i % 4], c, -base)), p1 = exp2_hw(__builtin_fmaf(s[i / 2][2 * i % 4 + 1], c, -base));
         sum += p0 + p1;
-        pf[i] = pack2<DT>(p0, p1);
+        pf[i] = pack2<OT>(p0, p1);
+        if constexpr (TWO) pl[i] = pack2<OT>(p0 - h2f<OT>(pf[i] & 0xFFFFu), p1 - __uint_as_float(pf[i] & 0xFFFF0000u));
       }
       // keys past the end or on a missing page hold anything, a NaN included:
       // their values must be zero, not only weighted with zero
       float sc[8];
       const int g = D == 128 ? m >> 2 : m >> 3;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sc[i] = value_scale<DT, D>(t.vsc, i, g);
+      for (int i = 0; i < 8; ++i) sc[i] = value_scale<OT, D>(t.vsc, i, g);
       if (!all) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sc[i] = i < last ? sc[i] : 0.0f;
       }
+      auto add = [&](int x, u32x4 f0, u32x4 f1) {
+        o[x] = mfma16<OT>(f0, pf, o[x]);
+        o[x + 1] = mfma16<OT>(f1, pf, o[x + 1]);
+        if constexpr (TWO) {
+          o[x] = mfma16<OT>(f0, pl, o[x]);
+          o[x + 1] = mfma16<OT>(f1, pl, o[x + 1]);
+        }
+      };
       u32x4 f0, f1;
-      value_pair_mx<DT, 0>(t.v, sc, &f0, &f1);
-      o[0] = mfma16<DT>(f0, pf, o[0]);
-      o[1] = mfma16<DT>(f1, pf, o[1]);
-      value_pair_mx<DT, 1>(t.v, sc, &f0, &f1);
-      o[2] = mfma16<DT>(f0, pf, o[2]);
-      o[3] = mfma16<DT>(f1, pf, o[3]);
+      value_pair_mx<OT, 0>(t.v, sc, &f0, &f1);
+      add(0, f0, f1);
+      value_pair_mx<OT, 1>(t.v, sc, &f0, &f1);
+      add(2, f0, f1);
       if constexpr (D == 128) {
-        value_pair_mx<DT, 2>(t.v, sc, &f0, &f1);
-        o[4] = mfma16<DT>(f0, pf, o[4]);
-        o[5] = mfma16<DT>(f1, pf, o[5]);
-        value_pair_mx<DT, 3>(t.v, sc, &f0, &f1);
-        o[6] = mfma16<DT>(f0, pf, o[6]);
-        o[7] = mfma16<DT>(f1, pf, o[7]);
+        value_pair_mx<OT, 2>(t.v, sc, &f0, &f1);
+        add(4, f0, f1);
+        value_pair_mx<OT, 3>(t.v, sc, &f0, &f1);
+        add(6, f0, f1);
       }
     } else {
       // The value scales are on the probabilities, one operand per scale
@@ -498,10 +564,11 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int64_t token, in
 // One workgroup: 16 query rows that share a cache head, one chunk of keys, four
 // waves that take its 32-key tiles in turn and meet in LDS at the end.
 template <int DT, int FMT, int D>
-__global__ __launch_bounds__(256, 3) void k_attn16(AttnParams p) {
-  constexpr int NJ = D / 32, NX = D / 16, PER = D / 16, LD = D + 4;
+__global__ __launch_bounds__(256, D == 64 ? 4 : 3) void k_attn16(AttnParams p) {
+  constexpr int NX = D / 16, PER = D / 16, LD = D + 4;
   __shared__ float so[4][16][LD];
   __shared__ float sb[4][16], ss[4][16];
+  __shared__ u32x4 sq[4 * Rows16<DT, FMT, D>::LOW];
   const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
   // workgroup -> (request, head, row tile, chunk), chunk fastest
   unsigned id = blockIdx.x;
@@ -519,18 +586,9 @@ __global__ __launch_bounds__(256, 3) void k_attn16(AttnParams p) {
   const int row = rt * 16 + m;
   const int qi = min(row / p.group, r.rows - 1), qh = h * p.group + row % p.group;
   Rows16<DT, FMT, D> w;
-  w.clear();
+  w.start(p.q + int64_t(r.first + qi) * p.qt + int64_t(qh) * p.qh, p.c < 0.0f, lane, sq + wave * Rows16<DT, FMT, D>::LOW);
   w.low = r.low(p, qi);
   w.high = row < rows ? r.high(p, qi) : 0;
-  {
-    const uint16_t* q = p.q + int64_t(r.first + qi) * p.qt + int64_t(qh) * p.qh;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) w.q[j] = query_order<FMT>(*reinterpret_cast<const u32x4*>(q + frag_dim<FMT, D>(j, b)));
-    if (p.c < 0.0f) {       // the sign of the scale goes to the query: the largest product is the largest logit
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) w.q[j] ^= 0x80008000u;
-    }
-  }
   const int from = range.chunk_from(p, split), to = range.chunk_to(p, split);
   const int32_t* table = p.table + int64_t(req) * p.table_stride;
   const int last_col = (r.len - 1) >> p.page_shift;
@@ -600,7 +658,7 @@ __global__ __launch_bounds__(256, 3) void k_attn16(AttnParams p) {
   }
   const int64_t tok = int64_t(r.first) + row_o / p.group;
   const int head = h * p.group + row_o % p.group;
-  const float inv = sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int i = 0; i < PER; ++i) f[i] *= inv;
   store_row<DT, D>(p, tok, head, d, f);
@@ -675,6 +733,57 @@ struct Stage {
   u32x4 vsc[D == 128 ? 2 : 1];   // the 8 keys' scales (of a key: D / 32 bytes)
 };
 
+// A wave's 32 rows over the keys [from, to) where f16 does not take every
+// MXFP4 scale of the chunk: 16 at a time, as k_attn16 does them (4608 tokens, 24
+// heads of 128, all workgroups: three times the time).
+template <int D>
+__device__ __forceinline__ void exact_32(const AttnParams& p, const Request& r, int req, int h, int wrow, int rows, int split,
+                                         int from, int to, bool whole, int lane, u32x4* wave_low) {
+  constexpr int DT = SVDQ_F16, FMT = SVDQ_FMT_MXFP4_G32, PER = D / 16;
+  const int m = lane & 15, b = lane >> 4, last_col = (r.len - 1) >> p.page_shift;
+  const int32_t* table = p.table + int64_t(req) * p.table_stride;
+  for (int row0 = wrow; row0 < smaller(rows, wrow + 32); row0 += 16) {
+    const int row = row0 + m, q0 = row0 / p.group, q1 = smaller((row0 + 15) / p.group, r.rows - 1);
+    const int qi = smaller(row / p.group, r.rows - 1), qh = h * p.group + row % p.group;
+    Rows16<DT, FMT, D> w;
+    w.low = r.low(p, qi);
+    w.high = row < rows ? r.high(p, qi) : 0;
+    w.start(p.q + int64_t(r.first + qi) * p.qt + int64_t(qh) * p.qh, p.c < 0.0f, lane, wave_low);
+    const int end = smaller(to, r.high(p, q1)), all_low = r.low(p, q1), all_high = r.high(p, q0);
+    for (int token = larger(from, r.low(p, q0) & ~31); token < end; token += 32) {
+      Tile32<FMT, D> t;
+      const int page = table[smaller(token >> p.page_shift, last_col)];
+      t.load(p, token, page, p.page_shift > 4 ? page : table[smaller((token + 16) >> p.page_shift, last_col)], h, lane);
+      w.step(t, token, r.len, token >= all_low && token + 32 <= all_high && t.ok0 && t.ok1, fabsf(p.c), lane);
+    }
+    const float sum = quad_sum(w.sum);
+    if (row >= rows) continue;
+    const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t tok = int64_t(r.first) + qi, slot = ((int64_t(req) * p.heads + h) * p.row_slots + row) * p.splits + split;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[PER];
+#pragma unroll
+      for (int x = 0; x < PER; ++x) f[x] = w.o[x][i] * inv;
+      const int d = PER * (4 * b + i);             // value_col
+      if (whole) {
+        store_row<DT, D>(p, tok, qh, d, f);
+      } else {
+#pragma unroll
+        for (int x = 0; x < PER; x += 4) *reinterpret_cast<f32x4*>(p.part + slot * D + d + x) = f32x4{f[x], f[x + 1], f[x + 2], f[x + 3]};
+      }
+    }
+    if (b != 0) continue;
+    if (!whole) {
+      float* bs = p.part + int64_t(p.requests) * p.heads * p.row_slots * p.splits * D + slot * 2;
+      bs[0] = w.base;
+      bs[1] = sum;
+    } else if (p.lse) {
+      p.lse[tok * p.q_heads + qh] = row_lse(w.base, sum);
+    }
+  }
+}
+
 template <int DT, int FMT, int D, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   using St = Stage<FMT, D, NW>;
@@ -724,7 +833,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       for (int e = 0; e < NS; ++e) q[e] ^= 0x80008000u;
     }
   }
-  const float c = fabsf(p.c);
+  const float c = fabsf(p.c) * value_gain<DT, FMT>();
   f32x16 o[NX];
 #pragma unroll
   for (int x = 0; x < NX; ++x)
@@ -734,6 +843,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
   // (-infinity until the row has seen a key).
   float base = 0.0f, limit = -__builtin_inff(), sum = 0.0f;
   const float zero = hidden_zero();
+  bool off = false;                     // a scale that f16 does not take has been met
 
   const int from = range.chunk_from(p, split), to = range.chunk_to(p, split);
   const int32_t* table = p.table + int64_t(req) * p.table_stride;
@@ -778,22 +888,39 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     }
   };
   // Keys past the end or on a missing page may hold a NaN: their value scales
-  // become zero (MXFP4: the smallest), before the stage is turned into operands.
+  // become zero (MXFP4: the smallest; f16: one, and the key's), before the stage is
+  // turned into operands.
   auto mend = [&](St& st, int token, unsigned bad) {
     if (bad == 0u && token + KT <= r.len) return;       // the same for all threads
     const bool gone = (bad >> (vkeys / 16)) & 1u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const bool zero = gone || token + vkeys + i >= r.len;
-      if constexpr (D == 128) st.vsc[i / 4][i % 4] = zero ? 0u : st.vsc[i / 4][i % 4];
-      else st.vsc[0][i / 2] = zero ? st.vsc[0][i / 2] & (i % 2 ? 0x0000FFFFu : 0xFFFF0000u) : st.vsc[0][i / 2];
+      constexpr unsigned none = checks_scales<DT, FMT>() ? 0x7F7F7F7Fu : 0u;
+      if constexpr (D == 128) {
+        st.vsc[i / 4][i % 4] = zero ? none : st.vsc[i / 4][i % 4];
+      } else {
+        const unsigned other = i % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+        st.vsc[0][i / 2] = zero ? (st.vsc[0][i / 2] & other) | (none & ~other) : st.vsc[0][i / 2];
+      }
     }
+    if constexpr (checks_scales<DT, FMT>()) st.ke = ((bad >> (kkey / 16)) & 1u) != 0u || token + kkey >= r.len ? 127u : st.ke;
   };
   auto write = [&](const St& st, int buf) {
     // K: key row with bits 2 and 3 exchanged, and an exchange of neighbours by
     // block that spreads the writes over the banks
     const int krow = ((kkey & ~12) | ((kkey & 4) << 1) | ((kkey & 8) >> 1)) ^ (kb << 1);
     const float ks = MX ? mx_scale<DT>(st.ke) : 0.0f;
+    if constexpr (checks_scales<DT, FMT>()) {
+      unsigned any = off_scale(st.ke);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) any += off_scale(value_exponent<D>(st.vsc, i, vn >> 3));
+      if (any != 0u) {                  // of values other than zeros?
+        off |= off_scale(st.ke) != 0u && ((st.k[0] | st.k[1] | st.k[2] | st.k[3]) & 0x77777777u) != 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) off |= off_scale(value_exponent<D>(st.vsc, i, vn >> 3)) != 0u && (st.v[i] & 0x7777u) != 0u;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) sk[buf][(4 * kb + j) * KT + krow] = key_frag<DT, FMT>(st.k[j], ks);
     const int slot = 64 * (vn / 16) + vn % 16;                 // column 4 vn + j: slot + 16 j
@@ -1051,11 +1178,18 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
       buf ^= 1;
     }
   }
+  const bool whole = range.n <= 1;
+  if constexpr (checks_scales<DT, FMT>()) {
+    if (__syncthreads_or(off)) {
+      static_assert(NW * Rows16<DT, FMT, D>::LOW <= NC * KT, "the queries' second terms lie where the keys were");
+      exact_32<D>(p, r, req, h, wrow, rows, split, from, to, whole, lane, sk[0] + wave * Rows16<DT, FMT, D>::LOW);
+      return;
+    }
+  }
   sum = half_sum(sum);
   if (limit < 0.0f) base = LOWEST;
   if (row >= rows) return;
-  const bool whole = range.n <= 1;
-  const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
+  const float inv = !whole ? value_gain<DT, FMT>() : sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
   const int64_t tok = int64_t(r.first) + row / p.group;
   const int head = h * p.group + row % p.group;
   const int64_t slot = ((int64_t(req) * p.heads + h) * p.row_slots + row) * p.splits + split;
@@ -1080,7 +1214,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
 
 // Joins the chunks of a row.  Few chunks: D / 4 lanes a row, several rows a
 // workgroup.
-template <int DT, int FMT, int D, int ROWS>
+template <int DT, int D, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join_few(AttnParams p) {
   constexpr int L = D / 4, G = 256 / L;
   const int64_t slot = int64_t(blockIdx.x) * G + int(threadIdx.x) / L, slots = int64_t(p.requests) * p.heads * p.row_slots;
@@ -1112,7 +1246,7 @@ __global__ __launch_bounds__(256) void k_attn_join_few(AttnParams p) {
   }
   const int64_t tok = int64_t(r.first) + row / p.group;
   const int head = h * p.group + row % p.group;
-  const float inv = sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   *reinterpret_cast<u32x2*>(p.out + tok * p.ot + head * p.oh + d) = u32x2{pack2<DT>(f[0] * inv, f[1] * inv), pack2<DT>(f[2] * inv, f[3] * inv)};
   if (p.lse && d == 0) p.lse[tok * p.q_heads + head] = row_lse(base, sum);
 }
@@ -1120,7 +1254,7 @@ __global__ __launch_bounds__(256) void k_attn_join_few(AttnParams p) {
 // Many chunks: a workgroup a row.  Its threads fetch all references at once,
 // then 1024 / D groups of D / 4 threads walk the chunks and meet in LDS in a
 // fixed order.
-template <int DT, int FMT, int D, int ROWS>
+template <int DT, int D, int ROWS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnParams p) {
   constexpr int L = D / 4, G = 256 / L;
   __shared__ float sw[256];             // weights of 256 chunks
@@ -1178,7 +1312,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnParams p) {
   for (int i = 0; i < G; ++i) { f0 += red[i][2 * tid]; f1 += red[i][2 * tid + 1]; }
   const int64_t tok = int64_t(r.first) + row / p.group;
   const int head = h * p.group + row % p.group;
-  const float inv = sum == 0.0f ? 0.0f : value_gain<DT, FMT>() / sum;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   *reinterpret_cast<unsigned*>(p.out + tok * p.ot + head * p.oh + 2 * tid) = pack2<DT>(f0 * inv, f1 * inv);
   if (p.lse && tid == 0) p.lse[tok * p.q_heads + head] = row_lse(base, sum);
 }
@@ -1206,11 +1340,11 @@ svdq_status check_attn(const svdq_attn_desc* d, const svdq_kv_cache* c) {
   return d->q_heads % c->heads != 0 ? SVDQ_ERR_SHAPE : SVDQ_OK;
 }
 
-template <int DT, int FMT, int D, int ROWS>
+template <int DT, int D, int ROWS>
 void launch_join(const AttnParams& p, const Cut& t, hipStream_t st) {
   const int64_t slots = int64_t(p.requests) * p.heads * t.row_slots;
-  if (t.splits <= 16) k_attn_join_few<DT, FMT, D, ROWS><<<dim3(unsigned(ceil_div(slots, 1024 / D))), 256, 0, st>>>(p);
-  else k_attn_join<DT, FMT, D, ROWS><<<dim3(unsigned(slots)), 256, 0, st>>>(p);
+  if (t.splits <= 16) k_attn_join_few<DT, D, ROWS><<<dim3(unsigned(ceil_div(slots, 1024 / D))), 256, 0, st>>>(p);
+  else k_attn_join<DT, D, ROWS><<<dim3(unsigned(slots)), 256, 0, st>>>(p);
 }
 
 template <int DT, int FMT, int D>
@@ -1218,13 +1352,13 @@ void launch_attn(const AttnParams& p, const Cut& t, hipStream_t st) {
   const dim3 grid(unsigned(t.items * t.splits));
   if (t.rows == 16) {
     k_attn16<DT, FMT, D><<<grid, 256, 0, st>>>(p);
-    if (t.splits > 1) launch_join<DT, FMT, D, 16>(p, t, st);
+    if (t.splits > 1) launch_join<DT, D, 16>(p, t, st);
   } else if (t.rows == 128) {
     k_attn_rows<DT, FMT, D, 4><<<grid, 256, 0, st>>>(p);
-    if (t.splits > 1) launch_join<DT, FMT, D, 128>(p, t, st);
+    if (t.splits > 1) launch_join<DT, D, 128>(p, t, st);
   } else {
     k_attn_rows<DT, FMT, D, 8><<<grid, 512, 0, st>>>(p);
-    if (t.splits > 1) launch_join<DT, FMT, D, 256>(p, t, st);
+    if (t.splits > 1) launch_join<DT, D, 256>(p, t, st);
   }
 }
 
@@ -1284,7 +1418,7 @@ extern "C" svdq_status svdq_kv_attention(const svdq_attn_desc* d, const svdq_hea
   p.page_shift = page_shift(c->page_size);
   p.row_tiles = t.row_tiles; p.row_slots = int32_t(t.row_slots); p.splits = t.splits; p.chunk = t.chunk;
   const bool mx = c->fmt == SVDQ_FMT_MXFP4_G32, bf = d->dtype == SVDQ_BF16;
-  p.c = d->scale * 1.44269504088896341f * (mx && !bf ? 8.0f : 1.0f);
+  p.c = d->scale * 1.44269504088896341f;
   if (p.c == 0.0f) p.c = 1.2e-38f;      // every logit is zero to fp32, and a masked -infinity stays one
   if (bf) {
     if (mx) launch_attn<SVDQ_BF16, SVDQ_FMT_MXFP4_G32>(p, t, c->head_dim, stream);

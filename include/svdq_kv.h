@@ -179,8 +179,9 @@ typedef struct {
  * Products are on the 16-bit matrix cores with fp32 accumulation, softmax
  * statistics are fp32, the probabilities (INT4: times the value scale, or, with
  * bf16 and many rows, they and the values to f16's 11 bits) are rounded to 16
- * bits for the second product.  With f16, MXFP4 scales above 2^15 count as 2^15 and ones
- * below 2^-124 as 2^-124.  ws: >= svdq_kv_attention_workspace
+ * bits for the second product.  The cached values enter the products exactly but for
+ * that, MXFP4 under every scale with f16, too (prompts with scales outside 2^-20 ..
+ * 2^15 take three times as long there).  ws: >= svdq_kv_attention_workspace
  * bytes, 256-byte aligned (may be NULL where that is 0); its content need
  * not be kept between calls.  The size goes by requests, tokens, q_heads,
  * max_q, max_kv and the cache's shape alone, and is enough for every call with

@@ -173,3 +173,76 @@ def test_page_numbers_past_every_cache_give_no_slot(page):
     table = torch.tensor([[1 << 28, -1]], **i32)
     p = kv.plan(torch.tensor([2], **i32), torch.tensor([3], **i32), table, free, torch.tensor([6], **i32), page, 3)
     assert p.slots.tolist() == [-1] * 3
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("fresh,lens", [([1], [1]), ([1, 3], [40, 300]), ([1], [5200]), ([90], [400]), ([90], [2500]), ([200] * 20, [260] * 20)])
+@pytest.mark.parametrize("which", ["small values", "small values in some keys", "small keys", "large keys", "large values", "all"])
+def test_mxfp4_scales_that_f16_does_not_hold(dtype, dim, fresh, lens, which):
+    """f16 has 40 binades, the cache's scales 253: values down to half an f16's
+    last step and up to its end, keys under large and small queries, in all
+    keys and in a few (so that some row tiles and chunks meet them and others
+    do not)."""
+    torch, kv, _ = _mods()
+    group = 2 if len(fresh) < 3 else 3
+    heads = 1 if len(fresh) < 3 else 7
+    q_size = {"small keys": 20000.0, "large keys": 2.0 ** -17}.get(which, 1.5)
+    cache, table, slots, q, start, length = _setup("mxfp4_g32", dtype, dim, 32, heads, group, fresh, lens, q_size=q_size)
+    q.clamp_(-6e4, 6e4)
+    at = slots.long()
+    page, row = at // 32, at % 32
+    ks, vs, vc = (t[page, :, row].clone() for t in (cache.k_scales, cache.v_scales, cache.v_codes))
+    some = torch.arange(at.numel(), device="cuda") % 97 == 0
+    some[:1] = True
+    if which in ("small values", "all"):
+        vs[:] = 127 - 21 - (torch.arange(dim // 32, device="cuda") % 4).byte()
+    if which == "small values in some keys":
+        vs[some] = 127 - 24
+    if which in ("small keys", "all"):
+        ks[:] -= 15 if which == "small keys" else 0
+        ks[some] -= 10
+    if which == "large keys":
+        ks[:] += 17
+    if which in ("large values", "all"):
+        vs[some], vc[some] = 143, 0x91                     # 0.5 and -0.5 times 2^16
+    cache.k_scales[page, :, row], cache.v_scales[page, :, row], cache.v_codes[page, :, row] = ks, vs, vc
+    out, lse = kv.attention(q, cache, table, start, length, max(fresh), max(lens), return_lse=True)
+    k, v = _values64(cache, slots, "mxfp4_g32")
+    few = 1 if len(fresh) > 2 else len(fresh)
+    n, keys = sum(fresh[:few]), sum(lens[:few])
+    ref = _reference(q[:n], k[:keys], v[:keys], fresh[:few], lens[:few], group, True, 0, dim ** -0.5)
+    _check(out[:n], lse[:n], ref, dtype, dim, which)
+
+
+@pytest.mark.parametrize("rows", [1, 90])
+def test_mxfp4_groups_of_zeros_and_scales_next_to_nothing(rows):
+    """All-zero groups have the smallest scale there is, and stand beside
+    ordinary ones."""
+    torch, kv, _ = _mods()
+    cache, table, slots, q, start, length = _setup("mxfp4_g32", "f16", 128, 32, 1, 2, [rows], [200])
+    v = torch.randn((200, 1, 128), device="cuda").half()
+    v[::3] = 0
+    v[:, :, 32:64] = 0
+    cache.append(v, v, slots)
+    k64, v64 = _values64(cache, slots, "mxfp4_g32")
+    out, lse = kv.attention(q, cache, table, start, length, rows, 200, return_lse=True)
+    _check(out, lse, _reference(q, k64, v64, [rows], [200], 2, True, 0, 128 ** -0.5), "f16", 128)
+    assert bool((out[..., 32:64] == 0).all())
+
+
+def test_offsets_that_are_no_offsets():
+    """Request 0 says that it has 2^30 rows: those there are stand before its
+    first token and see nothing; request 1 has none."""
+    torch, kv, _ = _mods()
+    for rows in (2, 34):
+        cache, table, _, q, _, length = _setup("mxfp4_g32", "bf16", 64, 16, 1, 2, [rows, 3], [90, 70])
+        wild = torch.tensor([0, 1 << 30, -5], dtype=torch.int32, device="cuda")
+        out = torch.full_like(q, 3.0)
+        _, lse = kv.attention(q, cache, table, wild, length, rows - 1, 90, out=out, return_lse=True)
+        assert bool((out[:rows - 1] == 0).all()) and bool((out[rows - 1:] == 3.0).all())
+        assert bool((lse[:rows - 1] == -float("inf")).all())
+        for wild in ([-7, -3, 2], [rows + 3, rows + 9, 1 << 30], [5, 2, 2], [-(1 << 31), (1 << 31) - 1, (1 << 31) - 1]):
+            out.fill_(3.0)
+            kv.attention(q, cache, table, torch.tensor(wild, dtype=torch.int32, device="cuda"), length, rows, 90, out=out)
+            assert bool((out == 3.0).all()), wild
