@@ -905,6 +905,16 @@ extern "C" svdq_status svdq_kv_plan(const int32_t* past, const int32_t* fresh, i
   if (!q_start || !free_count || !free_left || !missing || free_left == free_count) return SVDQ_ERR_INVALID_ARG;
   if (requests > 0 && (!past || !fresh || !kv_len || (table_stride > 0 && !block_table))) return SVDQ_ERR_INVALID_ARG;
   if ((tokens > 0 && (!slots || !positions)) || (free_capacity > 0 && !free_pages)) return SVDQ_ERR_INVALID_ARG;
+  // workgroups read the inputs while another writes: no output may be one of them
+  struct Range {
+    uintptr_t from, to;
+    Range(const int32_t* p, int64_t n) : from(reinterpret_cast<uintptr_t>(p)), to(from + 4 * uintptr_t(n < (int64_t(1) << 40) ? n : int64_t(1) << 40)) {}
+  };
+  const int64_t cells = product_below(requests, table_stride, 1, int64_t(1) << 40);
+  for (const Range out : {Range{q_start, requests + 1}, Range{kv_len, requests}, Range{slots, tokens}, Range{positions, tokens},
+                          Range{free_left, 1}, Range{missing, 1}, Range{block_table, cells < 0 ? int64_t(1) << 40 : cells}})
+    for (const Range in : {Range{past, requests}, Range{fresh, requests}, Range{free_pages, free_capacity}, Range{free_count, 1}})
+      if (out.from < in.to && in.from < out.to) return SVDQ_ERR_INVALID_ARG;
   PlanParams p;
   p.past = past; p.fresh = fresh;
   p.free_pages = free_pages; p.free_count = free_count;

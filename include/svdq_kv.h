@@ -138,7 +138,8 @@ svdq_status svdq_kv_read(const svdq_kv_cache* cache, const int32_t* slots, int64
  *               past the sum of fresh: slot -1, position 0
  *   free_left [1]            pages left in the free list
  *   missing [1]              pages that were wanted and not there
- * free_left must not be free_count.  requests <= SVDQ_KV_MAX_REQUESTS.
+ * No output may overlap past, fresh, free_pages or free_count (refused).
+ * requests <= SVDQ_KV_MAX_REQUESTS.
  * Entries of past or fresh below zero count as zero; past[r] + fresh[r] and
  * the sum of fresh stay below 2^31. */
 #define SVDQ_KV_MAX_REQUESTS 8192
