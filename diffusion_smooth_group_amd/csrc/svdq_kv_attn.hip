@@ -135,19 +135,21 @@ __device__ __forceinline__ float row_lse(float base, float sum) {
 // neighbouring keys, MXFP4 after the conversion (each key has its own scale),
 // INT4 before it.  The cache's bytes bound it (136 a key and head of 128): the
 // codes go from memory to registers and are turned there, with two tiles in
-// flight a wave and three waves a SIMD (four with D = 64).  48 requests of up to
-// 16384 tokens, 8 heads of 128, 4 query heads each: MXFP4 114 us, 4.8 TB/s; INT4
-// 129 us (f16 136), where the vector unit is the bound: bits to fp8, conversion,
-// and scales on both sums.  With the converted values paired instead of their
-// codes, and 190 registers, two waves, it took 180.  20 heads of 64 with a query
-// head each: MXFP4 198 us, INT4 208, 3.4 and 3.3 TB/s, the vector unit again (as
-// many instructions for half the bytes a key).  Two row tiles
-// a wave on the same operands were slower for MXFP4 (40 rows: 309 us against 199
-// with three tiles of 16: two waves a SIMD instead of three).
+// flight a wave and three waves a SIMD (four with D = 64).  Times are those of
+// the call, the join of its chunks (5 us) included.  48 requests of up to 16384
+// tokens, 8 heads of 128, 4 query heads each: MXFP4 117 us, 4.6 TB/s (f16 130:
+// Rows16), INT4 133 us (f16 139), where the vector unit is the bound: bits to fp8,
+// conversion, and scales on both sums.  20 heads of 64 with a query head each:
+// MXFP4 197 us (f16 223), INT4 207, 3.4 and 3.3 TB/s, the vector unit again (as
+// many instructions for half the bytes a key).  Measured while it was built, each
+// against the form before it: INT4 with the converted values paired instead of
+// their codes, 190 registers and two waves, 180 us against 133; two row tiles a
+// wave on the same operands, MXFP4, 40 rows, two waves, 309 against 199 with three
+// tiles of 16.
 template <int FMT, int D>
 struct Tile32 {
   static constexpr int NJ = D / 32;
-  static constexpr int NS = FMT == SVDQ_FMT_MXFP4_G32 ? (D == 128 ? 2 : 1) : (D == 128 ? 2 : 1);
+  static constexpr int NS = D / 64;         // 8 keys' scales are 16 bytes a 64 elements in either format
   unsigned k[2][NJ];        // codes of the lane's key row in each K tile
   unsigned ke[2];           // MXFP4: e8m0 of the lane's key rows and group
   u32x4 ksc[NS];            // INT4: fp16 scales of the keys [8b, 8b + 8)
@@ -680,17 +682,21 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 3) void k_attn16(AttnParams p) {
 // multiply-add that takes the reference off.  V, for bf16, goes in times its
 // scales as f16, beside f16 probabilities: two roundings to 11 bits instead of
 // one of the probabilities to 8 (relative error 1.7e-3 against 2.3e-3), and 5 x
-// 2047 rows take 902 us instead of 1017 with the scales on the probabilities.
+// 2047 rows take 852 us where the scales on the probabilities take 931.
 // For f16 that second rounding costs precision (3.4e-4 against 2.8e-4): there
-// the integers go in and the scales stay on the probabilities.
+// the integers go in and the scales stay on the probabilities.  MXFP4: the
+// probabilities are rounded to the type's bits, as usual for attention; a second
+// term for the rest would be half as many matrix instructions again.
 // The matrix products bound it, and the vector work beside them: a matrix
 // instruction keeps the SIMD from issuing vector ones for half its time.  4608
-// tokens, 24 heads of 128, no mask, MXFP4: 262 us, 995 TFLOP/s (a large bf16
+// tokens, 24 heads of 128, no mask, MXFP4: 261 us, 1000 TFLOP/s (a large bf16
 // matrix product: 1250), of which 16% is the second round of 432 workgroups on
-// 256 compute units.  5 x 2047 rows behind up to 8191 tokens, 32 heads over 8:
-// INT4 845 us, 809 TFLOP/s (f16: 960); MXFP4 705, 970.  Tried and slower: the
-// next products under this softmax (281 us), the two waves of a SIMD one phase
-// apart (306), 64 rows a wave (434), no running maximum (282).
+// 256 compute units (f16: 274).  5 x 2047 rows behind up to 8191 tokens, 32 heads
+// over 8: INT4 830 .. 850 us, 815 TFLOP/s (f16: 955); MXFP4 695, 985 (f16: 726).
+// These are calls back to back; one at a time they run 5 to 15% longer, and cards
+// differ by 3%.  Slower when they were tried, against 262 us: the next products
+// under this softmax (281 us), the two waves of a SIMD one phase apart (306), 64
+// rows a wave (434), no running maximum (282).
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
   if constexpr (DT == SVDQ_BF16)
@@ -991,9 +997,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
 
   // Logits of 64 keys of stage `buf` from key `at` of it on.  INT4: in powers of
   // two and less the reference so far, one multiply-add a logit and scale group
-  // (866 us where the reference took one of its own, 905).  MXFP4: as they come
-  // from the product (taken here, before the maximum, the multiply-add that it
-  // needs all the same costs 270 us instead of 262).
+  // (5 x 2047 rows 4% faster than with one of its own for the reference).  MXFP4:
+  // as they come from the product (taken here, before the maximum, the
+  // multiply-add that it needs all the same costs 270 us instead of 262).
   auto logits = [&](int buf, int at, f32x16* s) {
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
@@ -1051,7 +1057,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_rows(AttnParams p) {
     }
     float top = s[0][0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);     // `maximum` was no faster here (INT4 840 us, 834)
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);     // `maximum` is no faster here (INT4 856 us, 852)
     top = half_max(top);
     if constexpr (MX) top = __builtin_fmaf(top, c, -base);
     else top += most;

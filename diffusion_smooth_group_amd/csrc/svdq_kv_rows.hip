@@ -206,7 +206,8 @@ __device__ __forceinline__ void store_quantized(const RowParams& p, int which, i
 // are in flight to cover the loads (two rows a thread: 25.7 us, four 27.6, one
 // 24.8), and streaming stores leave the caches to the angles (27.6 us without).
 // 4608 tokens x (24 + 24) heads of 128, bf16: 23.5 us, 4.9 TB/s, the rate of a
-// large copy.  The append of the same keys and values (MXFP4): 19 us.
+// large copy.  The append of the same keys and values (MXFP4): 19 us; with norm,
+// rotation and the queries in the same launch, 30 us, 4.3 TB/s.
 template <int DT, int L, int FMT>
 __global__ __launch_bounds__(256) void k_rows(RowParams p) {
   const int which = int(blockIdx.y) + p.skip;
@@ -274,6 +275,8 @@ __global__ __launch_bounds__(256) void k_rows(RowParams p) {
 // 6 bytes an element: bound by memory, less closely than the forward because a
 // lane's sums and the next row take 144 registers (three waves a SIMD).  4607
 // tokens x (24 + 24) heads of 128, bf16: 38 us, 4.5 TB/s, and 5 us for the sums.
+// 2048 x (20 + 20) heads of 64, f16: 12 and 4 us, 2.7 TB/s: 640 groups of rows on
+// 384 workgroups are two rounds for some, and the sums cost as much as a row.
 template <int DT, int L>
 __global__ __launch_bounds__(256) void k_rows_grad(RowParams p) {
   const int which = int(blockIdx.y);
@@ -382,9 +385,9 @@ __global__ __launch_bounds__(256) void k_rows_grad(RowParams p) {
   }
 }
 
-// Weight gradient = sum of the partial rows, in a fixed order: 64 groups of 4
-// lanes (16 columns) walk the partials, four loads in flight each, then meet in
-// LDS.
+// Weight gradient = sum of the partial rows, in a fixed order: 64 groups of 16
+// lanes (a column each) walk the partials, four loads in flight each, then meet
+// in LDS.
 __global__ __launch_bounds__(1024) void k_rows_grad_sum(const float* pq, const float* pk, float* dq, float* dk, int parts, int D) {
   const float* part = blockIdx.y == 0 ? pq : pk;
   float* out = blockIdx.y == 0 ? dq : dk;
@@ -577,7 +580,9 @@ struct ReleaseParams {
   int32_t requests, page_shift;
 };
 
-// One workgroup: requests in order, the pages of a request in order.
+// One workgroup: requests in order, the pages of a request in order, which is the
+// order that they have in the list.  Bound by latency, a load of done[r] and then
+// of the table a request: 512 requests, every fourth ended with 63 pages, 127 us.
 __global__ __launch_bounds__(256) void k_release(ReleaseParams p) {
   __shared__ int wave_n[4];
   const int tid = int(threadIdx.x);
@@ -678,8 +683,8 @@ void launch_append(const RowParams& p, int lanes, int64_t rows, int ops, hipStre
 
 // Workgroups an operand: q's and k's together are three a compute unit, as many
 // as the registers hold at once (4607 tokens, 24 heads of 128: 43 us; 512
-// blocks, a second round, 50; 1024 47).  The weight gradients' partial rows, and
-// with them the workspace, go by this number.
+// blocks, a second round, 50; 1024 47; other shapes were not measured).  The
+// weight gradients' partial rows, and with them the workspace, go by this number.
 constexpr int64_t GRAD_BLOCKS = 384;
 int grad_blocks(int64_t rows, int lanes) {
   const int64_t blocks = ceil_div(rows, 256 / lanes);

@@ -90,8 +90,9 @@ svdq_status svdq_qk_norm_rope_backward(const svdq_qk_desc* desc, const svdq_head
  *   scales  [n_pages][heads][page_size][D / G]
  * SVDQ_FMT_MXFP4_G32: E2M1 codes, G = 32, one e8m0 byte per group.
  * SVDQ_FMT_INT4_G64: sign (bit 3) and magnitude (bits 0-2), G = 64, one fp16
- * per group.  Codes and scales follow the quantizers of svdq.h.  Codes are
- * 16-byte aligned, scales 16-byte aligned. */
+ * per group.  Codes and scales follow the quantizers of svdq.h, but the e8m0
+ * byte is at most 252 (2^125), so that every held value is finite in bf16.
+ * Codes are 16-byte aligned, scales 16-byte aligned. */
 typedef struct {
   void *k_codes, *k_scales, *v_codes, *v_scales;
   int64_t n_pages;
@@ -182,7 +183,9 @@ typedef struct {
  * bf16 and many rows, they and the values to f16's 11 bits) are rounded to 16
  * bits for the second product.  The cached values enter the products exactly but for
  * that, MXFP4 under every scale with f16, too (prompts with scales outside 2^-20 ..
- * 2^15 take three times as long there).  ws: >= svdq_kv_attention_workspace
+ * 2^15 take three times as long there).  f16 over INT4: probability times value
+ * scale keeps its 11 bits down to 2^-20 of the largest one among 32 to 64 keys.
+ * ws: >= svdq_kv_attention_workspace
  * bytes, 256-byte aligned (may be NULL where that is 0); its content need
  * not be kept between calls.  The size goes by requests, tokens, q_heads,
  * max_q, max_kv and the cache's shape alone, and is enough for every call with
