@@ -183,8 +183,10 @@ typedef struct {
  * bf16 and many rows, they and the values to f16's 11 bits) are rounded to 16
  * bits for the second product.  The cached values enter the products exactly but for
  * that, MXFP4 under every scale with f16, too (prompts with scales outside 2^-20 ..
- * 2^15 take three times as long there).  f16 over INT4: probability times value
- * scale keeps its 11 bits down to 2^-20 of the largest one among 32 to 64 keys.
+ * 2^15 take three times as long there).  Where the operands of the second product
+ * are f16 (f16 over INT4; many rows: f16, and bf16 over INT4), values up to 2^16 below
+ * others of the request and head, by their scales, are as precise as those; further
+ * below they lose bits.
  * ws: >= svdq_kv_attention_workspace
  * bytes, 256-byte aligned (may be NULL where that is 0); its content need
  * not be kept between calls.  The size goes by requests, tokens, q_heads,

@@ -246,3 +246,57 @@ def test_offsets_that_are_no_offsets():
             out.fill_(3.0)
             kv.attention(q, cache, table, torch.tensor(wild, dtype=torch.int32, device="cuda"), length, rows, 90, out=out)
             assert bool((out == 3.0).all()), wild
+
+
+ROWS = [([1], 300, 1), ([1], 5200, 1), ([90], 400, 1), ([90], 2500, 1), ([200] * 20, 260, 7)]
+
+
+def _bf16_operands(fmt, dtype, fresh):
+    """Of the second product: few rows but f16 over INT4, many in bf16 over MXFP4."""
+    return (fmt, dtype) == ("mxfp4_g32", "bf16") or fresh == [1] and (fmt, dtype) != ("int4_g64", "f16")
+
+
+SPREADS = [(f, t, d, k, e, *r) for f in ("mxfp4_g32", "int4_g64") for t in ("f16", "bf16") for d in (64, 128)
+           for k in ("groups", "keys", "one key", "unlikely key") for e in (16, 21, 26, 31) for r in ROWS
+           if e == 16 or _bf16_operands(f, t, r[0])]
+
+
+@pytest.mark.parametrize("fmt,dtype,dim,kind,apart,fresh,length,heads", SPREADS)
+def test_value_scales_far_apart(fmt, dtype, dim, kind, apart, fresh, length, heads):
+    """Values 2^apart below others: of the other column groups, of most keys, of
+    all keys but one, and beside one key of next to no probability whose values
+    make up for it.  The result is as precise where they count: up to 2^16 in
+    every form, and without a limit where the second product's operands are bf16."""
+    torch, kv, _ = _mods()
+    group = 2
+    lens = [length] * len(fresh)
+    cache, table, slots, q, start, kv_len = _setup(fmt, dtype, dim, 32, heads, group, fresh, lens)
+    at = slots.long()
+    page, row = at // 32, at % 32
+    mx = fmt == "mxfp4_g32"
+    vs = cache.v_scales[page, :, row].clone()              # [tokens, heads, groups]
+    top, step = (138, lambda e: 138 - e) if mx else (2048.0, lambda e: 2048.0 * 2.0 ** -e)
+    low = step(apart)
+    if kind == "groups":
+        vs[..., 0] = top
+        vs[..., 1:] = low
+    elif kind == "keys":
+        vs[:] = low
+        vs[::61] = top
+    else:
+        vs[:] = low
+        vs[length // 3::length] = top
+    if kind == "unlikely key":                             # keys against positive queries: about e^-16 of the others
+        q.copy_(q.abs().clamp_(0.5, 2.0))
+        ks, kc = cache.k_scales[page, :, row].clone(), cache.k_codes[page, :, row].clone()
+        ks[length // 3::length] = 126 if mx else 0.25      # 2^-1 and -3, 1/4 and -6: -1.5 each
+        kc[length // 3::length] = 0xDD if mx else 0xEE
+        if dim == 64:
+            ks[length // 3::length] = 127 if mx else 0.5
+        cache.k_scales[page, :, row], cache.k_codes[page, :, row] = ks, kc
+    cache.v_scales[page, :, row] = vs
+    out, lse = kv.attention(q, cache, table, start, kv_len, max(fresh), length, return_lse=True)
+    k, v = _values64(cache, slots, fmt)
+    n = fresh[0]
+    ref = _reference(q[:n], k[:length], v[:length], fresh[:1], lens[:1], group, True, 0, dim ** -0.5)
+    _check(out[:n], lse[:n], ref, dtype, dim, kind)
