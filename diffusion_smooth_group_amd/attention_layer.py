@@ -55,13 +55,14 @@ class SVDQAttention:
         request's new and cached tokens.  Rows past the last request's (a padded
         step) come out as the projection of zeros.  ws: the attention's workspace, or None
         for one of the call's own."""
-        tokens, d, hq, hk = x.shape[0], self.cache.head_dim, self.q_heads, self.cache.heads
-        rows = self._linear(self.qkv, x).view(tokens, hq + 2 * hk, d)
-        q, k, v = rows[:, :hq], rows[:, hq:hq + hk], rows[:, hq + hk:]
-        self.cache.append(k, v, step.slots, q=q, q_out=q, positions=step.positions, **self.how)
-        o = torch.zeros((tokens, hq, d), dtype=x.dtype, device=x.device)
-        kv.attention(q, self.cache, step.block_table, step.q_start, step.kv_len, max_q, max_kv, causal=self.causal, window=self.window, out=o,
-                     ws=ws)
-        return self._linear(self.out, o.view(tokens, hq * d))
+        with kv._on(None, x):           # the linears, too, launch on the current device
+            tokens, d, hq, hk = x.shape[0], self.cache.head_dim, self.q_heads, self.cache.heads
+            rows = self._linear(self.qkv, x).view(tokens, hq + 2 * hk, d)
+            q, k, v = rows[:, :hq], rows[:, hq:hq + hk], rows[:, hq + hk:]
+            self.cache.append(k, v, step.slots, q=q, q_out=q, positions=step.positions, **self.how)
+            o = torch.zeros((tokens, hq, d), dtype=x.dtype, device=x.device)
+            kv.attention(q, self.cache, step.block_table, step.q_start, step.kv_len, max_q, max_kv, causal=self.causal,
+                         window=self.window, out=o, ws=ws)
+            return self._linear(self.out, o.view(tokens, hq * d))
 
     __call__ = forward

@@ -155,6 +155,29 @@ def test_cache_and_page_sizes_that_do_not_fit_are_refused(devices):
     assert not devices.launches
 
 
+@pytest.mark.parametrize("device", [0, 3])
+def test_the_layers_linears_go_to_its_device(devices, monkeypatch, device):
+    from diffusion_smooth_group_amd.attention_layer import SVDQAttention
+
+    class X:
+        shape, dtype, device = (6, 256), torch.float16, "cpu"
+
+        def get_device(self):
+            return device
+    net = SVDQAttention.__new__(SVDQAttention)
+    net.qkv, net.out, net.q_heads, net.cache, net.how, net.window, net.causal = None, None, 4, cache(device), {}, 0, True
+    seen = []
+
+    def linear(self, layer, x):
+        seen.append(("linear", devices.now))
+        return torch.zeros(6, 8 * 64)
+    monkeypatch.setattr(SVDQAttention, "_linear", linear)
+    net.cache.append = lambda *a, **k: seen.append(("append", devices.now))
+    monkeypatch.setattr(kv, "attention", lambda *a, **k: seen.append(("attention", devices.now)))
+    net(X(), kv.Plan(*[None] * 7), 1, 10)
+    assert seen == [("linear", device), ("append", device), ("attention", device), ("linear", device)] and devices.now == 0
+
+
 # ------------------------------------------------------------------------ autograd
 @pytest.fixture
 def taken(monkeypatch):
