@@ -1,0 +1,1067 @@
+// svdq_image_attn.hip -- gfx950 (MI355X) cross attention to an encoder's 16-bit
+// keys and values, and its gradient (include/svdq_image.h).
+//
+//   s_it = scale q_i . k_t,  p_it = exp(s_it - lse_i),  out_i = sum_t p_it v_t
+//   dv_t = sum_i p_it g_i,   ds_it = p_it (g_i . v_t - delta_i),  delta_i = g_i . out_i
+//   dq_i = scale sum_t ds_it k_t,  dk_t = scale sum_i ds_it q_i
+//
+// A pair is a request and a key head; its rows are (query, head of the group),
+// heads fastest.
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "svdq_image.h"
+#include "svdq_image_cut.h"
+#include "svdq_kv_common.h"
+
+namespace {
+
+using namespace svdq_kv;
+using namespace svdq_image;
+
+struct Rows {               // an operand of heads
+  uint16_t* data;
+  int64_t token, head;
+};
+
+struct CrossParams {
+  Rows q, k, v, out, g, dq, dk, dv;
+  float *lse, *delta, *part, *key_part;
+  const int32_t *q_start, *k_start;
+  const uint8_t* mask;
+  int32_t tokens, states, max_q, max_k, q_heads, heads, group, pairs, D;
+  int32_t row_slots, row_tiles, splits, chunk;
+  int32_t key_tiles, row_splits, row_chunk;
+  float c, scale;           // c = scale log2(e); forward: |scale|, and q's signs are turned
+  unsigned turn;            // bits of two 16-bit values to turn
+};
+
+constexpr float LOWEST = -3.0e38f;   // reference of a row that has seen no key
+constexpr float LOG2E = 1.44269504088896341f;
+constexpr int PAD = 16;              // elements behind each row in LDS: rows 8 (D = 128, 96: 72, 56 words) or 40 words
+                                     // apart modulo 64, so that eight rows' 16 bytes and four rows' 32 lie in banks of their own
+
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (DT == SVDQ_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (DT == SVDQ_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// A block of 16-bit values in LDS, four rows of 16 for every 16 lanes (lane i
+// names row i / 4, columns 4 (i % 4) ..), transposed: lane i gets column i's
+// four rows.
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2 read_turned(const uint16_t* at) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)(at)));
+}
+__device__ __forceinline__ u32x4 joined(u32x2 a, u32x2 b) { return u32x4{a[0], a[1], b[0], b[1]}; }
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// over the two lanes l, l ^ 32, and over the four l, l ^ 16, l ^ 32, l ^ 48
+__device__ __forceinline__ float half_max(float x) {
+  const unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ float quad_max(float x) {
+  const unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return half_max(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  const unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return half_sum(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+}
+
+__device__ __forceinline__ float row_lse(float base, float sum) {
+  return sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0.69314718055994531f;
+}
+
+// A row's reference is raised only when its maximum has passed it by 2^SLACK;
+// between that no accumulator is touched.  f16: probabilities are held at 2^6 of
+// their size, so that f16's subnormals start far below any that counts.
+template <int DT>
+constexpr float p_shift() { return DT == SVDQ_F16 ? 6.0f : 0.0f; }
+constexpr float SLACK = 8.0f;
+
+// f16, gradient: ds is rounded under a power of two, `gain`, that is lowered
+// where the row's (or state's) largest passes 2^15, so that all but what is
+// 2^-21 below the largest of its sum keeps f16's 11 bits.  top: largest |ds|.
+__device__ __forceinline__ float lower_gain(float top) {      // 2^7 / 2^floor(log2 top)
+  return __uint_as_float((261u - (__float_as_uint(top) >> 23)) << 23);
+}
+constexpr float FIRST_GAIN = 0x1p100f, MOST = 0x1p15f;
+constexpr float P_UP = 10.0f;           // f16, gradient of values: probabilities are held at 2^10 of their size
+
+// 16-bit values of the columns of a 32 x 32 result (lane: column lane % 32, rows
+// 8 (i / 4) + 4 (lane / 32) + i % 4) as they are stored: eight neighbouring rows,
+// [16 y + 8 (lane / 32), ..), in w[4 y ..].
+template <int DT>
+__device__ __forceinline__ void columns(const f32x16& o, float by, unsigned* w) {
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const unsigned a0 = pack2<DT>(o[8 * y] * by, o[8 * y + 1] * by), a1 = pack2<DT>(o[8 * y + 2] * by, o[8 * y + 3] * by);
+    const unsigned b0 = pack2<DT>(o[8 * y + 4] * by, o[8 * y + 5] * by), b1 = pack2<DT>(o[8 * y + 6] * by, o[8 * y + 7] * by);
+    const auto s0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+    const auto s1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+    w[4 * y] = s0[0];
+    w[4 * y + 1] = s1[0];
+    w[4 * y + 2] = s0[1];
+    w[4 * y + 3] = s1[1];
+  }
+}
+
+// KT rows of `heads` operands on their way into LDS, NT threads.
+template <int DP, int KT, int NT>
+struct Piece {
+  static constexpr int CH = DP / 8, N = KT * CH / NT;   // 16-byte pieces a row, pieces a thread
+  static constexpr int LD = DP + PAD;
+  static_assert(KT * CH % NT == 0, "whole pieces");
+  u32x4 v[N];
+  static __device__ __forceinline__ int row(int tid, int i) { return (tid + NT * i) / CH; }
+  static __device__ __forceinline__ int col(int tid, int i) { return (tid + NT * i) % CH * 8; }
+  // rows [0, n) of `base`, `stride` elements apart; zeros behind them and from column D on
+  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int n, int D, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = u32x4{0, 0, 0, 0};
+      if (row(tid, i) < n && col(tid, i) < D) v[i] = *reinterpret_cast<const u32x4*>(base + row(tid, i) * stride + col(tid, i));
+    }
+  }
+  __device__ __forceinline__ void write(uint16_t* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + row(tid, i) * LD + col(tid, i)) = v[i];
+  }
+  // rows whose bit in `see` is not set become zeros
+  __device__ __forceinline__ void hide(uint64_t see, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!((see >> row(tid, i)) & 1u)) v[i] = u32x4{0, 0, 0, 0};
+  }
+};
+
+// bit t: state `at` + t of the request is seen, t < 64
+__device__ __forceinline__ uint64_t seen(const CrossParams& p, const CrossRange& r, int at, int lane) {
+  bool on = at + lane < r.keys;
+  if (p.mask && on) on = p.mask[int64_t(r.k_first) + at + lane] != 0;
+  return __ballot(on);
+}
+
+// Largest of 16 logits times nothing else; what is not seen becomes -infinity.
+// see: the 32 keys' bits from the lane half's first on.
+__device__ __forceinline__ void hide16(f32x16& s, unsigned see) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = (see >> (8 * (i / 4) + i % 4)) & 1u ? s[i] : -__builtin_inff();
+}
+
+// ------------------------------------------------------------ forward, many rows
+// 32 rows a wave on 32x32x16: S^T = K Q^T leaves a lane with 16 of 32 keys of
+// one row, two runs of four neighbours for every 16, which is the operand of
+// O^T = V^T P^T as it stands; V^T comes out of LDS by transposing reads of four
+// keys each.
+template <int DT, int DP>
+__global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
+  constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = DP + PAD;
+  __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * LD];
+  __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * LD];
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 31, hb = lane >> 5;
+  const PairWork work(blockIdx.x, p.pairs, p.row_tiles * p.splits);
+  const int tile = work.tile / p.splits, split = work.tile % p.splits, req = work.pair / p.heads, h = work.pair % p.heads;
+  const CrossRange r(p, req);
+  const int rows = r.rows * p.group;
+  if (tile * 128 >= rows) return;
+  const int chunks = (r.keys + p.chunk - 1) / p.chunk;
+  if (split > 0 && split >= chunks) return;
+  const int from = split * p.chunk, to = smaller(r.keys, from + p.chunk);
+  const int row = tile * 128 + wave * 32 + m;
+  const bool active = tile * 128 + wave * 32 < rows;     // of the wave
+  const int64_t tok = int64_t(r.q_first) + (row < rows ? row / p.group : 0);
+  const int head = h * p.group + (row < rows ? row % p.group : 0);
+  u32x4 q[NE];
+#pragma unroll
+  for (int e = 0; e < NE; ++e) {
+    q[e] = u32x4{0, 0, 0, 0};
+    if (row < rows && 16 * e + 8 * hb < p.D) {
+      q[e] = *reinterpret_cast<const u32x4*>(p.q.data + tok * p.q.token + head * p.q.head + 16 * e + 8 * hb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[e][i] ^= p.turn;
+    }
+  }
+  f32x16 o[NX];
+#pragma unroll
+  for (int x = 0; x < NX; ++x)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[x][i] = 0.0f;
+  float base = 0.0f, limit = -__builtin_inff(), sum = 0.0f;
+
+  const uint16_t* kp = p.k.data + (int64_t(r.k_first) + from) * p.k.token + h * p.k.head;
+  const uint16_t* vp = p.v.data + (int64_t(r.k_first) + from) * p.v.token + h * p.v.head;
+  Piece<DP, KT, 256> pk, pv;
+  uint64_t see = 0;
+  if (from < to) {
+    pk.load(kp, p.k.token, to - from, p.D, tid);
+    pv.load(vp, p.v.token, to - from, p.D, tid);
+    see = seen(p, r, from, lane);
+    if (see != ~uint64_t(0)) pv.hide(see, tid);
+    pk.write(sk[0], tid);
+    pv.write(sv[0], tid);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int at = from; at < to; at += KT) {
+    const bool more = at + KT < to;
+    uint64_t next = 0;
+    if (more) {
+      kp += KT * p.k.token;
+      vp += KT * p.v.token;
+      pk.load(kp, p.k.token, to - at - KT, p.D, tid);
+      pv.load(vp, p.v.token, to - at - KT, p.D, tid);
+    }
+    if (see != 0 && active) {
+      f32x16 s[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+          const u32x4 a = *reinterpret_cast<const u32x4*>(&sk[buf][(32 * t + m) * LD + 16 * e + 8 * hb]);
+          s[t] = mfma32<DT>(a, q[e], s[t]);
+        }
+      }
+      if (see != ~uint64_t(0)) {
+        hide16(s[0], unsigned(see) >> (4 * hb));
+        hide16(s[1], unsigned(see >> 32) >> (4 * hb));
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+      top = __builtin_fmaf(half_max(top), p.c, -base);
+      if (__any(top > limit)) {
+        const bool first_keys = limit < 0.0f, some = top > -__builtin_inff();
+        const float up = first_keys ? (some ? top - p_shift<DT>() : 0.0f) : fmaxf(top - p_shift<DT>(), 0.0f);
+        const float alpha = first_keys ? 1.0f : exp2_hw(-up);
+        base += up;
+        limit = first_keys && !some ? limit : p_shift<DT>() + SLACK;
+        sum *= alpha;
+#pragma unroll
+        for (int x = 0; x < NX; ++x) o[x] *= alpha;
+      }
+      u32x4 pf[4];
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        s[i / 16][i % 16] = exp2_hw(__builtin_fmaf(s[i / 16][i % 16], p.c, -base));
+        part += s[i / 16][i % 16];
+      }
+      sum += part;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pf[i / 4][i % 4] = pack2<DT>(s[i / 8][2 * i % 16], s[i / 8][2 * i % 16 + 1]);
+      const int g = lane >> 4, i4 = lane & 15;
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint16_t* b = &sv[buf][(16 * j + 4 * (g >> 1) + (i4 >> 2)) * LD + 32 * x + 16 * (g & 1) + 4 * (i4 & 3)];
+          o[x] = mfma32<DT>(joined(read_turned(b), read_turned(b + 8 * LD)), pf[j], o[x]);
+        }
+      }
+    }
+    if (more) {
+      next = seen(p, r, at + KT, lane);
+      if (next != ~uint64_t(0)) pv.hide(next, tid);
+      pk.write(sk[buf ^ 1], tid);
+      pv.write(sv[buf ^ 1], tid);
+    }
+    see = next;
+    buf ^= 1;
+    __syncthreads();
+  }
+  sum = half_sum(sum);
+  if (limit < 0.0f) base = LOWEST;
+  const bool whole = chunks <= 1;
+  if (whole) {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      unsigned w[8];
+      columns<DT>(o[x], inv, w);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        if (row < rows && 32 * x + 16 * y + 8 * hb < p.D)
+          *reinterpret_cast<u32x4*>(p.out.data + tok * p.out.token + head * p.out.head + 32 * x + 16 * y + 8 * hb) =
+              u32x4{w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]};
+    }
+    if (p.lse && row < rows && hb == 0) p.lse[tok * p.q_heads + head] = row_lse(base, sum);
+    return;
+  }
+  if (row >= rows) return;
+  const int64_t slot = (int64_t(work.pair) * p.row_slots + row) * p.splits + split;
+#pragma unroll
+  for (int x = 0; x < NX; ++x)
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      if (32 * x + 8 * y + 4 * hb < p.D)
+        *reinterpret_cast<f32x4*>(p.part + slot * p.D + 32 * x + 8 * y + 4 * hb) =
+            f32x4{o[x][4 * y], o[x][4 * y + 1], o[x][4 * y + 2], o[x][4 * y + 3]};
+  if (hb == 0)
+    *reinterpret_cast<f32x2*>(p.part + int64_t(p.pairs) * p.row_slots * p.splits * p.D + slot * 2) = f32x2{base, sum};
+}
+
+// ------------------------------------------------------------- forward, few rows
+// 16 rows a workgroup on 16x16x32, 32 keys a wave and step, straight from memory:
+// K as operands, V through a piece of LDS of the wave's own for its transposition.
+// The waves meet at the end.
+template <int DT, int DP>
+__global__ __launch_bounds__(256) void k_cross_few(CrossParams p) {
+  constexpr int NJ = DP / 32, NX = DP / 16, LD = DP + PAD, CH = DP / 8, NV = 32 * CH / 64;
+  __shared__ __attribute__((aligned(16))) uint16_t sv[4][32 * LD];
+  __shared__ float wave_base[4][16], wave_sum[4][16];
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 15, b = lane >> 4;
+  const PairWork work(blockIdx.x, p.pairs, p.row_tiles * p.splits);
+  const int tile = work.tile / p.splits, split = work.tile % p.splits, req = work.pair / p.heads, h = work.pair % p.heads;
+  const CrossRange r(p, req);
+  const int rows = r.rows * p.group;
+  if (tile * 16 >= rows) return;
+  const int chunks = (r.keys + p.chunk - 1) / p.chunk;
+  if (split > 0 && split >= chunks) return;
+  const int from = split * p.chunk, to = smaller(r.keys, from + p.chunk);
+  const int row = tile * 16 + m;
+  u32x4 q[NJ];
+  {
+    const int64_t tok = int64_t(r.q_first) + (row < rows ? row / p.group : 0);
+    const int head = h * p.group + (row < rows ? row % p.group : 0);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      q[j] = u32x4{0, 0, 0, 0};
+      if (row < rows && 32 * j + 8 * b < p.D) {
+        q[j] = *reinterpret_cast<const u32x4*>(p.q.data + tok * p.q.token + head * p.q.head + 32 * j + 8 * b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[j][i] ^= p.turn;
+      }
+    }
+  }
+  f32x4 o[NX];
+#pragma unroll
+  for (int x = 0; x < NX; ++x) o[x] = f32x4{0, 0, 0, 0};
+  float base = 0.0f, limit = -__builtin_inff(), sum = 0.0f;
+  uint16_t* mine = sv[wave];
+  u32x4 kf[2][NJ], vf[NV];
+  bool on = false;
+  auto fetch = [&](int at) {            // keys at .. at + 31, within [from, to)
+    const uint16_t* k = p.k.data + (int64_t(r.k_first) + at) * p.k.token + h * p.k.head;
+    const uint16_t* v = p.v.data + (int64_t(r.k_first) + at) * p.v.token + h * p.v.head;
+    const int n = to - at;
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        kf[a][j] = u32x4{0, 0, 0, 0};
+        if (16 * a + m < n && 32 * j + 8 * b < p.D)
+          kf[a][j] = *reinterpret_cast<const u32x4*>(k + (16 * a + m) * p.k.token + 32 * j + 8 * b);
+      }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int t = (lane + 64 * i) / CH, d = (lane + 64 * i) % CH * 8;
+      vf[i] = u32x4{0, 0, 0, 0};
+      if (t < n && d < p.D) vf[i] = *reinterpret_cast<const u32x4*>(v + t * p.v.token + d);
+    }
+    on = lane < 32 && lane < n;
+    if (p.mask && on) on = p.mask[int64_t(r.k_first) + at + lane] != 0;
+  };
+  int at = from + 32 * wave;
+  if (at < to) fetch(at);
+  for (; at < to; at += 128) {
+    const unsigned see = unsigned(__ballot(on));
+    if (see == 0u) {
+      if (at + 128 < to) fetch(at + 128);
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int t = (lane + 64 * i) / CH, d = (lane + 64 * i) % CH * 8;
+      if (see != ~0u && !((see >> t) & 1u)) vf[i] = u32x4{0, 0, 0, 0};
+      *reinterpret_cast<u32x4*>(mine + t * LD + d) = vf[i];
+    }
+    f32x4 s[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      s[a] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) s[a] = mfma16<DT>(kf[a][j], q[j], s[a]);
+    }
+    if (at + 128 < to) fetch(at + 128);
+    if (see != ~0u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i / 4][i % 4] = (see >> (16 * (i / 4) + 4 * b + i % 4)) & 1u ? s[i / 4][i % 4] : -__builtin_inff();
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i / 4][i % 4]);
+    top = __builtin_fmaf(quad_max(top), p.c, -base);
+    if (__any(top > limit)) {
+      const bool first_keys = limit < 0.0f, some = top > -__builtin_inff();
+      const float up = first_keys ? (some ? top - p_shift<DT>() : 0.0f) : fmaxf(top - p_shift<DT>(), 0.0f);
+      const float alpha = first_keys ? 1.0f : exp2_hw(-up);
+      base += up;
+      limit = first_keys && !some ? limit : p_shift<DT>() + SLACK;
+      sum *= alpha;
+#pragma unroll
+      for (int x = 0; x < NX; ++x) o[x] *= alpha;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[i / 4][i % 4] = exp2_hw(__builtin_fmaf(s[i / 4][i % 4], p.c, -base));
+      sum += s[i / 4][i % 4];
+    }
+    const u32x4 pf = {pack2<DT>(s[0][0], s[0][1]), pack2<DT>(s[0][2], s[0][3]), pack2<DT>(s[1][0], s[1][1]), pack2<DT>(s[1][2], s[1][3])};
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      const uint16_t* t = mine + (4 * b + (m >> 2)) * LD + 16 * x + 4 * (m & 3);
+      o[x] = mfma16<DT>(joined(read_turned(t), read_turned(t + 16 * LD)), pf, o[x]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  sum = quad_sum(sum);
+  if (limit < 0.0f) base = LOWEST;
+  float* mo = reinterpret_cast<float*>(mine);             // [16][DP], what was the wave's V
+#pragma unroll
+  for (int x = 0; x < NX; ++x) *reinterpret_cast<f32x4*>(mo + m * DP + 16 * x + 4 * b) = o[x];
+  if (b == 0) {
+    wave_base[wave][m] = base;
+    wave_sum[wave][m] = sum;
+  }
+  __syncthreads();
+  const bool whole = chunks <= 1;
+  for (int u = tid; u < 16 * DP / 4; u += 256) {
+    const int i = u / (DP / 4), d = u % (DP / 4) * 4, rw = tile * 16 + i;
+    if (rw >= rows || d >= p.D) continue;
+    float top = wave_base[0][i], total = 0.0f;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, wave_base[w][i]);
+    f32x4 f = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float a = exp2_hw(wave_base[w][i] - top);
+      const f32x4 y = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(sv[w]) + i * DP + d);
+      total += a * wave_sum[w][i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] += a * y[e];
+    }
+    const int64_t tok = int64_t(r.q_first) + rw / p.group;
+    const int head = h * p.group + rw % p.group;
+    if (whole) {
+      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+      *reinterpret_cast<u32x2*>(p.out.data + tok * p.out.token + head * p.out.head + d) =
+          u32x2{pack2<DT>(f[0] * inv, f[1] * inv), pack2<DT>(f[2] * inv, f[3] * inv)};
+      if (p.lse && d == 0) p.lse[tok * p.q_heads + head] = row_lse(top, total);
+    } else {
+      const int64_t slot = (int64_t(work.pair) * p.row_slots + rw) * p.splits + split;
+      *reinterpret_cast<f32x4*>(p.part + slot * p.D + d) = f;
+      if (d == 0) *reinterpret_cast<f32x2*>(p.part + int64_t(p.pairs) * p.row_slots * p.splits * p.D + slot * 2) = f32x2{top, total};
+    }
+  }
+}
+
+// Joins a row's chunks: a wave a row, 32 lanes for its columns, the two halves
+// take every other chunk.  GRAD: partial rows of dq, which are only added.
+template <int DT, bool GRAD>
+__global__ __launch_bounds__(256) void k_cross_join(CrossParams p) {
+  const int lane = int(threadIdx.x) & 63;
+  const int64_t slot = int64_t(blockIdx.x) * 4 + (int(threadIdx.x) >> 6), slots = int64_t(p.pairs) * p.row_slots;
+  if (slot >= slots) return;
+  const int pair = int(slot / p.row_slots), row = int(slot % p.row_slots);
+  const CrossRange r(p, pair / p.heads);
+  if (row >= r.rows * p.group) return;
+  const int n = (r.keys + p.chunk - 1) / p.chunk;
+  if (n <= 1) return;
+  const int d = (lane & 31) * 4, half = lane >> 5;
+  const int64_t at = slot * p.splits;
+  const float* y = p.part + at * p.D + (d < p.D ? d : 0);
+  f32x4 f = {0, 0, 0, 0};
+  float top = LOWEST, total = 0.0f;
+  if constexpr (!GRAD) {
+    const f32x2* bs = reinterpret_cast<const f32x2*>(p.part + slots * p.splits * p.D) + at;
+    for (int i = lane; i < n; i += 64) top = fmaxf(top, bs[i][0]);
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
+#pragma unroll 4
+    for (int i = half; i < n; i += 2) {
+      const f32x2 v = bs[i];
+      const f32x4 u = *reinterpret_cast<const f32x4*>(y + int64_t(i) * p.D);
+      const float a = exp2_hw(v[0] - top);
+      total += a * v[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] += a * u[e];
+    }
+    total = half_sum(total);
+  } else {
+#pragma unroll 4
+    for (int i = half; i < n; i += 2) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(y + int64_t(i) * p.D);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] += u[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = half_sum(f[e]);
+  if (half != 0 || d >= p.D) return;
+  const int64_t tok = int64_t(r.q_first) + row / p.group;
+  const int head = pair % p.heads * p.group + row % p.group;
+  const float inv = GRAD ? 1.0f : total == 0.0f ? 0.0f : 1.0f / total;
+  const Rows& to = GRAD ? p.dq : p.out;
+  *reinterpret_cast<u32x2*>(to.data + tok * to.token + head * to.head + d) =
+      u32x2{pack2<DT>(f[0] * inv, f[1] * inv), pack2<DT>(f[2] * inv, f[3] * inv)};
+  if (!GRAD && p.lse && d == 0) p.lse[tok * p.q_heads + head] = row_lse(top, total);
+}
+
+// --------------------------------------------------------------- gradient of q
+// As k_cross_rows, with dP^T = V G^T beside S^T; dQ^T += K^T dS^T, K^T by
+// transposing reads.  Leaves delta for k_cross_dkv.
+template <int DT, int DP>
+__global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
+  constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = DP + PAD;
+  __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * LD];
+  __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * LD];
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 31, hb = lane >> 5;
+  const PairWork work(blockIdx.x, p.pairs, p.row_tiles * p.splits);
+  const int tile = work.tile / p.splits, split = work.tile % p.splits, req = work.pair / p.heads, h = work.pair % p.heads;
+  const CrossRange r(p, req);
+  const int rows = r.rows * p.group;
+  if (tile * 128 >= rows) return;
+  const int chunks = (r.keys + p.chunk - 1) / p.chunk;
+  if (split > 0 && split >= chunks) return;
+  const int from = split * p.chunk, to = smaller(r.keys, from + p.chunk);
+  const int row = tile * 128 + wave * 32 + m;
+  const bool active = tile * 128 + wave * 32 < rows;
+  const int64_t tok = int64_t(r.q_first) + (row < rows ? row / p.group : 0);
+  const int head = h * p.group + (row < rows ? row % p.group : 0);
+  u32x4 q[NE], g[NE];
+  float delta = 0.0f;
+#pragma unroll
+  for (int e = 0; e < NE; ++e) {
+    q[e] = g[e] = u32x4{0, 0, 0, 0};
+    const int d = 16 * e + 8 * hb;
+    if (row < rows && d < p.D) {
+      q[e] = *reinterpret_cast<const u32x4*>(p.q.data + tok * p.q.token + head * p.q.head + d);
+      g[e] = *reinterpret_cast<const u32x4*>(p.g.data + tok * p.g.token + head * p.g.head + d);
+      const u32x4 y = *reinterpret_cast<const u32x4*>(p.out.data + tok * p.out.token + head * p.out.head + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        delta = __builtin_fmaf(h2f<DT>(g[e][i] & 0xFFFFu), h2f<DT>(y[i] & 0xFFFFu), delta);
+        delta = __builtin_fmaf(h2f<DT>(g[e][i] >> 16), h2f<DT>(y[i] >> 16), delta);
+      }
+    }
+  }
+  delta = half_sum(delta);
+  float lse = __builtin_inff();
+  if (row < rows) {
+    const float l = p.lse[tok * p.q_heads + head];
+    lse = l == -__builtin_inff() ? __builtin_inff() : l * LOG2E;
+    if (split == 0 && hb == 0) p.delta[tok * p.q_heads + head] = delta;
+  }
+  f32x16 acc[NX];
+#pragma unroll
+  for (int x = 0; x < NX; ++x)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[x][i] = 0.0f;
+  float gain = FIRST_GAIN;
+
+  const uint16_t* kp = p.k.data + (int64_t(r.k_first) + from) * p.k.token + h * p.k.head;
+  const uint16_t* vp = p.v.data + (int64_t(r.k_first) + from) * p.v.token + h * p.v.head;
+  Piece<DP, KT, 256> pk, pv;
+  uint64_t see = 0;
+  if (from < to) {
+    pk.load(kp, p.k.token, to - from, p.D, tid);
+    pv.load(vp, p.v.token, to - from, p.D, tid);
+    see = seen(p, r, from, lane);
+    if (see != ~uint64_t(0)) { pk.hide(see, tid); pv.hide(see, tid); }
+    pk.write(sk[0], tid);
+    pv.write(sv[0], tid);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int at = from; at < to; at += KT) {
+    const bool more = at + KT < to;
+    uint64_t next = 0;
+    if (more) {
+      kp += KT * p.k.token;
+      vp += KT * p.v.token;
+      pk.load(kp, p.k.token, to - at - KT, p.D, tid);
+      pv.load(vp, p.v.token, to - at - KT, p.D, tid);
+    }
+    if (see != 0 && active) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x16 s, dp;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+          s = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sk[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), q[e], s);
+          dp = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sv[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), g[e], dp);
+        }
+        const unsigned bits = t ? unsigned(see >> 32) : unsigned(see);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[i] = exp2_hw(__builtin_fmaf(s[i], p.c, -lse)) * (dp[i] - delta);
+        if (bits != ~0u) {
+          const unsigned mybits = bits >> (4 * hb);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dp[i] = (mybits >> (8 * (i / 4) + i % 4)) & 1u ? dp[i] : 0.0f;
+        }
+        if constexpr (DT == SVDQ_F16) {
+          float top = __builtin_fabsf(dp[0]);
+#pragma unroll
+          for (int i = 1; i < 16; ++i) top = fmaxf(top, __builtin_fabsf(dp[i]));
+          top = half_max(top);
+          const bool over = top * gain > MOST;
+          if (__any(over)) {
+            const float lower = over ? lower_gain(top) : gain, by = lower / gain;
+            gain = lower;
+#pragma unroll
+            for (int x = 0; x < NX; ++x) acc[x] *= by;
+          }
+          dp *= gain;
+        }
+        u32x4 ds[2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ds[i / 4][i % 4] = pack2<DT>(dp[2 * i], dp[2 * i + 1]);
+        const int gr = lane >> 4, i4 = lane & 15;
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint16_t* b = &sk[buf][(32 * t + 16 * j + 4 * (gr >> 1) + (i4 >> 2)) * LD + 32 * x + 16 * (gr & 1) + 4 * (i4 & 3)];
+            acc[x] = mfma32<DT>(joined(read_turned(b), read_turned(b + 8 * LD)), ds[j], acc[x]);
+          }
+        }
+      }
+    }
+    if (more) {
+      next = seen(p, r, at + KT, lane);
+      if (next != ~uint64_t(0)) { pk.hide(next, tid); pv.hide(next, tid); }
+      pk.write(sk[buf ^ 1], tid);
+      pv.write(sv[buf ^ 1], tid);
+    }
+    see = next;
+    buf ^= 1;
+    __syncthreads();
+  }
+  const float by = DT == SVDQ_F16 ? p.scale / gain : p.scale;
+  if (chunks <= 1) {
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      unsigned w[8];
+      columns<DT>(acc[x], by, w);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        if (row < rows && 32 * x + 16 * y + 8 * hb < p.D)
+          *reinterpret_cast<u32x4*>(p.dq.data + tok * p.dq.token + head * p.dq.head + 32 * x + 16 * y + 8 * hb) =
+              u32x4{w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]};
+    }
+    return;
+  }
+  if (row >= rows) return;
+  const int64_t slot = (int64_t(work.pair) * p.row_slots + row) * p.splits + split;
+#pragma unroll
+  for (int x = 0; x < NX; ++x)
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      if (32 * x + 8 * y + 4 * hb < p.D)
+        *reinterpret_cast<f32x4*>(p.part + slot * p.D + 32 * x + 8 * y + 4 * hb) =
+            f32x4{acc[x][4 * y] * by, acc[x][4 * y + 1] * by, acc[x][4 * y + 2] * by, acc[x][4 * y + 3] * by};
+}
+
+// -------------------------------------------------------- gradient of k and v
+// 32 keys a wave, whose K and V stay in registers as operands, 128 a workgroup;
+// rows pass by in LDS, 64 a stage.  S = Q K^T leaves a lane with 16 rows of one
+// key: the operand of dV^T += G^T P and dK^T += Q^T dS, G^T and Q^T by
+// transposing reads.  A key that is not seen spoils only its own lane's sums,
+// which are not stored.
+template <int DT, int DP>
+__global__ __launch_bounds__(256, DP == 64 ? 2 : 1) void k_cross_dkv(CrossParams p) {
+  constexpr int RT = 64, NE = DP / 16, NX = DP / 32, LD = DP + PAD, CH = DP / 8, NP = RT * CH / 256;
+  __shared__ __attribute__((aligned(16))) uint16_t sq[2][RT * LD];
+  __shared__ __attribute__((aligned(16))) uint16_t sg[2][RT * LD];
+  __shared__ __attribute__((aligned(16))) float sl[2][RT], sd[2][RT];
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 31, hb = lane >> 5;
+  const PairWork work(blockIdx.x, p.pairs, p.key_tiles * p.row_splits);
+  const int tile = work.tile / p.row_splits, split = work.tile % p.row_splits, req = work.pair / p.heads, h = work.pair % p.heads;
+  const CrossRange r(p, req);
+  if (tile * KEY_TILE >= r.keys) return;
+  const int rows = r.rows * p.group, chunks = (rows + p.row_chunk - 1) / p.row_chunk;
+  if (split > 0 && split >= chunks) return;
+  const int from = split * p.row_chunk, to = smaller(rows, from + p.row_chunk);
+  const int key = tile * KEY_TILE + wave * 32 + m;
+  const bool active = tile * KEY_TILE + wave * 32 < r.keys, held = key < r.keys;
+  const int64_t state = int64_t(r.k_first) + (held ? key : 0);
+  const bool shown = held && (!p.mask || p.mask[state] != 0);
+  u32x4 k[NE], v[NE];
+#pragma unroll
+  for (int e = 0; e < NE; ++e) {
+    k[e] = v[e] = u32x4{0, 0, 0, 0};
+    const int d = 16 * e + 8 * hb;
+    if (shown && d < p.D) {
+      k[e] = *reinterpret_cast<const u32x4*>(p.k.data + state * p.k.token + h * p.k.head + d);
+      v[e] = *reinterpret_cast<const u32x4*>(p.v.data + state * p.v.token + h * p.v.head + d);
+    }
+  }
+  f32x16 dk[NX], dv[NX];
+#pragma unroll
+  for (int x = 0; x < NX; ++x)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dk[x][i] = dv[x][i] = 0.0f;
+  float gain = FIRST_GAIN;
+
+  u32x4 vq[NP], vg[NP];
+  float l = 0.0f, dl = 0.0f;
+  auto fetch = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int rw = at + (tid + 256 * i) / CH, d = (tid + 256 * i) % CH * 8;
+      vq[i] = vg[i] = u32x4{0, 0, 0, 0};
+      if (rw < to && d < p.D) {
+        const int64_t tok = int64_t(r.q_first) + rw / p.group;
+        const int head = h * p.group + rw % p.group;
+        vq[i] = *reinterpret_cast<const u32x4*>(p.q.data + tok * p.q.token + head * p.q.head + d);
+        vg[i] = *reinterpret_cast<const u32x4*>(p.g.data + tok * p.g.token + head * p.g.head + d);
+      }
+    }
+    if (tid < RT) {
+      l = __builtin_inff();
+      dl = 0.0f;
+      const int rw = at + tid;
+      if (rw < to) {
+        const int64_t i = (int64_t(r.q_first) + rw / p.group) * p.q_heads + h * p.group + rw % p.group;
+        const float y = p.lse[i];
+        if (y != -__builtin_inff()) l = y * LOG2E - (DT == SVDQ_F16 ? P_UP : 0.0f);
+        dl = p.delta[i];
+      }
+    }
+  };
+  auto write = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int at = (tid + 256 * i) / CH * LD + (tid + 256 * i) % CH * 8;
+      *reinterpret_cast<u32x4*>(&sq[buf][at]) = vq[i];
+      *reinterpret_cast<u32x4*>(&sg[buf][at]) = vg[i];
+    }
+    if (tid < RT) {
+      sl[buf][tid] = l;
+      sd[buf][tid] = dl;
+    }
+  };
+  if (from < to) {
+    fetch(from);
+    write(0);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int at = from; at < to; at += RT) {
+    const bool more = at + RT < to;
+    if (more) fetch(at + RT);
+    if (active) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x16 s, dp;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+          s = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sq[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), k[e], s);
+          dp = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sg[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), v[e], dp);
+        }
+        u32x4 pf[2], ds[2];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const f32x4 ll = *reinterpret_cast<const f32x4*>(&sl[buf][32 * t + 8 * y + 4 * hb]);
+          const f32x4 dd = *reinterpret_cast<const f32x4*>(&sd[buf][32 * t + 8 * y + 4 * hb]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[4 * y + i] = exp2_hw(__builtin_fmaf(s[4 * y + i], p.c, -ll[i]));
+            dp[4 * y + i] = s[4 * y + i] * (dp[4 * y + i] - dd[i]);
+          }
+        }
+        if constexpr (DT == SVDQ_F16) {
+          float top = __builtin_fabsf(dp[0]);
+#pragma unroll
+          for (int i = 1; i < 16; ++i) top = fmaxf(top, __builtin_fabsf(dp[i]));
+          top = half_max(top);
+          const bool over = top * gain > MOST;
+          if (__any(over)) {
+            const float lower = over ? lower_gain(top) : gain, by = lower / gain;
+            gain = lower;
+#pragma unroll
+            for (int x = 0; x < NX; ++x) dk[x] *= by;
+          }
+          dp *= gain;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          pf[i / 4][i % 4] = pack2<DT>(s[2 * i], s[2 * i + 1]);
+          ds[i / 4][i % 4] = pack2<DT>(dp[2 * i], dp[2 * i + 1]);
+        }
+        const int gr = lane >> 4, i4 = lane & 15;
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int b = (32 * t + 16 * j + 4 * (gr >> 1) + (i4 >> 2)) * LD + 32 * x + 16 * (gr & 1) + 4 * (i4 & 3);
+            dv[x] = mfma32<DT>(joined(read_turned(&sg[buf][b]), read_turned(&sg[buf][b + 8 * LD])), pf[j], dv[x]);
+            dk[x] = mfma32<DT>(joined(read_turned(&sq[buf][b]), read_turned(&sq[buf][b + 8 * LD])), ds[j], dk[x]);
+          }
+        }
+      }
+    }
+    if (more) write(buf ^ 1);
+    buf ^= 1;
+    __syncthreads();
+  }
+  if (!active) return;
+  const float kby = DT == SVDQ_F16 ? p.scale / gain * 0x1p-10f : p.scale, vby = DT == SVDQ_F16 ? 0x1p-10f : 1.0f;
+  if (!shown) {
+#pragma unroll
+    for (int x = 0; x < NX; ++x)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dk[x][i] = dv[x][i] = 0.0f;
+  }
+  if (chunks <= 1) {
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      unsigned wk[8], wv[8];
+      columns<DT>(dk[x], shown ? kby : 0.0f, wk);
+      columns<DT>(dv[x], vby, wv);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int d = 32 * x + 16 * y + 8 * hb;
+        if (held && d < p.D) {
+          *reinterpret_cast<u32x4*>(p.dk.data + state * p.dk.token + h * p.dk.head + d) = u32x4{wk[4 * y], wk[4 * y + 1], wk[4 * y + 2], wk[4 * y + 3]};
+          *reinterpret_cast<u32x4*>(p.dv.data + state * p.dv.token + h * p.dv.head + d) = u32x4{wv[4 * y], wv[4 * y + 1], wv[4 * y + 2], wv[4 * y + 3]};
+        }
+      }
+    }
+    return;
+  }
+  if (!held) return;
+  // [pair][split][key of the tiles][2][D]
+  float* to_part = p.key_part + ((int64_t(work.pair) * p.row_splits + split) * (int64_t(p.key_tiles) * KEY_TILE) + key) * 2 * p.D;
+#pragma unroll
+  for (int x = 0; x < NX; ++x)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int d = 32 * x + 8 * y + 4 * hb;
+      if (d < p.D) {
+        const float by = shown ? kby : 0.0f;
+        *reinterpret_cast<f32x4*>(to_part + d) = f32x4{dk[x][4 * y] * by, dk[x][4 * y + 1] * by, dk[x][4 * y + 2] * by, dk[x][4 * y + 3] * by};
+        *reinterpret_cast<f32x4*>(to_part + p.D + d) = f32x4{dv[x][4 * y] * vby, dv[x][4 * y + 1] * vby, dv[x][4 * y + 2] * vby, dv[x][4 * y + 3] * vby};
+      }
+    }
+}
+
+// Adds the chunks of a key's gradients: a wave a key, the lower half dk, the
+// upper dv.
+template <int DT>
+__global__ __launch_bounds__(256) void k_cross_key_join(CrossParams p) {
+  const int lane = int(threadIdx.x) & 63, width = p.key_tiles * KEY_TILE;
+  const int64_t slot = int64_t(blockIdx.x) * 4 + (int(threadIdx.x) >> 6);
+  if (slot >= int64_t(p.pairs) * width) return;
+  const int pair = int(slot / width), key = int(slot % width);
+  const CrossRange r(p, pair / p.heads);
+  if (key >= r.keys) return;
+  const int n = (r.rows * p.group + p.row_chunk - 1) / p.row_chunk;
+  if (n <= 1) return;
+  const int d = (lane & 31) * 4, half = lane >> 5;
+  if (d >= p.D) return;
+  const float* y = p.key_part + (int64_t(pair) * p.row_splits * width + key) * 2 * p.D + half * p.D + d;
+  f32x4 f = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const f32x4 u = *reinterpret_cast<const f32x4*>(y + int64_t(i) * width * 2 * p.D);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] += u[e];
+  }
+  const Rows& to = half ? p.dv : p.dk;
+  *reinterpret_cast<u32x2*>(to.data + (int64_t(r.k_first) + key) * to.token + pair % p.heads * to.head + d) =
+      u32x2{pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3])};
+}
+
+// ---------------------------------------------------------------- host side
+int device_cus() {
+  static std::atomic<int> cus[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  int v = cus[dev].load(std::memory_order_relaxed);
+  if (v <= 0) {
+    if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0) v = 256;
+    cus[dev].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
+svdq_status check_cross(const svdq_cross_desc* d, int q_heads, int k_heads) {
+  if (!d || d->requests < 0 || d->tokens < 0 || d->states < 0 || !dtype_ok(d->dtype) || d->max_q < 0 || d->max_k < 0 || q_heads < 1 ||
+      k_heads < 1 || !(d->scale - d->scale == 0.0f))
+    return SVDQ_ERR_INVALID_ARG;
+  if (d->head_dim < 8 || d->head_dim % 8 != 0 || q_heads % k_heads != 0) return SVDQ_ERR_SHAPE;
+  if (d->head_dim > 128) return SVDQ_ERR_UNSUPPORTED;
+  if (d->requests >= (int64_t(1) << 30) || d->tokens >= (int64_t(1) << 31) - 512 || d->states >= (int64_t(1) << 31) - 512)
+    return SVDQ_ERR_UNSUPPORTED;
+  if (!d->q_start && d->tokens != d->requests * d->max_q) return SVDQ_ERR_SHAPE;
+  if (!d->k_start && d->states != d->requests * d->max_k) return SVDQ_ERR_SHAPE;
+  return SVDQ_OK;
+}
+
+Rows rows_of(const svdq_heads* h) { return Rows{static_cast<uint16_t*>(h->data), h->token_stride, h->head_stride}; }
+
+svdq_status check_scratch(const void* ws, size_t have, size_t need) {
+  if (need == 0) return SVDQ_OK;
+  if (!ws) return SVDQ_ERR_INVALID_ARG;
+  if (have < need) return SVDQ_ERR_CAPACITY;
+  return aligned(ws, 256) ? SVDQ_OK : SVDQ_ERR_INVALID_ARG;
+}
+
+CrossParams params_of(const svdq_cross_desc* d, const CrossCut& t, int q_heads, int k_heads) {
+  CrossParams p = {};
+  p.q_start = d->q_start; p.k_start = d->k_start; p.mask = d->mask;
+  p.tokens = t.tokens; p.states = t.states; p.max_q = d->max_q; p.max_k = d->max_k;
+  p.q_heads = q_heads; p.heads = k_heads; p.group = t.group; p.pairs = t.pairs; p.D = d->head_dim;
+  p.row_slots = t.row_slots; p.row_tiles = t.row_tiles; p.splits = t.splits; p.chunk = t.chunk;
+  p.key_tiles = t.key_tiles; p.row_splits = t.row_splits; p.row_chunk = t.row_chunk;
+  p.scale = d->scale;
+  p.c = d->scale * LOG2E;
+  return p;
+}
+
+template <int DT, int DP>
+void launch_forward(const CrossParams& p, const CrossCut& t, hipStream_t st) {
+  const dim3 grid(unsigned(t.pairs) * unsigned(t.row_tiles) * unsigned(t.splits));
+  if (t.rows == 16) k_cross_few<DT, DP><<<grid, 256, 0, st>>>(p);
+  else k_cross_rows<DT, DP><<<grid, 256, 0, st>>>(p);
+  if (t.splits > 1) k_cross_join<DT, false><<<dim3(unsigned(ceil_div(int64_t(t.pairs) * t.row_slots, 4))), 256, 0, st>>>(p);
+}
+
+template <int DT, int DP>
+void launch_backward(const CrossParams& p, const CrossCut& t, hipStream_t st) {
+  if (t.row_tiles > 0) {
+    k_cross_dq<DT, DP><<<dim3(unsigned(t.pairs) * unsigned(t.row_tiles) * unsigned(t.splits)), 256, 0, st>>>(p);
+    if (t.splits > 1) k_cross_join<DT, true><<<dim3(unsigned(ceil_div(int64_t(t.pairs) * t.row_slots, 4))), 256, 0, st>>>(p);
+  }
+  if (t.key_tiles == 0) return;
+  k_cross_dkv<DT, DP><<<dim3(unsigned(t.pairs) * unsigned(t.key_tiles) * unsigned(t.row_splits)), 256, 0, st>>>(p);
+  if (t.row_splits > 1)
+    k_cross_key_join<DT><<<dim3(unsigned(int64_t(t.pairs) * t.key_tiles * (KEY_TILE / 4))), 256, 0, st>>>(p);
+}
+
+template <int DT>
+void launch(const CrossParams& p, const CrossCut& t, bool grad, hipStream_t st) {
+  if (p.D <= 64) grad ? launch_backward<DT, 64>(p, t, st) : launch_forward<DT, 64>(p, t, st);
+  else if (p.D <= 96) grad ? launch_backward<DT, 96>(p, t, st) : launch_forward<DT, 96>(p, t, st);
+  else grad ? launch_backward<DT, 128>(p, t, st) : launch_forward<DT, 128>(p, t, st);
+}
+
+}  // namespace
+
+extern "C" svdq_status svdq_cross_attention_workspace(const svdq_cross_desc* d, int32_t q_heads, int32_t k_heads, size_t* bytes) {
+  svdq_status st = check_cross(d, q_heads, k_heads);
+  if (st != SVDQ_OK) return st;
+  if (!bytes) return SVDQ_ERR_INVALID_ARG;
+  CrossCut t;
+  if ((st = cross_cut(d, q_heads, k_heads, device_cus(), false, &t)) != SVDQ_OK) return st;
+  *bytes = size_t(cross_part_floats(d, t, false)) * 4;
+  return SVDQ_OK;
+}
+
+extern "C" svdq_status svdq_cross_attention(const svdq_cross_desc* d, const svdq_heads* q, const svdq_heads* k, const svdq_heads* v,
+                                            const svdq_heads* out, float* lse, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!q || !k || !v || !out) return SVDQ_ERR_INVALID_ARG;
+  svdq_status st = check_cross(d, q->heads, k->heads);
+  if (st != SVDQ_OK) return st;
+  if (v->heads != k->heads || out->heads != q->heads) return SVDQ_ERR_SHAPE;
+  if (d->requests == 0 || d->tokens == 0 || d->max_q == 0) return SVDQ_OK;
+  CrossCut t;
+  if ((st = cross_cut(d, q->heads, k->heads, device_cus(), false, &t)) != SVDQ_OK) return st;
+  for (const svdq_heads* h : {q, out})
+    if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
+  if (d->states > 0)                    // without states there need be none
+    for (const svdq_heads* h : {k, v})
+      if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
+  if ((st = check_scratch(ws, ws_bytes, size_t(cross_part_floats(d, t, false)) * 4)) != SVDQ_OK) return st;
+  CrossParams p = params_of(d, t, q->heads, k->heads);
+  p.q = rows_of(q); p.k = rows_of(k); p.v = rows_of(v); p.out = rows_of(out);
+  p.lse = lse;
+  p.part = static_cast<float*>(ws);
+  if (p.c < 0.0f) {                     // so that a row's largest logit is that of its largest product
+    p.c = -p.c;
+    p.turn = 0x80008000u;
+  }
+  if (p.c == 0.0f) p.c = 1.2e-38f;      // every logit is zero to fp32, and a hidden -infinity stays one
+  if (d->dtype == SVDQ_BF16) launch<SVDQ_BF16>(p, t, false, stream);
+  else launch<SVDQ_F16>(p, t, false, stream);
+  return launch_ok();
+}
+
+extern "C" svdq_status svdq_cross_attention_backward_workspace(const svdq_cross_desc* d, int32_t q_heads, int32_t k_heads, size_t* bytes) {
+  svdq_status st = check_cross(d, q_heads, k_heads);
+  if (st != SVDQ_OK) return st;
+  if (!bytes) return SVDQ_ERR_INVALID_ARG;
+  CrossCut t;
+  if ((st = cross_cut(d, q_heads, k_heads, device_cus(), true, &t)) != SVDQ_OK) return st;
+  *bytes = size_t(cross_delta_floats(t, q_heads) + ceil_div(cross_part_floats(d, t, true), 64) * 64 + cross_key_floats(d, t)) * 4;
+  return SVDQ_OK;
+}
+
+extern "C" svdq_status svdq_cross_attention_backward(const svdq_cross_desc* d, const svdq_heads* q, const svdq_heads* k,
+                                                     const svdq_heads* v, const svdq_heads* out, const float* lse,
+                                                     const svdq_heads* g, const svdq_heads* dq, const svdq_heads* dk,
+                                                     const svdq_heads* dv, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!q || !k || !v || !out || !g || !dq || !dk || !dv) return SVDQ_ERR_INVALID_ARG;
+  svdq_status st = check_cross(d, q->heads, k->heads);
+  if (st != SVDQ_OK) return st;
+  if (out->heads != q->heads || g->heads != q->heads || dq->heads != q->heads || v->heads != k->heads || dk->heads != k->heads ||
+      dv->heads != k->heads)
+    return SVDQ_ERR_SHAPE;
+  if (d->requests == 0) return SVDQ_OK;
+  CrossCut t;
+  if ((st = cross_cut(d, q->heads, k->heads, device_cus(), true, &t)) != SVDQ_OK) return st;
+  if (d->tokens > 0) {
+    for (const svdq_heads* h : {q, out, g, dq})
+      if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
+    if (!lse) return SVDQ_ERR_INVALID_ARG;
+  }
+  if (d->states > 0)
+    for (const svdq_heads* h : {k, v, dk, dv})
+      if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
+  const int64_t delta = cross_delta_floats(t, q->heads), part = ceil_div(cross_part_floats(d, t, true), 64) * 64;
+  if ((st = check_scratch(ws, ws_bytes, size_t(delta + part + cross_key_floats(d, t)) * 4)) != SVDQ_OK) return st;
+  CrossParams p = params_of(d, t, q->heads, k->heads);
+  p.q = rows_of(q); p.k = rows_of(k); p.v = rows_of(v); p.out = rows_of(out); p.g = rows_of(g);
+  p.dq = rows_of(dq); p.dk = rows_of(dk); p.dv = rows_of(dv);
+  p.lse = const_cast<float*>(lse);
+  p.delta = static_cast<float*>(ws);
+  p.part = p.delta + delta;
+  p.key_part = p.part + part;
+  if (d->dtype == SVDQ_BF16) launch<SVDQ_BF16>(p, t, true, stream);
+  else launch<SVDQ_F16>(p, t, true, stream);
+  return launch_ok();
+}

@@ -1,0 +1,165 @@
+// svdq_image_cut.h -- how the calls of include/svdq_image.h are cut into
+// workgroups.  Integer arithmetic only, shared by the host, the kernels and the
+// CPU tests.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+#include "svdq_image.h"
+#include "svdq_kv_cut.h"
+
+namespace svdq_image {
+
+using svdq_kv::ceil_div;
+using svdq_kv::larger;
+using svdq_kv::product_below;
+using svdq_kv::smaller;
+
+// ------------------------------------------------------------------ group norm
+constexpr int NORM_MAX_BLOCK = 32;      // groups of a workgroup of the one-launch form
+
+struct NormCut {
+  int threads;
+  int cv, rows;             // 16-byte pieces of a pixel that a workgroup takes, pixels in flight in it
+  int block, pieces;        // one launch: groups of a workgroup, pieces a thread; block = 0: two launches
+  int chunks;               // two launches: chunks of a sample's pixels, of
+  int64_t chunk;            // so many pixels (the last: the rest)
+};
+
+inline svdq_status norm_cut(const svdq_norm_desc* d, bool grad, NormCut* out) {
+  NormCut t = {};
+  const int per = d->channels / d->groups;
+  t.chunks = 1;
+  t.chunk = d->pixels;
+  int block = 1;
+  while (block * per % 8 != 0) block *= 2;
+  const int cv = block * per / 8;
+  if (cv <= 512) {
+    const int64_t room = 512 / cv, rows = d->pixels < room ? (d->pixels < 1 ? 1 : d->pixels) : room;
+    const int64_t pieces = ceil_div(d->pixels, rows);
+    if (pieces <= (grad ? 4 : 8)) {
+      t.cv = cv; t.rows = int(rows); t.block = block; t.pieces = int(pieces);
+      t.threads = int(ceil_div(int64_t(cv) * rows, 64)) * 64;
+      if (product_below(d->samples, d->groups / block, 512, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
+      *out = t;
+      return SVDQ_OK;
+    }
+  }
+  t.cv = d->channels / 8;
+  // as many threads as leave the fewest of a wave idle
+  int best = 0;
+  for (int n = 256; n <= 1024; n += 64) {
+    const int rows = n / t.cv;
+    if (rows < 1 || (n > 512 && best > 0)) continue;
+    const int used = rows * t.cv * 1024 / n;
+    if (used > best) { best = used; t.threads = n; t.rows = rows; }
+  }
+  const int64_t want = d->samples < 1 ? 512 : ceil_div(512, d->samples);
+  t.chunk = ceil_div(ceil_div(d->pixels, want), t.rows) * t.rows;
+  t.chunks = int(ceil_div(d->pixels, t.chunk));
+  if (product_below(d->samples, int64_t(t.chunks) + 1024, 1024, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
+  *out = t;
+  return SVDQ_OK;
+}
+
+// LDS of one sum a channel and row of pixels.  Rows of an odd length in the
+// kernels that walk a channel's rows by one thread a channel (norm_rows).
+inline int norm_rows(int rows) { return rows | 1; }
+inline size_t norm_lds(const NormCut& t) { return size_t(t.cv) * 8 * size_t(norm_rows(t.rows)) * 4; }
+
+inline size_t norm_bytes(const svdq_norm_desc* d, const NormCut& t, bool grad) {
+  if (d->samples == 0) return 0;
+  const size_t n = size_t(d->samples);
+  if (t.block > 0) return grad && d->samples > 1 ? n * size_t(d->channels) * 8 : 0;
+  return n * size_t(t.chunks) * size_t(d->groups + (grad ? d->channels : 0)) * 8;
+}
+
+// ------------------------------------------------------------- cross attention
+// A request's rows and states; offsets outside the operands give none.
+struct CrossRange {
+  int q_first, rows, k_first, keys;
+  template <class P>
+  SVDQ_HD CrossRange(const P& p, int r) {
+    span(p.q_start, r, p.max_q, p.tokens, &q_first, &rows);
+    span(p.k_start, r, p.max_k, p.states, &k_first, &keys);
+  }
+  SVDQ_HD static void span(const int32_t* start, int r, int most, int all, int* first, int* n) {
+    const int s = start ? start[r] : r * most, e = start ? smaller(start[r + 1], all) : s + most;
+    *first = s;
+    *n = s < 0 || e <= s ? 0 : smaller(e - s, most);
+  }
+};
+
+// Pairs (request, key head) with `tiles` workgroups each.  Workgroups go to the
+// chip's eight dies in turn, each with a cache of its own: where the pairs
+// divide by eight a pair's workgroups are eight apart, so that its keys and
+// values are read into one of the caches only.
+struct PairWork {
+  int pair, tile;
+  SVDQ_HD PairWork(unsigned id, int pairs, int tiles) {
+    if (pairs % 8 == 0) {
+      pair = int(id / 8u / unsigned(tiles) * 8u + id % 8u);
+      tile = int(id / 8u % unsigned(tiles));
+    } else {
+      pair = int(id % unsigned(pairs));
+      tile = int(id / unsigned(pairs));
+    }
+  }
+};
+
+struct CrossCut {
+  int group, pairs;         // query heads a key head, requests x key heads
+  int tokens, states;
+  int row_slots;            // rows of a pair: query tokens x heads of the group, the heads fastest
+  int rows;                 // rows of a tile: 16 or 128
+  int row_tiles, splits, chunk;   // and chunks of a pair's keys
+  int key_tiles, row_splits, row_chunk;   // gradient of keys: tiles of 128 keys, chunks of a pair's rows
+};
+
+constexpr int KEY_TILE = 128;
+
+inline svdq_status cross_cut(const svdq_cross_desc* d, int q_heads, int k_heads, int cus, bool grad, CrossCut* out) {
+  CrossCut t = {};
+  t.group = q_heads / k_heads;
+  const int64_t max_q = d->max_q < d->tokens ? d->max_q : d->tokens, max_k = d->max_k < d->states ? d->max_k : d->states;
+  const int64_t slots = max_q * t.group;
+  const int64_t pairs = product_below(d->requests, k_heads, 1, int64_t(1) << 30);
+  if (pairs < 0 || product_below(pairs, slots, 1, (int64_t(1) << 31) - 512) < 0 || max_k > (int64_t(1) << 31) - 512 ||
+      product_below(pairs, max_k, 1, int64_t(1) << 40) < 0)
+    return SVDQ_ERR_UNSUPPORTED;
+  t.pairs = int(pairs);
+  t.tokens = int(d->tokens);
+  t.states = int(d->states);
+  t.row_slots = int(slots);
+  auto clamp = [](int64_t v, int64_t most) { v = v > most ? most : v; return v < 1 ? int64_t(1) : v; };
+  const int64_t per = pairs > 0 ? pairs : 1;
+  t.rows = !grad && slots <= 64 ? 16 : 128;
+  t.row_tiles = int(ceil_div(slots, t.rows));
+  const int64_t items = per * larger(t.row_tiles, 1);
+  const int64_t n = t.rows == 16 ? clamp(int64_t(cus) * 4 / items, ceil_div(max_k, 256)) : clamp(int64_t(cus) * 2 / items, ceil_div(max_k, 512));
+  const int64_t unit = 128;
+  t.chunk = int(ceil_div(ceil_div(max_k > 0 ? max_k : 1, n), unit) * unit);
+  t.splits = int(ceil_div(max_k > 0 ? max_k : 1, t.chunk));
+  t.key_tiles = int(ceil_div(max_k, KEY_TILE));
+  const int64_t kitems = per * larger(t.key_tiles, 1);
+  const int64_t m = clamp(int64_t(cus) * 2 / kitems, ceil_div(slots, 128));
+  t.row_chunk = int(ceil_div(ceil_div(slots > 0 ? slots : 1, m), 64) * 64);
+  t.row_splits = int(ceil_div(slots > 0 ? slots : 1, t.row_chunk));
+  if (product_below(pairs, t.row_tiles, t.splits, svdq_kv::MAX_THREADS / 512) < 0 ||
+      product_below(pairs, t.key_tiles, t.row_splits, svdq_kv::MAX_THREADS / 512) < 0 ||
+      product_below(pairs, int64_t(t.key_tiles) * KEY_TILE, 1, svdq_kv::MAX_THREADS / 64) < 0)
+    return SVDQ_ERR_UNSUPPORTED;
+  *out = t;
+  return SVDQ_OK;
+}
+
+// bytes of the workspace: partial rows of the forward call or of dq
+inline int64_t cross_part_floats(const svdq_cross_desc* d, const CrossCut& t, bool grad) {
+  return t.splits > 1 ? int64_t(t.pairs) * t.row_slots * t.splits * (d->head_dim + (grad ? 0 : 2)) : 0;
+}
+inline int64_t cross_delta_floats(const CrossCut& t, int q_heads) { return ceil_div(int64_t(t.tokens) * q_heads, 64) * 64; }
+inline int64_t cross_key_floats(const svdq_cross_desc* d, const CrossCut& t) {
+  return t.row_splits > 1 ? int64_t(t.pairs) * t.key_tiles * KEY_TILE * t.row_splits * d->head_dim * 2 : 0;
+}
+
+}  // namespace svdq_image

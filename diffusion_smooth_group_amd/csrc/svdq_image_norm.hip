@@ -1,0 +1,789 @@
+// svdq_image_norm.hip -- gfx950 (MI355X) group norm with an activation over a
+// channels-last map, and its gradient (include/svdq_image.h).
+//
+// A thread has eight neighbouring channels (16 bytes) of every R-th pixel, so
+// weights, sums and scales of a channel stay in its registers.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "svdq_image.h"
+#include "svdq_image_cut.h"
+#include "svdq_kv_common.h"
+
+namespace {
+
+using namespace svdq_kv;
+using namespace svdq_image;
+
+struct NormParams {
+  const uint16_t *x, *g;
+  uint16_t* y;              // or dx
+  const uint16_t *w, *b;
+  float* stats;             // [samples][groups][2]
+  float* part;              // [samples][chunks][groups][2]: mean and square deviations (gradient: sums of u and u xh)
+  float* chan;              // gradient: [samples][chunks][channels][2], sums of dz and dz xh
+  float *dw, *db;
+  int64_t xs, xp, gs, gp, ys, yp;
+  int64_t pixels, chunk;    // pixels of a chunk
+  int32_t samples, channels, groups, per;   // per = channels / groups
+  int32_t cv, rows;         // 8-channel pieces of a pixel that a workgroup takes; pixels in flight in it
+  int32_t block;            // groups a workgroup takes (k_norm_whole)
+  int32_t chunks, act;
+  float eps;
+};
+
+template <int DT>
+__device__ __forceinline__ void unpack8(u32x4 v, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == SVDQ_BF16) {
+      f[2 * i] = __uint_as_float(v[i] << 16);
+      f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    } else {
+      f[2 * i] = h2f<DT>(v[i] & 0xFFFFu);
+      f[2 * i + 1] = h2f<DT>(v[i] >> 16);
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ u32x4 pack8(const float* f) {
+  return u32x4{pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]), pack2<DT>(f[4], f[5]), pack2<DT>(f[6], f[7])};
+}
+
+constexpr float LOG2E = 1.44269504088896341f;
+
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * z)); }
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == SVDQ_ACT_SILU) return z * sigmoid(z);
+  if constexpr (ACT == SVDQ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  return z;
+}
+// derivative of the activation
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+  if constexpr (ACT == SVDQ_ACT_SILU) {
+    const float p = sigmoid(z);
+    return __builtin_fmaf(z * p, 1.0f - p, p);
+  }
+  if constexpr (ACT == SVDQ_ACT_GELU)
+    return __builtin_fmaf(z * 0.39894228040143268f, __builtin_amdgcn_exp2f(-0.5f * LOG2E * z * z),
+                          0.5f * (1.0f + erff(z * 0.70710678118654752f)));
+  return 1.0f;
+}
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) x += __shfl_xor(x, m);
+  return x;
+}
+
+// Weights of eight channels; ones and zeros where there are none.
+template <int DT>
+__device__ __forceinline__ void weights8(const uint16_t* w, int c, float none, float* f) {
+  if (w) unpack8<DT>(*reinterpret_cast<const u32x4*>(w + c), f);
+  else
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = none;
+}
+
+// What a group sums over a workgroup: every thread leaves its eight channels'
+// values in LDS as [channel][row of pixels], so that a group's are contiguous;
+// a wave a group adds them up, in a fixed order.  Two sums at once.
+__device__ __forceinline__ void leave8(float* red, int stride, const float* v, int piece, int row, bool on) {
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[(8 * piece + i) * stride + row] = v[i];
+}
+
+// ------------------------------------------------------------ one launch
+// A workgroup has `block` groups of a sample: reads them once into registers
+// (NV pieces of 16 bytes a thread), mean first and square deviations after it,
+// writes them once.
+template <int DT, int ACT, int NV>
+__global__ __launch_bounds__(512) void k_norm_whole(NormParams p) {
+  extern __shared__ float red[];
+  __shared__ float sm[NORM_MAX_BLOCK];
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
+  const int blocks = p.groups / p.block, sample = int(blockIdx.x) / blocks, first = int(blockIdx.x) % blocks * p.block;
+  const int row = tid / p.cv, piece = tid % p.cv;
+  const bool on = row < p.rows;
+  const int c0 = first * p.per + 8 * piece;
+  const uint16_t* x = p.x + int64_t(sample) * p.xs + c0;
+  u32x4 v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t at = row + int64_t(i) * p.rows;
+    v[i] = u32x4{0, 0, 0, 0};
+    if (on && at < p.pixels) v[i] = *reinterpret_cast<const u32x4*>(x + at * p.xp);
+  }
+  float w[8], b[8];
+  if (on) {
+    weights8<DT>(p.w, c0, 1.0f, w);
+    weights8<DT>(p.b, c0, 0.0f, b);
+  }
+  const float inv_n = 1.0f / (float(p.pixels) * float(p.per));
+  const int span = p.per * p.rows;
+  float s[8] = {}, mean[8], f[8];
+  int gi[8];                            // group within the block
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // about the group's first value, so that a mean far from zero costs nothing
+    gi[e] = on ? (8 * piece + e) / p.per : 0;
+    mean[e] = h2f<DT>(p.x[int64_t(sample) * p.xs + (first + gi[e]) * p.per]);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (!on || row + int64_t(i) * p.rows >= p.pixels) continue;
+    unpack8<DT>(v[i], f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += f[e] - mean[e];
+  }
+  auto sums = [&]() {                   // sm[group] = sums of s
+    leave8(red, p.rows, s, piece, row, on);
+    __syncthreads();
+    for (int g = wave; g < p.block; g += waves) {
+      float t = 0.0f;
+      for (int e = lane; e < span; e += 64) t += red[g * span + e];
+      t = wave_sum(t);
+      if (lane == 0) sm[g] = t;
+    }
+    __syncthreads();
+  };
+  sums();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    mean[e] = __builtin_fmaf(sm[gi[e]], inv_n, mean[e]);
+    s[e] = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (on && row + int64_t(i) * p.rows < p.pixels) {
+      unpack8<DT>(v[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = f[e] - mean[e];
+        s[e] = __builtin_fmaf(d, d, s[e]);
+      }
+    }
+  }
+  __syncthreads();                      // the means have been read
+  sums();
+  float a[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(sm[gi[e]], inv_n, p.eps));
+    if (p.stats && on && row == 0 && (8 * piece + e) % p.per == 0) {
+      float* st = p.stats + (int64_t(sample) * p.groups + first + gi[e]) * 2;
+      st[0] = mean[e];
+      st[1] = rstd;
+    }
+    a[e] = rstd * w[e];
+  }
+  uint16_t* y = p.y + int64_t(sample) * p.ys + c0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t at = row + int64_t(i) * p.rows;
+    if (!on || at >= p.pixels) continue;
+    unpack8<DT>(v[i], f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = activate<ACT>(__builtin_fmaf(f[e] - mean[e], a[e], b[e]));
+    *reinterpret_cast<u32x4*>(y + at * p.yp) = pack8<DT>(f);
+  }
+}
+
+// ----------------------------------------------------------- two launches
+// Statistics of a chunk of pixels, all channels: sums of the deviations from the
+// chunk's first pixel and of their squares, channel by channel; channels of a
+// group are joined by their means and square deviations.
+template <int DT>
+__global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
+  extern __shared__ float red[];        // [2][channels][rows]
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
+  const int sample = int(blockIdx.x) / p.chunks, chunk = int(blockIdx.x) % p.chunks;
+  const int64_t from = int64_t(chunk) * p.chunk, n = min(p.pixels - from, p.chunk);
+  const int row = tid / p.cv, piece = tid % p.cv;
+  const bool on = row < p.rows;
+  float s[8] = {}, q[8] = {}, k[8], f[8];
+  if (on) {
+    const uint16_t* x = p.x + int64_t(sample) * p.xs + from * p.xp + 8 * piece;
+    unpack8<DT>(*reinterpret_cast<const u32x4*>(x), k);
+    const int64_t step = int64_t(p.rows) * p.xp;
+    x += int64_t(row) * p.xp;
+#pragma unroll 4
+    for (int64_t at = row; at < n; at += p.rows, x += step) {
+      unpack8<DT>(*reinterpret_cast<const u32x4*>(x), f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = f[e] - k[e];
+        s[e] += d;
+        q[e] = __builtin_fmaf(d, d, q[e]);
+      }
+    }
+  }
+  // channel sums: by thread, then one thread a channel
+  const int ld = p.rows | 1, size = p.channels * ld;
+  leave8(red, ld, s, piece, row, on);
+  leave8(red + size, ld, q, piece, row, on);
+  __syncthreads();
+  const float inv = 1.0f / float(n);
+  float mean = 0.0f, dev = 0.0f;
+  for (int c = tid; c < p.channels; c += int(blockDim.x)) {
+    float s0 = 0.0f, q0 = 0.0f;
+    for (int r = 0; r < p.rows; ++r) {
+      s0 += red[c * ld + r];
+      q0 += red[size + c * ld + r];
+    }
+    // in the places of the channel's own first row: nobody else reads these
+    const float k0 = h2f<DT>(p.x[int64_t(sample) * p.xs + from * p.xp + c]);
+    mean = s0 * inv;
+    dev = __builtin_fmaf(-s0, mean, q0);
+    red[c * ld] = k0 + mean;
+    red[size + c * ld] = fmaxf(dev, 0.0f);
+  }
+  __syncthreads();
+  for (int g = wave; g < p.groups; g += waves) {
+    const float* m0 = red + g * p.per * ld;
+    const float* d0 = m0 + size;
+    // about the group's first channel's mean, for the same reason as above
+    const float k0 = m0[0];
+    float t = 0.0f, u = 0.0f, d = 0.0f;
+    for (int c = lane; c < p.per; c += 64) {
+      const float e = m0[c * ld] - k0;
+      t += e;
+      u = __builtin_fmaf(e, e, u);
+      d += d0[c * ld];
+    }
+    t = wave_sum(t);
+    u = wave_sum(u);
+    d = wave_sum(d);
+    if (lane == 0) {
+      const float m = t / float(p.per);
+      float* out = p.part + (int64_t(blockIdx.x) * p.groups + g) * 2;
+      out[0] = k0 + m;
+      out[1] = __builtin_fmaf(float(n), fmaxf(__builtin_fmaf(-t, m, u), 0.0f), d);
+    }
+  }
+}
+
+// Mean and rstd of every group of a sample from its chunks' (in LDS).  All
+// chunks but the last have the same number of pixels.
+__device__ __forceinline__ void join_stats(const NormParams& p, int sample, int tid, float* sm) {
+  const int lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
+  const int64_t tail = p.pixels - int64_t(p.chunks - 1) * p.chunk;
+  const float share = float(double(p.chunk) / double(p.pixels)), last = float(double(tail) / double(p.pixels));
+  const float per_pixel = 1.0f / float(p.per);
+  const float2* part = reinterpret_cast<const float2*>(p.part) + int64_t(sample) * p.chunks * p.groups;
+  // 16 lanes a group, four groups a wave and step: the chunks of neighbouring
+  // groups are neighbours in memory
+  for (int g0 = wave * 4; g0 < p.groups; g0 += waves * 4) {
+    const int g = g0 + (lane & 3), at = lane >> 2;
+    const bool on = g < p.groups;
+    const float2* q = part + (on ? g : 0);
+    const float k = q[0].x;
+    float m = 0.0f, u = 0.0f, d = 0.0f;
+    for (int i = at; i < p.chunks; i += 16) {
+      const float2 v = q[int64_t(i) * p.groups];
+      const float wt = i + 1 < p.chunks ? share : last, e = v.x - k;
+      m = __builtin_fmaf(wt, e, m);
+      u = __builtin_fmaf(wt * e, e, u);
+      d += v.y;
+    }
+#pragma unroll
+    for (int s = 4; s < 64; s *= 2) {
+      m += __shfl_xor(m, s);
+      u += __shfl_xor(u, s);
+      d += __shfl_xor(d, s);
+    }
+    if (on && at == 0) {
+      const float between = fmaxf(__builtin_fmaf(-m, m, u), 0.0f);
+      const float within = d * (per_pixel / float(p.pixels));
+      sm[2 * g] = k + m;
+      sm[2 * g + 1] = 1.0f / __builtin_sqrtf(between + within + p.eps);
+    }
+  }
+  __syncthreads();
+}
+
+template <int DT, int ACT>
+__global__ __launch_bounds__(1024) void k_norm_apply(NormParams p) {
+  extern __shared__ float sm[];         // [groups][2]
+  const int tid = int(threadIdx.x);
+  const int sample = int(blockIdx.x) / p.chunks, chunk = int(blockIdx.x) % p.chunks;
+  join_stats(p, sample, tid, sm);
+  if (p.stats && chunk == 0)
+    for (int i = tid; i < 2 * p.groups; i += int(blockDim.x)) p.stats[int64_t(sample) * p.groups * 2 + i] = sm[i];
+  const int row = tid / p.cv, piece = tid % p.cv;
+  if (row >= p.rows) return;
+  float w[8], b[8], a[8], m[8], f[8];
+  weights8<DT>(p.w, 8 * piece, 1.0f, w);
+  weights8<DT>(p.b, 8 * piece, 0.0f, b);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int g = (8 * piece + e) / p.per;
+    m[e] = sm[2 * g];
+    a[e] = sm[2 * g + 1] * w[e];
+  }
+  const int64_t from = int64_t(chunk) * p.chunk, n = min(p.pixels - from, p.chunk);
+  const uint16_t* x = p.x + int64_t(sample) * p.xs + (from + row) * p.xp + 8 * piece;
+  uint16_t* y = p.y + int64_t(sample) * p.ys + (from + row) * p.yp + 8 * piece;
+  const int64_t xstep = int64_t(p.rows) * p.xp, ystep = int64_t(p.rows) * p.yp;
+  int64_t at = row;
+  for (; at + 3 * int64_t(p.rows) < n; at += 4 * int64_t(p.rows), x += 4 * xstep, y += 4 * ystep) {
+    u32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const u32x4*>(x + i * xstep);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unpack8<DT>(v[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = activate<ACT>(__builtin_fmaf(f[e] - m[e], a[e], b[e]));
+      *reinterpret_cast<u32x4*>(y + i * ystep) = pack8<DT>(f);
+    }
+  }
+  for (; at < n; at += p.rows, x += xstep, y += ystep) {
+    unpack8<DT>(*reinterpret_cast<const u32x4*>(x), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = activate<ACT>(__builtin_fmaf(f[e] - m[e], a[e], b[e]));
+    *reinterpret_cast<u32x4*>(y) = pack8<DT>(f);
+  }
+}
+
+// ------------------------------------------------------------- gradient
+// dz and xh of eight elements
+template <int DT, int ACT>
+__device__ __forceinline__ void back8(u32x4 xv, u32x4 gv, const float* m, const float* r, const float* w, const float* b,
+                                      float* dz, float* xh) {
+  float f[8];
+  unpack8<DT>(xv, f);
+  unpack8<DT>(gv, dz);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    xh[e] = (f[e] - m[e]) * r[e];
+    if constexpr (ACT != SVDQ_ACT_NONE) dz[e] *= slope<ACT>(__builtin_fmaf(xh[e], w[e], b[e]));
+  }
+}
+
+// One launch: as k_norm_whole.  A sample's channel sums go to dw and db, or,
+// with several samples, to `chan` for k_norm_sum.
+template <int DT, int ACT, int NV>
+__global__ __launch_bounds__(512) void k_norm_grad_whole(NormParams p) {
+  extern __shared__ float red[];        // [2][channels of the block][rows]
+  __shared__ float sm[2 * NORM_MAX_BLOCK];
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
+  const int blocks = p.groups / p.block, sample = int(blockIdx.x) / blocks, first = int(blockIdx.x) % blocks * p.block;
+  const int row = tid / p.cv, piece = tid % p.cv;
+  const bool on = row < p.rows;
+  const int c0 = first * p.per + 8 * piece;
+  u32x4 xv[NV], gv[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t at = row + int64_t(i) * p.rows;
+    xv[i] = gv[i] = u32x4{0, 0, 0, 0};
+    if (on && at < p.pixels) {
+      xv[i] = *reinterpret_cast<const u32x4*>(p.x + int64_t(sample) * p.xs + at * p.xp + c0);
+      gv[i] = *reinterpret_cast<const u32x4*>(p.g + int64_t(sample) * p.gs + at * p.gp + c0);
+    }
+  }
+  float w[8] = {}, b[8] = {}, m[8] = {}, r[8] = {}, s[8] = {}, q[8] = {}, dz[8], xh[8];
+  int gi[8] = {};
+  if (on) {
+    weights8<DT>(p.w, c0, 1.0f, w);
+    weights8<DT>(p.b, c0, 0.0f, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      gi[e] = (8 * piece + e) / p.per;
+      const float* st = p.stats + (int64_t(sample) * p.groups + first + gi[e]) * 2;
+      m[e] = st[0];
+      r[e] = st[1];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (!on || row + int64_t(i) * p.rows >= p.pixels) continue;
+    back8<DT, ACT>(xv[i], gv[i], m, r, w, b, dz, xh);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s[e] += dz[e];
+      q[e] = __builtin_fmaf(dz[e], xh[e], q[e]);
+    }
+  }
+  const int wide = 8 * p.cv, ld = p.rows | 1, size = wide * ld;
+  leave8(red, ld, s, piece, row, on);
+  leave8(red + size, ld, q, piece, row, on);
+  __syncthreads();
+  for (int c = tid; c < wide; c += int(blockDim.x)) {
+    float s0 = 0.0f, q0 = 0.0f;
+    for (int i = 0; i < p.rows; ++i) {
+      s0 += red[c * ld + i];
+      q0 += red[size + c * ld + i];
+    }
+    const int ch = first * p.per + c;
+    if (p.samples > 1) {
+      *reinterpret_cast<float2*>(p.chan + (int64_t(sample) * p.channels + ch) * 2) = float2{s0, q0};
+    } else {
+      if (p.db) p.db[ch] = s0;
+      if (p.dw) p.dw[ch] = q0;
+    }
+    const float wc = p.w ? h2f<DT>(p.w[ch]) : 1.0f;
+    red[c * ld] = s0 * wc;          // (the channel's own places: nobody else reads these)
+    red[size + c * ld] = q0 * wc;
+  }
+  __syncthreads();
+  const float inv_n = 1.0f / (float(p.pixels) * float(p.per));
+  for (int g = wave; g < p.block; g += waves) {
+    float t = 0.0f, u = 0.0f;
+    for (int c = lane; c < p.per; c += 64) {
+      t += red[(g * p.per + c) * ld];
+      u += red[size + (g * p.per + c) * ld];
+    }
+    t = wave_sum(t);
+    u = wave_sum(u);
+    if (lane == 0) {
+      sm[2 * g] = t * inv_n;
+      sm[2 * g + 1] = u * inv_n;
+    }
+  }
+  __syncthreads();
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t at = row + int64_t(i) * p.rows;
+    if (at >= p.pixels) continue;
+    back8<DT, ACT>(xv[i], gv[i], m, r, w, b, dz, xh);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      dz[e] = r[e] * (__builtin_fmaf(dz[e], w[e], -sm[2 * gi[e]]) - xh[e] * sm[2 * gi[e] + 1]);
+    *reinterpret_cast<u32x4*>(p.y + int64_t(sample) * p.ys + at * p.yp + c0) = pack8<DT>(dz);
+  }
+}
+
+// Two launches: channel and group sums of a chunk ...
+template <int DT, int ACT>
+__global__ __launch_bounds__(1024) void k_norm_grad_sums(NormParams p) {
+  extern __shared__ float red[];        // [2][channels][rows]
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
+  const int sample = int(blockIdx.x) / p.chunks, chunk = int(blockIdx.x) % p.chunks;
+  const int64_t from = int64_t(chunk) * p.chunk, n = min(p.pixels - from, p.chunk);
+  const int row = tid / p.cv, piece = tid % p.cv;
+  const bool on = row < p.rows;
+  float s[8] = {}, q[8] = {};
+  if (on) {
+    float w[8], b[8], m[8], r[8], dz[8], xh[8];
+    weights8<DT>(p.w, 8 * piece, 1.0f, w);
+    weights8<DT>(p.b, 8 * piece, 0.0f, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float* st = p.stats + (int64_t(sample) * p.groups + (8 * piece + e) / p.per) * 2;
+      m[e] = st[0];
+      r[e] = st[1];
+    }
+    const uint16_t* x = p.x + int64_t(sample) * p.xs + (from + row) * p.xp + 8 * piece;
+    const uint16_t* g = p.g + int64_t(sample) * p.gs + (from + row) * p.gp + 8 * piece;
+    const int64_t xstep = int64_t(p.rows) * p.xp, gstep = int64_t(p.rows) * p.gp;
+    auto add = [&](u32x4 xv, u32x4 gv) {
+      back8<DT, ACT>(xv, gv, m, r, w, b, dz, xh);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[e] += dz[e];
+        q[e] = __builtin_fmaf(dz[e], xh[e], q[e]);
+      }
+    };
+    int64_t at = row;
+    for (; at + int64_t(p.rows) < n; at += 2 * int64_t(p.rows), x += 2 * xstep, g += 2 * gstep) {
+      const u32x4 x0 = *reinterpret_cast<const u32x4*>(x), g0 = *reinterpret_cast<const u32x4*>(g);
+      const u32x4 x1 = *reinterpret_cast<const u32x4*>(x + xstep), g1 = *reinterpret_cast<const u32x4*>(g + gstep);
+      add(x0, g0);
+      add(x1, g1);
+    }
+    if (at < n) add(*reinterpret_cast<const u32x4*>(x), *reinterpret_cast<const u32x4*>(g));
+  }
+  const int ld = p.rows | 1, size = p.channels * ld;
+  leave8(red, ld, s, piece, row, on);
+  leave8(red + size, ld, q, piece, row, on);
+  __syncthreads();
+  for (int c = tid; c < p.channels; c += int(blockDim.x)) {
+    float s0 = 0.0f, q0 = 0.0f;
+    for (int i = 0; i < p.rows; ++i) {
+      s0 += red[c * ld + i];
+      q0 += red[size + c * ld + i];
+    }
+    *reinterpret_cast<float2*>(p.chan + (int64_t(blockIdx.x) * p.channels + c) * 2) = float2{s0, q0};
+    const float wc = p.w ? h2f<DT>(p.w[c]) : 1.0f;
+    red[c * ld] = s0 * wc;          // (the channel's own places: nobody else reads these)
+    red[size + c * ld] = q0 * wc;
+  }
+  __syncthreads();
+  for (int g = wave; g < p.groups; g += waves) {
+    float t = 0.0f, u = 0.0f;
+    for (int c = lane; c < p.per; c += 64) {
+      t += red[(g * p.per + c) * ld];
+      u += red[size + (g * p.per + c) * ld];
+    }
+    t = wave_sum(t);
+    u = wave_sum(u);
+    if (lane == 0) *reinterpret_cast<float2*>(p.part + (int64_t(blockIdx.x) * p.groups + g) * 2) = float2{t, u};
+  }
+}
+
+// dw and db of 32 channels: sums over `n` rows of [channels][2], eight walks and
+// then one thread a channel.
+__device__ __forceinline__ void sum_channels(const NormParams& p, int64_t n, int c0, int tid, float* red) {
+  const int c = c0 + (tid & 31), walk = tid >> 5;
+  const bool on = walk < 8 && c < p.channels;
+  if (on) {
+    float s = 0.0f, q = 0.0f;
+    const float2* at = reinterpret_cast<const float2*>(p.chan) + c;
+#pragma unroll 4
+    for (int64_t i = walk; i < n; i += 8) {
+      const float2 v = at[i * p.channels];
+      s += v.x;
+      q += v.y;
+    }
+    red[2 * tid] = s;
+    red[2 * tid + 1] = q;
+  }
+  __syncthreads();
+  if (!on || walk != 0) return;
+  float s = 0.0f, q = 0.0f;
+  for (int i = 0; i < 8; ++i) {
+    s += red[2 * (tid + 32 * i)];
+    q += red[2 * (tid + 32 * i) + 1];
+  }
+  if (p.db) p.db[c] = s;
+  if (p.dw) p.dw[c] = q;
+}
+
+__global__ __launch_bounds__(256) void k_norm_sum(NormParams p) {
+  __shared__ float red[512];
+  sum_channels(p, int64_t(p.samples) * p.chunks, int(blockIdx.x) * 32, int(threadIdx.x), red);
+}
+
+// ... and the map's gradient; workgroups past the chunks' have the channels' sums.
+template <int DT, int ACT>
+__global__ __launch_bounds__(1024) void k_norm_grad_apply(NormParams p) {
+  extern __shared__ float sm[];         // [groups][2], or 512 for the channels' sums
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
+  const int work = p.samples * p.chunks;
+  if (int(blockIdx.x) >= work) {
+    sum_channels(p, work, (int(blockIdx.x) - work) * 32, tid, sm);
+    return;
+  }
+  const int sample = int(blockIdx.x) / p.chunks, chunk = int(blockIdx.x) % p.chunks;
+  const float inv_n = 1.0f / (float(p.pixels) * float(p.per));
+  const float2* part = reinterpret_cast<const float2*>(p.part) + int64_t(sample) * p.chunks * p.groups;
+  for (int g0 = wave * 4; g0 < p.groups; g0 += waves * 4) {
+    const int g = g0 + (lane & 3);
+    const bool in = g < p.groups;
+    float t = 0.0f, u = 0.0f;
+    for (int i = lane >> 2; i < p.chunks; i += 16) {
+      const float2 v = part[int64_t(i) * p.groups + (in ? g : 0)];
+      t += v.x;
+      u += v.y;
+    }
+#pragma unroll
+    for (int s = 4; s < 64; s *= 2) {
+      t += __shfl_xor(t, s);
+      u += __shfl_xor(u, s);
+    }
+    if (in && lane < 4) {
+      sm[2 * g] = t * inv_n;
+      sm[2 * g + 1] = u * inv_n;
+    }
+  }
+  __syncthreads();
+  const int row = tid / p.cv, piece = tid % p.cv;
+  if (row >= p.rows) return;
+  float w[8], b[8], m[8], r[8], t[8], u[8];
+  weights8<DT>(p.w, 8 * piece, 1.0f, w);
+  weights8<DT>(p.b, 8 * piece, 0.0f, b);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int g = (8 * piece + e) / p.per;
+    const float* st = p.stats + (int64_t(sample) * p.groups + g) * 2;
+    m[e] = st[0];
+    r[e] = st[1];
+    t[e] = sm[2 * g];
+    u[e] = sm[2 * g + 1];
+  }
+  const int64_t from = int64_t(chunk) * p.chunk, n = min(p.pixels - from, p.chunk);
+  const uint16_t* x = p.x + int64_t(sample) * p.xs + (from + row) * p.xp + 8 * piece;
+  const uint16_t* g = p.g + int64_t(sample) * p.gs + (from + row) * p.gp + 8 * piece;
+  uint16_t* y = p.y + int64_t(sample) * p.ys + (from + row) * p.yp + 8 * piece;
+  const int64_t xstep = int64_t(p.rows) * p.xp, gstep = int64_t(p.rows) * p.gp, ystep = int64_t(p.rows) * p.yp;
+  auto one = [&](u32x4 xv, u32x4 gv, uint16_t* to) {
+    float dz[8], xh[8];
+    back8<DT, ACT>(xv, gv, m, r, w, b, dz, xh);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dz[e] = r[e] * (__builtin_fmaf(dz[e], w[e], -t[e]) - xh[e] * u[e]);
+    *reinterpret_cast<u32x4*>(to) = pack8<DT>(dz);
+  };
+  int64_t at = row;
+  for (; at + int64_t(p.rows) < n; at += 2 * int64_t(p.rows), x += 2 * xstep, g += 2 * gstep, y += 2 * ystep) {
+    const u32x4 x0 = *reinterpret_cast<const u32x4*>(x), g0 = *reinterpret_cast<const u32x4*>(g);
+    const u32x4 x1 = *reinterpret_cast<const u32x4*>(x + xstep), g1 = *reinterpret_cast<const u32x4*>(g + gstep);
+    one(x0, g0, y);
+    one(x1, g1, y + ystep);
+  }
+  if (at < n) one(*reinterpret_cast<const u32x4*>(x), *reinterpret_cast<const u32x4*>(g), y);
+}
+
+// dw = db = 0 (a call without samples)
+__global__ void k_norm_zero(float* dw, float* db, int n) {
+  const int i = int(blockIdx.x * blockDim.x + threadIdx.x);
+  if (i >= n) return;
+  if (dw) dw[i] = 0.0f;
+  if (db) db[i] = 0.0f;
+}
+
+// ---------------------------------------------------------------- host side
+svdq_status check_norm(const svdq_norm_desc* d) {
+  if (!d || d->samples < 0 || d->pixels < 0 || !dtype_ok(d->dtype) || d->groups < 1 || d->channels < 1 || d->act < SVDQ_ACT_NONE ||
+      d->act > SVDQ_ACT_GELU || !(d->eps >= 0.0f) || !(d->eps <= 3.0e38f))
+    return SVDQ_ERR_INVALID_ARG;
+  if (d->samples > 0 && d->pixels < 1) return SVDQ_ERR_INVALID_ARG;
+  if (d->channels % 8 != 0 || d->channels % d->groups != 0 || !aligned(d->weight, 16) || !aligned(d->bias, 16)) return SVDQ_ERR_SHAPE;
+  if (d->channels > SVDQ_NORM_MAX_CHANNELS) return SVDQ_ERR_UNSUPPORTED;
+  if (d->samples >= (int64_t(1) << 31) || product_below(d->samples, d->pixels, d->channels, int64_t(1) << 60) < 0) return SVDQ_ERR_UNSUPPORTED;
+  return SVDQ_OK;
+}
+
+svdq_status check_map(const svdq_norm_desc* d, const svdq_map* m) {
+  if (!m || !m->data) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned(m->data, 16) || m->sample_stride % 8 != 0 || m->pixel_stride % 8 != 0 || m->sample_stride < 0 || m->pixel_stride < 0)
+    return SVDQ_ERR_SHAPE;
+  if (d->pixels > 1 && m->pixel_stride < d->channels) return SVDQ_ERR_SHAPE;
+  return SVDQ_OK;
+}
+
+svdq_status check_ws(const void* ws, size_t have, size_t need) {
+  if (need == 0) return SVDQ_OK;
+  if (!ws) return SVDQ_ERR_INVALID_ARG;
+  if (have < need) return SVDQ_ERR_CAPACITY;
+  return aligned(ws, 16) ? SVDQ_OK : SVDQ_ERR_INVALID_ARG;
+}
+
+NormParams params_of(const svdq_norm_desc* d, const NormCut& t) {
+  NormParams p = {};
+  p.w = static_cast<const uint16_t*>(d->weight);
+  p.b = static_cast<const uint16_t*>(d->bias);
+  p.pixels = d->pixels; p.chunk = t.chunk;
+  p.samples = int32_t(d->samples); p.channels = d->channels; p.groups = d->groups; p.per = d->channels / d->groups;
+  p.cv = t.cv; p.rows = t.rows; p.block = t.block; p.chunks = t.chunks; p.act = d->act; p.eps = d->eps;
+  return p;
+}
+
+template <int DT, int ACT>
+void launch_norm(const NormParams& p, const NormCut& t, hipStream_t st) {
+  const size_t red = norm_lds(t);
+  if (t.block > 0) {
+    const dim3 grid(unsigned(p.samples) * unsigned(p.groups / t.block));
+    if (t.pieces <= 1) k_norm_whole<DT, ACT, 1><<<grid, t.threads, red, st>>>(p);
+    else if (t.pieces <= 2) k_norm_whole<DT, ACT, 2><<<grid, t.threads, red, st>>>(p);
+    else if (t.pieces <= 4) k_norm_whole<DT, ACT, 4><<<grid, t.threads, red, st>>>(p);
+    else k_norm_whole<DT, ACT, 8><<<grid, t.threads, red, st>>>(p);
+    return;
+  }
+  const dim3 grid(unsigned(p.samples) * unsigned(t.chunks));
+  k_norm_stats<DT><<<grid, t.threads, 2 * red, st>>>(p);
+  k_norm_apply<DT, ACT><<<grid, t.threads, size_t(p.groups) * 8, st>>>(p);
+}
+
+template <int DT, int ACT>
+void launch_norm_grad(const NormParams& p, const NormCut& t, hipStream_t st) {
+  const size_t red = 2 * norm_lds(t);
+  const bool sums = p.dw || p.db;
+  const unsigned tiles = unsigned((p.channels + 31) / 32);
+  if (t.block > 0) {
+    const dim3 grid(unsigned(p.samples) * unsigned(p.groups / t.block));
+    if (t.pieces <= 1) k_norm_grad_whole<DT, ACT, 1><<<grid, t.threads, red, st>>>(p);
+    else if (t.pieces <= 2) k_norm_grad_whole<DT, ACT, 2><<<grid, t.threads, red, st>>>(p);
+    else k_norm_grad_whole<DT, ACT, 4><<<grid, t.threads, red, st>>>(p);
+    if (p.samples > 1 && sums) k_norm_sum<<<dim3(tiles), 256, 0, st>>>(p);
+    return;
+  }
+  const unsigned work = unsigned(p.samples) * unsigned(t.chunks);
+  k_norm_grad_sums<DT, ACT><<<dim3(work), t.threads, red, st>>>(p);
+  const size_t lds = size_t(p.groups) * 8 > 2048 ? size_t(p.groups) * 8 : 2048;
+  k_norm_grad_apply<DT, ACT><<<dim3(work + (sums ? tiles : 0)), t.threads, lds, st>>>(p);
+}
+
+template <int DT>
+void launch(const NormParams& p, const NormCut& t, bool grad, hipStream_t st) {
+  if (p.act == SVDQ_ACT_NONE) grad ? launch_norm_grad<DT, SVDQ_ACT_NONE>(p, t, st) : launch_norm<DT, SVDQ_ACT_NONE>(p, t, st);
+  else if (p.act == SVDQ_ACT_SILU) grad ? launch_norm_grad<DT, SVDQ_ACT_SILU>(p, t, st) : launch_norm<DT, SVDQ_ACT_SILU>(p, t, st);
+  else grad ? launch_norm_grad<DT, SVDQ_ACT_GELU>(p, t, st) : launch_norm<DT, SVDQ_ACT_GELU>(p, t, st);
+}
+
+}  // namespace
+
+extern "C" svdq_status svdq_group_norm_workspace(const svdq_norm_desc* d, size_t* bytes) {
+  svdq_status st = check_norm(d);
+  if (st != SVDQ_OK) return st;
+  if (!bytes) return SVDQ_ERR_INVALID_ARG;
+  NormCut t;
+  if ((st = norm_cut(d, false, &t)) != SVDQ_OK) return st;
+  *bytes = norm_bytes(d, t, false);
+  return SVDQ_OK;
+}
+
+extern "C" svdq_status svdq_group_norm(const svdq_norm_desc* d, const svdq_map* x, const svdq_map* y, float* stats, void* ws,
+                                       size_t ws_bytes, hipStream_t stream) {
+  svdq_status st = check_norm(d);
+  if (st != SVDQ_OK) return st;
+  if (!x || !y) return SVDQ_ERR_INVALID_ARG;
+  if (d->samples == 0) return SVDQ_OK;
+  if ((st = check_map(d, x)) != SVDQ_OK || (st = check_map(d, y)) != SVDQ_OK) return st;
+  NormCut t;
+  if ((st = norm_cut(d, false, &t)) != SVDQ_OK || (st = check_ws(ws, ws_bytes, norm_bytes(d, t, false))) != SVDQ_OK) return st;
+  NormParams p = params_of(d, t);
+  p.x = static_cast<const uint16_t*>(x->data);
+  p.y = static_cast<uint16_t*>(y->data);
+  p.xs = x->sample_stride; p.xp = x->pixel_stride; p.ys = y->sample_stride; p.yp = y->pixel_stride;
+  p.stats = stats;
+  p.part = static_cast<float*>(ws);
+  if (d->dtype == SVDQ_BF16) launch<SVDQ_BF16>(p, t, false, stream);
+  else launch<SVDQ_F16>(p, t, false, stream);
+  return launch_ok();
+}
+
+extern "C" svdq_status svdq_group_norm_backward_workspace(const svdq_norm_desc* d, size_t* bytes) {
+  svdq_status st = check_norm(d);
+  if (st != SVDQ_OK) return st;
+  if (!bytes) return SVDQ_ERR_INVALID_ARG;
+  NormCut t;
+  if ((st = norm_cut(d, true, &t)) != SVDQ_OK) return st;
+  *bytes = norm_bytes(d, t, true);
+  return SVDQ_OK;
+}
+
+extern "C" svdq_status svdq_group_norm_backward(const svdq_norm_desc* d, const svdq_map* x, const svdq_map* g, const float* stats,
+                                                const svdq_map* dx, float* dw, float* db, void* ws, size_t ws_bytes,
+                                                hipStream_t stream) {
+  svdq_status st = check_norm(d);
+  if (st != SVDQ_OK) return st;
+  if (!x || !g || !dx) return SVDQ_ERR_INVALID_ARG;
+  if (d->samples == 0) {
+    if (dw || db) k_norm_zero<<<dim3(unsigned((d->channels + 255) / 256)), 256, 0, stream>>>(dw, db, d->channels);
+    return launch_ok();
+  }
+  if (!stats) return SVDQ_ERR_INVALID_ARG;
+  if ((st = check_map(d, x)) != SVDQ_OK || (st = check_map(d, g)) != SVDQ_OK || (st = check_map(d, dx)) != SVDQ_OK) return st;
+  NormCut t;
+  if ((st = norm_cut(d, true, &t)) != SVDQ_OK || (st = check_ws(ws, ws_bytes, norm_bytes(d, t, true))) != SVDQ_OK) return st;
+  NormParams p = params_of(d, t);
+  p.x = static_cast<const uint16_t*>(x->data);
+  p.g = static_cast<const uint16_t*>(g->data);
+  p.y = static_cast<uint16_t*>(dx->data);
+  p.xs = x->sample_stride; p.xp = x->pixel_stride; p.gs = g->sample_stride; p.gp = g->pixel_stride;
+  p.ys = dx->sample_stride; p.yp = dx->pixel_stride;
+  p.stats = const_cast<float*>(stats);
+  p.chan = static_cast<float*>(ws);
+  p.part = p.chan + (t.block > 0 ? 0 : int64_t(d->samples) * t.chunks * d->channels * 2);
+  p.dw = dw; p.db = db;
+  if (d->dtype == SVDQ_BF16) launch<SVDQ_BF16>(p, t, true, stream);
+  else launch<SVDQ_F16>(p, t, true, stream);
+  return launch_ok();
+}

@@ -1,0 +1,347 @@
+"""ctypes binding of the operators of an image model's conditioned blocks
+(include/svdq_image.h): what runs between the 4-bit linears where an encoder's
+states enter.
+
+    y = group_norm(x, groups, weight, bias, act="silu")      x [samples, height, width, channels]
+    o = cross_attention(q, k, v, mask=mask)                  q, k, v [requests, tokens, heads, D]
+
+Argument marshalling only, as in ``kv.py``, whose conventions hold: a call runs
+on the current stream or, with stream=, as if made under
+``torch.cuda.stream(stream)``; all its tensors are on one device, which need not
+be the current one; a wrong argument raises ValueError here or SvdqError with
+the library's status.
+
+Maps are channels last: the last dimension has unit stride and the dimensions
+between the first and the last are one run of pixels (views of wider rows are
+taken as they are; a torch ``channels_last`` tensor is passed as
+``x.permute(0, 2, 3, 1)``).  ``*_autograd`` are the operators under
+torch.autograd; their gradients can not be differentiated again (torch raises an
+error).
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import kv
+from . import svdq as S
+from .kv import SvdqError, _code, _on, _scratch, _size, _stream, svdq_heads  # noqa: F401
+
+ACT = {None: 0, "silu": 1, "gelu": 2}
+
+_P, _I64, _I32, _F, _SZ = C.c_void_p, C.c_int64, C.c_int32, C.c_float, C.c_size_t
+
+
+class svdq_map(C.Structure):
+    _fields_ = [("data", _P), ("sample_stride", _I64), ("pixel_stride", _I64)]
+
+
+class svdq_norm_desc(C.Structure):
+    _fields_ = [("samples", _I64), ("pixels", _I64), ("channels", _I32), ("groups", _I32), ("dtype", _I32), ("act", _I32), ("eps", _F),
+                ("weight", _P), ("bias", _P)]
+
+
+class svdq_cross_desc(C.Structure):
+    _fields_ = [("requests", _I64), ("tokens", _I64), ("states", _I64), ("head_dim", _I32), ("dtype", _I32), ("max_q", _I32),
+                ("max_k", _I32), ("scale", _F), ("q_start", _P), ("k_start", _P), ("mask", _P)]
+
+
+_NP, _MP, _XP, _HP = C.POINTER(svdq_norm_desc), C.POINTER(svdq_map), C.POINTER(svdq_cross_desc), C.POINTER(svdq_heads)
+_SIGS = {
+    "svdq_group_norm_workspace": [_NP, C.POINTER(_SZ)],
+    "svdq_group_norm": [_NP, _MP, _MP, _P, _P, _SZ, _P],
+    "svdq_group_norm_backward_workspace": [_NP, C.POINTER(_SZ)],
+    "svdq_group_norm_backward": [_NP, _MP, _MP, _P, _MP, _P, _P, _P, _SZ, _P],
+    "svdq_cross_attention_workspace": [_XP, _I32, _I32, C.POINTER(_SZ)],
+    "svdq_cross_attention": [_XP, _HP, _HP, _HP, _HP, _P, _P, _SZ, _P],
+    "svdq_cross_attention_backward_workspace": [_XP, _I32, _I32, C.POINTER(_SZ)],
+    "svdq_cross_attention_backward": [_XP, _HP, _HP, _HP, _HP, _P, _HP, _HP, _HP, _HP, _P, _SZ, _P],
+}
+_FN = {}
+
+
+def _call(name, *args):
+    fn = _FN.get(name)
+    if fn is None:
+        fn = getattr(S.lib_handle(), name)
+        fn.argtypes, fn.restype = _SIGS[name], C.c_int
+        _FN[name] = fn
+    rc = fn(*args)
+    if rc != 0:
+        raise SvdqError(name, rc)
+
+
+def _workspace(ws, like, name, *args):
+    """Address and bytes of the call's workspace: the caller's, or one of the call's own."""
+    if ws is None:
+        need = _SZ(0)
+        _call(name, *args, need)
+        if need.value == 0:
+            return None, 0
+        ws = like.new_empty(need.value, dtype=torch.uint8)
+        return ws, need.value
+    return ws, _scratch(ws, like.get_device())[1]
+
+
+def _address(ws):
+    return None if ws is None else ws.data_ptr()
+
+
+# ------------------------------------------------------------------ group norm
+def _run(t):
+    """Stride between the pixels of t [samples, ..., channels], None where they are not one run."""
+    step = None
+    for n, s in zip(t.shape[-2:0:-1], t.stride()[-2:0:-1]):
+        if n == 1:
+            continue
+        if step is None:
+            step, span = s, s * n
+        elif s != span:
+            return None
+        else:
+            span *= n
+    return 0 if step is None else step
+
+
+def _map(t, name, like, dev):
+    if t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: a {like.dtype} tensor {tuple(like.shape)} on cuda:{dev} is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    step = _run(t)
+    if step is None or t.stride(-1) != 1:
+        raise ValueError(f"{name}: channels last with unit stride and one run of pixels is needed, got {tuple(t.shape)} with strides {t.stride()}")
+    return svdq_map(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, step)
+
+
+def _norm_desc(x, groups, weight, bias, eps, act, dev):
+    if x.dim() < 2:
+        raise ValueError(f"x: [samples, ..., channels] is needed, got {tuple(x.shape)}")
+    if act not in ACT:
+        raise ValueError(f"act: one of {list(ACT)} is needed, got {act!r}")
+    n, c = x.shape[0], x.shape[-1]
+    p = [None, None]
+    for i, (w, name) in enumerate(((weight, "weight"), (bias, "bias"))):
+        if w is not None:
+            p[i] = kv._weight(w, name, c, x.dtype, dev)
+    return svdq_norm_desc(n, math.prod(x.shape[1:-1]), _size(c, "channels"), _size(groups, "groups"), _code(x.dtype), ACT[act], eps, *p)
+
+
+def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: Optional[str] = None, out=None, ws=None,
+               return_stats: bool = False, stream=None):
+    """act((x - mean) / sqrt(var + eps) * weight + bias) over the pixels and the
+    channels / groups channels of each group of x [samples, ..., channels].
+    weight, bias [channels] (None: ones, zeros); act: None, "silu" or "gelu".
+    out=x works in place.  Returns out, or (out, stats): mean and 1 / sqrt(var +
+    eps), fp32 [samples, groups, 2]."""
+    with _on(stream, x):
+        dev = kv._current_device()
+        d = _norm_desc(x, groups, weight, bias, eps, act, dev)
+        mx = _map(x, "x", x, dev)
+        if out is None:
+            out = torch.empty_like(x)
+            if _run(out) is None or out.stride(-1) != 1:
+                out = x.new_empty(x.shape)
+        mo = _map(out, "out", x, dev)
+        stats = x.new_empty((x.shape[0], groups, 2), dtype=torch.float32) if return_stats else None
+        ws, n = _workspace(ws, x, "svdq_group_norm_workspace", d)
+        _call("svdq_group_norm", d, mx, mo, _address(stats), _address(ws), n, _stream(x))
+        return (out, stats) if return_stats else out
+
+
+def group_norm_backward(g, x, stats, groups: int, weight=None, bias=None, act: Optional[str] = None, dx=None, ws=None, stream=None):
+    """Gradient of ``group_norm`` from g (with respect to its output), its input
+    and its stats.  Returns (dx, dw, db), the sums over samples and pixels fp32
+    [channels].  dx=g and dx=x work in place."""
+    with _on(stream, x):
+        dev = kv._current_device()
+        d = _norm_desc(x, groups, weight, bias, 0.0, act, dev)
+        mx, mg = _map(x, "x", x, dev), _map(g, "g", x, dev)
+        if dx is None:
+            dx = torch.empty_like(x)
+            if _run(dx) is None or dx.stride(-1) != 1:
+                dx = x.new_empty(x.shape)
+        md = _map(dx, "dx", x, dev)
+        if stats.dtype is not torch.float32 or stats.shape != (x.shape[0], groups, 2) or not stats.is_contiguous() or stats.get_device() != dev:
+            raise ValueError(f"stats: a contiguous float32 tensor {(x.shape[0], groups, 2)} on cuda:{dev} is needed, "
+                             f"got {stats.dtype} {tuple(stats.shape)} on {stats.device}")
+        dw, db = x.new_empty((2, x.shape[-1]), dtype=torch.float32).unbind()
+        ws, n = _workspace(ws, x, "svdq_group_norm_backward_workspace", d)
+        _call("svdq_group_norm_backward", d, mx, mg, stats.data_ptr(), md, dw.data_ptr(), db.data_ptr(), _address(ws), n, _stream(x))
+        return dx, dw, db
+
+
+def _as_map(t):
+    """t as the library takes a map; what it does not (a gradient that is
+    broadcast over pixels) is written out."""
+    step = _run(t)
+    fits = t.stride(-1) == 1 and step is not None and step % 8 == 0 and t.stride(0) % 8 == 0 and t.data_ptr() % 16 == 0 \
+        and (step >= t.shape[-1] or math.prod(t.shape[1:-1]) <= 1)
+    return t if fits else t.contiguous()
+
+
+class _GroupNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, groups, eps, act):
+        x = _as_map(x)
+        y, stats = group_norm(x, groups, weight, bias, eps, act, return_stats=True)
+        ctx.save_for_backward(x, stats, weight, bias)
+        ctx.how = groups, act
+        return y
+
+    @staticmethod
+    @once_differentiable        # a second derivative raises: without this it would be missing without a word
+    def backward(ctx, g):
+        x, stats, weight, bias = ctx.saved_tensors
+        groups, act = ctx.how
+        dx, dw, db = group_norm_backward(_as_map(g), x, stats, groups, weight, bias, act)
+        return dx, None if weight is None else dw.to(weight.dtype), None if bias is None else db.to(bias.dtype), None, None, None
+
+
+def group_norm_autograd(x, weight, bias, groups: int, eps: float = 1e-5, act: Optional[str] = None):
+    """``group_norm`` under torch.autograd: gradients of x, weight and bias."""
+    return _GroupNorm.apply(x, weight, bias, groups, eps, act)
+
+
+# ------------------------------------------------------------- cross attention
+def _stride(t):
+    """Stride between the tokens of t [tokens, heads, D] or [requests, tokens,
+    heads, D], None where they are not one run."""
+    if t.dim() == 3:
+        return t.stride(0)
+    b, n = t.shape[:2]
+    if n <= 1:
+        return t.stride(0)
+    return t.stride(1) if b == 1 or t.stride(0) == n * t.stride(1) else None
+
+
+def _rows(t, name, lead, dim, dtype, dev):
+    step = _stride(t)
+    if t.shape[:-2] != lead or t.shape[-1] != dim or t.stride(-1) != 1 or step is None or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: a {dtype} tensor {(*lead, 'heads', dim)} on cuda:{dev} with unit stride in the last dimension and one run "
+                         f"of tokens is needed, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    h = t.shape[-2]
+    return svdq_heads(t.data_ptr(), step if math.prod(lead) > 1 else 0, t.stride(-2) if h > 1 else 0, h)
+
+
+def _out(t, name, like, dev):
+    """An output like `like`, a new one where t is None, and its view for the call."""
+    if t is None:
+        t = torch.empty_like(like)
+        if _stride(t) is None or t.stride(-1) != 1:
+            t = like.new_empty(like.shape)
+    elif t.shape != like.shape:
+        raise ValueError(f"{name}: {tuple(like.shape)} is needed, got {tuple(t.shape)}")
+    return t, _rows(t, name, like.shape[:-2], like.shape[-1], like.dtype, dev)
+
+
+def _cross_desc(q, k, q_start, k_start, max_q, max_k, mask, scale, dev):
+    if q.dim() == 4 and k.dim() == 4:
+        if q_start is not None or k_start is not None or max_q is not None or max_k is not None:
+            raise ValueError("q_start, k_start, max_q and max_k go with rows [tokens, heads, D]")
+        b, max_q, max_k = q.shape[0], q.shape[1], k.shape[1]
+        if k.shape[0] != b:
+            raise ValueError(f"k: states of {b} requests are needed, got {tuple(k.shape)}")
+        tokens, states, qs, ks = b * max_q, b * max_k, None, None
+    elif q.dim() == 3 and k.dim() == 3:
+        if q_start is None or k_start is None or max_q is None or max_k is None:
+            raise ValueError("rows [tokens, heads, D] need q_start, k_start, max_q and max_k")
+        b, tokens, states = q_start.numel() - 1, q.shape[0], k.shape[0]
+        if b < 0:
+            raise ValueError("q_start: [requests + 1] is needed, got no entry")
+        qs, ks = kv._int32(q_start, "q_start", b + 1, dev), kv._int32(k_start, "k_start", b + 1, dev)
+    else:
+        raise ValueError(f"q and k: both [tokens, heads, D] or both [requests, tokens, heads, D] are needed, got {tuple(q.shape)} and {tuple(k.shape)}")
+    pm = None
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8) or mask.numel() != states or not mask.is_contiguous() or mask.get_device() != dev:
+            raise ValueError(f"mask: a contiguous bool tensor of {states} entries on cuda:{dev} is needed, got {mask.dtype} {tuple(mask.shape)} on {mask.device}")
+        pm = mask.data_ptr()
+    dim = q.shape[-1]
+    return svdq_cross_desc(b, tokens, states, _size(dim, "head_dim"), _code(q.dtype), _size(max_q, "max_q"), _size(max_k, "max_k"),
+                           (1.0 / math.sqrt(dim) if dim else 1.0) if scale is None else scale, qs, ks, pm)
+
+
+def cross_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] = None, max_k: Optional[int] = None, mask=None,
+                    scale: Optional[float] = None, out=None, ws=None, return_lse: bool = False, stream=None):
+    """softmax(scale q k^T) v of queries over an encoder's keys and values.
+
+    q [requests, tokens, heads, D], k and v [requests, states, k_heads, D]; or
+    requests of different lengths one after the other: q [tokens, heads, D], rows
+    q_start[r] .. q_start[r + 1] are request r's, k and v [states, k_heads, D]
+    with k_start (int32 [requests + 1] both), and max_q, max_k, which bound a
+    request's rows and states.  k_heads divides heads.  mask: bool or uint8,
+    one entry a state, in the states' order; false (0): not seen.  scale: 1 /
+    sqrt(D) by default.  A row that sees nothing gives zeros; a row of no
+    request is not written.  Returns out, or (out, lse): lse fp32, q's shape
+    without D."""
+    with _on(stream, q):
+        dev = kv._current_device()
+        d = _cross_desc(q, k, q_start, k_start, max_q, max_k, mask, scale, dev)
+        dim, lead, kept, dtype = q.shape[-1], q.shape[:-2], k.shape[:-2], q.dtype
+        hq, hk, hv = _rows(q, "q", lead, dim, dtype, dev), _rows(k, "k", kept, dim, dtype, dev), _rows(v, "v", kept, dim, dtype, dev)
+        out, ho = _out(out, "out", q, dev)
+        lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if return_lse else None
+        ws, n = _workspace(ws, q, "svdq_cross_attention_workspace", d, q.shape[-2], k.shape[-2])
+        _call("svdq_cross_attention", d, hq, hk, hv, ho, _address(lse), _address(ws), n, _stream(q))
+        return (out, lse) if return_lse else out
+
+
+def cross_attention_backward(g, q, k, v, out, lse, q_start=None, k_start=None, max_q: Optional[int] = None, max_k: Optional[int] = None,
+                             mask=None, scale: Optional[float] = None, dq=None, dk=None, dv=None, ws=None, stream=None):
+    """Gradient of ``cross_attention`` from g (with respect to its output), its
+    inputs, its output and lse.  Returns (dq, dk, dv).  States that the mask
+    hides get zeros; rows and states of no request are not written."""
+    with _on(stream, q):
+        dev = kv._current_device()
+        d = _cross_desc(q, k, q_start, k_start, max_q, max_k, mask, scale, dev)
+        dim, lead, kept, dtype = q.shape[-1], q.shape[:-2], k.shape[:-2], q.dtype
+        hq, ho, hg = (_rows(t, n, lead, dim, dtype, dev) for t, n in ((q, "q"), (out, "out"), (g, "g")))
+        hk, hv = _rows(k, "k", kept, dim, dtype, dev), _rows(v, "v", kept, dim, dtype, dev)
+        if lse.dtype is not torch.float32 or lse.shape != q.shape[:-1] or not lse.is_contiguous() or lse.get_device() != dev:
+            raise ValueError(f"lse: a contiguous float32 tensor {tuple(q.shape[:-1])} on cuda:{dev} is needed, got {lse.dtype} {tuple(lse.shape)} on {lse.device}")
+        (dq, hdq), (dk, hdk), (dv, hdv) = _out(dq, "dq", q, dev), _out(dk, "dk", k, dev), _out(dv, "dv", v, dev)
+        ws, n = _workspace(ws, q, "svdq_cross_attention_backward_workspace", d, q.shape[-2], k.shape[-2])
+        _call("svdq_cross_attention_backward", d, hq, hk, hv, ho, lse.data_ptr(), hg, hdq, hdk, hdv, _address(ws), n, _stream(q))
+        return dq, dk, dv
+
+
+def _as_rows(t):
+    """t as the library takes rows; what it does not (states that requests
+    share by a stride of 0, a gradient that is broadcast over heads) is written out."""
+    step, h = _stride(t), t.stride(-2)
+    fits = t.stride(-1) == 1 and step is not None and step >= 0 and step % 8 == 0 and h % 8 == 0 and (h >= t.shape[-1] or t.shape[-2] == 1) \
+        and t.data_ptr() % 16 == 0
+    return t if fits else t.contiguous()
+
+
+class _CrossAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, q_start, k_start, max_q, max_k, mask, scale):
+        q, k, v = _as_rows(q), _as_rows(k), _as_rows(v)
+        out = None if q_start is None else q.new_zeros(q.shape)     # rows of no request are defined here
+        out, lse = cross_attention(q, k, v, q_start, k_start, max_q, max_k, mask, scale, out=out, return_lse=True)
+        ctx.save_for_backward(q, k, v, out, lse, q_start, k_start, mask)
+        ctx.how = max_q, max_k, scale
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        q, k, v, out, lse, q_start, k_start, mask = ctx.saved_tensors
+        max_q, max_k, scale = ctx.how
+        dq = dk = dv = None
+        if q_start is not None:
+            dq, dk, dv = (t.new_zeros(t.shape) for t in (q, k, v))
+        grads = cross_attention_backward(_as_rows(g), q, k, v, out, lse, q_start, k_start, max_q, max_k, mask, scale, dq, dk, dv)
+        return *grads, *[None] * 6
+
+
+def cross_attention_autograd(q, k, v, q_start=None, k_start=None, max_q: Optional[int] = None, max_k: Optional[int] = None, mask=None,
+                             scale: Optional[float] = None):
+    """``cross_attention`` under torch.autograd: gradients of q, k and v.
+    States shared by ``expand`` are taken (and written out); rows of no request
+    are zeros."""
+    return _CrossAttention.apply(q, k, v, q_start, k_start, max_q, max_k, mask, scale)
