@@ -33,15 +33,25 @@ struct CrossParams {
   const uint8_t* mask;
   int32_t tokens, states, max_q, max_k, q_heads, heads, group, pairs, D;
   int32_t row_slots, row_tiles, splits, chunk;
-  int32_t key_tiles, row_splits, row_chunk;
+  int32_t key_tile, key_tiles, row_splits, row_chunk;
+  unsigned by_group;        // 2^32 / group, rounded up (group > 1)
   float c, scale;           // c = scale log2(e); forward: |scale|, and q's signs are turned
   unsigned turn;            // bits of two 16-bit values to turn
+
+  // row / group: the product may be one too high
+  __device__ __forceinline__ int token_of(int row) const {
+    if (group == 1) return row;
+    const int t = int(__umulhi(unsigned(row), by_group));
+    return t * group > row ? t - 1 : t;
+  }
 };
 
 constexpr float LOWEST = -3.0e38f;   // reference of a row that has seen no key
 constexpr float LOG2E = 1.44269504088896341f;
-constexpr int PAD = 16;              // elements behind each row in LDS: rows 8 (D = 128, 96: 72, 56 words) or 40 words
-                                     // apart modulo 64, so that eight rows' 16 bytes and four rows' 32 lie in banks of their own
+// Elements of a row in LDS: 36, 52 or 72 words, so that eight rows' 16 bytes and
+// four rows' 32 lie in banks of their own.
+template <int DP>
+constexpr int row_of() { return DP + (DP == 128 ? 16 : 8); }
 
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
@@ -67,7 +77,25 @@ __device__ __forceinline__ u32x2 read_turned(const uint16_t* at) {
 }
 __device__ __forceinline__ u32x4 joined(u32x2 a, u32x2 b) { return u32x4{a[0], a[1], b[0], b[1]}; }
 
+// The reads of N times M matrix instructions, R each time, run ahead of them:
+// EXTRA and those of the first AHEAD, then R behind each (left alone, the compiler
+// waits for nearly every read right where it is used).
+template <int N, int R, int AHEAD, int M = 1, int EXTRA = 0>
+__device__ __forceinline__ void reads_ahead() {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * R + EXTRA, 0);
+#pragma unroll
+  for (int i = 0; i < N - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, AHEAD * M, 0);
+}
+
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// NaN if either is one: one instruction for three, where fmaxf has to quiet its
+// operands first.  A row with a NaN gives NaN by its probabilities.
+__device__ __forceinline__ float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 // over the two lanes l, l ^ 32, and over the four l, l ^ 16, l ^ 32, l ^ 48
 __device__ __forceinline__ float half_max(float x) {
@@ -111,6 +139,15 @@ __device__ __forceinline__ float lower_gain(float top) {      // 2^7 / 2^floor(l
 constexpr float FIRST_GAIN = 0x1p100f, MOST = 0x1p15f;
 constexpr float P_UP = 10.0f;           // f16, gradient of values: probabilities are held at 2^10 of their size
 
+// the two 16-bit values of a word as floats
+template <int DT>
+__device__ __forceinline__ float first_half(unsigned w) { return h2f<DT>(w & 0xFFFFu); }
+template <int DT>
+__device__ __forceinline__ float second_half(unsigned w) {
+  if constexpr (DT == SVDQ_BF16) return __uint_as_float(w & 0xFFFF0000u);
+  else return h2f<DT>(w >> 16);
+}
+
 // 16-bit values of the columns of a 32 x 32 result (lane: column lane % 32, rows
 // 8 (i / 4) + 4 (lane / 32) + i % 4) as they are stored: eight neighbouring rows,
 // [16 y + 8 (lane / 32), ..), in w[4 y ..].
@@ -129,21 +166,44 @@ __device__ __forceinline__ void columns(const f32x16& o, float by, unsigned* w) 
   }
 }
 
-// KT rows of `heads` operands on their way into LDS, NT threads.
-template <int DP, int KT, int NT>
+// Rows on their way into LDS by buffer loads, whose addresses are a scalar base
+// and a lane's fixed offset, and which give zeros for the offset OUT: no vector
+// instruction a stage but for the last.
+constexpr unsigned OUT = 0x80000000u;   // = the buffers' size: host checks keep every other offset below it
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t from, unsigned at, unsigned base = 0) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at, base, 0));
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint16_t* base) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, OUT, 0x00020000);
+}
+
+// KT rows of an operand, 256 threads
+template <int DP, int KT>
 struct Piece {
-  static constexpr int CH = DP / 8, N = KT * CH / NT;   // 16-byte pieces a row, pieces a thread
-  static constexpr int LD = DP + PAD;
-  static_assert(KT * CH % NT == 0, "whole pieces");
+  static constexpr int CH = DP / 8, N = KT * CH / 256;   // 16-byte pieces a row, pieces a thread
+  static constexpr bool EVEN = 256 % CH == 0;            // a thread's pieces are whole rows apart: one offset, and a scalar for the rest
+  static constexpr int LD = row_of<DP>();
+  static_assert(KT * CH % 256 == 0, "whole pieces");
   u32x4 v[N];
-  static __device__ __forceinline__ int row(int tid, int i) { return (tid + NT * i) / CH; }
-  static __device__ __forceinline__ int col(int tid, int i) { return (tid + NT * i) % CH * 8; }
-  // rows [0, n) of `base`, `stride` elements apart; zeros behind them and from column D on
-  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int n, int D, int tid) {
+  unsigned off[EVEN ? 1 : N], step;
+  static __device__ __forceinline__ int row(int tid, int i) { return EVEN ? tid / CH + 256 / CH * i : (tid + 256 * i) / CH; }
+  static __device__ __forceinline__ int col(int tid, int i) { return (EVEN ? tid : tid + 256 * i) % CH * 8; }
+  // rows `stride` elements apart
+  __device__ __forceinline__ void rows(int64_t stride, int D, int tid) {
+    step = EVEN ? unsigned(256 / CH) * unsigned(stride) * 2u : 0u;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] = u32x4{0, 0, 0, 0};
-      if (row(tid, i) < n && col(tid, i) < D) v[i] = *reinterpret_cast<const u32x4*>(base + row(tid, i) * stride + col(tid, i));
+    for (int i = 0; i < (EVEN ? 1 : N); ++i)
+      off[i] = col(tid, i) < D ? unsigned(row(tid, i)) * unsigned(stride) * 2u + unsigned(col(tid, i)) * 2u : OUT;
+  }
+  // the `n` first rows from `base` on; zeros behind them
+  __device__ __forceinline__ void load(const uint16_t* base, int n, int tid) {
+    const __amdgpu_buffer_rsrc_t from = buffer(base);
+    if (n >= KT) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = load16(from, off[EVEN ? 0 : i], i * step);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = load16(from, row(tid, i) < n ? off[EVEN ? 0 : i] : OUT, i * step);
     }
   }
   __device__ __forceinline__ void write(uint16_t* lds, int tid) const {
@@ -158,6 +218,26 @@ struct Piece {
   }
 };
 
+// The same for rows (query, head of a group): every piece has its own offset.
+template <int DP, int KT>
+struct RowPiece {
+  static constexpr int CH = DP / 8, N = KT * CH / 256, LD = row_of<DP>();
+  static_assert(KT * CH % 256 == 0, "whole pieces");
+  u32x4 v[N];
+  unsigned off[N];
+  static __device__ __forceinline__ int row(int tid, int i) { return (tid + 256 * i) / CH; }
+  static __device__ __forceinline__ int col(int tid, int i) { return (tid + 256 * i) % CH * 8; }
+  __device__ __forceinline__ void load(const uint16_t* base, int n, int tid) {
+    const __amdgpu_buffer_rsrc_t from = buffer(base);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = load16(from, n >= KT || row(tid, i) < n ? off[i] : OUT);
+  }
+  __device__ __forceinline__ void write(uint16_t* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + row(tid, i) * LD + col(tid, i)) = v[i];
+  }
+};
+
 // bit t: state `at` + t of the request is seen, t < 64
 __device__ __forceinline__ uint64_t seen(const CrossParams& p, const CrossRange& r, int at, int lane) {
   bool on = at + lane < r.keys;
@@ -165,11 +245,29 @@ __device__ __forceinline__ uint64_t seen(const CrossParams& p, const CrossRange&
   return __ballot(on);
 }
 
-// Largest of 16 logits times nothing else; what is not seen becomes -infinity.
-// see: the 32 keys' bits from the lane half's first on.
+// Logits of 32 keys; what is not seen becomes -infinity.  see: the keys' bits from
+// the lane half's first on.
 __device__ __forceinline__ void hide16(f32x16& s, unsigned see) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] = (see >> (8 * (i / 4) + i % 4)) & 1u ? s[i] : -__builtin_inff();
+}
+
+// A stage's keys as what their logits start from, 0 or (not seen) -infinity, or
+// +infinity where they are multiplied by a negative number: the matrix core adds it,
+// so that a mask costs no vector instruction.  By one wave.
+__device__ __forceinline__ void leave_bias(float* bias, uint64_t see, float c, int lane) {
+  bias[lane] = (see >> lane) & 1u ? 0.0f : c < 0.0f ? __builtin_inff() : -__builtin_inff();
+}
+// the 16 rows of a lane of a 32 x 32 result
+__device__ __forceinline__ f32x16 rows16(const float* at, int hb) {
+  f32x16 v;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const f32x4 u = *reinterpret_cast<const f32x4*>(at + 8 * y + 4 * hb);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * y + i] = u[i];
+  }
+  return v;
 }
 
 // ------------------------------------------------------------ forward, many rows
@@ -179,7 +277,7 @@ __device__ __forceinline__ void hide16(f32x16& s, unsigned see) {
 // keys each.
 template <int DT, int DP>
 __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
-  constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = DP + PAD;
+  constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
   __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * LD];
   __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * LD];
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 31, hb = lane >> 5;
@@ -193,7 +291,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
   const int from = split * p.chunk, to = smaller(r.keys, from + p.chunk);
   const int row = tile * 128 + wave * 32 + m;
   const bool active = tile * 128 + wave * 32 < rows;     // of the wave
-  const int64_t tok = int64_t(r.q_first) + (row < rows ? row / p.group : 0);
+  const int64_t tok = int64_t(r.q_first) + (row < rows ? p.token_of(row) : 0);
   const int head = h * p.group + (row < rows ? row % p.group : 0);
   u32x4 q[NE];
 #pragma unroll
@@ -214,11 +312,13 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
 
   const uint16_t* kp = p.k.data + (int64_t(r.k_first) + from) * p.k.token + h * p.k.head;
   const uint16_t* vp = p.v.data + (int64_t(r.k_first) + from) * p.v.token + h * p.v.head;
-  Piece<DP, KT, 256> pk, pv;
+  Piece<DP, KT> pk, pv;
+  pk.rows(p.k.token, p.D, tid);
+  pv.rows(p.v.token, p.D, tid);
   uint64_t see = 0;
   if (from < to) {
-    pk.load(kp, p.k.token, to - from, p.D, tid);
-    pv.load(vp, p.v.token, to - from, p.D, tid);
+    pk.load(kp, to - from, tid);
+    pv.load(vp, to - from, tid);
     see = seen(p, r, from, lane);
     if (see != ~uint64_t(0)) pv.hide(see, tid);
     pk.write(sk[0], tid);
@@ -232,13 +332,15 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
     if (more) {
       kp += KT * p.k.token;
       vp += KT * p.v.token;
-      pk.load(kp, p.k.token, to - at - KT, p.D, tid);
-      pv.load(vp, p.v.token, to - at - KT, p.D, tid);
+      pk.load(kp, to - at - KT, tid);
+      pv.load(vp, to - at - KT, tid);
     }
     if (see != 0 && active) {
-      f32x16 s[2];
+      constexpr int T = 2;              // tiles of 32 keys
+      f32x16 s[T];
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < T; ++t) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
 #pragma unroll
@@ -246,14 +348,16 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
           const u32x4 a = *reinterpret_cast<const u32x4*>(&sk[buf][(32 * t + m) * LD + 16 * e + 8 * hb]);
           s[t] = mfma32<DT>(a, q[e], s[t]);
         }
+        reads_ahead<NE, 1, 4>();
       }
+      __builtin_amdgcn_s_setprio(0);
       if (see != ~uint64_t(0)) {
         hide16(s[0], unsigned(see) >> (4 * hb));
         hide16(s[1], unsigned(see >> 32) >> (4 * hb));
       }
       float top = s[0][0];
 #pragma unroll
-      for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+      for (int i = 1; i < 16 * T; ++i) top = maximum(top, s[i / 16][i % 16]);
       top = __builtin_fmaf(half_max(top), p.c, -base);
       if (__any(top > limit)) {
         const bool first_keys = limit < 0.0f, some = top > -__builtin_inff();
@@ -265,25 +369,28 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
 #pragma unroll
         for (int x = 0; x < NX; ++x) o[x] *= alpha;
       }
-      u32x4 pf[4];
       float part = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < 16 * T; ++i) {
         s[i / 16][i % 16] = exp2_hw(__builtin_fmaf(s[i / 16][i % 16], p.c, -base));
         part += s[i / 16][i % 16];
       }
       sum += part;
+      u32x4 pf[2 * T];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) pf[i / 4][i % 4] = pack2<DT>(s[i / 8][2 * i % 16], s[i / 8][2 * i % 16 + 1]);
+      for (int i = 0; i < 8 * T; ++i) pf[i / 4][i % 4] = pack2<DT>(s[i / 8][2 * i % 16], s[i / 8][2 * i % 16 + 1]);
       const int g = lane >> 4, i4 = lane & 15;
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int x = 0; x < NX; ++x) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2 * T; ++j) {
           const uint16_t* b = &sv[buf][(16 * j + 4 * (g >> 1) + (i4 >> 2)) * LD + 32 * x + 16 * (g & 1) + 4 * (i4 & 3)];
           o[x] = mfma32<DT>(joined(read_turned(b), read_turned(b + 8 * LD)), pf[j], o[x]);
         }
       }
+      reads_ahead<2 * T * NX, 2, 4>();
+      __builtin_amdgcn_s_setprio(0);
     }
     if (more) {
       next = seen(p, r, at + KT, lane);
@@ -332,7 +439,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
 // The waves meet at the end.
 template <int DT, int DP>
 __global__ __launch_bounds__(256) void k_cross_few(CrossParams p) {
-  constexpr int NJ = DP / 32, NX = DP / 16, LD = DP + PAD, CH = DP / 8, NV = 32 * CH / 64;
+  constexpr int NJ = DP / 32, NX = DP / 16, LD = row_of<DP>(), CH = DP / 8, NV = 32 * CH / 64;
   __shared__ __attribute__((aligned(16))) uint16_t sv[4][32 * LD];
   __shared__ float wave_base[4][16], wave_sum[4][16];
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 15, b = lane >> 4;
@@ -347,7 +454,7 @@ __global__ __launch_bounds__(256) void k_cross_few(CrossParams p) {
   const int row = tile * 16 + m;
   u32x4 q[NJ];
   {
-    const int64_t tok = int64_t(r.q_first) + (row < rows ? row / p.group : 0);
+    const int64_t tok = int64_t(r.q_first) + (row < rows ? p.token_of(row) : 0);
     const int head = h * p.group + (row < rows ? row % p.group : 0);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -415,7 +522,7 @@ __global__ __launch_bounds__(256) void k_cross_few(CrossParams p) {
     }
     float top = s[0][0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i / 4][i % 4]);
+    for (int i = 1; i < 8; ++i) top = maximum(top, s[i / 4][i % 4]);
     top = __builtin_fmaf(quad_max(top), p.c, -base);
     if (__any(top > limit)) {
       const bool first_keys = limit < 0.0f, some = top > -__builtin_inff();
@@ -541,9 +648,10 @@ __global__ __launch_bounds__(256) void k_cross_join(CrossParams p) {
 // transposing reads.  Leaves delta for k_cross_dkv.
 template <int DT, int DP>
 __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
-  constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = DP + PAD;
+  constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
   __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * LD];
   __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * LD];
+  __shared__ __attribute__((aligned(16))) float sb[2][KT];
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 31, hb = lane >> 5;
   const PairWork work(blockIdx.x, p.pairs, p.row_tiles * p.splits);
   const int tile = work.tile / p.splits, split = work.tile % p.splits, req = work.pair / p.heads, h = work.pair % p.heads;
@@ -555,7 +663,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
   const int from = split * p.chunk, to = smaller(r.keys, from + p.chunk);
   const int row = tile * 128 + wave * 32 + m;
   const bool active = tile * 128 + wave * 32 < rows;
-  const int64_t tok = int64_t(r.q_first) + (row < rows ? row / p.group : 0);
+  const int64_t tok = int64_t(r.q_first) + (row < rows ? p.token_of(row) : 0);
   const int head = h * p.group + (row < rows ? row % p.group : 0);
   u32x4 q[NE], g[NE];
   float delta = 0.0f;
@@ -590,13 +698,16 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
 
   const uint16_t* kp = p.k.data + (int64_t(r.k_first) + from) * p.k.token + h * p.k.head;
   const uint16_t* vp = p.v.data + (int64_t(r.k_first) + from) * p.v.token + h * p.v.head;
-  Piece<DP, KT, 256> pk, pv;
+  Piece<DP, KT> pk, pv;
+  pk.rows(p.k.token, p.D, tid);
+  pv.rows(p.v.token, p.D, tid);
   uint64_t see = 0;
   if (from < to) {
-    pk.load(kp, p.k.token, to - from, p.D, tid);
-    pv.load(vp, p.v.token, to - from, p.D, tid);
+    pk.load(kp, to - from, tid);
+    pv.load(vp, to - from, tid);
     see = seen(p, r, from, lane);
     if (see != ~uint64_t(0)) { pk.hide(see, tid); pv.hide(see, tid); }
+    if (wave == 0) leave_bias(sb[0], see, p.c, lane);
     pk.write(sk[0], tid);
     pv.write(sv[0], tid);
   }
@@ -608,32 +719,31 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
     if (more) {
       kp += KT * p.k.token;
       vp += KT * p.v.token;
-      pk.load(kp, p.k.token, to - at - KT, p.D, tid);
-      pv.load(vp, p.v.token, to - at - KT, p.D, tid);
+      pk.load(kp, to - at - KT, tid);
+      pv.load(vp, to - at - KT, tid);
     }
     if (see != 0 && active) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        f32x16 s, dp;
+        const unsigned bits = t ? unsigned(see >> 32) : unsigned(see);
+        if (bits == 0u) continue;
+        f32x16 s = rows16(&sb[buf][32 * t], hb), dp;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+        for (int i = 0; i < 16; ++i) dp[i] = 0.0f;
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
           s = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sk[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), q[e], s);
           dp = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sv[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), g[e], dp);
         }
-        const unsigned bits = t ? unsigned(see >> 32) : unsigned(see);
+        reads_ahead<2 * NE, 1, 4>();
+        __builtin_amdgcn_s_setprio(0);
 #pragma unroll
         for (int i = 0; i < 16; ++i) dp[i] = exp2_hw(__builtin_fmaf(s[i], p.c, -lse)) * (dp[i] - delta);
-        if (bits != ~0u) {
-          const unsigned mybits = bits >> (4 * hb);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) dp[i] = (mybits >> (8 * (i / 4) + i % 4)) & 1u ? dp[i] : 0.0f;
-        }
         if constexpr (DT == SVDQ_F16) {
           float top = __builtin_fabsf(dp[0]);
 #pragma unroll
-          for (int i = 1; i < 16; ++i) top = fmaxf(top, __builtin_fabsf(dp[i]));
+          for (int i = 1; i < 16; ++i) top = maximum(top, __builtin_fabsf(dp[i]));
           top = half_max(top);
           const bool over = top * gain > MOST;
           if (__any(over)) {
@@ -644,23 +754,34 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
           }
           dp *= gain;
         }
-        u32x4 ds[2];
+        // in two terms of 16 bits: one alone costs as much precision as the result's own rounding
+        u32x4 ds[2], low[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ds[i / 4][i % 4] = pack2<DT>(dp[2 * i], dp[2 * i + 1]);
+        for (int i = 0; i < 8; ++i) {
+          const unsigned w = pack2<DT>(dp[2 * i], dp[2 * i + 1]);
+          ds[i / 4][i % 4] = w;
+          low[i / 4][i % 4] = pack2<DT>(dp[2 * i] - first_half<DT>(w), dp[2 * i + 1] - second_half<DT>(w));
+        }
         const int gr = lane >> 4, i4 = lane & 15;
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int x = 0; x < NX; ++x) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint16_t* b = &sk[buf][(32 * t + 16 * j + 4 * (gr >> 1) + (i4 >> 2)) * LD + 32 * x + 16 * (gr & 1) + 4 * (i4 & 3)];
-            acc[x] = mfma32<DT>(joined(read_turned(b), read_turned(b + 8 * LD)), ds[j], acc[x]);
+            const u32x4 a = joined(read_turned(b), read_turned(b + 8 * LD));
+            acc[x] = mfma32<DT>(a, ds[j], acc[x]);
+            acc[x] = mfma32<DT>(a, low[j], acc[x]);
           }
         }
+        reads_ahead<2 * NX, 2, 4, 2>();
+        __builtin_amdgcn_s_setprio(0);
       }
     }
     if (more) {
       next = seen(p, r, at + KT, lane);
       if (next != ~uint64_t(0)) { pk.hide(next, tid); pv.hide(next, tid); }
+      if (wave == 0) leave_bias(sb[buf ^ 1], next, p.c, lane);
       pk.write(sk[buf ^ 1], tid);
       pv.write(sv[buf ^ 1], tid);
     }
@@ -694,66 +815,94 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
 }
 
 // -------------------------------------------------------- gradient of k and v
-// 32 keys a wave, whose K and V stay in registers as operands, 128 a workgroup;
-// rows pass by in LDS, 64 a stage.  S = Q K^T leaves a lane with 16 rows of one
-// key: the operand of dV^T += G^T P and dK^T += Q^T dS, G^T and Q^T by
-// transposing reads.  A key that is not seen spoils only its own lane's sums,
+// 32 NK keys a wave, whose K and V stay in registers as operands, 128 NK a
+// workgroup; rows pass by in LDS, RT a stage.  S = Q K^T leaves a lane with 16
+// rows of one key: the operand of dV^T += G^T P and dK^T += Q^T dS, G^T and Q^T
+// by transposing reads.  A key that is not seen spoils only its own lane's sums,
 // which are not stored.
-template <int DT, int DP>
-__global__ __launch_bounds__(256, DP == 64 ? 2 : 1) void k_cross_dkv(CrossParams p) {
-  constexpr int RT = 64, NE = DP / 16, NX = DP / 32, LD = DP + PAD, CH = DP / 8, NP = RT * CH / 256;
+template <int DT, int DP, int NK>
+__global__ __launch_bounds__(256, NK == 1 ? 2 : 1) void k_cross_dkv(CrossParams p) {
+  constexpr int RT = DP == 96 ? 64 : 32, NE = DP / 16, NX = DP / 32, LD = row_of<DP>(), WIDE = 128 * NK;
   __shared__ __attribute__((aligned(16))) uint16_t sq[2][RT * LD];
   __shared__ __attribute__((aligned(16))) uint16_t sg[2][RT * LD];
   __shared__ __attribute__((aligned(16))) float sl[2][RT], sd[2][RT];
+  // Of the NE operands of K and V each, the last LE lie in LDS: what does not fit
+  // the registers of two waves a SIMD would otherwise come back from scratch memory
+  // every stage, behind the rows that are on their way.
+  constexpr int LE = NK > 1 || DP == 64 ? 0 : DP == 96 ? 2 : 4, HE = NE - LE;
+  __shared__ u32x4 sx[4][2 * LE + 1][64];
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 31, hb = lane >> 5;
   const PairWork work(blockIdx.x, p.pairs, p.key_tiles * p.row_splits);
   const int tile = work.tile / p.row_splits, split = work.tile % p.row_splits, req = work.pair / p.heads, h = work.pair % p.heads;
   const CrossRange r(p, req);
-  if (tile * KEY_TILE >= r.keys) return;
+  if (tile * WIDE >= r.keys) return;
   const int rows = r.rows * p.group, chunks = (rows + p.row_chunk - 1) / p.row_chunk;
   if (split > 0 && split >= chunks) return;
   const int from = split * p.row_chunk, to = smaller(rows, from + p.row_chunk);
-  const int key = tile * KEY_TILE + wave * 32 + m;
-  const bool active = tile * KEY_TILE + wave * 32 < r.keys, held = key < r.keys;
-  const int64_t state = int64_t(r.k_first) + (held ? key : 0);
-  const bool shown = held && (!p.mask || p.mask[state] != 0);
-  u32x4 k[NE], v[NE];
+  const int first = tile * WIDE + wave * 32 * NK;
+  const bool active = first < r.keys;
+  u32x4 k[NK][HE], v[NK][HE];
+  bool shown[NK];
 #pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    k[e] = v[e] = u32x4{0, 0, 0, 0};
-    const int d = 16 * e + 8 * hb;
-    if (shown && d < p.D) {
-      k[e] = *reinterpret_cast<const u32x4*>(p.k.data + state * p.k.token + h * p.k.head + d);
-      v[e] = *reinterpret_cast<const u32x4*>(p.v.data + state * p.v.token + h * p.v.head + d);
-    }
-  }
-  f32x16 dk[NX], dv[NX];
+  for (int n = 0; n < NK; ++n) {
+    const int key = first + 32 * n + m;
+    const int64_t state = int64_t(r.k_first) + (key < r.keys ? key : 0);
+    shown[n] = key < r.keys && (!p.mask || p.mask[state] != 0);
 #pragma unroll
-  for (int x = 0; x < NX; ++x)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dk[x][i] = dv[x][i] = 0.0f;
-  float gain = FIRST_GAIN;
-
-  u32x4 vq[NP], vg[NP];
-  float l = 0.0f, dl = 0.0f;
-  auto fetch = [&](int at) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int rw = at + (tid + 256 * i) / CH, d = (tid + 256 * i) % CH * 8;
-      vq[i] = vg[i] = u32x4{0, 0, 0, 0};
-      if (rw < to && d < p.D) {
-        const int64_t tok = int64_t(r.q_first) + rw / p.group;
-        const int head = h * p.group + rw % p.group;
-        vq[i] = *reinterpret_cast<const u32x4*>(p.q.data + tok * p.q.token + head * p.q.head + d);
-        vg[i] = *reinterpret_cast<const u32x4*>(p.g.data + tok * p.g.token + head * p.g.head + d);
+    for (int e = 0; e < NE; ++e) {
+      u32x4 a = {0, 0, 0, 0}, c = {0, 0, 0, 0};
+      const int d = 16 * e + 8 * hb;
+      if (shown[n] && d < p.D) {
+        a = *reinterpret_cast<const u32x4*>(p.k.data + state * p.k.token + h * p.k.head + d);
+        c = *reinterpret_cast<const u32x4*>(p.v.data + state * p.v.token + h * p.v.head + d);
+      }
+      if (e < HE) {
+        k[n][e < HE ? e : 0] = a;
+        v[n][e < HE ? e : 0] = c;
+      } else {                          // the wave's own: it reads them itself
+        sx[wave][e - HE][lane] = a;
+        sx[wave][LE + e - HE][lane] = c;
       }
     }
+  }
+  f32x16 dk[NK][NX], dv[NK][NX];
+  float gain[NK];
+#pragma unroll
+  for (int n = 0; n < NK; ++n) {
+    gain[n] = FIRST_GAIN;
+#pragma unroll
+    for (int x = 0; x < NX; ++x)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dk[n][x][i] = dv[n][x][i] = 0.0f;
+  }
+
+  RowPiece<DP, RT> pq, pg;
+  // a row's offset from its stage's first; where heads of a group divide the
+  // stage it is the same for all stages
+  const bool fixed = RT % p.group == 0;
+  auto offsets = [&](int at) {
+    const int t0 = p.token_of(at);
+#pragma unroll
+    for (int i = 0; i < pq.N; ++i) {
+      const int rw = at + pq.row(tid, i), t = p.token_of(rw), gh = rw - t * p.group, d = pq.col(tid, i);
+      pq.off[i] = d < p.D ? (unsigned(t - t0) * unsigned(p.q.token) + unsigned(gh) * unsigned(p.q.head) + unsigned(d)) * 2u : OUT;
+      pg.off[i] = d < p.D ? (unsigned(t - t0) * unsigned(p.g.token) + unsigned(gh) * unsigned(p.g.head) + unsigned(d)) * 2u : OUT;
+    }
+  };
+  if (fixed) offsets(from);
+  float l = 0.0f, dl = 0.0f;
+  auto fetch = [&](int at) {
+    if (!fixed) offsets(at);
+    const int64_t tok = int64_t(r.q_first) + p.token_of(at);
+    pq.load(p.q.data + tok * p.q.token + h * p.group * p.q.head, to - at, tid);
+    pg.load(p.g.data + tok * p.g.token + h * p.group * p.g.head, to - at, tid);
     if (tid < RT) {
       l = __builtin_inff();
       dl = 0.0f;
       const int rw = at + tid;
       if (rw < to) {
-        const int64_t i = (int64_t(r.q_first) + rw / p.group) * p.q_heads + h * p.group + rw % p.group;
+        const int t = p.token_of(rw);
+        const int64_t i = (int64_t(r.q_first) + t) * p.q_heads + h * p.group + rw - t * p.group;
         const float y = p.lse[i];
         if (y != -__builtin_inff()) l = y * LOG2E - (DT == SVDQ_F16 ? P_UP : 0.0f);
         dl = p.delta[i];
@@ -761,15 +910,11 @@ __global__ __launch_bounds__(256, DP == 64 ? 2 : 1) void k_cross_dkv(CrossParams
     }
   };
   auto write = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int at = (tid + 256 * i) / CH * LD + (tid + 256 * i) % CH * 8;
-      *reinterpret_cast<u32x4*>(&sq[buf][at]) = vq[i];
-      *reinterpret_cast<u32x4*>(&sg[buf][at]) = vg[i];
-    }
+    pq.write(sq[buf], tid);
+    pg.write(sg[buf], tid);
     if (tid < RT) {
       sl[buf][tid] = l;
-      sd[buf][tid] = dl;
+      sd[buf][tid] = -dl;
     }
   };
   if (from < to) {
@@ -783,55 +928,80 @@ __global__ __launch_bounds__(256, DP == 64 ? 2 : 1) void k_cross_dkv(CrossParams
     if (more) fetch(at + RT);
     if (active) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x16 s, dp;
+      for (int t = 0; t < RT / 32; ++t) {
+        if (at + 32 * t >= to) continue;
+        f32x16 s[NK], dp[NK];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+        for (int n = 0; n < NK; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NK; ++n) dp[n] = rows16(&sd[buf][32 * t], hb);      // - delta
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-          s = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sq[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), k[e], s);
-          dp = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sg[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), v[e], dp);
+          const u32x4 a = *reinterpret_cast<const u32x4*>(&sq[buf][(32 * t + m) * LD + 16 * e + 8 * hb]);
+#pragma unroll
+          for (int n = 0; n < NK; ++n) s[n] = mfma32<DT>(a, e < HE ? k[n][e < HE ? e : 0] : sx[wave][e < HE ? 0 : e - HE][lane], s[n]);
         }
-        u32x4 pf[2], ds[2];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const f32x4 ll = *reinterpret_cast<const f32x4*>(&sl[buf][32 * t + 8 * y + 4 * hb]);
-          const f32x4 dd = *reinterpret_cast<const f32x4*>(&sd[buf][32 * t + 8 * y + 4 * hb]);
+        for (int e = 0; e < NE; ++e) {
+          const u32x4 a = *reinterpret_cast<const u32x4*>(&sg[buf][(32 * t + m) * LD + 16 * e + 8 * hb]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[4 * y + i] = exp2_hw(__builtin_fmaf(s[4 * y + i], p.c, -ll[i]));
-            dp[4 * y + i] = s[4 * y + i] * (dp[4 * y + i] - dd[i]);
+          for (int n = 0; n < NK; ++n) dp[n] = mfma32<DT>(a, e < HE ? v[n][e < HE ? e : 0] : sx[wave][e < HE ? 0 : LE + e - HE][lane], dp[n]);
+        }
+        reads_ahead<2 * NE, 1, DP == 96 ? 2 : 3, NK, DP == 96 ? 0 : 4>();
+        __builtin_amdgcn_s_setprio(0);
+        u32x4 pf[NK][2], ds[NK][2];
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const f32x4 ll = *reinterpret_cast<const f32x4*>(&sl[buf][32 * t + 8 * y + 4 * hb]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s[n][4 * y + i] = exp2_hw(__builtin_fmaf(s[n][4 * y + i], p.c, -ll[i]));
+              dp[n][4 * y + i] *= s[n][4 * y + i];
+            }
           }
-        }
-        if constexpr (DT == SVDQ_F16) {
-          float top = __builtin_fabsf(dp[0]);
+          if constexpr (DT == SVDQ_F16) {
+            float top = __builtin_fabsf(dp[n][0]);
 #pragma unroll
-          for (int i = 1; i < 16; ++i) top = fmaxf(top, __builtin_fabsf(dp[i]));
-          top = half_max(top);
-          const bool over = top * gain > MOST;
-          if (__any(over)) {
-            const float lower = over ? lower_gain(top) : gain, by = lower / gain;
-            gain = lower;
+            for (int i = 1; i < 16; ++i) top = maximum(top, __builtin_fabsf(dp[n][i]));
+            top = half_max(top);
+            const bool over = top * gain[n] > MOST;
+            if (__any(over)) {
+              const float lower = over ? lower_gain(top) : gain[n], by = lower / gain[n];
+              gain[n] = lower;
 #pragma unroll
-            for (int x = 0; x < NX; ++x) dk[x] *= by;
+              for (int x = 0; x < NX; ++x) dk[n][x] *= by;
+            }
+            dp[n] *= gain[n];
           }
-          dp *= gain;
-        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          pf[i / 4][i % 4] = pack2<DT>(s[2 * i], s[2 * i + 1]);
-          ds[i / 4][i % 4] = pack2<DT>(dp[2 * i], dp[2 * i + 1]);
+          for (int i = 0; i < 8; ++i) {
+            pf[n][i / 4][i % 4] = pack2<DT>(s[n][2 * i], s[n][2 * i + 1]);
+            ds[n][i / 4][i % 4] = pack2<DT>(dp[n][2 * i], dp[n][2 * i + 1]);
+          }
         }
         const int gr = lane >> 4, i4 = lane & 15;
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int x = 0; x < NX; ++x) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int b = (32 * t + 16 * j + 4 * (gr >> 1) + (i4 >> 2)) * LD + 32 * x + 16 * (gr & 1) + 4 * (i4 & 3);
-            dv[x] = mfma32<DT>(joined(read_turned(&sg[buf][b]), read_turned(&sg[buf][b + 8 * LD])), pf[j], dv[x]);
-            dk[x] = mfma32<DT>(joined(read_turned(&sq[buf][b]), read_turned(&sq[buf][b + 8 * LD])), ds[j], dk[x]);
+            const u32x4 ga = joined(read_turned(&sg[buf][b]), read_turned(&sg[buf][b + 8 * LD]));
+            const u32x4 qa = joined(read_turned(&sq[buf][b]), read_turned(&sq[buf][b + 8 * LD]));
+#pragma unroll
+            for (int n = 0; n < NK; ++n) {
+              dv[n][x] = mfma32<DT>(ga, pf[n][j], dv[n][x]);
+              dk[n][x] = mfma32<DT>(qa, ds[n][j], dk[n][x]);
+            }
           }
         }
+        reads_ahead<4 * NX, 2, DP == 96 ? 2 : 3, NK>();
+        __builtin_amdgcn_s_setprio(0);
       }
     }
     if (more) write(buf ^ 1);
@@ -839,51 +1009,56 @@ __global__ __launch_bounds__(256, DP == 64 ? 2 : 1) void k_cross_dkv(CrossParams
     __syncthreads();
   }
   if (!active) return;
-  const float kby = DT == SVDQ_F16 ? p.scale / gain * 0x1p-10f : p.scale, vby = DT == SVDQ_F16 ? 0x1p-10f : 1.0f;
-  if (!shown) {
 #pragma unroll
-    for (int x = 0; x < NX; ++x)
+  for (int n = 0; n < NK; ++n) {
+    const int key = first + 32 * n + m;
+    const bool held = key < r.keys;
+    const int64_t state = int64_t(r.k_first) + (held ? key : 0);
+    const float kby = !shown[n] ? 0.0f : DT == SVDQ_F16 ? p.scale / gain[n] * 0x1p-10f : p.scale, vby = DT == SVDQ_F16 ? 0x1p-10f : 1.0f;
+    if (!shown[n]) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) dk[x][i] = dv[x][i] = 0.0f;
-  }
-  if (chunks <= 1) {
+      for (int x = 0; x < NX; ++x)
 #pragma unroll
-    for (int x = 0; x < NX; ++x) {
-      unsigned wk[8], wv[8];
-      columns<DT>(dk[x], shown ? kby : 0.0f, wk);
-      columns<DT>(dv[x], vby, wv);
+        for (int i = 0; i < 16; ++i) dk[n][x][i] = dv[n][x][i] = 0.0f;
+    }
+    if (chunks <= 1) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int d = 32 * x + 16 * y + 8 * hb;
-        if (held && d < p.D) {
-          *reinterpret_cast<u32x4*>(p.dk.data + state * p.dk.token + h * p.dk.head + d) = u32x4{wk[4 * y], wk[4 * y + 1], wk[4 * y + 2], wk[4 * y + 3]};
-          *reinterpret_cast<u32x4*>(p.dv.data + state * p.dv.token + h * p.dv.head + d) = u32x4{wv[4 * y], wv[4 * y + 1], wv[4 * y + 2], wv[4 * y + 3]};
+      for (int x = 0; x < NX; ++x) {
+        unsigned wk[8], wv[8];
+        columns<DT>(dk[n][x], kby, wk);
+        columns<DT>(dv[n][x], vby, wv);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int d = 32 * x + 16 * y + 8 * hb;
+          if (held && d < p.D) {
+            *reinterpret_cast<u32x4*>(p.dk.data + state * p.dk.token + h * p.dk.head + d) = u32x4{wk[4 * y], wk[4 * y + 1], wk[4 * y + 2], wk[4 * y + 3]};
+            *reinterpret_cast<u32x4*>(p.dv.data + state * p.dv.token + h * p.dv.head + d) = u32x4{wv[4 * y], wv[4 * y + 1], wv[4 * y + 2], wv[4 * y + 3]};
+          }
         }
       }
+    } else if (held) {
+      // [pair][split][key of the tiles][2][D]
+      float* part = p.key_part + ((int64_t(work.pair) * p.row_splits + split) * (int64_t(p.key_tiles) * WIDE) + key) * 2 * p.D;
+#pragma unroll
+      for (int x = 0; x < NX; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int d = 32 * x + 8 * y + 4 * hb;
+          if (d < p.D) {
+            const f32x16 &a = dk[n][x], &b = dv[n][x];
+            *reinterpret_cast<f32x4*>(part + d) = f32x4{a[4 * y] * kby, a[4 * y + 1] * kby, a[4 * y + 2] * kby, a[4 * y + 3] * kby};
+            *reinterpret_cast<f32x4*>(part + p.D + d) = f32x4{b[4 * y] * vby, b[4 * y + 1] * vby, b[4 * y + 2] * vby, b[4 * y + 3] * vby};
+          }
+        }
     }
-    return;
   }
-  if (!held) return;
-  // [pair][split][key of the tiles][2][D]
-  float* to_part = p.key_part + ((int64_t(work.pair) * p.row_splits + split) * (int64_t(p.key_tiles) * KEY_TILE) + key) * 2 * p.D;
-#pragma unroll
-  for (int x = 0; x < NX; ++x)
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const int d = 32 * x + 8 * y + 4 * hb;
-      if (d < p.D) {
-        const float by = shown ? kby : 0.0f;
-        *reinterpret_cast<f32x4*>(to_part + d) = f32x4{dk[x][4 * y] * by, dk[x][4 * y + 1] * by, dk[x][4 * y + 2] * by, dk[x][4 * y + 3] * by};
-        *reinterpret_cast<f32x4*>(to_part + p.D + d) = f32x4{dv[x][4 * y] * vby, dv[x][4 * y + 1] * vby, dv[x][4 * y + 2] * vby, dv[x][4 * y + 3] * vby};
-      }
-    }
 }
 
 // Adds the chunks of a key's gradients: a wave a key, the lower half dk, the
 // upper dv.
 template <int DT>
 __global__ __launch_bounds__(256) void k_cross_key_join(CrossParams p) {
-  const int lane = int(threadIdx.x) & 63, width = p.key_tiles * KEY_TILE;
+  const int lane = int(threadIdx.x) & 63, width = p.key_tiles * p.key_tile;
   const int64_t slot = int64_t(blockIdx.x) * 4 + (int(threadIdx.x) >> 6);
   if (slot >= int64_t(p.pairs) * width) return;
   const int pair = int(slot / width), key = int(slot % width);
@@ -941,15 +1116,26 @@ svdq_status check_scratch(const void* ws, size_t have, size_t need) {
   return aligned(ws, 256) ? SVDQ_OK : SVDQ_ERR_INVALID_ARG;
 }
 
+// 64 rows and a group's heads apart stay below OUT bytes
+bool strides_fit(std::initializer_list<const svdq_heads*> of, int group) {
+  for (const svdq_heads* h : of) {
+    const int64_t heads = h->heads > 1 ? h->head_stride : 0;
+    if (h->token_stride >= (int64_t(1) << 23) || (group > 1 && product_below(heads, group, 1, int64_t(1) << 28) < 0)) return false;
+  }
+  return true;
+}
+
 CrossParams params_of(const svdq_cross_desc* d, const CrossCut& t, int q_heads, int k_heads) {
   CrossParams p = {};
   p.q_start = d->q_start; p.k_start = d->k_start; p.mask = d->mask;
   p.tokens = t.tokens; p.states = t.states; p.max_q = d->max_q; p.max_k = d->max_k;
   p.q_heads = q_heads; p.heads = k_heads; p.group = t.group; p.pairs = t.pairs; p.D = d->head_dim;
   p.row_slots = t.row_slots; p.row_tiles = t.row_tiles; p.splits = t.splits; p.chunk = t.chunk;
-  p.key_tiles = t.key_tiles; p.row_splits = t.row_splits; p.row_chunk = t.row_chunk;
+  p.key_tile = t.key_tile; p.key_tiles = t.key_tiles; p.row_splits = t.row_splits; p.row_chunk = t.row_chunk;
+  p.by_group = t.group > 1 ? unsigned((uint64_t(1) << 32) / unsigned(t.group)) + 1 : 0;
   p.scale = d->scale;
   p.c = d->scale * LOG2E;
+  if (p.c == 0.0f) p.c = 1.2e-38f;      // every logit is zero to fp32, and a hidden -infinity stays one
   return p;
 }
 
@@ -968,9 +1154,15 @@ void launch_backward(const CrossParams& p, const CrossCut& t, hipStream_t st) {
     if (t.splits > 1) k_cross_join<DT, true><<<dim3(unsigned(ceil_div(int64_t(t.pairs) * t.row_slots, 4))), 256, 0, st>>>(p);
   }
   if (t.key_tiles == 0) return;
-  k_cross_dkv<DT, DP><<<dim3(unsigned(t.pairs) * unsigned(t.key_tiles) * unsigned(t.row_splits)), 256, 0, st>>>(p);
+  const dim3 grid(unsigned(t.pairs) * unsigned(t.key_tiles) * unsigned(t.row_splits));
+  if constexpr (DP == 64) {
+    if (t.key_tile == 256) k_cross_dkv<DT, DP, 2><<<grid, 256, 0, st>>>(p);
+    else k_cross_dkv<DT, DP, 1><<<grid, 256, 0, st>>>(p);
+  } else {
+    k_cross_dkv<DT, DP, 1><<<grid, 256, 0, st>>>(p);
+  }
   if (t.row_splits > 1)
-    k_cross_key_join<DT><<<dim3(unsigned(int64_t(t.pairs) * t.key_tiles * (KEY_TILE / 4))), 256, 0, st>>>(p);
+    k_cross_key_join<DT><<<dim3(unsigned(int64_t(t.pairs) * t.key_tiles * (t.key_tile / 4))), 256, 0, st>>>(p);
 }
 
 template <int DT>
@@ -1006,6 +1198,7 @@ extern "C" svdq_status svdq_cross_attention(const svdq_cross_desc* d, const svdq
   if (d->states > 0)                    // without states there need be none
     for (const svdq_heads* h : {k, v})
       if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
+  if (!strides_fit({k, v}, 1)) return SVDQ_ERR_UNSUPPORTED;
   if ((st = check_scratch(ws, ws_bytes, size_t(cross_part_floats(d, t, false)) * 4)) != SVDQ_OK) return st;
   CrossParams p = params_of(d, t, q->heads, k->heads);
   p.q = rows_of(q); p.k = rows_of(k); p.v = rows_of(v); p.out = rows_of(out);
@@ -1015,7 +1208,6 @@ extern "C" svdq_status svdq_cross_attention(const svdq_cross_desc* d, const svdq
     p.c = -p.c;
     p.turn = 0x80008000u;
   }
-  if (p.c == 0.0f) p.c = 1.2e-38f;      // every logit is zero to fp32, and a hidden -infinity stays one
   if (d->dtype == SVDQ_BF16) launch<SVDQ_BF16>(p, t, false, stream);
   else launch<SVDQ_F16>(p, t, false, stream);
   return launch_ok();
@@ -1052,6 +1244,7 @@ extern "C" svdq_status svdq_cross_attention_backward(const svdq_cross_desc* d, c
   if (d->states > 0)
     for (const svdq_heads* h : {k, v, dk, dv})
       if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
+  if (!strides_fit({q, g}, t.group) || !strides_fit({k, v}, 1)) return SVDQ_ERR_UNSUPPORTED;
   const int64_t delta = cross_delta_floats(t, q->heads), part = ceil_div(cross_part_floats(d, t, true), 64) * 64;
   if ((st = check_scratch(ws, ws_bytes, size_t(delta + part + cross_key_floats(d, t)) * 4)) != SVDQ_OK) return st;
   CrossParams p = params_of(d, t, q->heads, k->heads);

@@ -16,6 +16,12 @@ using svdq_kv::product_below;
 using svdq_kv::smaller;
 
 // ------------------------------------------------------------------ group norm
+#ifndef NORM_CHUNKS
+#define NORM_CHUNKS 256
+#endif
+#ifndef NORM_T
+#define NORM_T 1024
+#endif
 constexpr int NORM_MAX_BLOCK = 32;      // groups of a workgroup of the one-launch form
 
 struct NormCut {
@@ -48,13 +54,13 @@ inline svdq_status norm_cut(const svdq_norm_desc* d, bool grad, NormCut* out) {
   t.cv = d->channels / 8;
   // as many threads as leave the fewest of a wave idle
   int best = 0;
-  for (int n = 256; n <= 1024; n += 64) {
+  for (int n = NORM_T / 2; n <= 1024; n += 64) {
     const int rows = n / t.cv;
-    if (rows < 1 || (n > 512 && best > 0)) continue;
+    if (rows < 1 || (n > NORM_T && best > 0)) continue;
     const int used = rows * t.cv * 1024 / n;
-    if (used > best) { best = used; t.threads = n; t.rows = rows; }
+    if (used >= best) { best = used; t.threads = n; t.rows = rows; }
   }
-  const int64_t want = d->samples < 1 ? 512 : ceil_div(512, d->samples);
+  const int64_t want = d->samples < 1 ? NORM_CHUNKS : NORM_CHUNKS / d->samples < 1 ? 1 : NORM_CHUNKS / d->samples;
   t.chunk = ceil_div(ceil_div(d->pixels, want), t.rows) * t.rows;
   t.chunks = int(ceil_div(d->pixels, t.chunk));
   if (product_below(d->samples, int64_t(t.chunks) + 1024, 1024, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
@@ -66,6 +72,9 @@ inline svdq_status norm_cut(const svdq_norm_desc* d, bool grad, NormCut* out) {
 // kernels that walk a channel's rows by one thread a channel (norm_rows).
 inline int norm_rows(int rows) { return rows | 1; }
 inline size_t norm_lds(const NormCut& t) { return size_t(t.cv) * 8 * size_t(norm_rows(t.rows)) * 4; }
+
+// and of the join of chunks: three sums a group, three a thread where a group has several
+inline size_t norm_join_lds(int groups, int threads) { return size_t(3) * size_t(groups + threads) * 4; }
 
 inline size_t norm_bytes(const svdq_norm_desc* d, const NormCut& t, bool grad) {
   if (d->samples == 0) return 0;
@@ -113,10 +122,8 @@ struct CrossCut {
   int row_slots;            // rows of a pair: query tokens x heads of the group, the heads fastest
   int rows;                 // rows of a tile: 16 or 128
   int row_tiles, splits, chunk;   // and chunks of a pair's keys
-  int key_tiles, row_splits, row_chunk;   // gradient of keys: tiles of 128 keys, chunks of a pair's rows
+  int key_tile, key_tiles, row_splits, row_chunk;   // gradient of keys: keys of a tile, tiles, chunks of a pair's rows
 };
-
-constexpr int KEY_TILE = 128;
 
 inline svdq_status cross_cut(const svdq_cross_desc* d, int q_heads, int k_heads, int cus, bool grad, CrossCut* out) {
   CrossCut t = {};
@@ -140,14 +147,15 @@ inline svdq_status cross_cut(const svdq_cross_desc* d, int q_heads, int k_heads,
   const int64_t unit = 128;
   t.chunk = int(ceil_div(ceil_div(max_k > 0 ? max_k : 1, n), unit) * unit);
   t.splits = int(ceil_div(max_k > 0 ? max_k : 1, t.chunk));
-  t.key_tiles = int(ceil_div(max_k, KEY_TILE));
+  t.key_tile = max_k <= 128 || d->head_dim > 64 ? 128 : 256;
+  t.key_tiles = int(ceil_div(max_k, t.key_tile));
   const int64_t kitems = per * larger(t.key_tiles, 1);
   const int64_t m = clamp(int64_t(cus) * 2 / kitems, ceil_div(slots, 128));
   t.row_chunk = int(ceil_div(ceil_div(slots > 0 ? slots : 1, m), 64) * 64);
   t.row_splits = int(ceil_div(slots > 0 ? slots : 1, t.row_chunk));
   if (product_below(pairs, t.row_tiles, t.splits, svdq_kv::MAX_THREADS / 512) < 0 ||
       product_below(pairs, t.key_tiles, t.row_splits, svdq_kv::MAX_THREADS / 512) < 0 ||
-      product_below(pairs, int64_t(t.key_tiles) * KEY_TILE, 1, svdq_kv::MAX_THREADS / 64) < 0)
+      product_below(pairs, int64_t(t.key_tiles) * t.key_tile, 1, svdq_kv::MAX_THREADS / 64) < 0)
     return SVDQ_ERR_UNSUPPORTED;
   *out = t;
   return SVDQ_OK;
@@ -159,7 +167,7 @@ inline int64_t cross_part_floats(const svdq_cross_desc* d, const CrossCut& t, bo
 }
 inline int64_t cross_delta_floats(const CrossCut& t, int q_heads) { return ceil_div(int64_t(t.tokens) * q_heads, 64) * 64; }
 inline int64_t cross_key_floats(const svdq_cross_desc* d, const CrossCut& t) {
-  return t.row_splits > 1 ? int64_t(t.pairs) * t.key_tiles * KEY_TILE * t.row_splits * d->head_dim * 2 : 0;
+  return t.row_splits > 1 ? int64_t(t.pairs) * t.key_tiles * t.key_tile * t.row_splits * d->head_dim * 2 : 0;
 }
 
 }  // namespace svdq_image

@@ -74,6 +74,14 @@ __device__ __forceinline__ float slope(float z) {
   return 1.0f;
 }
 
+// groups of the channels c .. c + 7
+__device__ __forceinline__ void groups8(const NormParams& p, int c, int* g) {
+  const bool one = p.per % 8 == 0;      // the same for all threads
+  g[0] = int(unsigned(c) / unsigned(p.per));
+#pragma unroll
+  for (int e = 1; e < 8; ++e) g[e] = one ? g[0] : int(unsigned(c + e) / unsigned(p.per));
+}
+
 __device__ __forceinline__ float wave_sum(float x) {
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) x += __shfl_xor(x, m);
@@ -125,15 +133,14 @@ __global__ __launch_bounds__(512) void k_norm_whole(NormParams p) {
     weights8<DT>(p.b, c0, 0.0f, b);
   }
   const float inv_n = 1.0f / (float(p.pixels) * float(p.per));
-  const int span = p.per * p.rows;
+  const bool even = p.per % 8 == 0;     // then a thread's channels are of one group: it leaves one sum
+  const int span = even ? p.per / 8 * p.rows : p.per * p.rows;
   float s[8] = {}, mean[8], f[8];
   int gi[8];                            // group within the block
+  groups8(p, on ? 8 * piece : 0, gi);
+  // about the group's first value, so that a mean far from zero costs nothing
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // about the group's first value, so that a mean far from zero costs nothing
-    gi[e] = on ? (8 * piece + e) / p.per : 0;
-    mean[e] = h2f<DT>(p.x[int64_t(sample) * p.xs + (first + gi[e]) * p.per]);
-  }
+  for (int e = 0; e < 8; ++e) mean[e] = h2f<DT>(p.x[int64_t(sample) * p.xs + (first + gi[e]) * p.per]);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     if (!on || row + int64_t(i) * p.rows >= p.pixels) continue;
@@ -142,10 +149,12 @@ __global__ __launch_bounds__(512) void k_norm_whole(NormParams p) {
     for (int e = 0; e < 8; ++e) s[e] += f[e] - mean[e];
   }
   auto sums = [&]() {                   // sm[group] = sums of s
-    leave8(red, p.rows, s, piece, row, on);
+    if (!even) leave8(red, p.rows, s, piece, row, on);
+    else if (on) red[piece * p.rows + row] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     __syncthreads();
     for (int g = wave; g < p.block; g += waves) {
       float t = 0.0f;
+#pragma unroll 4
       for (int e = lane; e < span; e += 64) t += red[g * span + e];
       t = wave_sum(t);
       if (lane == 0) sm[g] = t;
@@ -175,7 +184,7 @@ __global__ __launch_bounds__(512) void k_norm_whole(NormParams p) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(sm[gi[e]], inv_n, p.eps));
-    if (p.stats && on && row == 0 && (8 * piece + e) % p.per == 0) {
+    if (p.stats && on && row == 0 && 8 * piece + e == gi[e] * p.per) {
       float* st = p.stats + (int64_t(sample) * p.groups + first + gi[e]) * 2;
       st[0] = mean[e];
       st[1] = rstd;
@@ -268,63 +277,81 @@ __global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
   }
 }
 
-// Mean and rstd of every group of a sample from its chunks' (in LDS).  All
-// chunks but the last have the same number of pixels.
+// Adds two values a chunk and group over a sample's chunks: all threads at once,
+// thread t has group t % groups and every (threads / groups)-th chunk, so that
+// few loads wait for another; add(group, chunk, value, sums of three).  In LDS
+// the sums of a group end up at sm[3 group ..].
+template <class F>
+__device__ __forceinline__ void join_chunks(const NormParams& p, int sample, int tid, float* sm, F add) {
+  const int threads = int(blockDim.x), wide = min(p.groups, threads), walks = threads / wide;
+  const float2* part = reinterpret_cast<const float2*>(p.part) + int64_t(sample) * p.chunks * p.groups;
+  for (int g0 = 0; g0 < p.groups; g0 += wide) {
+    const int g = g0 + tid % wide, walk = tid / wide;
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    const bool on = walk < walks && g < p.groups;
+    if (on) {
+      const float2* q = part + g;
+      const float first = q[0].x;
+#pragma unroll 8
+      for (int i = walk; i < p.chunks; i += walks) add(first, i, q[int64_t(i) * p.groups], s);
+    }
+    float* mine = sm + 3 * p.groups;
+    if (walks > 1) {
+      if (g0 > 0) __syncthreads();
+      if (on)
+        for (int e = 0; e < 3; ++e) mine[3 * tid + e] = s[e];
+      __syncthreads();
+      if (on && walk == 0)
+        for (int w = 1; w < walks; ++w)
+          for (int e = 0; e < 3; ++e) s[e] += mine[3 * (tid + w * wide) + e];
+    }
+    if (on && walk == 0)
+      for (int e = 0; e < 3; ++e) sm[3 * g + e] = s[e];
+  }
+  __syncthreads();
+}
+
+// Mean and rstd of every group of a sample from its chunks' (in LDS, [groups][3]).
+// All chunks but the last have the same number of pixels.
 __device__ __forceinline__ void join_stats(const NormParams& p, int sample, int tid, float* sm) {
-  const int lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
   const int64_t tail = p.pixels - int64_t(p.chunks - 1) * p.chunk;
   const float share = float(double(p.chunk) / double(p.pixels)), last = float(double(tail) / double(p.pixels));
-  const float per_pixel = 1.0f / float(p.per);
+  join_chunks(p, sample, tid, sm, [&](float first, int i, float2 v, float* s) {
+    const float wt = i + 1 < p.chunks ? share : last, e = v.x - first;
+    s[0] = __builtin_fmaf(wt, e, s[0]);
+    s[1] = __builtin_fmaf(wt * e, e, s[1]);
+    s[2] += v.y;
+  });
   const float2* part = reinterpret_cast<const float2*>(p.part) + int64_t(sample) * p.chunks * p.groups;
-  // 16 lanes a group, four groups a wave and step: the chunks of neighbouring
-  // groups are neighbours in memory
-  for (int g0 = wave * 4; g0 < p.groups; g0 += waves * 4) {
-    const int g = g0 + (lane & 3), at = lane >> 2;
-    const bool on = g < p.groups;
-    const float2* q = part + (on ? g : 0);
-    const float k = q[0].x;
-    float m = 0.0f, u = 0.0f, d = 0.0f;
-    for (int i = at; i < p.chunks; i += 16) {
-      const float2 v = q[int64_t(i) * p.groups];
-      const float wt = i + 1 < p.chunks ? share : last, e = v.x - k;
-      m = __builtin_fmaf(wt, e, m);
-      u = __builtin_fmaf(wt * e, e, u);
-      d += v.y;
-    }
-#pragma unroll
-    for (int s = 4; s < 64; s *= 2) {
-      m += __shfl_xor(m, s);
-      u += __shfl_xor(u, s);
-      d += __shfl_xor(d, s);
-    }
-    if (on && at == 0) {
-      const float between = fmaxf(__builtin_fmaf(-m, m, u), 0.0f);
-      const float within = d * (per_pixel / float(p.pixels));
-      sm[2 * g] = k + m;
-      sm[2 * g + 1] = 1.0f / __builtin_sqrtf(between + within + p.eps);
-    }
+  for (int g = tid; g < p.groups; g += int(blockDim.x)) {
+    const float m = sm[3 * g], u = sm[3 * g + 1], d = sm[3 * g + 2];
+    const float between = fmaxf(__builtin_fmaf(-m, m, u), 0.0f);
+    const float within = d / (float(p.per) * float(p.pixels));
+    sm[3 * g] = part[g].x + m;
+    sm[3 * g + 1] = 1.0f / __builtin_sqrtf(between + within + p.eps);
   }
   __syncthreads();
 }
 
 template <int DT, int ACT>
 __global__ __launch_bounds__(1024) void k_norm_apply(NormParams p) {
-  extern __shared__ float sm[];         // [groups][2]
+  extern __shared__ float sm[];         // [groups][3], and three a thread
   const int tid = int(threadIdx.x);
   const int sample = int(blockIdx.x) / p.chunks, chunk = int(blockIdx.x) % p.chunks;
   join_stats(p, sample, tid, sm);
   if (p.stats && chunk == 0)
-    for (int i = tid; i < 2 * p.groups; i += int(blockDim.x)) p.stats[int64_t(sample) * p.groups * 2 + i] = sm[i];
+    for (int i = tid; i < 2 * p.groups; i += int(blockDim.x)) p.stats[int64_t(sample) * p.groups * 2 + i] = sm[i / 2 * 3 + i % 2];
   const int row = tid / p.cv, piece = tid % p.cv;
   if (row >= p.rows) return;
   float w[8], b[8], a[8], m[8], f[8];
   weights8<DT>(p.w, 8 * piece, 1.0f, w);
   weights8<DT>(p.b, 8 * piece, 0.0f, b);
+  int g[8];
+  groups8(p, 8 * piece, g);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int g = (8 * piece + e) / p.per;
-    m[e] = sm[2 * g];
-    a[e] = sm[2 * g + 1] * w[e];
+    m[e] = sm[3 * g[e]];
+    a[e] = sm[3 * g[e] + 1] * w[e];
   }
   const int64_t from = int64_t(chunk) * p.chunk, n = min(p.pixels - from, p.chunk);
   const uint16_t* x = p.x + int64_t(sample) * p.xs + (from + row) * p.xp + 8 * piece;
@@ -392,9 +419,9 @@ __global__ __launch_bounds__(512) void k_norm_grad_whole(NormParams p) {
   if (on) {
     weights8<DT>(p.w, c0, 1.0f, w);
     weights8<DT>(p.b, c0, 0.0f, b);
+    groups8(p, 8 * piece, gi);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      gi[e] = (8 * piece + e) / p.per;
       const float* st = p.stats + (int64_t(sample) * p.groups + first + gi[e]) * 2;
       m[e] = st[0];
       r[e] = st[1];
@@ -474,9 +501,11 @@ __global__ __launch_bounds__(1024) void k_norm_grad_sums(NormParams p) {
     float w[8], b[8], m[8], r[8], dz[8], xh[8];
     weights8<DT>(p.w, 8 * piece, 1.0f, w);
     weights8<DT>(p.b, 8 * piece, 0.0f, b);
+    int gi[8];
+    groups8(p, 8 * piece, gi);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float* st = p.stats + (int64_t(sample) * p.groups + (8 * piece + e) / p.per) * 2;
+      const float* st = p.stats + (int64_t(sample) * p.groups + gi[e]) * 2;
       m[e] = st[0];
       r[e] = st[1];
     }
@@ -564,8 +593,8 @@ __global__ __launch_bounds__(256) void k_norm_sum(NormParams p) {
 // ... and the map's gradient; workgroups past the chunks' have the channels' sums.
 template <int DT, int ACT>
 __global__ __launch_bounds__(1024) void k_norm_grad_apply(NormParams p) {
-  extern __shared__ float sm[];         // [groups][2], or 512 for the channels' sums
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
+  extern __shared__ float sm[];         // [groups][3], and three a thread
+  const int tid = int(threadIdx.x);
   const int work = p.samples * p.chunks;
   if (int(blockIdx.x) >= work) {
     sum_channels(p, work, (int(blockIdx.x) - work) * 32, tid, sm);
@@ -573,40 +602,24 @@ __global__ __launch_bounds__(1024) void k_norm_grad_apply(NormParams p) {
   }
   const int sample = int(blockIdx.x) / p.chunks, chunk = int(blockIdx.x) % p.chunks;
   const float inv_n = 1.0f / (float(p.pixels) * float(p.per));
-  const float2* part = reinterpret_cast<const float2*>(p.part) + int64_t(sample) * p.chunks * p.groups;
-  for (int g0 = wave * 4; g0 < p.groups; g0 += waves * 4) {
-    const int g = g0 + (lane & 3);
-    const bool in = g < p.groups;
-    float t = 0.0f, u = 0.0f;
-    for (int i = lane >> 2; i < p.chunks; i += 16) {
-      const float2 v = part[int64_t(i) * p.groups + (in ? g : 0)];
-      t += v.x;
-      u += v.y;
-    }
-#pragma unroll
-    for (int s = 4; s < 64; s *= 2) {
-      t += __shfl_xor(t, s);
-      u += __shfl_xor(u, s);
-    }
-    if (in && lane < 4) {
-      sm[2 * g] = t * inv_n;
-      sm[2 * g + 1] = u * inv_n;
-    }
-  }
-  __syncthreads();
+  join_chunks(p, sample, tid, sm, [](float, int, float2 v, float* s) {
+    s[0] += v.x;
+    s[1] += v.y;
+  });
   const int row = tid / p.cv, piece = tid % p.cv;
   if (row >= p.rows) return;
   float w[8], b[8], m[8], r[8], t[8], u[8];
   weights8<DT>(p.w, 8 * piece, 1.0f, w);
   weights8<DT>(p.b, 8 * piece, 0.0f, b);
+  int gi[8];
+  groups8(p, 8 * piece, gi);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int g = (8 * piece + e) / p.per;
-    const float* st = p.stats + (int64_t(sample) * p.groups + g) * 2;
+    const float* st = p.stats + (int64_t(sample) * p.groups + gi[e]) * 2;
     m[e] = st[0];
     r[e] = st[1];
-    t[e] = sm[2 * g];
-    u[e] = sm[2 * g + 1];
+    t[e] = sm[3 * gi[e]] * inv_n;
+    u[e] = sm[3 * gi[e] + 1] * inv_n;
   }
   const int64_t from = int64_t(chunk) * p.chunk, n = min(p.pixels - from, p.chunk);
   const uint16_t* x = p.x + int64_t(sample) * p.xs + (from + row) * p.xp + 8 * piece;
@@ -688,7 +701,7 @@ void launch_norm(const NormParams& p, const NormCut& t, hipStream_t st) {
   }
   const dim3 grid(unsigned(p.samples) * unsigned(t.chunks));
   k_norm_stats<DT><<<grid, t.threads, 2 * red, st>>>(p);
-  k_norm_apply<DT, ACT><<<grid, t.threads, size_t(p.groups) * 8, st>>>(p);
+  k_norm_apply<DT, ACT><<<grid, t.threads, norm_join_lds(p.groups, t.threads), st>>>(p);
 }
 
 template <int DT, int ACT>
@@ -706,8 +719,7 @@ void launch_norm_grad(const NormParams& p, const NormCut& t, hipStream_t st) {
   }
   const unsigned work = unsigned(p.samples) * unsigned(t.chunks);
   k_norm_grad_sums<DT, ACT><<<dim3(work), t.threads, red, st>>>(p);
-  const size_t lds = size_t(p.groups) * 8 > 2048 ? size_t(p.groups) * 8 : 2048;
-  k_norm_grad_apply<DT, ACT><<<dim3(work + (sums ? tiles : 0)), t.threads, lds, st>>>(p);
+  k_norm_grad_apply<DT, ACT><<<dim3(work + (sums ? tiles : 0)), t.threads, norm_join_lds(p.groups, t.threads), st>>>(p);
 }
 
 template <int DT>

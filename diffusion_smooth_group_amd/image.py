@@ -108,12 +108,25 @@ def _run(t):
 
 
 def _map(t, name, like, dev):
-    if t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != dev:
-        raise ValueError(f"{name}: a {like.dtype} tensor {tuple(like.shape)} on cuda:{dev} is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    step = _run(t)
-    if step is None or t.stride(-1) != 1:
-        raise ValueError(f"{name}: channels last with unit stride and one run of pixels is needed, got {tuple(t.shape)} with strides {t.stride()}")
-    return svdq_map(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, step)
+    shape = like.shape
+    if t.is_contiguous():
+        c = shape[-1]
+        step, first = c, (t.numel() // shape[0] if shape[0] > 1 else 0)
+    else:
+        step, first = _run(t), (t.stride(0) if shape[0] > 1 else 0)
+        if step is None or t.stride(-1) != 1:
+            raise ValueError(f"{name}: channels last with unit stride and one run of pixels is needed, got {tuple(t.shape)} with strides {t.stride()}")
+    if t is not like and t.shape != shape or t.dtype is not like.dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: a {like.dtype} tensor {tuple(shape)} on cuda:{dev} is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return svdq_map(t.data_ptr(), first, step)
+
+
+def _new_map(like, dev):
+    """An output like `like`, channels last, and its view for the call."""
+    t = torch.empty_like(like)
+    if not t.is_contiguous() and (t.stride(-1) != 1 or _run(t) is None):
+        t = like.new_empty(like.shape)
+    return t, _map(t, "out", like, dev)
 
 
 def _norm_desc(x, groups, weight, bias, eps, act, dev):
@@ -122,11 +135,9 @@ def _norm_desc(x, groups, weight, bias, eps, act, dev):
     if act not in ACT:
         raise ValueError(f"act: one of {list(ACT)} is needed, got {act!r}")
     n, c = x.shape[0], x.shape[-1]
-    p = [None, None]
-    for i, (w, name) in enumerate(((weight, "weight"), (bias, "bias"))):
-        if w is not None:
-            p[i] = kv._weight(w, name, c, x.dtype, dev)
-    return svdq_norm_desc(n, math.prod(x.shape[1:-1]), _size(c, "channels"), _size(groups, "groups"), _code(x.dtype), ACT[act], eps, *p)
+    dtype = x.dtype
+    return svdq_norm_desc(n, math.prod(x.shape[1:-1]), _size(c, "channels"), _size(groups, "groups"), _code(dtype), ACT[act], eps,
+                          kv._weight(weight, "weight", c, dtype, dev), kv._weight(bias, "bias", c, dtype, dev))
 
 
 def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: Optional[str] = None, out=None, ws=None,
@@ -141,10 +152,9 @@ def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: O
         d = _norm_desc(x, groups, weight, bias, eps, act, dev)
         mx = _map(x, "x", x, dev)
         if out is None:
-            out = torch.empty_like(x)
-            if _run(out) is None or out.stride(-1) != 1:
-                out = x.new_empty(x.shape)
-        mo = _map(out, "out", x, dev)
+            out, mo = _new_map(x, dev)
+        else:
+            mo = _map(out, "out", x, dev)
         stats = x.new_empty((x.shape[0], groups, 2), dtype=torch.float32) if return_stats else None
         ws, n = _workspace(ws, x, "svdq_group_norm_workspace", d)
         _call("svdq_group_norm", d, mx, mo, _address(stats), _address(ws), n, _stream(x))
@@ -160,10 +170,9 @@ def group_norm_backward(g, x, stats, groups: int, weight=None, bias=None, act: O
         d = _norm_desc(x, groups, weight, bias, 0.0, act, dev)
         mx, mg = _map(x, "x", x, dev), _map(g, "g", x, dev)
         if dx is None:
-            dx = torch.empty_like(x)
-            if _run(dx) is None or dx.stride(-1) != 1:
-                dx = x.new_empty(x.shape)
-        md = _map(dx, "dx", x, dev)
+            dx, md = _new_map(x, dev)
+        else:
+            md = _map(dx, "dx", x, dev)
         if stats.dtype is not torch.float32 or stats.shape != (x.shape[0], groups, 2) or not stats.is_contiguous() or stats.get_device() != dev:
             raise ValueError(f"stats: a contiguous float32 tensor {(x.shape[0], groups, 2)} on cuda:{dev} is needed, "
                              f"got {stats.dtype} {tuple(stats.shape)} on {stats.device}")
@@ -209,59 +218,70 @@ def group_norm_autograd(x, weight, bias, groups: int, eps: float = 1e-5, act: Op
 def _stride(t):
     """Stride between the tokens of t [tokens, heads, D] or [requests, tokens,
     heads, D], None where they are not one run."""
-    if t.dim() == 3:
-        return t.stride(0)
+    s = t.stride()
+    if len(s) == 3:
+        return s[0]
     b, n = t.shape[:2]
-    if n <= 1:
-        return t.stride(0)
-    return t.stride(1) if b == 1 or t.stride(0) == n * t.stride(1) else None
+    return s[0] if n <= 1 else s[1] if b == 1 or s[0] == n * s[1] else None
 
 
-def _rows(t, name, lead, dim, dtype, dev):
-    step = _stride(t)
-    if t.shape[:-2] != lead or t.shape[-1] != dim or t.stride(-1) != 1 or step is None or t.dtype is not dtype or t.get_device() != dev:
-        raise ValueError(f"{name}: a {dtype} tensor {(*lead, 'heads', dim)} on cuda:{dev} with unit stride in the last dimension and one run "
-                         f"of tokens is needed, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    h = t.shape[-2]
-    return svdq_heads(t.data_ptr(), step if math.prod(lead) > 1 else 0, t.stride(-2) if h > 1 else 0, h)
+def _rows(t, name, b, n, dim, dtype, dev):
+    """t as rows of heads: [n, heads, dim], or [b, n, heads, dim] where b is not None."""
+    s = t.stride()
+    if b is None:
+        (m, h, d), (step, wide, one) = t.shape, s
+        fits = m == n
+    else:
+        (r, m, h, d), (far, step, wide, one) = t.shape, s
+        fits = r == b and m == n
+        if n <= 1:
+            step = far
+        elif b > 1 and far != n * step:
+            fits = False
+    if not fits or d != dim or one != 1 or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: a {dtype} tensor {(n, 'heads', dim) if b is None else (b, n, 'heads', dim)} on cuda:{dev} with unit stride in the "
+                         f"last dimension and one run of tokens is needed, got {t.dtype} {tuple(t.shape)} with strides {s} on {t.device}")
+    return svdq_heads(t.data_ptr(), step if n * (b or 1) > 1 else 0, wide if h > 1 else 0, h)
 
 
-def _out(t, name, like, dev):
+def _out(t, name, like, b, n, dim, dtype, dev):
     """An output like `like`, a new one where t is None, and its view for the call."""
     if t is None:
         t = torch.empty_like(like)
-        if _stride(t) is None or t.stride(-1) != 1:
+        if not t.is_contiguous() and (t.stride(-1) != 1 or _stride(t) is None):
             t = like.new_empty(like.shape)
     elif t.shape != like.shape:
         raise ValueError(f"{name}: {tuple(like.shape)} is needed, got {tuple(t.shape)}")
-    return t, _rows(t, name, like.shape[:-2], like.shape[-1], like.dtype, dev)
+    return t, _rows(t, name, b, n, dim, dtype, dev)
 
 
-def _cross_desc(q, k, q_start, k_start, max_q, max_k, mask, scale, dev):
-    if q.dim() == 4 and k.dim() == 4:
+def _cross_desc(q, k, v, q_start, k_start, max_q, max_k, mask, scale, dev):
+    """The call's descriptor, and (requests or None, tokens, states) as _rows takes them."""
+    dims = q.dim(), k.dim(), v.dim()
+    if dims == (4, 4, 4):
         if q_start is not None or k_start is not None or max_q is not None or max_k is not None:
             raise ValueError("q_start, k_start, max_q and max_k go with rows [tokens, heads, D]")
-        b, max_q, max_k = q.shape[0], q.shape[1], k.shape[1]
-        if k.shape[0] != b:
-            raise ValueError(f"k: states of {b} requests are needed, got {tuple(k.shape)}")
-        tokens, states, qs, ks = b * max_q, b * max_k, None, None
-    elif q.dim() == 3 and k.dim() == 3:
+        b, n, _, dim = q.shape
+        m = k.shape[1]
+        requests, max_q, max_k, tokens, states, qs, ks = b, n, m, b * n, b * m, None, None
+    elif dims == (3, 3, 3):
         if q_start is None or k_start is None or max_q is None or max_k is None:
             raise ValueError("rows [tokens, heads, D] need q_start, k_start, max_q and max_k")
-        b, tokens, states = q_start.numel() - 1, q.shape[0], k.shape[0]
-        if b < 0:
+        b, (n, _, dim), m = None, q.shape, k.shape[0]
+        requests, tokens, states = q_start.numel() - 1, n, m
+        if requests < 0:
             raise ValueError("q_start: [requests + 1] is needed, got no entry")
-        qs, ks = kv._int32(q_start, "q_start", b + 1, dev), kv._int32(k_start, "k_start", b + 1, dev)
+        qs, ks = kv._int32(q_start, "q_start", requests + 1, dev), kv._int32(k_start, "k_start", requests + 1, dev)
     else:
-        raise ValueError(f"q and k: both [tokens, heads, D] or both [requests, tokens, heads, D] are needed, got {tuple(q.shape)} and {tuple(k.shape)}")
+        raise ValueError(f"q, k, v: all [tokens, heads, D] or all [requests, tokens, heads, D] are needed, got {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
     pm = None
     if mask is not None:
         if mask.dtype not in (torch.bool, torch.uint8) or mask.numel() != states or not mask.is_contiguous() or mask.get_device() != dev:
             raise ValueError(f"mask: a contiguous bool tensor of {states} entries on cuda:{dev} is needed, got {mask.dtype} {tuple(mask.shape)} on {mask.device}")
         pm = mask.data_ptr()
-    dim = q.shape[-1]
-    return svdq_cross_desc(b, tokens, states, _size(dim, "head_dim"), _code(q.dtype), _size(max_q, "max_q"), _size(max_k, "max_k"),
-                           (1.0 / math.sqrt(dim) if dim else 1.0) if scale is None else scale, qs, ks, pm)
+    d = svdq_cross_desc(requests, tokens, states, _size(dim, "head_dim"), _code(q.dtype), _size(max_q, "max_q"), _size(max_k, "max_k"),
+                        (1.0 / math.sqrt(dim) if dim else 1.0) if scale is None else scale, qs, ks, pm)
+    return d, b, n, m, dim
 
 
 def cross_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] = None, max_k: Optional[int] = None, mask=None,
@@ -279,13 +299,13 @@ def cross_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] = 
     without D."""
     with _on(stream, q):
         dev = kv._current_device()
-        d = _cross_desc(q, k, q_start, k_start, max_q, max_k, mask, scale, dev)
-        dim, lead, kept, dtype = q.shape[-1], q.shape[:-2], k.shape[:-2], q.dtype
-        hq, hk, hv = _rows(q, "q", lead, dim, dtype, dev), _rows(k, "k", kept, dim, dtype, dev), _rows(v, "v", kept, dim, dtype, dev)
-        out, ho = _out(out, "out", q, dev)
+        d, b, n, m, dim = _cross_desc(q, k, v, q_start, k_start, max_q, max_k, mask, scale, dev)
+        dtype = q.dtype
+        hq, hk, hv = _rows(q, "q", b, n, dim, dtype, dev), _rows(k, "k", b, m, dim, dtype, dev), _rows(v, "v", b, m, dim, dtype, dev)
+        out, ho = _out(out, "out", q, b, n, dim, dtype, dev)
         lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if return_lse else None
-        ws, n = _workspace(ws, q, "svdq_cross_attention_workspace", d, q.shape[-2], k.shape[-2])
-        _call("svdq_cross_attention", d, hq, hk, hv, ho, _address(lse), _address(ws), n, _stream(q))
+        ws, size = _workspace(ws, q, "svdq_cross_attention_workspace", d, hq.heads, hk.heads)
+        _call("svdq_cross_attention", d, hq, hk, hv, ho, _address(lse), _address(ws), size, _stream(q))
         return (out, lse) if return_lse else out
 
 
@@ -296,15 +316,17 @@ def cross_attention_backward(g, q, k, v, out, lse, q_start=None, k_start=None, m
     hides get zeros; rows and states of no request are not written."""
     with _on(stream, q):
         dev = kv._current_device()
-        d = _cross_desc(q, k, q_start, k_start, max_q, max_k, mask, scale, dev)
-        dim, lead, kept, dtype = q.shape[-1], q.shape[:-2], k.shape[:-2], q.dtype
-        hq, ho, hg = (_rows(t, n, lead, dim, dtype, dev) for t, n in ((q, "q"), (out, "out"), (g, "g")))
-        hk, hv = _rows(k, "k", kept, dim, dtype, dev), _rows(v, "v", kept, dim, dtype, dev)
+        d, b, n, m, dim = _cross_desc(q, k, v, q_start, k_start, max_q, max_k, mask, scale, dev)
+        dtype = q.dtype
+        hq, ho, hg = _rows(q, "q", b, n, dim, dtype, dev), _rows(out, "out", b, n, dim, dtype, dev), _rows(g, "g", b, n, dim, dtype, dev)
+        hk, hv = _rows(k, "k", b, m, dim, dtype, dev), _rows(v, "v", b, m, dim, dtype, dev)
         if lse.dtype is not torch.float32 or lse.shape != q.shape[:-1] or not lse.is_contiguous() or lse.get_device() != dev:
             raise ValueError(f"lse: a contiguous float32 tensor {tuple(q.shape[:-1])} on cuda:{dev} is needed, got {lse.dtype} {tuple(lse.shape)} on {lse.device}")
-        (dq, hdq), (dk, hdk), (dv, hdv) = _out(dq, "dq", q, dev), _out(dk, "dk", k, dev), _out(dv, "dv", v, dev)
-        ws, n = _workspace(ws, q, "svdq_cross_attention_backward_workspace", d, q.shape[-2], k.shape[-2])
-        _call("svdq_cross_attention_backward", d, hq, hk, hv, ho, lse.data_ptr(), hg, hdq, hdk, hdv, _address(ws), n, _stream(q))
+        dq, hdq = _out(dq, "dq", q, b, n, dim, dtype, dev)
+        dk, hdk = _out(dk, "dk", k, b, m, dim, dtype, dev)
+        dv, hdv = _out(dv, "dv", v, b, m, dim, dtype, dev)
+        ws, size = _workspace(ws, q, "svdq_cross_attention_backward_workspace", d, hq.heads, hk.heads)
+        _call("svdq_cross_attention_backward", d, hq, hk, hv, ho, lse.data_ptr(), hg, hdq, hdk, hdv, _address(ws), size, _stream(q))
         return dq, dk, dv
 
 

@@ -76,7 +76,8 @@ svdq_status svdq_group_norm_backward(const svdq_norm_desc* desc, const svdq_map*
 
 /* Which rows and encoder states belong together.  Rows of heads are svdq_heads
  * (svdq_kv.h); k and v have as many heads, which divides the number of q's:
- * query head h reads head h / (q_heads / k_heads). */
+ * query head h reads head h / (q_heads / k_heads).  Token strides are below
+ * 2^23 elements, and the heads of a group lie within 2^28. */
 typedef struct {
   int64_t requests;
   int64_t tokens, states;   /* query rows and encoder states in all, below 2^31 */
