@@ -238,6 +238,61 @@ struct RowPiece {
   }
 };
 
+// The 128 rows of a tile, by way of LDS: in memory they are whole lines (8 lanes a
+// row of 64), as operands and results 32 bytes of every row at a time, which memory
+// took 1.4 times as long for (2 x 4096 rows, 10 heads of 64, without any key: 7.9 us
+// against REPLACE).
+template <int DP>
+struct TileRows {
+  static constexpr int CH = DP / 8, N = 128 * CH / 256, LD = row_of<DP>();
+  u32x4 v[N];
+  __device__ __forceinline__ void load(const CrossParams& p, const CrossRange& r, const Rows& from, int first, int h, int tid) {
+    const int rows = r.rows * p.group;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int rw = first + (tid + 256 * i) / CH, d = (tid + 256 * i) % CH * 8;
+      v[i] = u32x4{0, 0, 0, 0};
+      if (rw < rows && d < p.D) {
+        const int t = p.token_of(rw);
+        v[i] = *reinterpret_cast<const u32x4*>(from.data + (int64_t(r.q_first) + t) * from.token + (h * p.group + rw - t * p.group) * from.head + d);
+      }
+    }
+  }
+  __device__ __forceinline__ void write(uint16_t* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + (tid + 256 * i) / CH * LD + (tid + 256 * i) % CH * 8) = v[i];
+  }
+};
+
+// A wave's 32 rows of a result (its transpose in o, times `by`) to memory by way of
+// its part of LDS, which no other wave uses.
+template <int DT, int DP>
+__device__ __forceinline__ void store_rows(const CrossParams& p, const CrossRange& r, const Rows& to, uint16_t* lds, const f32x16* o, float by,
+                                           int first, int h, int lane) {
+  constexpr int CH = DP / 8, LD = row_of<DP>();
+  const int m = lane & 31, hb = lane >> 5, rows = r.rows * p.group;
+#pragma unroll
+  for (int x = 0; x < DP / 32; ++x) {
+    unsigned w[8];
+    columns<DT>(o[x], by, w);
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      *reinterpret_cast<u32x4*>(lds + m * LD + 32 * x + 16 * y + 8 * hb) = u32x4{w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]};
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+  for (int i = 0; i < 32 * CH / 64; ++i) {
+    const int row = (lane + 64 * i) / CH, d = (lane + 64 * i) % CH * 8, rw = first + row;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * LD + d);
+    if (rw < rows && d < p.D) {
+      const int t = p.token_of(rw);
+      *reinterpret_cast<u32x4*>(to.data + (int64_t(r.q_first) + t) * to.token + (h * p.group + rw - t * p.group) * to.head + d) = v;
+    }
+  }
+}
+
 // bit t: state `at` + t of the request is seen, t < 64
 __device__ __forceinline__ uint64_t seen(const CrossParams& p, const CrossRange& r, int at, int lane) {
   bool on = at + lane < r.keys;
@@ -276,11 +331,11 @@ __device__ __forceinline__ f32x16 rows16(const float* at, int hb) {
 // O^T = V^T P^T as it stands; V^T comes out of LDS by transposing reads of four
 // keys each.
 template <int DT, int DP>
-__global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
+__global__ __launch_bounds__(256, DP == 128 ? 2 : 3) void k_cross_rows(CrossParams p) {
   constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
-  __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * LD];
+  __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * LD];     // 128 rows' room in all
   __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * LD];
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 31, hb = lane >> 5;
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 31, hb = lane >> 5;
   const PairWork work(blockIdx.x, p.pairs, p.row_tiles * p.splits);
   const int tile = work.tile / p.splits, split = work.tile % p.splits, req = work.pair / p.heads, h = work.pair % p.heads;
   const CrossRange r(p, req);
@@ -293,23 +348,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
   const bool active = tile * 128 + wave * 32 < rows;     // of the wave
   const int64_t tok = int64_t(r.q_first) + (row < rows ? p.token_of(row) : 0);
   const int head = h * p.group + (row < rows ? row % p.group : 0);
-  u32x4 q[NE];
-#pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    q[e] = u32x4{0, 0, 0, 0};
-    if (row < rows && 16 * e + 8 * hb < p.D) {
-      q[e] = *reinterpret_cast<const u32x4*>(p.q.data + tok * p.q.token + head * p.q.head + 16 * e + 8 * hb);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[e][i] ^= p.turn;
-    }
-  }
-  f32x16 o[NX];
-#pragma unroll
-  for (int x = 0; x < NX; ++x)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[x][i] = 0.0f;
-  float base = 0.0f, limit = -__builtin_inff(), sum = 0.0f;
-
+  // the first keys are on their way before the rows
   const uint16_t* kp = p.k.data + (int64_t(r.k_first) + from) * p.k.token + h * p.k.head;
   const uint16_t* vp = p.v.data + (int64_t(r.k_first) + from) * p.v.token + h * p.v.head;
   Piece<DP, KT> pk, pv;
@@ -320,6 +359,29 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
     pk.load(kp, to - from, tid);
     pv.load(vp, to - from, tid);
     see = seen(p, r, from, lane);
+  }
+  u32x4 q[NE];
+  {
+    TileRows<DP> all;
+    all.load(p, r, p.q, tile * 128, h, tid);
+    all.write(sk[0], tid);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      q[e] = *reinterpret_cast<const u32x4*>(&sk[0][(wave * 32 + m) * LD + 16 * e + 8 * hb]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[e][i] ^= p.turn;
+    }
+    __syncthreads();
+  }
+  f32x16 o[NX];
+#pragma unroll
+  for (int x = 0; x < NX; ++x)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[x][i] = 0.0f;
+  float base = 0.0f, limit = -__builtin_inff(), sum = 0.0f;
+
+  if (from < to) {
     if (see != ~uint64_t(0)) pv.hide(see, tid);
     pk.write(sk[0], tid);
     pv.write(sv[0], tid);
@@ -348,7 +410,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
           const u32x4 a = *reinterpret_cast<const u32x4*>(&sk[buf][(32 * t + m) * LD + 16 * e + 8 * hb]);
           s[t] = mfma32<DT>(a, q[e], s[t]);
         }
-        reads_ahead<NE, 1, 4>();
+        reads_ahead<NE, 1, DP == 96 ? 3 : 4>();
       }
       __builtin_amdgcn_s_setprio(0);
       if (see != ~uint64_t(0)) {
@@ -389,7 +451,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
           o[x] = mfma32<DT>(joined(read_turned(b), read_turned(b + 8 * LD)), pf[j], o[x]);
         }
       }
-      reads_ahead<2 * T * NX, 2, 4>();
+      reads_ahead<2 * T * NX, 2, DP == 96 ? 3 : 4>();
       __builtin_amdgcn_s_setprio(0);
     }
     if (more) {
@@ -407,16 +469,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
   const bool whole = chunks <= 1;
   if (whole) {
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int x = 0; x < NX; ++x) {
-      unsigned w[8];
-      columns<DT>(o[x], inv, w);
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-        if (row < rows && 32 * x + 16 * y + 8 * hb < p.D)
-          *reinterpret_cast<u32x4*>(p.out.data + tok * p.out.token + head * p.out.head + 32 * x + 16 * y + 8 * hb) =
-              u32x4{w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]};
-    }
+    store_rows<DT, DP>(p, r, p.out, sk[0] + wave * 32 * LD, o, inv, tile * 128 + wave * 32, h, lane);
     if (p.lse && row < rows && hb == 0) p.lse[tok * p.q_heads + head] = row_lse(base, sum);
     return;
   }
@@ -438,11 +491,11 @@ __global__ __launch_bounds__(256, 2) void k_cross_rows(CrossParams p) {
 // K as operands, V through a piece of LDS of the wave's own for its transposition.
 // The waves meet at the end.
 template <int DT, int DP>
-__global__ __launch_bounds__(256) void k_cross_few(CrossParams p) {
+__global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void k_cross_few(CrossParams p) {
   constexpr int NJ = DP / 32, NX = DP / 16, LD = row_of<DP>(), CH = DP / 8, NV = 32 * CH / 64;
   __shared__ __attribute__((aligned(16))) uint16_t sv[4][32 * LD];
   __shared__ float wave_base[4][16], wave_sum[4][16];
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 15, b = lane >> 4;
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 15, b = lane >> 4;
   const PairWork work(blockIdx.x, p.pairs, p.row_tiles * p.splits);
   const int tile = work.tile / p.splits, split = work.tile % p.splits, req = work.pair / p.heads, h = work.pair % p.heads;
   const CrossRange r(p, req);
@@ -473,24 +526,27 @@ __global__ __launch_bounds__(256) void k_cross_few(CrossParams p) {
   uint16_t* mine = sv[wave];
   u32x4 kf[2][NJ], vf[NV];
   bool on = false;
+  // offsets of a lane's pieces; pieces of V are whole rows apart where CH divides 64
+  constexpr bool EVEN = 64 % CH == 0;
+  unsigned koff[NJ], voff[EVEN ? 1 : NV];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) koff[j] = 32 * j + 8 * b < p.D ? (unsigned(m) * unsigned(p.k.token) + unsigned(32 * j + 8 * b)) * 2u : OUT;
+  auto vrow = [&](int i) { return EVEN ? lane / CH + 64 / CH * i : (lane + 64 * i) / CH; };
+  auto vcol = [&](int i) { return (EVEN ? lane : lane + 64 * i) % CH * 8; };
+#pragma unroll
+  for (int i = 0; i < (EVEN ? 1 : NV); ++i)
+    voff[i] = vcol(i) < p.D ? (unsigned(vrow(i)) * unsigned(p.v.token) + unsigned(vcol(i))) * 2u : OUT;
+  const unsigned kstep = 32u * unsigned(p.k.token), vstep = EVEN ? unsigned(64 / CH) * unsigned(p.v.token) * 2u : 0u;
   auto fetch = [&](int at) {            // keys at .. at + 31, within [from, to)
-    const uint16_t* k = p.k.data + (int64_t(r.k_first) + at) * p.k.token + h * p.k.head;
-    const uint16_t* v = p.v.data + (int64_t(r.k_first) + at) * p.v.token + h * p.v.head;
+    const __amdgpu_buffer_rsrc_t kb = buffer(p.k.data + (int64_t(r.k_first) + at) * p.k.token + h * p.k.head);
+    const __amdgpu_buffer_rsrc_t vb = buffer(p.v.data + (int64_t(r.k_first) + at) * p.v.token + h * p.v.head);
     const int n = to - at;
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        kf[a][j] = u32x4{0, 0, 0, 0};
-        if (16 * a + m < n && 32 * j + 8 * b < p.D)
-          kf[a][j] = *reinterpret_cast<const u32x4*>(k + (16 * a + m) * p.k.token + 32 * j + 8 * b);
-      }
+      for (int j = 0; j < NJ; ++j) kf[a][j] = load16(kb, 16 * a + m < n ? koff[j] : OUT, a * kstep);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int t = (lane + 64 * i) / CH, d = (lane + 64 * i) % CH * 8;
-      vf[i] = u32x4{0, 0, 0, 0};
-      if (t < n && d < p.D) vf[i] = *reinterpret_cast<const u32x4*>(v + t * p.v.token + d);
-    }
+    for (int i = 0; i < NV; ++i) vf[i] = load16(vb, vrow(i) < n ? voff[EVEN ? 0 : i] : OUT, i * vstep);
     on = lane < 32 && lane < n;
     if (p.mask && on) on = p.mask[int64_t(r.k_first) + at + lane] != 0;
   };
@@ -498,24 +554,23 @@ __global__ __launch_bounds__(256) void k_cross_few(CrossParams p) {
   if (at < to) fetch(at);
   for (; at < to; at += 128) {
     const unsigned see = unsigned(__ballot(on));
-    if (see == 0u) {
-      if (at + 128 < to) fetch(at + 128);
-      continue;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int t = (lane + 64 * i) / CH, d = (lane + 64 * i) % CH * 8;
-      if (see != ~0u && !((see >> t) & 1u)) vf[i] = u32x4{0, 0, 0, 0};
-      *reinterpret_cast<u32x4*>(mine + t * LD + d) = vf[i];
-    }
     f32x4 s[2];
+    if (see != 0u) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      s[a] = f32x4{0, 0, 0, 0};
+      for (int i = 0; i < NV; ++i) {
+        const int t = vrow(i), d = vcol(i);
+        if (see != ~0u && !((see >> t) & 1u)) vf[i] = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(mine + t * LD + d) = vf[i];
+      }
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) s[a] = mfma16<DT>(kf[a][j], q[j], s[a]);
+      for (int a = 0; a < 2; ++a) {
+        s[a] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) s[a] = mfma16<DT>(kf[a][j], q[j], s[a]);
+      }
     }
     if (at + 128 < to) fetch(at + 128);
+    if (see == 0u) continue;
     if (see != ~0u) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i / 4][i % 4] = (see >> (16 * (i / 4) + 4 * b + i % 4)) & 1u ? s[i / 4][i % 4] : -__builtin_inff();
@@ -652,7 +707,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
   __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * LD];
   __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * LD];
   __shared__ __attribute__((aligned(16))) float sb[2][KT];
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 31, hb = lane >> 5;
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 31, hb = lane >> 5;
   const PairWork work(blockIdx.x, p.pairs, p.row_tiles * p.splits);
   const int tile = work.tile / p.splits, split = work.tile % p.splits, req = work.pair / p.heads, h = work.pair % p.heads;
   const CrossRange r(p, req);
@@ -665,22 +720,47 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
   const bool active = tile * 128 + wave * 32 < rows;
   const int64_t tok = int64_t(r.q_first) + (row < rows ? p.token_of(row) : 0);
   const int head = h * p.group + (row < rows ? row % p.group : 0);
+  // the first keys are on their way before the rows
+  const uint16_t* kp = p.k.data + (int64_t(r.k_first) + from) * p.k.token + h * p.k.head;
+  const uint16_t* vp = p.v.data + (int64_t(r.k_first) + from) * p.v.token + h * p.v.head;
+  Piece<DP, KT> pk, pv;
+  pk.rows(p.k.token, p.D, tid);
+  pv.rows(p.v.token, p.D, tid);
+  uint64_t see = 0;
+  if (from < to) {
+    pk.load(kp, to - from, tid);
+    pv.load(vp, to - from, tid);
+    see = seen(p, r, from, lane);
+  }
   u32x4 q[NE], g[NE];
   float delta = 0.0f;
+  {
+    TileRows<DP> all, of_g, of_out;
+    all.load(p, r, p.q, tile * 128, h, tid);
+    of_g.load(p, r, p.g, tile * 128, h, tid);
+    of_out.load(p, r, p.out, tile * 128, h, tid);
+    all.write(sk[0], tid);
+    of_g.write(sv[0], tid);
+    __syncthreads();
+    const int mine = (wave * 32 + m) * LD + 8 * hb;
 #pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    q[e] = g[e] = u32x4{0, 0, 0, 0};
-    const int d = 16 * e + 8 * hb;
-    if (row < rows && d < p.D) {
-      q[e] = *reinterpret_cast<const u32x4*>(p.q.data + tok * p.q.token + head * p.q.head + d);
-      g[e] = *reinterpret_cast<const u32x4*>(p.g.data + tok * p.g.token + head * p.g.head + d);
-      const u32x4 y = *reinterpret_cast<const u32x4*>(p.out.data + tok * p.out.token + head * p.out.head + d);
+    for (int e = 0; e < NE; ++e) {
+      q[e] = *reinterpret_cast<const u32x4*>(&sk[0][mine + 16 * e]);
+      g[e] = *reinterpret_cast<const u32x4*>(&sv[0][mine + 16 * e]);
+    }
+    __syncthreads();
+    of_out.write(sk[0], tid);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      const u32x4 y = *reinterpret_cast<const u32x4*>(&sk[0][mine + 16 * e]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        delta = __builtin_fmaf(h2f<DT>(g[e][i] & 0xFFFFu), h2f<DT>(y[i] & 0xFFFFu), delta);
-        delta = __builtin_fmaf(h2f<DT>(g[e][i] >> 16), h2f<DT>(y[i] >> 16), delta);
+        delta = __builtin_fmaf(first_half<DT>(g[e][i]), first_half<DT>(y[i]), delta);
+        delta = __builtin_fmaf(second_half<DT>(g[e][i]), second_half<DT>(y[i]), delta);
       }
     }
+    __syncthreads();
   }
   delta = half_sum(delta);
   float lse = __builtin_inff();
@@ -696,16 +776,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
     for (int i = 0; i < 16; ++i) acc[x][i] = 0.0f;
   float gain = FIRST_GAIN;
 
-  const uint16_t* kp = p.k.data + (int64_t(r.k_first) + from) * p.k.token + h * p.k.head;
-  const uint16_t* vp = p.v.data + (int64_t(r.k_first) + from) * p.v.token + h * p.v.head;
-  Piece<DP, KT> pk, pv;
-  pk.rows(p.k.token, p.D, tid);
-  pv.rows(p.v.token, p.D, tid);
-  uint64_t see = 0;
   if (from < to) {
-    pk.load(kp, to - from, tid);
-    pv.load(vp, to - from, tid);
-    see = seen(p, r, from, lane);
     if (see != ~uint64_t(0)) { pk.hide(see, tid); pv.hide(see, tid); }
     if (wave == 0) leave_bias(sb[0], see, p.c, lane);
     pk.write(sk[0], tid);
@@ -791,16 +862,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
   }
   const float by = DT == SVDQ_F16 ? p.scale / gain : p.scale;
   if (chunks <= 1) {
-#pragma unroll
-    for (int x = 0; x < NX; ++x) {
-      unsigned w[8];
-      columns<DT>(acc[x], by, w);
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-        if (row < rows && 32 * x + 16 * y + 8 * hb < p.D)
-          *reinterpret_cast<u32x4*>(p.dq.data + tok * p.dq.token + head * p.dq.head + 32 * x + 16 * y + 8 * hb) =
-              u32x4{w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]};
-    }
+    store_rows<DT, DP>(p, r, p.dq, sk[0] + wave * 32 * LD, acc, by, tile * 128 + wave * 32, h, lane);
     return;
   }
   if (row >= rows) return;
@@ -831,7 +893,7 @@ __global__ __launch_bounds__(256, NK == 1 ? 2 : 1) void k_cross_dkv(CrossParams 
   // every stage, behind the rows that are on their way.
   constexpr int LE = NK > 1 || DP == 64 ? 0 : DP == 96 ? 2 : 4, HE = NE - LE;
   __shared__ u32x4 sx[4][2 * LE + 1][64];
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, m = lane & 31, hb = lane >> 5;
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 31, hb = lane >> 5;
   const PairWork work(blockIdx.x, p.pairs, p.key_tiles * p.row_splits);
   const int tile = work.tile / p.row_splits, split = work.tile % p.row_splits, req = work.pair / p.heads, h = work.pair % p.heads;
   const CrossRange r(p, req);

@@ -143,7 +143,7 @@ inline svdq_status cross_cut(const svdq_cross_desc* d, int q_heads, int k_heads,
   t.rows = !grad && slots <= 64 ? 16 : 128;
   t.row_tiles = int(ceil_div(slots, t.rows));
   const int64_t items = per * larger(t.row_tiles, 1);
-  const int64_t n = t.rows == 16 ? clamp(int64_t(cus) * 4 / items, ceil_div(max_k, 256)) : clamp(int64_t(cus) * 2 / items, ceil_div(max_k, 512));
+  const int64_t n = t.rows == 16 ? clamp(int64_t(cus) * 2 / items, ceil_div(max_k, 256)) : clamp(int64_t(cus) * 2 / items, ceil_div(max_k, 512));
   const int64_t unit = 128;
   t.chunk = int(ceil_div(ceil_div(max_k > 0 ? max_k : 1, n), unit) * unit);
   t.splits = int(ceil_div(max_k > 0 ? max_k : 1, t.chunk));
