@@ -700,8 +700,11 @@ __global__ __launch_bounds__(256) void k_cross_join(CrossParams p) {
 
 // --------------------------------------------------------------- gradient of q
 // As k_cross_rows, with dP^T = V G^T beside S^T; dQ^T += K^T dS^T, K^T by
-// transposing reads.  Leaves delta for k_cross_dkv.
-template <int DT, int DP>
+// transposing reads.  Leaves delta for k_cross_dkv.  SHORT: all keys (up to 128) are
+// in LDS at once, and delta_i = sum_t p_it (g_i . v_t) comes from a pass over them,
+// not from `out`, whose bytes are not read and whose rounding, which counts most over
+// few keys, does not enter.
+template <int DT, int DP, bool SHORT>
 __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
   constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
   __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * LD];
@@ -723,14 +726,21 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
   // the first keys are on their way before the rows
   const uint16_t* kp = p.k.data + (int64_t(r.k_first) + from) * p.k.token + h * p.k.head;
   const uint16_t* vp = p.v.data + (int64_t(r.k_first) + from) * p.v.token + h * p.v.head;
-  Piece<DP, KT> pk, pv;
+  Piece<DP, KT> pk, pv, pk1, pv1;
   pk.rows(p.k.token, p.D, tid);
   pv.rows(p.v.token, p.D, tid);
-  uint64_t see = 0;
+  uint64_t see = 0, see1 = 0;
   if (from < to) {
     pk.load(kp, to - from, tid);
     pv.load(vp, to - from, tid);
     see = seen(p, r, from, lane);
+    if constexpr (SHORT) {
+      pk1.rows(p.k.token, p.D, tid);
+      pv1.rows(p.v.token, p.D, tid);
+      pk1.load(kp + KT * p.k.token, to - from - KT, tid);
+      pv1.load(vp + KT * p.v.token, to - from - KT, tid);
+      see1 = seen(p, r, from + KT, lane);
+    }
   }
   u32x4 q[NE], g[NE];
   float delta = 0.0f;
@@ -738,7 +748,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
     TileRows<DP> all, of_g, of_out;
     all.load(p, r, p.q, tile * 128, h, tid);
     of_g.load(p, r, p.g, tile * 128, h, tid);
-    of_out.load(p, r, p.out, tile * 128, h, tid);
+    if constexpr (!SHORT) of_out.load(p, r, p.out, tile * 128, h, tid);
     all.write(sk[0], tid);
     of_g.write(sv[0], tid);
     __syncthreads();
@@ -749,25 +759,25 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
       g[e] = *reinterpret_cast<const u32x4*>(&sv[0][mine + 16 * e]);
     }
     __syncthreads();
-    of_out.write(sk[0], tid);
-    __syncthreads();
+    if constexpr (!SHORT) {
+      of_out.write(sk[0], tid);
+      __syncthreads();
 #pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const u32x4 y = *reinterpret_cast<const u32x4*>(&sk[0][mine + 16 * e]);
+      for (int e = 0; e < NE; ++e) {
+        const u32x4 y = *reinterpret_cast<const u32x4*>(&sk[0][mine + 16 * e]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        delta = __builtin_fmaf(first_half<DT>(g[e][i]), first_half<DT>(y[i]), delta);
-        delta = __builtin_fmaf(second_half<DT>(g[e][i]), second_half<DT>(y[i]), delta);
+        for (int i = 0; i < 4; ++i) {
+          delta = __builtin_fmaf(first_half<DT>(g[e][i]), first_half<DT>(y[i]), delta);
+          delta = __builtin_fmaf(second_half<DT>(g[e][i]), second_half<DT>(y[i]), delta);
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
-  delta = half_sum(delta);
   float lse = __builtin_inff();
   if (row < rows) {
     const float l = p.lse[tok * p.q_heads + head];
     lse = l == -__builtin_inff() ? __builtin_inff() : l * LOG2E;
-    if (split == 0 && hb == 0) p.delta[tok * p.q_heads + head] = delta;
   }
   f32x16 acc[NX];
 #pragma unroll
@@ -781,13 +791,50 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
     if (wave == 0) leave_bias(sb[0], see, p.c, lane);
     pk.write(sk[0], tid);
     pv.write(sv[0], tid);
+    if constexpr (SHORT) {
+      if (see1 != ~uint64_t(0)) { pk1.hide(see1, tid); pv1.hide(see1, tid); }
+      if (wave == 0) leave_bias(sb[1], see1, p.c, lane);
+      pk1.write(sk[1], tid);
+      pv1.write(sv[1], tid);
+    }
   }
   __syncthreads();
+  // logits, probabilities in their place, and g . v of 32 keys
+  auto products = [&](int buf, int t, f32x16& s, f32x16& dp) {
+    s = rows16(&sb[buf][32 * t], hb);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dp[i] = 0.0f;
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      s = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sk[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), q[e], s);
+      dp = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sv[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), g[e], dp);
+    }
+    reads_ahead<2 * NE, 1, 4>();
+    __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = exp2_hw(__builtin_fmaf(s[i], p.c, -lse));
+  };
+  if constexpr (SHORT) {
+    if (active) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint64_t of = t < 2 ? see : see1;
+        if (unsigned(of >> (32 * (t & 1))) == 0u) continue;
+        f32x16 s, dp;
+        products(t / 2, t & 1, s, dp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) delta = __builtin_fmaf(s[i], dp[i], delta);
+      }
+    }
+  }
+  delta = half_sum(delta);
+  if (row < rows && split == 0 && hb == 0) p.delta[tok * p.q_heads + head] = delta;
   int buf = 0;
   for (int at = from; at < to; at += KT) {
     const bool more = at + KT < to;
-    uint64_t next = 0;
-    if (more) {
+    uint64_t next = see1;
+    if (!SHORT && more) {
       kp += KT * p.k.token;
       vp += KT * p.v.token;
       pk.load(kp, to - at - KT, tid);
@@ -798,19 +845,10 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
       for (int t = 0; t < 2; ++t) {
         const unsigned bits = t ? unsigned(see >> 32) : unsigned(see);
         if (bits == 0u) continue;
-        f32x16 s = rows16(&sb[buf][32 * t], hb), dp;
+        f32x16 s, dp;
+        products(buf, t, s, dp);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dp[i] = 0.0f;
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int e = 0; e < NE; ++e) {
-          s = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sk[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), q[e], s);
-          dp = mfma32<DT>(*reinterpret_cast<const u32x4*>(&sv[buf][(32 * t + m) * LD + 16 * e + 8 * hb]), g[e], dp);
-        }
-        reads_ahead<2 * NE, 1, 4>();
-        __builtin_amdgcn_s_setprio(0);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dp[i] = exp2_hw(__builtin_fmaf(s[i], p.c, -lse)) * (dp[i] - delta);
+        for (int i = 0; i < 16; ++i) dp[i] = s[i] * (dp[i] - delta);
         if constexpr (DT == SVDQ_F16) {
           float top = __builtin_fabsf(dp[0]);
 #pragma unroll
@@ -825,13 +863,15 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
           }
           dp *= gain;
         }
-        // in two terms of 16 bits: one alone costs as much precision as the result's own rounding
-        u32x4 ds[2], low[2];
+        // Two terms of 16 bits where delta comes from `out`: one alone and the rounding
+        // of `out` cost more precision together than the result's own rounding.
+        constexpr int NT = SHORT ? 1 : 2;
+        u32x4 ds[NT][2];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const unsigned w = pack2<DT>(dp[2 * i], dp[2 * i + 1]);
-          ds[i / 4][i % 4] = w;
-          low[i / 4][i % 4] = pack2<DT>(dp[2 * i] - first_half<DT>(w), dp[2 * i + 1] - second_half<DT>(w));
+          ds[0][i / 4][i % 4] = w;
+          if constexpr (!SHORT) ds[NT - 1][i / 4][i % 4] = pack2<DT>(dp[2 * i] - first_half<DT>(w), dp[2 * i + 1] - second_half<DT>(w));
         }
         const int gr = lane >> 4, i4 = lane & 15;
         __builtin_amdgcn_s_setprio(1);
@@ -841,15 +881,15 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
           for (int j = 0; j < 2; ++j) {
             const uint16_t* b = &sk[buf][(32 * t + 16 * j + 4 * (gr >> 1) + (i4 >> 2)) * LD + 32 * x + 16 * (gr & 1) + 4 * (i4 & 3)];
             const u32x4 a = joined(read_turned(b), read_turned(b + 8 * LD));
-            acc[x] = mfma32<DT>(a, ds[j], acc[x]);
-            acc[x] = mfma32<DT>(a, low[j], acc[x]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[x] = mfma32<DT>(a, ds[n][j], acc[x]);
           }
         }
-        reads_ahead<2 * NX, 2, 4, 2>();
+        reads_ahead<2 * NX, 2, 4, NT>();
         __builtin_amdgcn_s_setprio(0);
       }
     }
-    if (more) {
+    if (!SHORT && more) {
       next = seen(p, r, at + KT, lane);
       if (next != ~uint64_t(0)) { pk.hide(next, tid); pv.hide(next, tid); }
       if (wave == 0) leave_bias(sb[buf ^ 1], next, p.c, lane);
@@ -858,7 +898,10 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
     }
     see = next;
     buf ^= 1;
-    __syncthreads();
+    if constexpr (!SHORT) __syncthreads();
+  }
+  if constexpr (SHORT) {
+    __syncthreads();                    // before results take the keys' place
   }
   const float by = DT == SVDQ_F16 ? p.scale / gain : p.scale;
   if (chunks <= 1) {
@@ -1212,7 +1255,9 @@ void launch_forward(const CrossParams& p, const CrossCut& t, hipStream_t st) {
 template <int DT, int DP>
 void launch_backward(const CrossParams& p, const CrossCut& t, hipStream_t st) {
   if (t.row_tiles > 0) {
-    k_cross_dq<DT, DP><<<dim3(unsigned(t.pairs) * unsigned(t.row_tiles) * unsigned(t.splits)), 256, 0, st>>>(p);
+    const dim3 grid(unsigned(t.pairs) * unsigned(t.row_tiles) * unsigned(t.splits));
+    if (t.few_keys) k_cross_dq<DT, DP, true><<<grid, 256, 0, st>>>(p);
+    else k_cross_dq<DT, DP, false><<<grid, 256, 0, st>>>(p);
     if (t.splits > 1) k_cross_join<DT, true><<<dim3(unsigned(ceil_div(int64_t(t.pairs) * t.row_slots, 4))), 256, 0, st>>>(p);
   }
   if (t.key_tiles == 0) return;

@@ -122,6 +122,7 @@ struct CrossCut {
   int row_slots;            // rows of a pair: query tokens x heads of the group, the heads fastest
   int rows;                 // rows of a tile: 16 or 128
   int row_tiles, splits, chunk;   // and chunks of a pair's keys
+  bool few_keys;            // gradient: 128 at most, which lie in LDS at once
   int key_tile, key_tiles, row_splits, row_chunk;   // gradient of keys: keys of a tile, tiles, chunks of a pair's rows
 };
 
@@ -147,6 +148,7 @@ inline svdq_status cross_cut(const svdq_cross_desc* d, int q_heads, int k_heads,
   const int64_t unit = 128;
   t.chunk = int(ceil_div(ceil_div(max_k > 0 ? max_k : 1, n), unit) * unit);
   t.splits = int(ceil_div(max_k > 0 ? max_k : 1, t.chunk));
+  t.few_keys = max_k <= 128;
   t.key_tile = max_k <= 128 || d->head_dim > 64 ? 128 : 256;
   t.key_tiles = int(ceil_div(max_k, t.key_tile));
   const int64_t kitems = per * larger(t.key_tiles, 1);

@@ -108,9 +108,13 @@ def check_backward(c, out, lse, dq, dk, dv, what=""):
         # the definition, from the given lse and output
         p = torch.exp(s - lse[rows, h].double()[:, None])
         e = e + 2.0 ** -21 * (1 + lse[rows, h].double().abs()[:, None])
-        dp, delta = g @ v.T, (g * o).sum(-1, keepdim=True)
+        dp = g @ v.T
+        # up to 128 states: delta of the probabilities themselves
+        delta = (p * dp).sum(-1, keepdim=True) if c.where["max_k"] <= 128 else (g * o).sum(-1, keepdim=True)
         ds = p * (dp - delta)
         near = (c.d + 16) * 2.0 ** -24 * (g.abs() @ v.abs().T + (g * o).abs().sum(-1, keepdim=True))
+        if c.where["max_k"] <= 128:     # the error of each probability and product, and of a sum of up to 128
+            near = near + (p * ((e + 128 * 2.0 ** -24) * dp.abs() + near)).sum(-1, keepdim=True)
         # ds: rounded to 16 bits, p's error, the products' errors; f16 under its gain: to 2^-30 of the largest of its row
         # (or state), which `least` bounds for either sum
         least = 2.0 ** -30 * torch.maximum(ds.abs().amax(-1, keepdim=True), ds.abs().amax(0, keepdim=True)) if c.dtype == "f16" else 0.0
