@@ -33,7 +33,7 @@ struct CrossParams {
   const uint8_t* mask;
   int32_t tokens, states, max_q, max_k, q_heads, heads, group, pairs, D;
   int32_t row_slots, row_tiles, splits, chunk;
-  int32_t key_tile, key_tiles, row_splits, row_chunk;
+  int32_t key_tiles, row_splits, row_chunk;
   unsigned by_group;        // 2^32 / group, rounded up (group > 1)
   float c, scale;           // c = scale log2(e); forward: |scale|, and q's signs are turned
   unsigned turn;            // bits of two 16-bit values to turn
@@ -920,66 +920,59 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
 }
 
 // -------------------------------------------------------- gradient of k and v
-// 32 NK keys a wave, whose K and V stay in registers as operands, 128 NK a
+// 32 keys a wave, whose K and V stay in registers as operands, KEY_TILE a
 // workgroup; rows pass by in LDS, RT a stage.  S = Q K^T leaves a lane with 16
 // rows of one key: the operand of dV^T += G^T P and dK^T += Q^T dS, G^T and Q^T
 // by transposing reads.  A key that is not seen spoils only its own lane's sums,
 // which are not stored.
-template <int DT, int DP, int NK>
-__global__ __launch_bounds__(256, NK == 1 ? 2 : 1) void k_cross_dkv(CrossParams p) {
-  constexpr int RT = DP == 96 ? 64 : 32, NE = DP / 16, NX = DP / 32, LD = row_of<DP>(), WIDE = 128 * NK;
+template <int DT, int DP>
+__global__ __launch_bounds__(256, 2) void k_cross_dkv(CrossParams p) {
+  constexpr int RT = DP == 96 ? 64 : 32, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
   __shared__ __attribute__((aligned(16))) uint16_t sq[2][RT * LD];
   __shared__ __attribute__((aligned(16))) uint16_t sg[2][RT * LD];
   __shared__ __attribute__((aligned(16))) float sl[2][RT], sd[2][RT];
   // Of the NE operands of K and V each, the last LE lie in LDS: what does not fit
   // the registers of two waves a SIMD would otherwise come back from scratch memory
   // every stage, behind the rows that are on their way.
-  constexpr int LE = NK > 1 || DP == 64 ? 0 : DP == 96 ? 2 : 4, HE = NE - LE;
+  constexpr int LE = DP == 64 ? 0 : DP == 96 ? 2 : 4, HE = NE - LE;
   __shared__ u32x4 sx[4][2 * LE + 1][64];
   const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 31, hb = lane >> 5;
   const PairWork work(blockIdx.x, p.pairs, p.key_tiles * p.row_splits);
   const int tile = work.tile / p.row_splits, split = work.tile % p.row_splits, req = work.pair / p.heads, h = work.pair % p.heads;
   const CrossRange r(p, req);
-  if (tile * WIDE >= r.keys) return;
+  if (tile * KEY_TILE >= r.keys) return;
   const int rows = r.rows * p.group, chunks = (rows + p.row_chunk - 1) / p.row_chunk;
   if (split > 0 && split >= chunks) return;
   const int from = split * p.row_chunk, to = smaller(rows, from + p.row_chunk);
-  const int first = tile * WIDE + wave * 32 * NK;
+  const int first = tile * KEY_TILE + wave * 32;
   const bool active = first < r.keys;
-  u32x4 k[NK][HE], v[NK][HE];
-  bool shown[NK];
+  u32x4 k[HE], v[HE];
+  const int key = first + m;
+  const bool held = key < r.keys;
+  const int64_t state = int64_t(r.k_first) + (held ? key : 0);
+  const bool shown = held && (!p.mask || p.mask[state] != 0);
 #pragma unroll
-  for (int n = 0; n < NK; ++n) {
-    const int key = first + 32 * n + m;
-    const int64_t state = int64_t(r.k_first) + (key < r.keys ? key : 0);
-    shown[n] = key < r.keys && (!p.mask || p.mask[state] != 0);
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      u32x4 a = {0, 0, 0, 0}, c = {0, 0, 0, 0};
-      const int d = 16 * e + 8 * hb;
-      if (shown[n] && d < p.D) {
-        a = *reinterpret_cast<const u32x4*>(p.k.data + state * p.k.token + h * p.k.head + d);
-        c = *reinterpret_cast<const u32x4*>(p.v.data + state * p.v.token + h * p.v.head + d);
-      }
-      if (e < HE) {
-        k[n][e < HE ? e : 0] = a;
-        v[n][e < HE ? e : 0] = c;
-      } else {                          // the wave's own: it reads them itself
-        sx[wave][e - HE][lane] = a;
-        sx[wave][LE + e - HE][lane] = c;
-      }
+  for (int e = 0; e < NE; ++e) {
+    u32x4 a = {0, 0, 0, 0}, c = {0, 0, 0, 0};
+    const int d = 16 * e + 8 * hb;
+    if (shown && d < p.D) {
+      a = *reinterpret_cast<const u32x4*>(p.k.data + state * p.k.token + h * p.k.head + d);
+      c = *reinterpret_cast<const u32x4*>(p.v.data + state * p.v.token + h * p.v.head + d);
+    }
+    if (e < HE) {
+      k[e < HE ? e : 0] = a;
+      v[e < HE ? e : 0] = c;
+    } else {                          // the wave's own: it reads them itself
+      sx[wave][e - HE][lane] = a;
+      sx[wave][LE + e - HE][lane] = c;
     }
   }
-  f32x16 dk[NK][NX], dv[NK][NX];
-  float gain[NK];
+  f32x16 dk[NX], dv[NX];
+  float gain = FIRST_GAIN;
 #pragma unroll
-  for (int n = 0; n < NK; ++n) {
-    gain[n] = FIRST_GAIN;
+  for (int x = 0; x < NX; ++x)
 #pragma unroll
-    for (int x = 0; x < NX; ++x)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) dk[n][x][i] = dv[n][x][i] = 0.0f;
-  }
+    for (int i = 0; i < 16; ++i) dk[x][i] = dv[x][i] = 0.0f;
 
   RowPiece<DP, RT> pq, pg;
   // a row's offset from its stage's first; where heads of a group divide the
@@ -1035,59 +1028,50 @@ __global__ __launch_bounds__(256, NK == 1 ? 2 : 1) void k_cross_dkv(CrossParams 
 #pragma unroll
       for (int t = 0; t < RT / 32; ++t) {
         if (at + 32 * t >= to) continue;
-        f32x16 s[NK], dp[NK];
+        f32x16 s, dp = rows16(&sd[buf][32 * t], hb);      // - delta
 #pragma unroll
-        for (int n = 0; n < NK; ++n)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NK; ++n) dp[n] = rows16(&sd[buf][32 * t], hb);      // - delta
+        for (int i = 0; i < 16; ++i) s[i] = 0.0f;
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
           const u32x4 a = *reinterpret_cast<const u32x4*>(&sq[buf][(32 * t + m) * LD + 16 * e + 8 * hb]);
-#pragma unroll
-          for (int n = 0; n < NK; ++n) s[n] = mfma32<DT>(a, e < HE ? k[n][e < HE ? e : 0] : sx[wave][e < HE ? 0 : e - HE][lane], s[n]);
+          s = mfma32<DT>(a, e < HE ? k[e < HE ? e : 0] : sx[wave][e < HE ? 0 : e - HE][lane], s);
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
           const u32x4 a = *reinterpret_cast<const u32x4*>(&sg[buf][(32 * t + m) * LD + 16 * e + 8 * hb]);
-#pragma unroll
-          for (int n = 0; n < NK; ++n) dp[n] = mfma32<DT>(a, e < HE ? v[n][e < HE ? e : 0] : sx[wave][e < HE ? 0 : LE + e - HE][lane], dp[n]);
+          dp = mfma32<DT>(a, e < HE ? v[e < HE ? e : 0] : sx[wave][e < HE ? 0 : LE + e - HE][lane], dp);
         }
-        reads_ahead<2 * NE, 1, DP == 96 ? 2 : 3, NK, DP == 96 ? 0 : 4>();
+        reads_ahead<2 * NE, 1, DP == 96 ? 2 : 3, 1, DP == 96 ? 0 : 4>();
         __builtin_amdgcn_s_setprio(0);
-        u32x4 pf[NK][2], ds[NK][2];
+        u32x4 pf[2], ds[2];
 #pragma unroll
-        for (int n = 0; n < NK; ++n) {
+        for (int y = 0; y < 4; ++y) {
+          const f32x4 ll = *reinterpret_cast<const f32x4*>(&sl[buf][32 * t + 8 * y + 4 * hb]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const f32x4 ll = *reinterpret_cast<const f32x4*>(&sl[buf][32 * t + 8 * y + 4 * hb]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              s[n][4 * y + i] = exp2_hw(__builtin_fmaf(s[n][4 * y + i], p.c, -ll[i]));
-              dp[n][4 * y + i] *= s[n][4 * y + i];
-            }
+          for (int i = 0; i < 4; ++i) {
+            s[4 * y + i] = exp2_hw(__builtin_fmaf(s[4 * y + i], p.c, -ll[i]));
+            dp[4 * y + i] *= s[4 * y + i];
           }
-          if constexpr (DT == SVDQ_F16) {
-            float top = __builtin_fabsf(dp[n][0]);
+        }
+        if constexpr (DT == SVDQ_F16) {
+          float top = __builtin_fabsf(dp[0]);
 #pragma unroll
-            for (int i = 1; i < 16; ++i) top = maximum(top, __builtin_fabsf(dp[n][i]));
-            top = half_max(top);
-            const bool over = top * gain[n] > MOST;
-            if (__any(over)) {
-              const float lower = over ? lower_gain(top) : gain[n], by = lower / gain[n];
-              gain[n] = lower;
+          for (int i = 1; i < 16; ++i) top = maximum(top, __builtin_fabsf(dp[i]));
+          top = half_max(top);
+          const bool over = top * gain > MOST;
+          if (__any(over)) {
+            const float lower = over ? lower_gain(top) : gain, by = lower / gain;
+            gain = lower;
 #pragma unroll
-              for (int x = 0; x < NX; ++x) dk[n][x] *= by;
-            }
-            dp[n] *= gain[n];
+            for (int x = 0; x < NX; ++x) dk[x] *= by;
           }
+          dp *= gain;
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            pf[n][i / 4][i % 4] = pack2<DT>(s[n][2 * i], s[n][2 * i + 1]);
-            ds[n][i / 4][i % 4] = pack2<DT>(dp[n][2 * i], dp[n][2 * i + 1]);
-          }
+        for (int i = 0; i < 8; ++i) {
+          pf[i / 4][i % 4] = pack2<DT>(s[2 * i], s[2 * i + 1]);
+          ds[i / 4][i % 4] = pack2<DT>(dp[2 * i], dp[2 * i + 1]);
         }
         const int gr = lane >> 4, i4 = lane & 15;
         __builtin_amdgcn_s_setprio(1);
@@ -1098,14 +1082,11 @@ __global__ __launch_bounds__(256, NK == 1 ? 2 : 1) void k_cross_dkv(CrossParams 
             const int b = (32 * t + 16 * j + 4 * (gr >> 1) + (i4 >> 2)) * LD + 32 * x + 16 * (gr & 1) + 4 * (i4 & 3);
             const u32x4 ga = joined(read_turned(&sg[buf][b]), read_turned(&sg[buf][b + 8 * LD]));
             const u32x4 qa = joined(read_turned(&sq[buf][b]), read_turned(&sq[buf][b + 8 * LD]));
-#pragma unroll
-            for (int n = 0; n < NK; ++n) {
-              dv[n][x] = mfma32<DT>(ga, pf[n][j], dv[n][x]);
-              dk[n][x] = mfma32<DT>(qa, ds[n][j], dk[n][x]);
-            }
+            dv[x] = mfma32<DT>(ga, pf[j], dv[x]);
+            dk[x] = mfma32<DT>(qa, ds[j], dk[x]);
           }
         }
-        reads_ahead<4 * NX, 2, DP == 96 ? 2 : 3, NK>();
+        reads_ahead<4 * NX, 2, DP == 96 ? 2 : 3>();
         __builtin_amdgcn_s_setprio(0);
       }
     }
@@ -1114,48 +1095,42 @@ __global__ __launch_bounds__(256, NK == 1 ? 2 : 1) void k_cross_dkv(CrossParams 
     __syncthreads();
   }
   if (!active) return;
+  const float kby = !shown ? 0.0f : DT == SVDQ_F16 ? p.scale / gain * 0x1p-10f : p.scale, vby = DT == SVDQ_F16 ? 0x1p-10f : 1.0f;
+  if (!shown) {
 #pragma unroll
-  for (int n = 0; n < NK; ++n) {
-    const int key = first + 32 * n + m;
-    const bool held = key < r.keys;
-    const int64_t state = int64_t(r.k_first) + (held ? key : 0);
-    const float kby = !shown[n] ? 0.0f : DT == SVDQ_F16 ? p.scale / gain[n] * 0x1p-10f : p.scale, vby = DT == SVDQ_F16 ? 0x1p-10f : 1.0f;
-    if (!shown[n]) {
+    for (int x = 0; x < NX; ++x)
 #pragma unroll
-      for (int x = 0; x < NX; ++x)
+      for (int i = 0; i < 16; ++i) dk[x][i] = dv[x][i] = 0.0f;
+  }
+  if (chunks <= 1) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dk[n][x][i] = dv[n][x][i] = 0.0f;
-    }
-    if (chunks <= 1) {
+    for (int x = 0; x < NX; ++x) {
+      unsigned wk[8], wv[8];
+      columns<DT>(dk[x], kby, wk);
+      columns<DT>(dv[x], vby, wv);
 #pragma unroll
-      for (int x = 0; x < NX; ++x) {
-        unsigned wk[8], wv[8];
-        columns<DT>(dk[n][x], kby, wk);
-        columns<DT>(dv[n][x], vby, wv);
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int d = 32 * x + 16 * y + 8 * hb;
-          if (held && d < p.D) {
-            *reinterpret_cast<u32x4*>(p.dk.data + state * p.dk.token + h * p.dk.head + d) = u32x4{wk[4 * y], wk[4 * y + 1], wk[4 * y + 2], wk[4 * y + 3]};
-            *reinterpret_cast<u32x4*>(p.dv.data + state * p.dv.token + h * p.dv.head + d) = u32x4{wv[4 * y], wv[4 * y + 1], wv[4 * y + 2], wv[4 * y + 3]};
-          }
+      for (int y = 0; y < 2; ++y) {
+        const int d = 32 * x + 16 * y + 8 * hb;
+        if (held && d < p.D) {
+          *reinterpret_cast<u32x4*>(p.dk.data + state * p.dk.token + h * p.dk.head + d) = u32x4{wk[4 * y], wk[4 * y + 1], wk[4 * y + 2], wk[4 * y + 3]};
+          *reinterpret_cast<u32x4*>(p.dv.data + state * p.dv.token + h * p.dv.head + d) = u32x4{wv[4 * y], wv[4 * y + 1], wv[4 * y + 2], wv[4 * y + 3]};
         }
       }
-    } else if (held) {
-      // [pair][split][key of the tiles][2][D]
-      float* part = p.key_part + ((int64_t(work.pair) * p.row_splits + split) * (int64_t(p.key_tiles) * WIDE) + key) * 2 * p.D;
-#pragma unroll
-      for (int x = 0; x < NX; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int d = 32 * x + 8 * y + 4 * hb;
-          if (d < p.D) {
-            const f32x16 &a = dk[n][x], &b = dv[n][x];
-            *reinterpret_cast<f32x4*>(part + d) = f32x4{a[4 * y] * kby, a[4 * y + 1] * kby, a[4 * y + 2] * kby, a[4 * y + 3] * kby};
-            *reinterpret_cast<f32x4*>(part + p.D + d) = f32x4{b[4 * y] * vby, b[4 * y + 1] * vby, b[4 * y + 2] * vby, b[4 * y + 3] * vby};
-          }
-        }
     }
+  } else if (held) {
+    // [pair][split][key of the tiles][2][D]
+    float* part = p.key_part + ((int64_t(work.pair) * p.row_splits + split) * (int64_t(p.key_tiles) * KEY_TILE) + key) * 2 * p.D;
+#pragma unroll
+    for (int x = 0; x < NX; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int d = 32 * x + 8 * y + 4 * hb;
+        if (d < p.D) {
+          const f32x16 &a = dk[x], &b = dv[x];
+          *reinterpret_cast<f32x4*>(part + d) = f32x4{a[4 * y] * kby, a[4 * y + 1] * kby, a[4 * y + 2] * kby, a[4 * y + 3] * kby};
+          *reinterpret_cast<f32x4*>(part + p.D + d) = f32x4{b[4 * y] * vby, b[4 * y + 1] * vby, b[4 * y + 2] * vby, b[4 * y + 3] * vby};
+        }
+      }
   }
 }
 
@@ -1163,7 +1138,7 @@ __global__ __launch_bounds__(256, NK == 1 ? 2 : 1) void k_cross_dkv(CrossParams 
 // upper dv.
 template <int DT>
 __global__ __launch_bounds__(256) void k_cross_key_join(CrossParams p) {
-  const int lane = int(threadIdx.x) & 63, width = p.key_tiles * p.key_tile;
+  const int lane = int(threadIdx.x) & 63, width = p.key_tiles * KEY_TILE;
   const int64_t slot = int64_t(blockIdx.x) * 4 + (int(threadIdx.x) >> 6);
   if (slot >= int64_t(p.pairs) * width) return;
   const int pair = int(slot / width), key = int(slot % width);
@@ -1236,7 +1211,7 @@ CrossParams params_of(const svdq_cross_desc* d, const CrossCut& t, int q_heads, 
   p.tokens = t.tokens; p.states = t.states; p.max_q = d->max_q; p.max_k = d->max_k;
   p.q_heads = q_heads; p.heads = k_heads; p.group = t.group; p.pairs = t.pairs; p.D = d->head_dim;
   p.row_slots = t.row_slots; p.row_tiles = t.row_tiles; p.splits = t.splits; p.chunk = t.chunk;
-  p.key_tile = t.key_tile; p.key_tiles = t.key_tiles; p.row_splits = t.row_splits; p.row_chunk = t.row_chunk;
+  p.key_tiles = t.key_tiles; p.row_splits = t.row_splits; p.row_chunk = t.row_chunk;
   p.by_group = t.group > 1 ? unsigned((uint64_t(1) << 32) / unsigned(t.group)) + 1 : 0;
   p.scale = d->scale;
   p.c = d->scale * LOG2E;
@@ -1262,14 +1237,9 @@ void launch_backward(const CrossParams& p, const CrossCut& t, hipStream_t st) {
   }
   if (t.key_tiles == 0) return;
   const dim3 grid(unsigned(t.pairs) * unsigned(t.key_tiles) * unsigned(t.row_splits));
-  if constexpr (DP == 64) {
-    if (t.key_tile == 256) k_cross_dkv<DT, DP, 2><<<grid, 256, 0, st>>>(p);
-    else k_cross_dkv<DT, DP, 1><<<grid, 256, 0, st>>>(p);
-  } else {
-    k_cross_dkv<DT, DP, 1><<<grid, 256, 0, st>>>(p);
-  }
+  k_cross_dkv<DT, DP><<<grid, 256, 0, st>>>(p);
   if (t.row_splits > 1)
-    k_cross_key_join<DT><<<dim3(unsigned(int64_t(t.pairs) * t.key_tiles * (t.key_tile / 4))), 256, 0, st>>>(p);
+    k_cross_key_join<DT><<<dim3(unsigned(int64_t(t.pairs) * t.key_tiles * (KEY_TILE / 4))), 256, 0, st>>>(p);
 }
 
 template <int DT>

@@ -106,12 +106,31 @@ __device__ __forceinline__ void leave8(float* red, int stride, const float* v, i
   for (int i = 0; i < 8; ++i) red[(8 * piece + i) * stride + row] = v[i];
 }
 
+// Both sums of channel c over the rows that leave8 left, by `lanes` lanes (all of
+// them get the sums): one up to 32 rows, where there are many channels (24 rows of
+// 320: 14.0 us against 16.9 for the whole kernel), else 16 (one thread a channel and
+// 102 rows are the longest part of a small call).
+__device__ __forceinline__ int sum_lanes(int rows) { return rows <= 32 ? 1 : 16; }
+__device__ __forceinline__ float2 channel_sums(const float* red, int size, int ld, int rows, int c, int lane, int lanes) {
+  float2 v = {0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = lane & (lanes - 1); i < rows; i += lanes) {
+    v.x += red[c * ld + i];
+    v.y += red[size + c * ld + i];
+  }
+  for (int m = 1; m < lanes; m *= 2) {
+    v.x += __shfl_xor(v.x, m);
+    v.y += __shfl_xor(v.y, m);
+  }
+  return v;
+}
+
 // ------------------------------------------------------------ one launch
 // A workgroup has `block` groups of a sample: reads them once into registers
 // (NV pieces of 16 bytes a thread), mean first and square deviations after it,
 // writes them once.
 template <int DT, int ACT, int NV>
-__global__ __launch_bounds__(512) void k_norm_whole(NormParams p) {
+__global__ __launch_bounds__(1024) void k_norm_whole(NormParams p) {
   extern __shared__ float red[];
   __shared__ float sm[NORM_MAX_BLOCK];
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
@@ -239,12 +258,11 @@ __global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
   __syncthreads();
   const float inv = 1.0f / float(n);
   float mean = 0.0f, dev = 0.0f;
-  for (int c = tid; c < p.channels; c += int(blockDim.x)) {
-    float s0 = 0.0f, q0 = 0.0f;
-    for (int r = 0; r < p.rows; ++r) {
-      s0 += red[c * ld + r];
-      q0 += red[size + c * ld + r];
-    }
+  const int lanes = sum_lanes(p.rows);
+  for (int c = tid / lanes; c < p.channels; c += int(blockDim.x) / lanes) {
+    const float2 v = channel_sums(red, size, ld, p.rows, c, lane, lanes);
+    if ((lane & (lanes - 1)) != 0) continue;
+    const float s0 = v.x, q0 = v.y;
     // in the places of the channel's own first row: nobody else reads these
     const float k0 = h2f<DT>(p.x[int64_t(sample) * p.xs + from * p.xp + c]);
     mean = s0 * inv;
@@ -393,97 +411,110 @@ __device__ __forceinline__ void back8(u32x4 xv, u32x4 gv, const float* m, const 
   }
 }
 
-// One launch: as k_norm_whole.  A sample's channel sums go to dw and db, or,
-// with several samples, to `chan` for k_norm_sum.
+// One launch: as k_norm_whole.  Few samples: a workgroup takes its groups of all of
+// them, one after the other, and ends with dw and db; many: of one, whose channel
+// sums go to `chan` for k_norm_sum.
 template <int DT, int ACT, int NV>
 __global__ __launch_bounds__(512) void k_norm_grad_whole(NormParams p) {
   extern __shared__ float red[];        // [2][channels of the block][rows]
   __shared__ float sm[2 * NORM_MAX_BLOCK];
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
-  const int blocks = p.groups / p.block, sample = int(blockIdx.x) / blocks, first = int(blockIdx.x) % blocks * p.block;
+  const int blocks = p.groups / p.block, first = int(blockIdx.x) % blocks * p.block;
+  const bool every = int(gridDim.x) == blocks;
+  const int from = every ? 0 : int(blockIdx.x) / blocks, to = every ? p.samples : from + 1;
   const int row = tid / p.cv, piece = tid % p.cv;
   const bool on = row < p.rows;
   const int c0 = first * p.per + 8 * piece;
-  u32x4 xv[NV], gv[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t at = row + int64_t(i) * p.rows;
-    xv[i] = gv[i] = u32x4{0, 0, 0, 0};
-    if (on && at < p.pixels) {
-      xv[i] = *reinterpret_cast<const u32x4*>(p.x + int64_t(sample) * p.xs + at * p.xp + c0);
-      gv[i] = *reinterpret_cast<const u32x4*>(p.g + int64_t(sample) * p.gs + at * p.gp + c0);
-    }
-  }
-  float w[8] = {}, b[8] = {}, m[8] = {}, r[8] = {}, s[8] = {}, q[8] = {}, dz[8], xh[8];
+  const int wide = 8 * p.cv, ld = p.rows | 1, size = wide * ld;
+  float* total = red + 2 * size;        // [2][channels of the block]
+  float w[8] = {}, b[8] = {};
   int gi[8] = {};
   if (on) {
     weights8<DT>(p.w, c0, 1.0f, w);
     weights8<DT>(p.b, c0, 0.0f, b);
     groups8(p, 8 * piece, gi);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float* st = p.stats + (int64_t(sample) * p.groups + first + gi[e]) * 2;
-      m[e] = st[0];
-      r[e] = st[1];
-    }
   }
+  for (int sample = from; sample < to; ++sample) {
+    u32x4 xv[NV], gv[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (!on || row + int64_t(i) * p.rows >= p.pixels) continue;
-    back8<DT, ACT>(xv[i], gv[i], m, r, w, b, dz, xh);
+    for (int i = 0; i < NV; ++i) {
+      const int64_t at = row + int64_t(i) * p.rows;
+      xv[i] = gv[i] = u32x4{0, 0, 0, 0};
+      if (on && at < p.pixels) {
+        xv[i] = *reinterpret_cast<const u32x4*>(p.x + int64_t(sample) * p.xs + at * p.xp + c0);
+        gv[i] = *reinterpret_cast<const u32x4*>(p.g + int64_t(sample) * p.gs + at * p.gp + c0);
+      }
+    }
+    float m[8] = {}, r[8] = {}, s[8] = {}, q[8] = {}, dz[8], xh[8];
+    if (on) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      s[e] += dz[e];
-      q[e] = __builtin_fmaf(dz[e], xh[e], q[e]);
+      for (int e = 0; e < 8; ++e) {
+        const float* st = p.stats + (int64_t(sample) * p.groups + first + gi[e]) * 2;
+        m[e] = st[0];
+        r[e] = st[1];
+      }
     }
-  }
-  const int wide = 8 * p.cv, ld = p.rows | 1, size = wide * ld;
-  leave8(red, ld, s, piece, row, on);
-  leave8(red + size, ld, q, piece, row, on);
-  __syncthreads();
-  for (int c = tid; c < wide; c += int(blockDim.x)) {
-    float s0 = 0.0f, q0 = 0.0f;
-    for (int i = 0; i < p.rows; ++i) {
-      s0 += red[c * ld + i];
-      q0 += red[size + c * ld + i];
-    }
-    const int ch = first * p.per + c;
-    if (p.samples > 1) {
-      *reinterpret_cast<float2*>(p.chan + (int64_t(sample) * p.channels + ch) * 2) = float2{s0, q0};
-    } else {
-      if (p.db) p.db[ch] = s0;
-      if (p.dw) p.dw[ch] = q0;
-    }
-    const float wc = p.w ? h2f<DT>(p.w[ch]) : 1.0f;
-    red[c * ld] = s0 * wc;          // (the channel's own places: nobody else reads these)
-    red[size + c * ld] = q0 * wc;
-  }
-  __syncthreads();
-  const float inv_n = 1.0f / (float(p.pixels) * float(p.per));
-  for (int g = wave; g < p.block; g += waves) {
-    float t = 0.0f, u = 0.0f;
-    for (int c = lane; c < p.per; c += 64) {
-      t += red[(g * p.per + c) * ld];
-      u += red[size + (g * p.per + c) * ld];
-    }
-    t = wave_sum(t);
-    u = wave_sum(u);
-    if (lane == 0) {
-      sm[2 * g] = t * inv_n;
-      sm[2 * g + 1] = u * inv_n;
-    }
-  }
-  __syncthreads();
-  if (!on) return;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t at = row + int64_t(i) * p.rows;
-    if (at >= p.pixels) continue;
-    back8<DT, ACT>(xv[i], gv[i], m, r, w, b, dz, xh);
+    for (int i = 0; i < NV; ++i) {
+      if (!on || row + int64_t(i) * p.rows >= p.pixels) continue;
+      back8<DT, ACT>(xv[i], gv[i], m, r, w, b, dz, xh);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      dz[e] = r[e] * (__builtin_fmaf(dz[e], w[e], -sm[2 * gi[e]]) - xh[e] * sm[2 * gi[e] + 1]);
-    *reinterpret_cast<u32x4*>(p.y + int64_t(sample) * p.ys + at * p.yp + c0) = pack8<DT>(dz);
+      for (int e = 0; e < 8; ++e) {
+        s[e] += dz[e];
+        q[e] = __builtin_fmaf(dz[e], xh[e], q[e]);
+      }
+    }
+    leave8(red, ld, s, piece, row, on);
+    leave8(red + size, ld, q, piece, row, on);
+    __syncthreads();
+    const int lanes = sum_lanes(p.rows);
+    for (int c = tid / lanes; c < wide; c += int(blockDim.x) / lanes) {
+      const float2 v = channel_sums(red, size, ld, p.rows, c, lane, lanes);
+      if ((lane & (lanes - 1)) != 0) continue;
+      const float s0 = v.x, q0 = v.y;
+      const int ch = first * p.per + c;
+      if (!every) {
+        *reinterpret_cast<float2*>(p.chan + (int64_t(sample) * p.channels + ch) * 2) = float2{s0, q0};
+      } else {                            // (the same thread for every sample)
+        const float s1 = sample > 0 ? total[c] + s0 : s0, q1 = sample > 0 ? total[wide + c] + q0 : q0;
+        total[c] = s1;
+        total[wide + c] = q1;
+        if (sample + 1 == to) {
+          if (p.db) p.db[ch] = s1;
+          if (p.dw) p.dw[ch] = q1;
+        }
+      }
+      const float wc = p.w ? h2f<DT>(p.w[ch]) : 1.0f;
+      red[c * ld] = s0 * wc;          // (the channel's own places: nobody else reads these)
+      red[size + c * ld] = q0 * wc;
+    }
+    __syncthreads();
+    const float inv_n = 1.0f / (float(p.pixels) * float(p.per));
+    for (int g = wave; g < p.block; g += waves) {
+      float t = 0.0f, u = 0.0f;
+      for (int c = lane; c < p.per; c += 64) {
+        t += red[(g * p.per + c) * ld];
+        u += red[size + (g * p.per + c) * ld];
+      }
+      t = wave_sum(t);
+      u = wave_sum(u);
+      if (lane == 0) {
+        sm[2 * g] = t * inv_n;
+        sm[2 * g + 1] = u * inv_n;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t at = row + int64_t(i) * p.rows;
+      if (!on || at >= p.pixels) continue;
+      back8<DT, ACT>(xv[i], gv[i], m, r, w, b, dz, xh);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        dz[e] = r[e] * (__builtin_fmaf(dz[e], w[e], -sm[2 * gi[e]]) - xh[e] * sm[2 * gi[e] + 1]);
+      *reinterpret_cast<u32x4*>(p.y + int64_t(sample) * p.ys + at * p.yp + c0) = pack8<DT>(dz);
+    }
+    __syncthreads();                    // sums and means have been read
   }
 }
 
@@ -533,12 +564,11 @@ __global__ __launch_bounds__(1024) void k_norm_grad_sums(NormParams p) {
   leave8(red, ld, s, piece, row, on);
   leave8(red + size, ld, q, piece, row, on);
   __syncthreads();
-  for (int c = tid; c < p.channels; c += int(blockDim.x)) {
-    float s0 = 0.0f, q0 = 0.0f;
-    for (int i = 0; i < p.rows; ++i) {
-      s0 += red[c * ld + i];
-      q0 += red[size + c * ld + i];
-    }
+  const int lanes = sum_lanes(p.rows);
+  for (int c = tid / lanes; c < p.channels; c += int(blockDim.x) / lanes) {
+    const float2 v = channel_sums(red, size, ld, p.rows, c, lane, lanes);
+    if ((lane & (lanes - 1)) != 0) continue;
+    const float s0 = v.x, q0 = v.y;
     *reinterpret_cast<float2*>(p.chan + (int64_t(blockIdx.x) * p.channels + c) * 2) = float2{s0, q0};
     const float wc = p.w ? h2f<DT>(p.w[c]) : 1.0f;
     red[c * ld] = s0 * wc;          // (the channel's own places: nobody else reads these)
@@ -710,11 +740,13 @@ void launch_norm_grad(const NormParams& p, const NormCut& t, hipStream_t st) {
   const bool sums = p.dw || p.db;
   const unsigned tiles = unsigned((p.channels + 31) / 32);
   if (t.block > 0) {
-    const dim3 grid(unsigned(p.samples) * unsigned(p.groups / t.block));
-    if (t.pieces <= 1) k_norm_grad_whole<DT, ACT, 1><<<grid, t.threads, red, st>>>(p);
-    else if (t.pieces <= 2) k_norm_grad_whole<DT, ACT, 2><<<grid, t.threads, red, st>>>(p);
-    else k_norm_grad_whole<DT, ACT, 4><<<grid, t.threads, red, st>>>(p);
-    if (p.samples > 1 && sums) k_norm_sum<<<dim3(tiles), 256, 0, st>>>(p);
+    const bool every = p.samples <= NORM_FEW_SAMPLES;
+    const dim3 grid((every ? 1u : unsigned(p.samples)) * unsigned(p.groups / t.block));
+    const size_t lds = red + size_t(t.cv) * 16 * 4;
+    if (t.pieces <= 1) k_norm_grad_whole<DT, ACT, 1><<<grid, t.threads, lds, st>>>(p);
+    else if (t.pieces <= 2) k_norm_grad_whole<DT, ACT, 2><<<grid, t.threads, lds, st>>>(p);
+    else k_norm_grad_whole<DT, ACT, 4><<<grid, t.threads, lds, st>>>(p);
+    if (!every && sums) k_norm_sum<<<dim3(tiles), 256, 0, st>>>(p);
     return;
   }
   const unsigned work = unsigned(p.samples) * unsigned(t.chunks);
