@@ -1,5 +1,6 @@
-"""An attention layer served over a 4-bit cache: two SVDQuant linears and, between
-them, the operators of ``kv.py``.
+"""Attention layers of two SVDQuant linears and, between them, the operators of
+``kv.py`` (self attention served over a 4-bit cache, ``SVDQAttention``) or of
+``image.py`` (an image's attention to an encoder's states, ``SVDQCrossAttention``).
 
     qkv = W_qkv x                               4-bit GEMM
     q, cache <- norm, rotation, quantization    one launch (KVCache.append)
@@ -11,10 +12,19 @@ step, then call every layer.
 """
 from __future__ import annotations
 
+import math
+from typing import Optional
+
 import torch
 
-from . import kv
+from . import image, kv
 from .svdq import SVDQLinear, workspace_size
+
+
+def _linear(linear: SVDQLinear, x):
+    """A linear with a workspace of the call's own."""
+    ws = torch.empty(workspace_size(linear.layer, x.shape[0]), dtype=torch.uint8, device=x.device)
+    return linear.forward(x, ws=ws)
 
 
 class SVDQAttention:
@@ -46,8 +56,7 @@ class SVDQAttention:
         return kv.attention_workspace(requests, tokens, self.q_heads, self.cache, max_q, max_kv)
 
     def _linear(self, linear: SVDQLinear, x):
-        ws = torch.empty(workspace_size(linear.layer, x.shape[0]), dtype=torch.uint8, device=x.device)
-        return linear.forward(x, ws=ws)
+        return _linear(linear, x)
 
     def forward(self, x, step: kv.Plan, max_q: int, max_kv: int, ws=None):
         """x [tokens, K]: the new tokens of all requests, request after request;
@@ -64,5 +73,40 @@ class SVDQAttention:
             kv.attention(q, self.cache, step.block_table, step.q_start, step.kv_len, max_q, max_kv, causal=self.causal,
                          window=self.window, out=o, ws=ws)
             return self._linear(self.out, o.view(tokens, hq * d))
+
+    __call__ = forward
+
+
+class SVDQCrossAttention:
+    """The part of an image model's block where an encoder's states enter,
+    between two SVDQuant linears:
+
+        h = group_norm(x)                       optional
+        q = W_q h                               4-bit GEMM
+        o = cross_attention(q, k, v, mask)      16-bit keys and values
+        y = W_out o                             4-bit GEMM
+
+    q: SVDQLinear C -> heads D; out: SVDQLinear heads D -> N; groups: of the norm
+    (0: none), weight, bias: its [C] or None, act: its activation.  k and v are the
+    encoder's states, projected by the caller (once for all the steps that use
+    them) and kept in 16 bits.  A call keeps nothing, as in SVDQAttention."""
+
+    def __init__(self, q: SVDQLinear, out: SVDQLinear, heads: int, groups: int = 0, weight=None, bias=None, eps: float = 1e-5,
+                 act: Optional[str] = None, scale: Optional[float] = None):
+        if heads < 1 or q.N % heads != 0 or out.K != q.N:
+            raise ValueError(f"{heads} heads need a projection to a multiple of them and one from as many, got {q.N} and {out.K}")
+        self.q, self.out, self.heads, self.groups, self.scale = q, out, heads, groups, scale
+        self.norm = dict(weight=weight, bias=bias, eps=eps, act=act)
+
+    def forward(self, x, k, v, mask=None):
+        """x [requests, ..., C]: the maps or tokens of all requests; k, v
+        [requests, states, k_heads, D]; mask [requests, states] or None: which
+        states are seen.  Returns [requests, ..., N]."""
+        with kv._on(None, x):
+            b, c, tokens = x.shape[0], x.shape[-1], math.prod(x.shape[1:-1])
+            h = image.group_norm(x, self.groups, **self.norm) if self.groups else x
+            q = _linear(self.q, h.reshape(b * tokens, c)).view(b, tokens, self.heads, self.q.N // self.heads)
+            o = image.cross_attention(q, k, v, mask=mask, scale=self.scale)
+            return _linear(self.out, o.view(b * tokens, self.q.N)).view(*x.shape[:-1], self.out.N)
 
     __call__ = forward

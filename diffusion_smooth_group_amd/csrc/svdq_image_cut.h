@@ -169,9 +169,9 @@ inline svdq_status cross_cut(const svdq_cross_desc* d, int q_heads, int k_heads,
   const int64_t m = clamp(int64_t(cus) * 2 / kitems, ceil_div(slots, 128));
   t.row_chunk = int(ceil_div(ceil_div(slots > 0 ? slots : 1, m), 64) * 64);
   t.row_splits = int(ceil_div(slots > 0 ? slots : 1, t.row_chunk));
-  if (product_below(pairs, t.row_tiles, t.splits, svdq_kv::MAX_THREADS / 512) < 0 ||
-      product_below(pairs, t.key_tiles, t.row_splits, svdq_kv::MAX_THREADS / 512) < 0 ||
-      product_below(pairs, int64_t(t.key_tiles) * KEY_TILE, 1, svdq_kv::MAX_THREADS / 64) < 0)
+  // (a join's launch is smaller: only calls of few tiles are cut)
+  if (product_below(pairs, t.row_tiles, t.splits, svdq_kv::MAX_THREADS / 256) < 0 ||
+      (grad && product_below(pairs, t.key_tiles, t.row_splits, svdq_kv::MAX_THREADS / 256) < 0))
     return SVDQ_ERR_UNSUPPORTED;
   *out = t;
   return SVDQ_OK;

@@ -810,7 +810,8 @@ extern "C" svdq_status svdq_group_norm_backward(const svdq_norm_desc* d, const s
   if (st != SVDQ_OK) return st;
   if (!x || !g || !dx) return SVDQ_ERR_INVALID_ARG;
   if (d->samples == 0) {
-    if (dw || db) k_norm_zero<<<dim3(unsigned((d->channels + 255) / 256)), 256, 0, stream>>>(dw, db, d->channels);
+    if (!dw && !db) return SVDQ_OK;
+    k_norm_zero<<<dim3(unsigned((d->channels + 255) / 256)), 256, 0, stream>>>(dw, db, d->channels);
     return launch_ok();
   }
   if (!stats) return SVDQ_ERR_INVALID_ARG;
