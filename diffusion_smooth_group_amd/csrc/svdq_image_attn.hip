@@ -1187,6 +1187,12 @@ svdq_status check_cross(const svdq_cross_desc* d, int q_heads, int k_heads) {
   return SVDQ_OK;
 }
 
+// rows that are written: no row lies on the next
+svdq_status check_result(const svdq_heads* h, int D, int64_t n) {
+  const svdq_status st = check_heads(h, D);
+  return st == SVDQ_OK && n > 1 && h->token_stride < D ? SVDQ_ERR_SHAPE : st;
+}
+
 Rows rows_of(const svdq_heads* h) { return Rows{static_cast<uint16_t*>(h->data), h->token_stride, h->head_stride}; }
 
 svdq_status check_scratch(const void* ws, size_t have, size_t need) {
@@ -1270,8 +1276,7 @@ extern "C" svdq_status svdq_cross_attention(const svdq_cross_desc* d, const svdq
   if (d->requests == 0 || d->tokens == 0 || d->max_q == 0) return SVDQ_OK;
   CrossCut t;
   if ((st = cross_cut(d, q->heads, k->heads, device_cus(), false, &t)) != SVDQ_OK) return st;
-  for (const svdq_heads* h : {q, out})
-    if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
+  if ((st = check_heads(q, d->head_dim)) != SVDQ_OK || (st = check_result(out, d->head_dim, d->tokens)) != SVDQ_OK) return st;
   if (d->states > 0)                    // without states there need be none
     for (const svdq_heads* h : {k, v})
       if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
@@ -1314,13 +1319,17 @@ extern "C" svdq_status svdq_cross_attention_backward(const svdq_cross_desc* d, c
   CrossCut t;
   if ((st = cross_cut(d, q->heads, k->heads, device_cus(), true, &t)) != SVDQ_OK) return st;
   if (d->tokens > 0) {
-    for (const svdq_heads* h : {q, out, g, dq})
+    for (const svdq_heads* h : {q, out, g})
       if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
+    if ((st = check_result(dq, d->head_dim, d->tokens)) != SVDQ_OK) return st;
     if (!lse) return SVDQ_ERR_INVALID_ARG;
   }
-  if (d->states > 0)
-    for (const svdq_heads* h : {k, v, dk, dv})
+  if (d->states > 0) {
+    for (const svdq_heads* h : {k, v})
       if ((st = check_heads(h, d->head_dim)) != SVDQ_OK) return st;
+    for (const svdq_heads* h : {dk, dv})
+      if ((st = check_result(h, d->head_dim, d->states)) != SVDQ_OK) return st;
+  }
   if (!strides_fit({q, g}, t.group) || !strides_fit({k, v}, 1)) return SVDQ_ERR_UNSUPPORTED;
   const int64_t delta = cross_delta_floats(t, q->heads), part = ceil_div(cross_part_floats(d, t, true), 64) * 64;
   if ((st = check_scratch(ws, ws_bytes, size_t(delta + part + cross_key_floats(d, t)) * 4)) != SVDQ_OK) return st;

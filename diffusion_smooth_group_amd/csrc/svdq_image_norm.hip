@@ -82,6 +82,9 @@ __device__ __forceinline__ void groups8(const NormParams& p, int c, int* g) {
   for (int e = 1; e < 8; ++e) g[e] = one ? g[0] : int(unsigned(c + e) / unsigned(p.per));
 }
 
+// a square deviation's rounding below zero is zero; a NaN stays one
+__device__ __forceinline__ float not_negative(float x) { return __builtin_elementwise_maximum(x, 0.0f); }
+
 __device__ __forceinline__ float wave_sum(float x) {
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) x += __shfl_xor(x, m);
@@ -268,7 +271,7 @@ __global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
     mean = s0 * inv;
     dev = __builtin_fmaf(-s0, mean, q0);
     red[c * ld] = k0 + mean;
-    red[size + c * ld] = fmaxf(dev, 0.0f);
+    red[size + c * ld] = not_negative(dev);
   }
   __syncthreads();
   for (int g = wave; g < p.groups; g += waves) {
@@ -290,7 +293,7 @@ __global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
       const float m = t / float(p.per);
       float* out = p.part + (int64_t(blockIdx.x) * p.groups + g) * 2;
       out[0] = k0 + m;
-      out[1] = __builtin_fmaf(float(n), fmaxf(__builtin_fmaf(-t, m, u), 0.0f), d);
+      out[1] = __builtin_fmaf(float(n), not_negative(__builtin_fmaf(-t, m, u)), d);
     }
   }
 }
@@ -343,7 +346,7 @@ __device__ __forceinline__ void join_stats(const NormParams& p, int sample, int 
   const float2* part = reinterpret_cast<const float2*>(p.part) + int64_t(sample) * p.chunks * p.groups;
   for (int g = tid; g < p.groups; g += int(blockDim.x)) {
     const float m = sm[3 * g], u = sm[3 * g + 1], d = sm[3 * g + 2];
-    const float between = fmaxf(__builtin_fmaf(-m, m, u), 0.0f);
+    const float between = not_negative(__builtin_fmaf(-m, m, u));
     const float within = d / (float(p.per) * float(p.pixels));
     sm[3 * g] = part[g].x + m;
     sm[3 * g + 1] = 1.0f / __builtin_sqrtf(between + within + p.eps);
@@ -701,6 +704,14 @@ svdq_status check_map(const svdq_norm_desc* d, const svdq_map* m) {
   return SVDQ_OK;
 }
 
+// a map that is written: no element lies on another
+svdq_status check_result(const svdq_norm_desc* d, const svdq_map* m) {
+  const svdq_status st = check_map(d, m);
+  if (st != SVDQ_OK || d->samples <= 1) return st;
+  const __int128 pixels = __int128(d->pixels - 1) * m->pixel_stride + d->channels, samples = __int128(d->samples - 1) * m->sample_stride + d->channels;
+  return m->sample_stride >= pixels || (d->pixels > 1 && m->pixel_stride >= samples && m->sample_stride >= d->channels) ? SVDQ_OK : SVDQ_ERR_SHAPE;
+}
+
 svdq_status check_ws(const void* ws, size_t have, size_t need) {
   if (need == 0) return SVDQ_OK;
   if (!ws) return SVDQ_ERR_INVALID_ARG;
@@ -779,7 +790,7 @@ extern "C" svdq_status svdq_group_norm(const svdq_norm_desc* d, const svdq_map* 
   if (st != SVDQ_OK) return st;
   if (!x || !y) return SVDQ_ERR_INVALID_ARG;
   if (d->samples == 0) return SVDQ_OK;
-  if ((st = check_map(d, x)) != SVDQ_OK || (st = check_map(d, y)) != SVDQ_OK) return st;
+  if ((st = check_map(d, x)) != SVDQ_OK || (st = check_result(d, y)) != SVDQ_OK) return st;
   NormCut t;
   if ((st = norm_cut(d, false, &t)) != SVDQ_OK || (st = check_ws(ws, ws_bytes, norm_bytes(d, t, false))) != SVDQ_OK) return st;
   NormParams p = params_of(d, t);
@@ -815,7 +826,7 @@ extern "C" svdq_status svdq_group_norm_backward(const svdq_norm_desc* d, const s
     return launch_ok();
   }
   if (!stats) return SVDQ_ERR_INVALID_ARG;
-  if ((st = check_map(d, x)) != SVDQ_OK || (st = check_map(d, g)) != SVDQ_OK || (st = check_map(d, dx)) != SVDQ_OK) return st;
+  if ((st = check_map(d, x)) != SVDQ_OK || (st = check_map(d, g)) != SVDQ_OK || (st = check_result(d, dx)) != SVDQ_OK) return st;
   NormCut t;
   if ((st = norm_cut(d, true, &t)) != SVDQ_OK || (st = check_ws(ws, ws_bytes, norm_bytes(d, t, true))) != SVDQ_OK) return st;
   NormParams p = params_of(d, t);

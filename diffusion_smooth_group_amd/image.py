@@ -276,8 +276,8 @@ def _cross_desc(q, k, v, q_start, k_start, max_q, max_k, mask, scale, dev):
         raise ValueError(f"q, k, v: all [tokens, heads, D] or all [requests, tokens, heads, D] are needed, got {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
     pm = None
     if mask is not None:
-        if mask.dtype not in (torch.bool, torch.uint8) or mask.numel() != states or not mask.is_contiguous() or mask.get_device() != dev:
-            raise ValueError(f"mask: a contiguous bool tensor of {states} entries on cuda:{dev} is needed, got {mask.dtype} {tuple(mask.shape)} on {mask.device}")
+        if mask.dtype not in (torch.bool, torch.uint8) or mask.shape != k.shape[:-2] or not mask.is_contiguous() or mask.get_device() != dev:
+            raise ValueError(f"mask: a contiguous bool tensor {tuple(k.shape[:-2])} on cuda:{dev} is needed, got {mask.dtype} {tuple(mask.shape)} on {mask.device}")
         pm = mask.data_ptr()
     d = svdq_cross_desc(requests, tokens, states, _size(dim, "head_dim"), _code(q.dtype), _size(max_q, "max_q"), _size(max_k, "max_k"),
                         (1.0 / math.sqrt(dim) if dim else 1.0) if scale is None else scale, qs, ks, pm)
@@ -292,8 +292,8 @@ def cross_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] = 
     requests of different lengths one after the other: q [tokens, heads, D], rows
     q_start[r] .. q_start[r + 1] are request r's, k and v [states, k_heads, D]
     with k_start (int32 [requests + 1] both), and max_q, max_k, which bound a
-    request's rows and states.  k_heads divides heads.  mask: bool or uint8,
-    one entry a state, in the states' order; false (0): not seen.  scale: 1 /
+    request's rows and states.  k_heads divides heads.  mask: bool or uint8, of
+    k's shape without heads and D; false (0): the state is not seen.  scale: 1 /
     sqrt(D) by default.  A row that sees nothing gives zeros; a row of no
     request is not written.  Returns out, or (out, lse): lse fp32, q's shape
     without D."""

@@ -410,3 +410,33 @@ def test_no_requests_and_no_states():
     out, lse = image.cross_attention(q, k, k, return_lse=True)
     _, dk, dv = image.cross_attention_backward(q, q, k, k, out, lse)
     assert bool((dk == 0).all()) and bool((dv == 0).all())
+
+
+@pytest.mark.parametrize("rows,keys", [(1, 9000), (9000, 150)])
+def test_offsets_past_32_bits(rows, keys):
+    """Operands whose tokens lie 2^18 elements apart: 2^31 elements and more in all."""
+    torch, image = _torch()
+    c = Case([rows], [keys], 2, 2, 64, "bf16")
+    if rows > keys:
+        far = torch.empty((rows, 1 << 18), dtype=torch.bfloat16, device="cuda")[:, :256].view(rows, 4, 64)
+        q, g = far[:, :2], far[:, 2:]
+        q.copy_(c.q)
+        g.copy_(c.g)
+        k, v = c.k, c.v
+    else:
+        far = torch.empty((keys, 1 << 18), dtype=torch.bfloat16, device="cuda")[:, :256].view(keys, 4, 64)
+        k, v = far[:, :2], far[:, 2:]
+        k.copy_(c.k)
+        v.copy_(c.v)
+        q, g = c.q, c.g
+    out, lse = image.cross_attention(q, k, v, return_lse=True, **c.where)
+    want, again = image.cross_attention(c.q, c.k, c.v, return_lse=True, **c.where)
+    assert torch.equal(out, want) and torch.equal(lse, again)
+    grads = image.cross_attention_backward(g, q, k, v, out, lse, **c.where)
+    assert all(torch.equal(a, b) for a, b in zip(grads, image.cross_attention_backward(c.g, c.q, c.k, c.v, out, lse, **c.where)))
+    far = torch.empty((max(rows, keys), 1 << 18), dtype=torch.bfloat16, device="cuda")[:, :128].view(-1, 2, 64)
+    if rows > keys:
+        assert torch.equal(image.cross_attention(q, k, v, out=far, **c.where), want)
+    else:
+        image.cross_attention_backward(g, q, k, v, out, lse, dk=far, **c.where)
+        assert torch.equal(far, grads[1])

@@ -76,6 +76,9 @@ def test_norm_operand_refusals():
             maps = [fmap(), fmap(), fmap()]
             maps[at] = bad
             assert b(big, maps[0], maps[1], P, maps[2], P, P, P, 1 << 40, None) == status
+    for lies_on_itself in (fmap(sample=0), fmap(sample=320), fmap(sample=320 * ((1 << 16) - 1)), fmap(sample=640, pixel=320)):
+        assert f(big, fmap(), lies_on_itself, None, P, need, None) == SHAPE
+        assert b(big, fmap(), fmap(), P, lies_on_itself, P, P, P, 1 << 40, None) == SHAPE
     assert f(big, fmap(), fmap(), None, None, need, None) == INVALID
     assert f(big, fmap(), fmap(), None, P, need - 1, None) == CAPACITY
     assert f(big, fmap(), fmap(), None, ODD, need, None) == INVALID
@@ -159,6 +162,10 @@ def test_cross_operand_refusals():
         assert run_backward(d, **{name: heads(4)}) == SHAPE
     for name in ("v", "dk", "dv"):
         assert run_backward(d, **{name: heads(8)}) == SHAPE
+    for stride in (0, 56):              # results whose rows lie on each other
+        assert run_forward(d, out=heads(8, token=stride)) == SHAPE
+        for name, n in (("dq", 8), ("dk", 4), ("dv", 4)):
+            assert run_backward(d, **{name: heads(n, token=stride)}) == SHAPE
     # strides whose offsets 32 bits do not hold
     far = 1 << 23
     assert run_forward(d, k=heads(4, token=far)) == UNSUPPORTED and run_forward(d, v=heads(4, token=far)) == UNSUPPORTED
