@@ -239,9 +239,10 @@ struct RowPiece {
 };
 
 // The 128 rows of a tile, by way of LDS: in memory they are whole lines (8 lanes a
-// row of 64), as operands and results 32 bytes of every row at a time, which memory
-// took 1.4 times as long for (2 x 4096 rows, 10 heads of 64, without any key: 7.9 us
-// against REPLACE).
+// row of 64), as operands and results 32 bytes of every row at a time, for which the
+// memory system takes longer (dq, q, g and out so: 2 x 4096 rows, 10 heads of 64,
+// over 77: 20.3 us, 16 of them without any key, and 16.4 by way of LDS; 1023 rows
+// over 2049, 32 heads of 128: 256 and 226).
 template <int DP>
 struct TileRows {
   static constexpr int CH = DP / 8, N = 128 * CH / 256, LD = row_of<DP>();
@@ -329,7 +330,16 @@ __device__ __forceinline__ f32x16 rows16(const float* at, int hb) {
 // 32 rows a wave on 32x32x16: S^T = K Q^T leaves a lane with 16 of 32 keys of
 // one row, two runs of four neighbours for every 16, which is the operand of
 // O^T = V^T P^T as it stands; V^T comes out of LDS by transposing reads of four
-// keys each.
+// keys each.  128 rows a workgroup share stages of 64 keys, the next one in
+// registers on its way; two workgroups a compute unit (three with heads up to 96: 3 x
+// 2047 rows over 300, 16 heads of 72, 20 us against 25).  One request, 4608 rows over
+// 4096, 24 heads of 128: 254 us, 910 TFLOP/s.  What bounds that: matrix and vector
+// instructions of two waves a SIMD that hardly overlap (without the exponentials 256
+// us of then 276, without the loads 254), and 864 tiles on 512 places.  Measured and
+// not kept: the reference raised by the probabilities' sum instead of a maximum (the
+// compiler copies the accumulators, 362 us against 298), the second tile's
+// exponentials between the first's products (325 against 281), masks as the logits'
+// start, from LDS (290 against 275 without a mask).
 template <int DT, int DP>
 __global__ __launch_bounds__(256, DP == 128 ? 2 : 3) void k_cross_rows(CrossParams p) {
   constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
@@ -489,7 +499,10 @@ __global__ __launch_bounds__(256, DP == 128 ? 2 : 3) void k_cross_rows(CrossPara
 // ------------------------------------------------------------- forward, few rows
 // 16 rows a workgroup on 16x16x32, 32 keys a wave and step, straight from memory:
 // K as operands, V through a piece of LDS of the wave's own for its transposition.
-// The waves meet at the end.
+// The waves meet at the end.  The states' bytes bound it: 64 requests with up to 4096,
+// 8 heads of 128 and four query heads each, 143 us, 4.8 TB/s; with the same loads
+// through 64-bit addresses of their own it needed all registers of one wave a SIMD
+// (184 us), at three waves with spills 159.
 template <int DT, int DP>
 __global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void k_cross_few(CrossParams p) {
   constexpr int NJ = DP / 32, NX = DP / 16, LD = row_of<DP>(), CH = DP / 8, NV = 32 * CH / 64;
@@ -703,7 +716,9 @@ __global__ __launch_bounds__(256) void k_cross_join(CrossParams p) {
 // transposing reads.  Leaves delta for k_cross_dkv.  SHORT: all keys (up to 128) are
 // in LDS at once, and delta_i = sum_t p_it (g_i . v_t) comes from a pass over them,
 // not from `out`, whose bytes are not read and whose rounding, which counts most over
-// few keys, does not enter.
+// few keys, does not enter.  5 x up to 1023 rows over 2049, 32 heads in groups of
+// four: 222 us of the call's 442; 4608 rows over 512, 24 heads, f16: 86 of 180; 2 x
+// 4096 over 77, 10 heads of 64: 16 of 35.  Bound as k_cross_rows.
 template <int DT, int DP, bool SHORT>
 __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
   constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
@@ -924,7 +939,12 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
 // workgroup; rows pass by in LDS, RT a stage.  S = Q K^T leaves a lane with 16
 // rows of one key: the operand of dV^T += G^T P and dK^T += Q^T dS, G^T and Q^T
 // by transposing reads.  A key that is not seen spoils only its own lane's sums,
-// which are not stored.
+// which are not stored.  delta is what the products with V start from.  5 x up to
+// 1023 rows over 2049, 32 heads of 128 in groups of four: 253 us; 4608 rows over 512,
+// 24 heads, f16: 87 and 13 for the join; 2 x 4096 over 77: 15 and 6.  LDS reads and
+// matrix instructions bound it (each row tile is read four times a wave).  64 keys a
+// wave would halve the reads but take all registers of one wave a SIMD: 10 heads of
+// 64, 2 x 4096 rows over 300, 99 us a call against 61; heads of 128 spill.
 template <int DT, int DP>
 __global__ __launch_bounds__(256, 2) void k_cross_dkv(CrossParams p) {
   constexpr int RT = DP == 96 ? 64 : 32, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
