@@ -947,7 +947,7 @@ __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
 // 64, 2 x 4096 rows over 300, 99 us a call against 61; heads of 128 spill.
 template <int DT, int DP>
 __global__ __launch_bounds__(256, 2) void k_cross_dkv(CrossParams p) {
-  constexpr int RT = DP == 96 ? 64 : 32, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
+  constexpr int RT = DP == 128 ? 32 : 64, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
   __shared__ __attribute__((aligned(16))) uint16_t sq[2][RT * LD];
   __shared__ __attribute__((aligned(16))) uint16_t sg[2][RT * LD];
   __shared__ __attribute__((aligned(16))) float sl[2][RT], sd[2][RT];

@@ -64,27 +64,42 @@ _SIGS = {
 _FN = {}
 
 
-def _call(name, *args):
+def _fn(name):
     fn = _FN.get(name)
     if fn is None:
         fn = getattr(S.lib_handle(), name)
         fn.argtypes, fn.restype = _SIGS[name], C.c_int
         _FN[name] = fn
-    rc = fn(*args)
+    return fn
+
+
+def _call(name, *args):
+    rc = _fn(name)(*args)
     if rc != 0:
         raise SvdqError(name, rc)
 
 
-def _workspace(ws, like, name, *args):
-    """Address and bytes of the call's workspace: the caller's, or one of the call's own."""
-    if ws is None:
-        need = _SZ(0)
-        _call(name, *args, need)
-        if need.value == 0:
-            return None, 0
-        ws = like.new_empty(need.value, dtype=torch.uint8)
-        return ws, need.value
-    return ws, _scratch(ws, like.get_device())[1]
+def _call_with_workspace(name, like, ws, size_of, before, stream, likely):
+    """The call with the caller's workspace, or with one of its own where it needs
+    one.  size_of: the arguments that tell its size.  Where a call is not `likely` to
+    need one it goes without first (it says so before anything is launched), so that
+    small calls are spared the question: 1 us of 9.5."""
+    if ws is not None:
+        _call(name, *before, *_scratch(ws, like.get_device()), stream)
+        return
+    if not likely:
+        rc = _fn(name)(*before, None, 0, stream)
+        if rc == 0:
+            return
+    need = _SZ(0)
+    _call(name + "_workspace", *size_of, need)
+    if need.value == 0:
+        if not likely:
+            raise SvdqError(name, rc)
+        _call(name, *before, None, 0, stream)
+        return
+    ws = like.new_empty(need.value, dtype=torch.uint8)
+    _call(name, *before, ws.data_ptr(), need.value, stream)
 
 
 def _address(ws):
@@ -121,9 +136,11 @@ def _map(t, name, like, dev):
     return svdq_map(t.data_ptr(), first, step)
 
 
-def _new_map(like, dev):
-    """An output like `like`, channels last, and its view for the call."""
+def _new_map(like, view, dev):
+    """An output like `like`, channels last, and its view for the call; view: like's."""
     t = torch.empty_like(like)
+    if t.stride() == like.stride():
+        return t, svdq_map(t.data_ptr(), view.sample_stride, view.pixel_stride)
     if not t.is_contiguous() and (t.stride(-1) != 1 or _run(t) is None):
         t = like.new_empty(like.shape)
     return t, _map(t, "out", like, dev)
@@ -152,12 +169,12 @@ def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: O
         d = _norm_desc(x, groups, weight, bias, eps, act, dev)
         mx = _map(x, "x", x, dev)
         if out is None:
-            out, mo = _new_map(x, dev)
+            out, mo = _new_map(x, mx, dev)
         else:
             mo = _map(out, "out", x, dev)
         stats = x.new_empty((x.shape[0], groups, 2), dtype=torch.float32) if return_stats else None
-        ws, n = _workspace(ws, x, "svdq_group_norm_workspace", d)
-        _call("svdq_group_norm", d, mx, mo, _address(stats), _address(ws), n, _stream(x))
+        _call_with_workspace("svdq_group_norm", x, ws, (d,), (d, mx, mo, _address(stats)), _stream(x),
+                             d.pixels * d.channels > 65536 * d.groups)
         return (out, stats) if return_stats else out
 
 
@@ -170,15 +187,15 @@ def group_norm_backward(g, x, stats, groups: int, weight=None, bias=None, act: O
         d = _norm_desc(x, groups, weight, bias, 0.0, act, dev)
         mx, mg = _map(x, "x", x, dev), _map(g, "g", x, dev)
         if dx is None:
-            dx, md = _new_map(x, dev)
+            dx, md = _new_map(x, mx, dev)
         else:
             md = _map(dx, "dx", x, dev)
         if stats.dtype is not torch.float32 or stats.shape != (x.shape[0], groups, 2) or not stats.is_contiguous() or stats.get_device() != dev:
             raise ValueError(f"stats: a contiguous float32 tensor {(x.shape[0], groups, 2)} on cuda:{dev} is needed, "
                              f"got {stats.dtype} {tuple(stats.shape)} on {stats.device}")
         dw, db = x.new_empty((2, x.shape[-1]), dtype=torch.float32).unbind()
-        ws, n = _workspace(ws, x, "svdq_group_norm_backward_workspace", d)
-        _call("svdq_group_norm_backward", d, mx, mg, stats.data_ptr(), md, dw.data_ptr(), db.data_ptr(), _address(ws), n, _stream(x))
+        _call_with_workspace("svdq_group_norm_backward", x, ws, (d,), (d, mx, mg, stats.data_ptr(), md, dw.data_ptr(), db.data_ptr()), _stream(x),
+                             d.samples > 2 or d.pixels * d.channels > 16384 * d.groups)
         return dx, dw, db
 
 
@@ -244,10 +261,13 @@ def _rows(t, name, b, n, dim, dtype, dev):
     return svdq_heads(t.data_ptr(), step if n * (b or 1) > 1 else 0, wide if h > 1 else 0, h)
 
 
-def _out(t, name, like, b, n, dim, dtype, dev):
-    """An output like `like`, a new one where t is None, and its view for the call."""
+def _out(t, name, like, view, b, n, dim, dtype, dev):
+    """An output like `like`, a new one where t is None, and its view for the call;
+    view: like's."""
     if t is None:
         t = torch.empty_like(like)
+        if t.stride() == like.stride():
+            return t, svdq_heads(t.data_ptr(), view.token_stride, view.head_stride, view.heads)
         if not t.is_contiguous() and (t.stride(-1) != 1 or _stride(t) is None):
             t = like.new_empty(like.shape)
     elif t.shape != like.shape:
@@ -302,10 +322,9 @@ def cross_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] = 
         d, b, n, m, dim = _cross_desc(q, k, v, q_start, k_start, max_q, max_k, mask, scale, dev)
         dtype = q.dtype
         hq, hk, hv = _rows(q, "q", b, n, dim, dtype, dev), _rows(k, "k", b, m, dim, dtype, dev), _rows(v, "v", b, m, dim, dtype, dev)
-        out, ho = _out(out, "out", q, b, n, dim, dtype, dev)
+        out, ho = _out(out, "out", q, hq, b, n, dim, dtype, dev)
         lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if return_lse else None
-        ws, size = _workspace(ws, q, "svdq_cross_attention_workspace", d, hq.heads, hk.heads)
-        _call("svdq_cross_attention", d, hq, hk, hv, ho, _address(lse), _address(ws), size, _stream(q))
+        _call_with_workspace("svdq_cross_attention", q, ws, (d, hq.heads, hk.heads), (d, hq, hk, hv, ho, _address(lse)), _stream(q), False)
         return (out, lse) if return_lse else out
 
 
@@ -322,11 +341,11 @@ def cross_attention_backward(g, q, k, v, out, lse, q_start=None, k_start=None, m
         hk, hv = _rows(k, "k", b, m, dim, dtype, dev), _rows(v, "v", b, m, dim, dtype, dev)
         if lse.dtype is not torch.float32 or lse.shape != q.shape[:-1] or not lse.is_contiguous() or lse.get_device() != dev:
             raise ValueError(f"lse: a contiguous float32 tensor {tuple(q.shape[:-1])} on cuda:{dev} is needed, got {lse.dtype} {tuple(lse.shape)} on {lse.device}")
-        dq, hdq = _out(dq, "dq", q, b, n, dim, dtype, dev)
-        dk, hdk = _out(dk, "dk", k, b, m, dim, dtype, dev)
-        dv, hdv = _out(dv, "dv", v, b, m, dim, dtype, dev)
-        ws, size = _workspace(ws, q, "svdq_cross_attention_backward_workspace", d, hq.heads, hk.heads)
-        _call("svdq_cross_attention_backward", d, hq, hk, hv, ho, lse.data_ptr(), hg, hdq, hdk, hdv, _address(ws), size, _stream(q))
+        dq, hdq = _out(dq, "dq", q, hq, b, n, dim, dtype, dev)
+        dk, hdk = _out(dk, "dk", k, hk, b, m, dim, dtype, dev)
+        dv, hdv = _out(dv, "dv", v, hv, b, m, dim, dtype, dev)
+        _call_with_workspace("svdq_cross_attention_backward", q, ws, (d, hq.heads, hk.heads),
+                             (d, hq, hk, hv, ho, lse.data_ptr(), hg, hdq, hdk, hdv), _stream(q), True)
         return dq, dk, dv
 
 

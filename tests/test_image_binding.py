@@ -11,17 +11,21 @@ from diffusion_smooth_group_amd import image, kv
 
 @pytest.fixture
 def calls(monkeypatch):
-    """The library's calls: name and arguments.  A workspace of 64 bytes is asked for."""
+    """The library's calls: name and arguments.  They need a workspace of 64 bytes."""
     seen = []
 
-    def call(name, *args):
-        if name.endswith("_workspace"):
-            args[-1].value = 64
-        seen.append((name, args))
+    def fn(name):
+        def call(*args):
+            seen.append((name, args))
+            if name.endswith("_workspace"):
+                args[-1].value = 64
+                return 0
+            return 0 if args[-2] == 64 else 1
+        return call
     monkeypatch.setattr(image, "_on", lambda stream, t: contextlib.nullcontext())
     monkeypatch.setattr(image, "_stream", lambda t: 17)
     monkeypatch.setattr(kv, "_current_device", lambda: -1)
-    monkeypatch.setattr(image, "_call", call)
+    monkeypatch.setattr(image, "_fn", fn)
     return seen
 
 
@@ -128,6 +132,20 @@ def test_gradient_outputs(calls):
             image.cross_attention_backward(q, q, k, k, q, bad)
     with pytest.raises(ValueError, match="dk"):
         image.cross_attention_backward(q, q, k, k, q, lse, dk=half(2, 9, 8, 64))
+
+
+def test_workspaces(calls):
+    x = half(3, 5, 7, 64)
+    image.group_norm(x, 8)
+    assert [n for n, _ in calls] == ["svdq_group_norm", "svdq_group_norm_workspace", "svdq_group_norm"]
+    ws = torch.zeros(64, dtype=torch.uint8)
+    image.group_norm(x, 8, ws=ws)
+    assert len(calls) == 4 and calls[-1][1][-3:-1] == (ws.data_ptr(), 64)
+    with pytest.raises(kv.SvdqError):                   # a workspace that is too small stays the caller's matter
+        image.group_norm(x, 8, ws=ws[:32])
+    assert len(calls) == 5
+    with pytest.raises(ValueError, match="ws"):
+        image.group_norm(x, 8, ws=torch.zeros(128, dtype=torch.uint8)[::2])
 
 
 def test_host_tensors_are_refused():
