@@ -194,6 +194,28 @@ def test_dense_requests_are_the_ragged_ones(rows, dtype):
     assert torch.equal(image.cross_attention(q, k, v, mask=c.mask.view(3, 90).to(torch.uint8)), got[0])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,hk,d", [(6, 2, 64), (5, 1, 128), (14, 2, 72), (33, 1, 40), (64, 1, 64), (80, 1, 96), (7, 7, 64), (24, 8, 128)])
+def test_heads_in_groups_of_any_size(hq, hk, d, dtype):
+    """Rows of a pair are (token, head of the group): groups that divide a stage of rows, that do not, and larger ones."""
+    _, image = _torch()
+    for rows, keys in (([1, 1], [70, 9]), ([37, 2, 5], [150, 300, 40])):
+        c = Case(rows, keys, hq, hk, d, dtype, seed=hq, mask="random")
+        out, lse = image.cross_attention(c.q, c.k, c.v, return_lse=True, **c.where)
+        check_forward(c, out, lse, f"{hq}/{hk}")
+        check_backward(c, out, lse, *image.cross_attention_backward(c.g, c.q, c.k, c.v, out, lse, **c.where), f"{hq}/{hk}")
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+def test_many_requests(rows):
+    _, image = _torch()
+    n = 203
+    c = Case([rows + i % 3 for i in range(n)], [(7 * i) % 90 for i in range(n)], 3, 3, 64, "bf16", mask="random")
+    out, lse = image.cross_attention(c.q, c.k, c.v, return_lse=True, **c.where)
+    check_forward(c, out, lse)
+    check_backward(c, out, lse, *image.cross_attention_backward(c.g, c.q, c.k, c.v, out, lse, **c.where))
+
+
 @pytest.mark.parametrize("rows", [[2, 1], [150, 40]])
 def test_what_is_of_no_request_is_left(rows):
     torch, image = _torch()
