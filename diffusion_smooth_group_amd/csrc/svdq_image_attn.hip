@@ -11,6 +11,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "svdq_image.h"
 #include "svdq_image_cut.h"
@@ -266,7 +267,9 @@ struct TileRows {
 };
 
 // A wave's 32 rows of a result (its transpose in o, times `by`) to memory by way of
-// its part of LDS, which no other wave uses.
+// its part of LDS, which no other wave uses; past the caches where a row is whole
+// lines (2 x 4096 rows of 64 over 77: 10.1 us, 11.3 through them; 3 x 2047 rows of 72
+// over 300: 21.1 past them, 19.7 through them).
 template <int DT, int DP>
 __device__ __forceinline__ void store_rows(const CrossParams& p, const CrossRange& r, const Rows& to, uint16_t* lds, const f32x16* o, float by,
                                            int first, int h, int lane) {
@@ -283,15 +286,21 @@ __device__ __forceinline__ void store_rows(const CrossParams& p, const CrossRang
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  auto put = [&](auto past) {
 #pragma unroll
-  for (int i = 0; i < 32 * CH / 64; ++i) {
-    const int row = (lane + 64 * i) / CH, d = (lane + 64 * i) % CH * 8, rw = first + row;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * LD + d);
-    if (rw < rows && d < p.D) {
+    for (int i = 0; i < 32 * CH / 64; ++i) {
+      const int row = (lane + 64 * i) / CH, d = (lane + 64 * i) % CH * 8, rw = first + row;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * LD + d);
+      if (rw >= rows || d >= p.D) continue;
       const int t = p.token_of(rw);
-      *reinterpret_cast<u32x4*>(to.data + (int64_t(r.q_first) + t) * to.token + (h * p.group + rw - t * p.group) * to.head + d) = v;
+      u32x4* at = reinterpret_cast<u32x4*>(to.data + (int64_t(r.q_first) + t) * to.token + (h * p.group + rw - t * p.group) * to.head + d);
+      if constexpr (decltype(past)::value) __builtin_nontemporal_store(v, at);
+      else *at = v;
     }
-  }
+    if constexpr (decltype(past)::value) asm volatile("" ::: "memory");    // else the last store of both forms becomes one
+  };
+  if (p.D % 64 == 0) put(std::true_type());
+  else put(std::false_type());
 }
 
 // bit t: state `at` + t of the request is seen, t < 64
