@@ -727,7 +727,7 @@ __global__ __launch_bounds__(256) void k_cross_join(CrossParams p) {
 // not from `out`, whose bytes are not read and whose rounding, which counts most over
 // few keys, does not enter.  5 x up to 1023 rows over 2049, 32 heads in groups of
 // four: 222 us of the call's 442; 4608 rows over 512, 24 heads, f16: 86 of 180; 2 x
-// 4096 over 77, 10 heads of 64: 16 of 35.  Bound as k_cross_rows.
+// 4096 over 77, 10 heads of 64: 15 of 33.  Bound as k_cross_rows.
 template <int DT, int DP, bool SHORT>
 __global__ __launch_bounds__(256, 2) void k_cross_dq(CrossParams p) {
   constexpr int KT = 64, NE = DP / 16, NX = DP / 32, LD = row_of<DP>();
