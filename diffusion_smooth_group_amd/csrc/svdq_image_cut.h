@@ -18,6 +18,7 @@ using svdq_kv::smaller;
 // ------------------------------------------------------------------ group norm
 constexpr int NORM_FEW_SAMPLES = 2;
 constexpr int NORM_MAX_BLOCK = 32;      // groups of a workgroup of the one-launch form
+constexpr int NORM_MOST_PIXELS = 256;   // pixels of a thread of the two-launch form: terms it adds one after the other
 
 struct NormCut {
   int threads;
@@ -34,8 +35,10 @@ struct NormCut {
 // NORM_FEW_SAMPLES the same launch takes the samples in turn (2 x 8 x 8 x 1280: 14.0 us
 // a call, 19.7 with a launch for the sums; four samples: 14.5 on the GPU against 7.3).
 // Two launches: a workgroup of about 1024 threads a compute unit (1 x 512 x 512 x
-// 128: 42.5 us with 256, 44 with 512 of 512 threads, 47 with 512 of 1024; the
-// gradient of 2 x 128 x 128 x 320: 30, 34, 40): each joins all chunks of its sample.
+// 128, when the kernels were slower: 42.5 us with 256, 44 with 512 of 512 threads, 47
+// with 512 of 1024; the gradient of 2 x 128 x 128 x 320: 30, 34, 40): each joins all
+// chunks of its sample.  More of them where a thread would have more than
+// NORM_MOST_PIXELS, so that no sum of one after the other is longer.
 inline svdq_status norm_cut(const svdq_norm_desc* d, bool grad, NormCut* out) {
   NormCut t = {};
   const int per = d->channels / d->groups;
@@ -66,8 +69,10 @@ inline svdq_status norm_cut(const svdq_norm_desc* d, bool grad, NormCut* out) {
   }
   const int64_t want = 256 / (d->samples < 1 ? 1 : d->samples);
   t.chunk = ceil_div(ceil_div(d->pixels, want < 1 ? 1 : want), t.rows) * t.rows;
-  t.chunks = int(ceil_div(d->pixels, t.chunk));
-  if (product_below(d->samples, int64_t(t.chunks) + 1024, 1024, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
+  if (t.chunk > int64_t(t.rows) * NORM_MOST_PIXELS) t.chunk = int64_t(t.rows) * NORM_MOST_PIXELS;
+  const int64_t chunks = ceil_div(d->pixels, t.chunk);
+  if (product_below(d->samples, chunks + 1024, 1024, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
+  t.chunks = int(chunks);
   *out = t;
   return SVDQ_OK;
 }

@@ -52,7 +52,7 @@ __device__ __forceinline__ u32x4 pack8(const float* f) {
 }
 
 // The last read of a map and the write of the result pass the caches by (1 x 512 x 512
-// x 128: 45.6 us a call without, 42.5 with the writes, 40.7 with both).
+// x 128, by itself: 5 us of a call of 45 less, 3 of them by the writes).
 __device__ __forceinline__ u32x4 last_read(const uint16_t* at) { return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at)); }
 __device__ __forceinline__ void write_past(u32x4 v, uint16_t* at) { __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(at)); }
 
@@ -95,6 +95,10 @@ __device__ __forceinline__ float wave_sum(float x) {
   for (int m = 1; m < 64; m *= 2) x += __shfl_xor(x, m);
   return x;
 }
+
+// The middle one of three: a reference that one value far from the rest does not
+// move (a NaN or an infinity among them reaches the sums by itself).
+__device__ __forceinline__ float middle(float a, float b, float c) { return __builtin_amdgcn_fmed3f(a, b, c); }
 
 // Weights of eight channels; ones and zeros where there are none.
 template <int DT>
@@ -232,78 +236,127 @@ __global__ __launch_bounds__(1024) void k_norm_whole(NormParams p) {
 }
 
 // ----------------------------------------------------------- two launches
-// Statistics of a chunk of pixels, all channels: sums of the deviations from the
-// chunk's first pixel and of their squares, channel by channel; channels of a
-// group are joined by their means and square deviations.  Memory bounds both
-// launches: 1 x 512 x 512 x 128 takes 16.5 us (4.1 TB/s) and k_norm_apply, which reads
-// the map again, 23 (5.8 TB/s).
+// Statistics of a chunk of pixels, all channels.  A thread takes its pixels in runs
+// of RUN, each about the mean of those before it (the first about its first pixel),
+// so that neither a mean far from zero nor a pixel far from the rest costs digits:
+// about the chunk's first pixel alone, one at zero among 65536 pixels of 512 +- 2 made
+// rstd wrong by 5 to 30 %.  With s and q the sums of d = x - mean and d^2 over a run and
+// n pixels after it, mean += s / n and the square deviations grow by q - s s / n.
+// Threads, channels of a group and chunks are joined by their means, square
+// deviations about the joined mean.  Means are held less one value of the chunk's
+// own.  Memory bounds both launches: 1 x 512 x 512 x 128 takes 19 us (3.5 TB/s; 16.5
+// about the chunk's first pixel) and k_norm_apply, which reads the map again, 23 (5.8
+// TB/s).
+constexpr int RUN = 32;
+
 template <int DT>
 __global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
   extern __shared__ float red[];        // [2][channels][rows]
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
   const int sample = int(blockIdx.x) / p.chunks, chunk = int(blockIdx.x) % p.chunks;
-  const int64_t from = int64_t(chunk) * p.chunk, n = min(p.pixels - from, p.chunk);
+  const int64_t from = int64_t(chunk) * p.chunk;
+  const int n = int(min(p.pixels - from, p.chunk));     // (a thread has at most NORM_MOST_PIXELS of them)
   const int row = tid / p.cv, piece = tid % p.cv;
   const bool on = row < p.rows;
-  float s[8] = {}, q[8] = {}, k[8], f[8];
-  if (on) {
-    const uint16_t* x = p.x + int64_t(sample) * p.xs + from * p.xp + 8 * piece;
-    unpack8<DT>(*reinterpret_cast<const u32x4*>(x), k);
+  const uint16_t* base = p.x + int64_t(sample) * p.xs + from * p.xp;
+  const int64_t k_at[3] = {int64_t(n / 4) * p.xp, int64_t(n / 2) * p.xp, (int64_t(n) * 3 / 4) * p.xp};
+  // pixels of row r of the chunk: every p.rows-th one
+  const int each = n / p.rows, over = n % p.rows;
+  float m[8] = {}, dev[8] = {}, f[8];
+  if (on && row < n) {
+    const uint16_t* x = base + 8 * piece;
+    float k[8], k1[8], k2[8];
+    unpack8<DT>(*reinterpret_cast<const u32x4*>(x + k_at[0]), k);
+    unpack8<DT>(*reinterpret_cast<const u32x4*>(x + k_at[1]), k1);
+    unpack8<DT>(*reinterpret_cast<const u32x4*>(x + k_at[2]), k2);
     const int64_t step = int64_t(p.rows) * p.xp;
     x += int64_t(row) * p.xp;
+    unpack8<DT>(*reinterpret_cast<const u32x4*>(x), m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      k[e] = middle(k[e], k1[e], k2[e]);
+      m[e] -= k[e];
+    }
+    const int mine = each + (row < over ? 1 : 0);
+    for (int done = 0; done < mine; done += RUN) {
+      const int run = min(RUN, mine - done);
+      float s[8] = {}, q[8] = {};
 #pragma unroll 4
-    for (int64_t at = row; at < n; at += p.rows, x += step) {
-      unpack8<DT>(*reinterpret_cast<const u32x4*>(x), f);
+      for (int i = 0; i < run; ++i, x += step) {
+        unpack8<DT>(*reinterpret_cast<const u32x4*>(x), f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = (f[e] - k[e]) - m[e];
+          s[e] += d;
+          q[e] = __builtin_fmaf(d, d, q[e]);
+        }
+      }
+      const float inv = 1.0f / float(done + run);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = f[e] - k[e];
-        s[e] += d;
-        q[e] = __builtin_fmaf(d, d, q[e]);
+        const float by = s[e] * inv;
+        m[e] += by;
+        dev[e] += not_negative(__builtin_fmaf(-s[e], by, q[e]));
       }
     }
   }
-  // channel sums: by thread, then one thread a channel
+  // channels: a row's mean counts by its pixels
   const int ld = p.rows | 1, size = p.channels * ld;
-  leave8(red, ld, s, piece, row, on);
-  leave8(red + size, ld, q, piece, row, on);
+  leave8(red, ld, m, piece, row, on);
+  leave8(red + size, ld, dev, piece, row, on);
   __syncthreads();
   const float inv = 1.0f / float(n);
-  float mean = 0.0f, dev = 0.0f;
   const int lanes = sum_lanes(p.rows);
   for (int c = tid / lanes; c < p.channels; c += int(blockDim.x) / lanes) {
-    const float2 v = channel_sums(red, size, ld, p.rows, c, lane, lanes);
-    if ((lane & (lanes - 1)) != 0) continue;
-    const float s0 = v.x, q0 = v.y;
+    const int first = lane & (lanes - 1);
+    const float k = middle(h2f<DT>(base[k_at[0] + c]), h2f<DT>(base[k_at[1] + c]), h2f<DT>(base[k_at[2] + c]));
+    auto pixels = [&](int r) { return float(each + (r < over ? 1 : 0)); };
+    float t = 0.0f, u = 0.0f, d = 0.0f;
+#pragma unroll 4
+    for (int r = first; r < p.rows; r += lanes) t = __builtin_fmaf(pixels(r), red[c * ld + r], t);
+    for (int i = 1; i < lanes; i *= 2) t += __shfl_xor(t, i);
+    const float mean = t * inv;
+#pragma unroll 4
+    for (int r = first; r < p.rows; r += lanes) {
+      const float e = red[c * ld + r] - mean;
+      u = __builtin_fmaf(pixels(r) * e, e, u);
+      d += red[size + c * ld + r];
+    }
+    for (int i = 1; i < lanes; i *= 2) {
+      u += __shfl_xor(u, i);
+      d += __shfl_xor(d, i);
+    }
+    if (first != 0) continue;
     // in the places of the channel's own first row: nobody else reads these
-    const float k0 = h2f<DT>(p.x[int64_t(sample) * p.xs + from * p.xp + c]);
-    mean = s0 * inv;
-    dev = __builtin_fmaf(-s0, mean, q0);
-    red[c * ld] = k0 + mean;
-    red[size + c * ld] = not_negative(dev);
+    red[c * ld] = k + mean;
+    red[size + c * ld] = u + d;
   }
   __syncthreads();
   for (int g = wave; g < p.groups; g += waves) {
     const float* m0 = red + g * p.per * ld;
     const float* d0 = m0 + size;
-    // about the group's first channel's mean, for the same reason as above
     const float k0 = m0[0];
     float t = 0.0f, u = 0.0f, d = 0.0f;
+    for (int c = lane; c < p.per; c += 64) t += m0[c * ld] - k0;
+    t = wave_sum(t) / float(p.per);
     for (int c = lane; c < p.per; c += 64) {
-      const float e = m0[c * ld] - k0;
-      t += e;
+      const float e = (m0[c * ld] - k0) - t;
       u = __builtin_fmaf(e, e, u);
       d += d0[c * ld];
     }
-    t = wave_sum(t);
     u = wave_sum(u);
     d = wave_sum(d);
     if (lane == 0) {
-      const float m = t / float(p.per);
       float* out = p.part + (int64_t(blockIdx.x) * p.groups + g) * 2;
-      out[0] = k0 + m;
-      out[1] = __builtin_fmaf(float(n), not_negative(__builtin_fmaf(-t, m, u)), d);
+      out[0] = k0 + t;
+      out[1] = __builtin_fmaf(float(n), u, d);
     }
   }
+}
+
+// What the means of a group's chunks are joined about: their middle one of three.
+__device__ __forceinline__ float reference(const float2* of, const NormParams& p) {
+  return middle(of[int64_t(p.chunks / 4) * p.groups].x, of[int64_t(p.chunks / 2) * p.groups].x, of[int64_t(p.chunks * 3LL / 4) * p.groups].x);
 }
 
 // Adds two values a chunk and group over a sample's chunks: all threads at once,
@@ -320,7 +373,7 @@ __device__ __forceinline__ void join_chunks(const NormParams& p, int sample, int
     const bool on = walk < walks && g < p.groups;
     if (on) {
       const float2* q = part + g;
-      const float first = q[0].x;
+      const float first = reference(q, p);
 #pragma unroll 8
       for (int i = walk; i < p.chunks; i += walks) add(first, i, q[int64_t(i) * p.groups], s);
     }
@@ -356,7 +409,7 @@ __device__ __forceinline__ void join_stats(const NormParams& p, int sample, int 
     const float m = sm[3 * g], u = sm[3 * g + 1], d = sm[3 * g + 2];
     const float between = not_negative(__builtin_fmaf(-m, m, u));
     const float within = d / (float(p.per) * float(p.pixels));
-    sm[3 * g] = part[g].x + m;
+    sm[3 * g] = reference(part + g, p) + m;
     sm[3 * g + 1] = 1.0f / __builtin_sqrtf(between + within + p.eps);
   }
   __syncthreads();

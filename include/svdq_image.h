@@ -53,9 +53,10 @@ typedef struct {
 
 /* y = act((x - mean) rstd w + b), mean and rstd = 1 / sqrt(var + eps) over the
  * pixels and the channels / groups channels of a group, sample by sample (var
- * is the mean square deviation).  Statistics are fp32, of deviations from a
- * value of the data's own, so that a mean far from zero costs no digits; one
- * rounding to 16 bits at the end.  y may be x (the same data and strides).
+ * is the mean square deviation).  Statistics are fp32, of deviations
+ * from the mean or from a mean of a part of the data, so that neither a mean far
+ * from zero nor values far from the rest cost digits; one rounding to 16 bits at
+ * the end.  y may be x (the same data and strides).
  * stats: NULL or fp32 [samples][groups][2], mean and rstd.
  * ws: >= svdq_group_norm_workspace bytes, 16-byte aligned (may be NULL where
  * that is 0). */

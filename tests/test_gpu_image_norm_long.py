@@ -1,0 +1,55 @@
+"""GPU tests of the group norm over long maps and many samples, where a sum has
+many terms and one value far from the rest may be what deviations are taken from."""
+import pytest
+
+from tests import test_gpu_image_norm as base
+
+pytestmark = pytest.mark.gpu
+
+
+def _stats64(x, groups):
+    """Mean and inverse deviation of every group in 64 bits, a few samples at a time."""
+    torch, _ = base._torch()
+    n, c = x.shape[0], x.shape[-1]
+    step = max(1, (1 << 28) // (x[0].numel()))
+    mean, rstd = [], []
+    for i in range(0, n, step):
+        y = x[i:i + step].double().reshape(min(step, n - i), -1, groups, c // groups)
+        var, mu = torch.var_mean(y, dim=(1, 3), unbiased=False)
+        mean.append(mu)
+        rstd.append(1 / torch.sqrt(var + 1e-5))
+    return torch.cat(mean), torch.cat(rstd)
+
+
+# Square deviations are sums of terms that are not negative: at most 32 a run of a thread and 8 runs, 64 rows of pixels and 4
+# steps of a tree, 128 channels and 6 steps, and the chunks' (64 and 32): below 2^9 roundings of 2^-24 each, 2^-15 of the
+# variance and 2^-16 of rstd.  The mean: as many of the deviations', and its own.
+def _check_stats(x, groups, stats):
+    mean, rstd = _stats64(x, groups)
+    base._check(stats[..., 0], mean, 2.0 ** -15 / rstd + 2.0 ** -23 * mean.abs(), "mean")
+    base._check(stats[..., 1], rstd, 2.0 ** -15 * rstd, "rstd")
+
+
+@pytest.mark.parametrize("far", ["first", "some", "rows", "channel"])
+@pytest.mark.parametrize("n,sides,c,groups", [(256, (256, 256), 8, 1), (32, (512, 512), 64, 4), (256, (64, 64), 2048, 8), (2, (64, 64), 8192, 1), (1, (1500, 1400), 16, 1)])
+def test_values_far_from_the_rest(n, sides, c, groups, far):
+    """512 +- 2 but for one pixel, a few, the upper rows of a map or one channel of a group, which are 0."""
+    torch, image = base._torch()
+    g = torch.Generator(device="cuda").manual_seed(n + c)
+    x = torch.empty((n, *sides, c), device="cuda", dtype=torch.float16)
+    for i in range(0, n, 16):
+        x[i:i + 16] = 512 + 2 * torch.randn((min(16, n - i), *sides, c), generator=g, device="cuda")
+    pixels = x.view(n, -1, c)
+    if far == "first":
+        pixels[:, 0] = 0
+    elif far == "some":
+        for at in (0, 1, 2, 4):             # the corner, and what lies a quarter of the map on
+            pixels[:, at * pixels.shape[1] // 4 if at < 4 else -1] = 0
+    elif far == "rows":
+        x[:, :max(1, sides[0] // 40)] = 0
+    else:
+        x[..., ::c // groups] = 0
+    y, stats = image.group_norm(x, groups, return_stats=True)
+    _check_stats(x, groups, stats)
+    few = x[-1:]
+    base._check_forward(few, groups, None, None, 1e-5, None, y[-1:], stats[-1:], "f16")
