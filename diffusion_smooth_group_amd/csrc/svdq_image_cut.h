@@ -18,7 +18,7 @@ using svdq_kv::smaller;
 // ------------------------------------------------------------------ group norm
 constexpr int NORM_FEW_SAMPLES = 2;
 constexpr int NORM_MAX_BLOCK = 32;      // groups of a workgroup of the one-launch form
-constexpr int NORM_MOST_PIXELS = 256;   // pixels of a thread of the two-launch form: terms it adds one after the other
+constexpr int NORM_MOST_PIXELS = 256;   // pixels of a thread of the two-launch form, more in samples of 2^29 elements and up
 
 struct NormCut {
   int threads;
@@ -38,7 +38,7 @@ struct NormCut {
 // 128, when the kernels were slower: 42.5 us with 256, 44 with 512 of 512 threads, 47
 // with 512 of 1024; the gradient of 2 x 128 x 128 x 320: 30, 34, 40): each joins all
 // chunks of its sample.  More of them where a thread would have more than
-// NORM_MOST_PIXELS, so that no sum of one after the other is longer.
+// NORM_MOST_PIXELS, up to 256 a sample, so that sums of one after the other stay short.
 inline svdq_status norm_cut(const svdq_norm_desc* d, bool grad, NormCut* out) {
   NormCut t = {};
   const int per = d->channels / d->groups;
@@ -68,9 +68,12 @@ inline svdq_status norm_cut(const svdq_norm_desc* d, bool grad, NormCut* out) {
     if (used >= best) { best = used; t.threads = n; t.rows = rows; }
   }
   const int64_t want = 256 / (d->samples < 1 ? 1 : d->samples);
-  t.chunk = ceil_div(ceil_div(d->pixels, want < 1 ? 1 : want), t.rows) * t.rows;
-  if (t.chunk > int64_t(t.rows) * NORM_MOST_PIXELS) t.chunk = int64_t(t.rows) * NORM_MOST_PIXELS;
+  auto chunk_of = [&](int64_t n) { return ceil_div(ceil_div(d->pixels, n), t.rows) * t.rows; };
+  t.chunk = chunk_of(want < 1 ? 1 : want);
+  const int64_t most = int64_t(t.rows) * NORM_MOST_PIXELS, least = chunk_of(256);
+  if (t.chunk > most) t.chunk = most > least ? most : least;
   const int64_t chunks = ceil_div(d->pixels, t.chunk);
+  if (t.chunk > int64_t(1) << 30) return SVDQ_ERR_UNSUPPORTED;      // a chunk's pixels are a 32-bit number in the kernels
   if (product_below(d->samples, chunks + 1024, 1024, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
   t.chunks = int(chunks);
   *out = t;

@@ -255,7 +255,7 @@ __global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
   const int sample = int(blockIdx.x) / p.chunks, chunk = int(blockIdx.x) % p.chunks;
   const int64_t from = int64_t(chunk) * p.chunk;
-  const int n = int(min(p.pixels - from, p.chunk));     // (a thread has at most NORM_MOST_PIXELS of them)
+  const int n = int(min(p.pixels - from, p.chunk));
   const int row = tid / p.cv, piece = tid % p.cv;
   const bool on = row < p.rows;
   const uint16_t* base = p.x + int64_t(sample) * p.xs + from * p.xp;
