@@ -53,3 +53,17 @@ def test_values_far_from_the_rest(n, sides, c, groups, far):
     _check_stats(x, groups, stats)
     few = x[-1:]
     base._check_forward(few, groups, None, None, 1e-5, None, y[-1:], stats[-1:], "f16")
+
+
+@pytest.mark.parametrize("n,sides,c", [(1000003, (), 8), (70001, (3,), 40)])
+def test_gradient_sums_over_many_samples(n, sides, c):
+    """dw and db are sums over all samples.  Weights of zero make every term of db the same, whose roundings all go one way.  A
+    sum of n equal terms is off by 2^-24 n / 2 at most: runs of 256, as many as there are (489), and eight walks, below 2^-15."""
+    torch, image = base._torch()
+    g = torch.Generator(device="cuda").manual_seed(c)
+    x = torch.randn((n, *sides, c), generator=g, device="cuda").bfloat16()
+    w, b = torch.zeros(c, device="cuda").bfloat16(), torch.ones(c, device="cuda").bfloat16()
+    grad = torch.ones_like(x)
+    _, stats = image.group_norm(x, 1, w, b, act="silu", return_stats=True)
+    grads = image.group_norm_backward(grad, x, stats, 1, w, b, act="silu")
+    base._check_gradient(x, grad, stats, 1, w, b, "silu", *grads, "bf16")
