@@ -60,10 +60,15 @@ constexpr float LOG2E = 1.44269504088896341f;
 
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * z)); }
 
+// Phi(z), the normal distribution: of erfc, since 1 + erf(z / sqrt 2) has lost every
+// digit at z = -5.5, where bf16 holds z Phi(z) to 2^-9 (1 x 512 x 512 x 128: 65 us, by
+// erf 53; its gradient 119, 111).
+__device__ __forceinline__ float normal_below(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
+
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == SVDQ_ACT_SILU) return z * sigmoid(z);
-  if constexpr (ACT == SVDQ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == SVDQ_ACT_GELU) return z * normal_below(z);
   return z;
 }
 // derivative of the activation
@@ -74,8 +79,7 @@ __device__ __forceinline__ float slope(float z) {
     return __builtin_fmaf(z * p, 1.0f - p, p);
   }
   if constexpr (ACT == SVDQ_ACT_GELU)
-    return __builtin_fmaf(z * 0.39894228040143268f, __builtin_amdgcn_exp2f(-0.5f * LOG2E * z * z),
-                          0.5f * (1.0f + erff(z * 0.70710678118654752f)));
+    return __builtin_fmaf(z * 0.39894228040143268f, __builtin_amdgcn_exp2f(-0.5f * LOG2E * z * z), normal_below(z));
   return 1.0f;
 }
 

@@ -1,5 +1,8 @@
 """GPU tests of the group norm over long maps and many samples, where a sum has
-many terms and one value far from the rest may be what deviations are taken from."""
+many terms and one value far from the rest may be what deviations are taken from,
+and of an activation's far ends."""
+import math
+
 import pytest
 
 from tests import test_gpu_image_norm as base
@@ -67,3 +70,23 @@ def test_gradient_sums_over_many_samples(n, sides, c):
     _, stats = image.group_norm(x, 1, w, b, act="silu", return_stats=True)
     grads = image.group_norm_backward(grad, x, stats, 1, w, b, act="silu")
     base._check_gradient(x, grad, stats, 1, w, b, "silu", *grads, "bf16")
+
+
+@pytest.mark.parametrize("sides", [(8, 8), (72, 64)])
+def test_gelu_far_below_zero(sides):
+    """z Phi(z) for z from -8 to -4 to a result's own rounding: weights of zero make z the bias.  Beside the rounding erfc's
+    argument counts (2^-24 of it, 64 times as much of the result) and erfc itself (16 steps), below 2^-17 in all; the slope's
+    exponent likewise (46 roundings of 2^-24), and its sum of equal terms (256 and 64 one after the other): 2^-15 is above both."""
+    torch, image = base._torch()
+    n, c = 2, 64
+    x = torch.randn((n, *sides, c), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    w, b = torch.zeros(c, device="cuda").bfloat16(), torch.linspace(-8, -4, c, device="cuda").bfloat16()
+    y, stats = image.group_norm(x, 8, w, b, act="gelu", return_stats=True)
+    z = b.double()
+    phi = 0.5 * torch.erfc(-z / math.sqrt(2))
+    want = (z * phi).expand_as(x)
+    base._check(y, want, (2.0 ** -8 * 1.01 + 2.0 ** -15) * want.abs(), "y")
+    dx, dw, db = image.group_norm_backward(torch.ones_like(x), x, stats, 8, w, b, act="gelu")
+    want = x.numel() // c * (phi + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi))
+    base._check(db, want, 2.0 ** -15 * want.abs(), "db")
+    assert bool((dx == 0).all())
