@@ -1216,10 +1216,14 @@ svdq_status check_cross(const svdq_cross_desc* d, int q_heads, int k_heads) {
   return SVDQ_OK;
 }
 
-// rows that are written: no row lies on the next
+// rows that are written: no element lies on another, whether a token's heads or a
+// head's tokens are the outer ones
 svdq_status check_result(const svdq_heads* h, int D, int64_t n) {
   const svdq_status st = check_heads(h, D);
-  return st == SVDQ_OK && n > 1 && h->token_stride < D ? SVDQ_ERR_SHAPE : st;
+  if (st != SVDQ_OK || n <= 1) return st;
+  const int64_t far = h->heads > 1 ? h->head_stride : 0;
+  const __int128 heads = __int128(h->heads - 1) * far + D, tokens = __int128(n - 1) * h->token_stride + D;
+  return h->token_stride >= heads || (h->heads > 1 && far >= tokens && h->token_stride >= D) ? SVDQ_OK : SVDQ_ERR_SHAPE;
 }
 
 Rows rows_of(const svdq_heads* h) { return Rows{static_cast<uint16_t*>(h->data), h->token_stride, h->head_stride}; }

@@ -203,3 +203,30 @@ def test_cross_with_nothing_to_do():
     assert run_forward(cross(requests=0, tokens=0, states=0), ws=None, size=0) == OK
     assert run_backward(cross(requests=0, tokens=0, states=0), ws=None, size=0) == OK
     assert run_forward(cross(tokens=0, max_q=0), ws=None, size=0, q=heads(data=None), out=heads(data=None)) == OK
+
+
+# (token, head) strides of results of 64 columns: the first head of a later token is another head of token 0, or half of it, or the last
+# token's is
+@pytest.mark.parametrize("token,head", [(64, 64), (128, 256), (64, 128), (96, 64), (64, 64 * 153), (192, 128)])
+@pytest.mark.parametrize("name", ["out", "dq", "dk", "dv"])
+def test_cross_results_whose_heads_lie_on_other_rows(name, token, head):
+    d, n = cross(), 8 if name in ("out", "dq") else 4
+    bad = heads(n, token=token, head=head)
+    if name == "out":
+        assert run_forward(d, out=bad, ws=None) == SHAPE
+    else:
+        assert run_backward(d, **{name: bad}) == SHAPE
+
+
+def test_cross_results_in_any_order_of_dimensions():
+    """What views of dense tensors look like passes the check (the workspace's, behind it, refuses the call)."""
+    d = cross(requests=1, tokens=300, states=100000, max_q=300, max_k=100000)
+    size = C.c_size_t()
+    assert fn("svdq_cross_attention_backward_workspace")(d, 8, 4, size) == OK and size.value > 0
+    for token, head in ((512, 64), (64, 64 * 100000), (2 * 512, 2 * 64), (96, 96 * 100000), (4 * 64, 64)):
+        for name, n in (("dq", 8), ("dk", 4), ("dv", 4)):
+            if n == 8 and token == 256:
+                continue                # eight heads in the place of four
+            assert run_backward(d, ws=None, **{name: heads(n, token=token, head=head)}) == INVALID, (name, token, head)
+    one = cross(requests=1, tokens=1, states=100000, max_q=1, max_k=100000)
+    assert run_forward(one, ws=None, out=heads(8, token=0, head=64)) == INVALID        # one token: its stride says nothing
