@@ -53,7 +53,7 @@ inline svdq_status norm_cut(const svdq_norm_desc* d, bool grad, NormCut* out) {
     if (pieces <= (most == 512 ? 4 : 8)) {
       t.cv = cv; t.rows = int(rows); t.block = block; t.pieces = int(pieces);
       t.threads = int(ceil_div(int64_t(cv) * rows, 64)) * 64;
-      if (product_below(d->samples, d->groups / block, 1024, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
+      if (product_below(d->samples, d->groups / block, t.threads, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
       *out = t;
       return SVDQ_OK;
     }
@@ -74,7 +74,9 @@ inline svdq_status norm_cut(const svdq_norm_desc* d, bool grad, NormCut* out) {
   if (t.chunk > most) t.chunk = most > least ? most : least;
   const int64_t chunks = ceil_div(d->pixels, t.chunk);
   if (t.chunk > int64_t(1) << 30) return SVDQ_ERR_UNSUPPORTED;      // a chunk's pixels are a 32-bit number in the kernels
-  if (product_below(d->samples, chunks + 1024, 1024, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
+  // the gradient's second launch has workgroups of 32 channels behind the chunks'
+  const int64_t work = product_below(d->samples, chunks, 1, svdq_kv::MAX_THREADS);
+  if (work < 0 || product_below(work + (grad ? ceil_div(d->channels, 32) : 0), t.threads, 1, svdq_kv::MAX_THREADS) < 0) return SVDQ_ERR_UNSUPPORTED;
   t.chunks = int(chunks);
   *out = t;
   return SVDQ_OK;

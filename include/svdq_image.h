@@ -41,7 +41,9 @@ enum {
 };
 
 typedef struct {
-  int64_t samples, pixels;  /* pixels: height x width, at least 1 where samples > 0 */
+  int64_t samples, pixels;  /* pixels: height x width, at least 1 where samples > 0.  A launch has
+                               fewer than 2^32 threads: more samples than that takes, 2^22 /
+                               groups at least, are SVDQ_ERR_UNSUPPORTED */
   int32_t channels;         /* multiple of 8 and of groups, at most SVDQ_NORM_MAX_CHANNELS */
   int32_t groups;
   int32_t dtype;            /* svdq_dtype of maps, weight and bias */

@@ -90,3 +90,29 @@ def test_gelu_far_below_zero(sides):
     want = x.numel() // c * (phi + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi))
     base._check(db, want, 2.0 ** -15 * want.abs(), "db")
     assert bool((dx == 0).all())
+
+
+@pytest.mark.parametrize("n,sides,c,groups", [(200001, (), 1280, 32), (4501, (50, 50), 32, 1)])
+def test_many_samples(n, sides, c, groups):
+    torch, image = base._torch()
+    x, w, b, g = base._inputs(n, "bf16", n, sides, c)
+    y, stats = image.group_norm(x, groups, w, b, act="silu", return_stats=True)
+    _check_stats(x, groups, stats)
+    part = slice(n - 1000, n)
+    base._check_forward(x[part], groups, w, b, 1e-5, "silu", y[part], stats[part], "bf16")
+    grads = image.group_norm_backward(g, x, stats, groups, w, b, act="silu")
+    few = image.group_norm_backward(g[part], x[part], stats[part], groups, w, b, act="silu")
+    base._check_gradient(x[part], g[part], stats[part], groups, w, b, "silu", *few, "bf16")
+    assert torch.equal(few[0], grads[0][part])
+    # dw and db in all: fewer than 2^9 terms one after the other on the way, so within 2^-15 of the terms' absolute values
+    total = [torch.zeros(c, device="cuda", dtype=torch.float64) for _ in range(4)]
+    for i in range(0, n, 2000):
+        at = slice(i, min(i + 2000, n))
+        xs, gs, st = x[at].double().reshape(-1, math.prod(sides), c), g[at].double().reshape(-1, math.prod(sides), c), stats[at].double()
+        xh = (xs - base._spread(st[..., 0], groups, c)) * base._spread(st[..., 1], groups, c)
+        dz = gs * base._act64(xh * w.double() + b.double(), "silu")[1]
+        for t, v in zip(total, (dz * xh, dz, (dz * xh).abs(), (gs * (1 + xh.abs())).abs())):
+            t += v.sum((0, 1))
+    # each term's own error: the slope to 2^-19 of g (and of g xh)
+    base._check(grads[1], total[0], 2.0 ** -15 * total[2] + 2.0 ** -18 * total[3], "dw")
+    base._check(grads[2], total[1], 2.0 ** -15 * total[3], "db")

@@ -230,3 +230,14 @@ def test_cross_results_in_any_order_of_dimensions():
             assert run_backward(d, ws=None, **{name: heads(n, token=token, head=head)}) == INVALID, (name, token, head)
     one = cross(requests=1, tokens=1, states=100000, max_q=1, max_k=100000)
     assert run_forward(one, ws=None, out=heads(8, token=0, head=64)) == INVALID        # one token: its stride says nothing
+
+
+# samples, pixels, channels, groups, and the most samples a launch of fewer than 2^32 threads takes: in one launch (64 threads a
+# group of 40 channels of one pixel), forward and gradient; in two (1024 threads a sample), of which the gradient's second has one more
+@pytest.mark.parametrize("pixels,channels,groups,forward,backward", [(1, 1280, 32, (1 << 21) - 1, (1 << 21) - 1), (96 * 96, 32, 32, (1 << 22) - 1, (1 << 22) - 2),
+                                                                     (1, 8, 1, (1 << 26) - 1, (1 << 26) - 1)])
+def test_most_samples(pixels, channels, groups, forward, backward):
+    for name, most in (("svdq_group_norm_workspace", forward), ("svdq_group_norm_backward_workspace", backward)):
+        for samples, status in ((4092, OK), (200000, OK), (most, OK), (most + 1, UNSUPPORTED)):
+            d, size = norm(samples=samples, pixels=pixels, channels=channels, groups=groups, weight=None, bias=None), C.c_size_t()
+            assert fn(name)(d, size) == status, (name, samples)
