@@ -349,34 +349,36 @@ def cross_attention_backward(g, q, k, v, out, lse, q_start=None, k_start=None, m
         return dq, dk, dv
 
 
-def _as_rows(t):
+def _as_rows(t, group=1):
     """t as the library takes rows; what it does not (states that requests
-    share by a stride of 0, a gradient that is broadcast over heads) is written out."""
+    share by a stride of 0, a gradient that is broadcast over heads, strides that its
+    32-bit offsets do not hold) is written out.  group: heads that share a key head."""
     step, h = _stride(t), t.stride(-2)
     fits = t.stride(-1) == 1 and step is not None and step >= 0 and step % 8 == 0 and h % 8 == 0 and (h >= t.shape[-1] or t.shape[-2] == 1) \
-        and t.data_ptr() % 16 == 0
+        and step < 1 << 23 and (group == 1 or h * group < 1 << 28) and t.data_ptr() % 16 == 0
     return t if fits else t.contiguous()
 
 
 class _CrossAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, q_start, k_start, max_q, max_k, mask, scale):
-        q, k, v = _as_rows(q), _as_rows(k), _as_rows(v)
+        group = q.shape[-2] // max(k.shape[-2], 1)
+        q, k, v = _as_rows(q, group), _as_rows(k), _as_rows(v)
         out = None if q_start is None else q.new_zeros(q.shape)     # rows of no request are defined here
         out, lse = cross_attention(q, k, v, q_start, k_start, max_q, max_k, mask, scale, out=out, return_lse=True)
         ctx.save_for_backward(q, k, v, out, lse, q_start, k_start, mask)
-        ctx.how = max_q, max_k, scale
+        ctx.how = max_q, max_k, scale, group
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g):
         q, k, v, out, lse, q_start, k_start, mask = ctx.saved_tensors
-        max_q, max_k, scale = ctx.how
+        max_q, max_k, scale, group = ctx.how
         dq = dk = dv = None
         if q_start is not None:
             dq, dk, dv = (t.new_zeros(t.shape) for t in (q, k, v))
-        grads = cross_attention_backward(_as_rows(g), q, k, v, out, lse, q_start, k_start, max_q, max_k, mask, scale, dq, dk, dv)
+        grads = cross_attention_backward(_as_rows(g, group), q, k, v, out, lse, q_start, k_start, max_q, max_k, mask, scale, dq, dk, dv)
         return *grads, *[None] * 6
 
 

@@ -148,6 +148,15 @@ def test_workspaces(calls):
         image.group_norm(x, 8, ws=torch.zeros(128, dtype=torch.uint8)[::2])
 
 
+def test_strides_that_32_bits_do_not_hold_are_written_out():
+    """Where the library takes no such strides the autograd form makes a copy, as of any other it does not take (here of tensors
+    without memory)."""
+    far = lambda *strides: torch.empty_strided((1, 5, 8, 64), strides, dtype=torch.float16, device="meta")
+    near, tokens, heads = far(0, 1 << 22, 64, 1), far(0, 1 << 23, 64, 1), far(0, 64, 1 << 26, 1)
+    assert image._as_rows(near, 8) is near and image._as_rows(heads) is heads and image._as_rows(heads, 2) is heads
+    assert image._as_rows(tokens).is_contiguous() and image._as_rows(heads, 4).is_contiguous()
+
+
 def test_host_tensors_are_refused():
     with pytest.raises(ValueError, match="GPU"):
         image.group_norm(half(2, 5, 64), 8)
