@@ -89,7 +89,9 @@ class SVDQCrossAttention:
     q: SVDQLinear C -> heads D; out: SVDQLinear heads D -> N; groups: of the norm
     (0: none), weight, bias: its [C] or None, act: its activation.  k and v are the
     encoder's states, projected by the caller (once for all the steps that use
-    them) and kept in 16 bits.  A call keeps nothing, as in SVDQAttention."""
+    them) and kept in 16 bits.  A call keeps nothing, as in SVDQAttention.  There is
+    no gradient through the 4-bit linears: a call of which one would be asked raises
+    ValueError (``image.*_autograd`` are the operators for training)."""
 
     def __init__(self, q: SVDQLinear, out: SVDQLinear, heads: int, groups: int = 0, weight=None, bias=None, eps: float = 1e-5,
                  act: Optional[str] = None, scale: Optional[float] = None):
@@ -102,6 +104,8 @@ class SVDQCrossAttention:
         """x [requests, ..., C]: the maps or tokens of all requests; k, v
         [requests, states, k_heads, D]; mask [requests, states] or None: which
         states are seen.  Returns [requests, ..., N]."""
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, k, v, self.norm["weight"], self.norm["bias"])):
+            raise ValueError("SVDQCrossAttention has no gradient: call it under torch.no_grad() or with tensors that do not require one")
         with kv._on(None, x):
             b, c, tokens = x.shape[0], x.shape[-1], math.prod(x.shape[1:-1])
             h = image.group_norm(x, self.groups, **self.norm) if self.groups else x

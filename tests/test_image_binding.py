@@ -157,6 +157,25 @@ def test_strides_that_32_bits_do_not_hold_are_written_out():
     assert image._as_rows(tokens).is_contiguous() and image._as_rows(heads, 4).is_contiguous()
 
 
+@pytest.mark.parametrize("name", ["x", "k", "v", "weight", "bias"])
+def test_layer_refuses_to_lose_a_gradient(monkeypatch, calls, name):
+    """A 4-bit linear has none: where one would be asked of the layer, it says so, and does not give a result without it."""
+    from diffusion_smooth_group_amd import attention_layer as layers
+    monkeypatch.setattr(kv, "_on", lambda stream, t: contextlib.nullcontext())
+    linear = type("Linear", (), {"N": 64, "K": 64})()
+    monkeypatch.setattr(layers, "_linear", lambda linear, x: x)
+    a = dict(x=half(2, 3, 3, 64), k=half(2, 9, 1, 64), v=half(2, 9, 1, 64), weight=half(64), bias=half(64))
+    layer = layers.SVDQCrossAttention(linear, linear, 1, groups=8, weight=a["weight"], bias=a["bias"])
+    assert layer(a["x"], a["k"], a["v"]).shape == a["x"].shape
+    a[name].requires_grad_()
+    n = len(calls)
+    with pytest.raises(ValueError, match="no gradient"):
+        layer(a["x"], a["k"], a["v"])
+    assert len(calls) == n
+    with torch.no_grad():
+        assert layer(a["x"], a["k"], a["v"]).shape == a["x"].shape
+
+
 def test_host_tensors_are_refused():
     with pytest.raises(ValueError, match="GPU"):
         image.group_norm(half(2, 5, 64), 8)
