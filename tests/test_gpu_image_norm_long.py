@@ -34,7 +34,8 @@ def _check_stats(x, groups, stats):
 
 
 @pytest.mark.parametrize("far", ["first", "some", "rows", "channel"])
-@pytest.mark.parametrize("n,sides,c,groups", [(256, (256, 256), 8, 1), (32, (512, 512), 64, 4), (256, (64, 64), 2048, 8), (2, (64, 64), 8192, 1), (1, (1500, 1400), 16, 1)])
+@pytest.mark.parametrize("n,sides,c,groups", [(256, (256, 256), 8, 1), (32, (512, 512), 64, 4), (256, (64, 64), 2048, 8), (2, (64, 64), 8192, 1), (1, (1500, 1400), 16, 1),
+                                              (3, (16, 16), 1280, 4), (2, (30, 30), 320, 32)])
 def test_values_far_from_the_rest(n, sides, c, groups, far):
     """512 +- 2 but for one pixel, a few, the upper rows of a map or one channel of a group, which are 0."""
     torch, image = base._torch()
