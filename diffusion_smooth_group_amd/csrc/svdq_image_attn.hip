@@ -38,6 +38,7 @@ struct CrossParams {
   unsigned by_group;        // 2^32 / group, rounded up (group > 1)
   float c, scale;           // c = scale log2(e); forward: |scale|, and q's signs are turned
   unsigned turn;            // bits of two 16-bit values to turn
+  bool past;                // rows of the result (out, dq) are whole lines
 
   // row / group: the product may be one too high
   __device__ __forceinline__ int token_of(int row) const {
@@ -268,8 +269,12 @@ struct TileRows {
 
 // A wave's 32 rows of a result (its transpose in o, times `by`) to memory by way of
 // its part of LDS, which no other wave uses; past the caches where a row is whole
-// lines (2 x 4096 rows of 64 over 77: 10.1 us, 11.3 through them; 3 x 2047 rows of 72
-// over 300: 21.1 past them, 19.7 through them).
+// 64-byte parts of lines (the call by itself: 2 x 4096 rows of 64 over 77, 11.3 us and
+// 12.2 through them; in a view 64 bytes on 10.8 and 11.6, in one 16 bytes on 12.7 and
+// 12.4; 2 x 16384 rows so 21.8 and 19.9; 3 x 2047 rows of 72 over 300 21.1 and 19.7).
+// What reads the result next finds it in memory: with a 4-bit linear behind it 2 x 4096
+// x 10 heads take 32.4 us and 33.9 through the caches, 2 x 16384 x 6 60.6 and 58.0, 4608
+// x 24 of 128 over 512 79.7 and 77.6; with an elementwise pass no more than through them.
 template <int DT, int DP>
 __device__ __forceinline__ void store_rows(const CrossParams& p, const CrossRange& r, const Rows& to, uint16_t* lds, const f32x16* o, float by,
                                            int first, int h, int lane) {
@@ -299,7 +304,7 @@ __device__ __forceinline__ void store_rows(const CrossParams& p, const CrossRang
     }
     if constexpr (decltype(past)::value) asm volatile("" ::: "memory");    // else the last store of both forms becomes one
   };
-  if (p.D % 64 == 0) put(std::true_type());
+  if (p.past) put(std::true_type());
   else put(std::false_type());
 }
 
@@ -1226,6 +1231,11 @@ svdq_status check_result(const svdq_heads* h, int D, int64_t n) {
   return h->token_stride >= heads || (h->heads > 1 && far >= tokens && h->token_stride >= D) ? SVDQ_OK : SVDQ_ERR_SHAPE;
 }
 
+// every row of 64 or 128 columns is whole 64-byte parts of lines
+bool whole_lines(const svdq_heads* h, int D) {
+  return D % 64 == 0 && aligned(h->data, 64) && h->token_stride % 32 == 0 && (h->heads == 1 || h->head_stride % 32 == 0);
+}
+
 Rows rows_of(const svdq_heads* h) { return Rows{static_cast<uint16_t*>(h->data), h->token_stride, h->head_stride}; }
 
 svdq_status check_scratch(const void* ws, size_t have, size_t need) {
@@ -1317,6 +1327,7 @@ extern "C" svdq_status svdq_cross_attention(const svdq_cross_desc* d, const svdq
   if ((st = check_scratch(ws, ws_bytes, size_t(cross_part_floats(d, t, false)) * 4)) != SVDQ_OK) return st;
   CrossParams p = params_of(d, t, q->heads, k->heads);
   p.q = rows_of(q); p.k = rows_of(k); p.v = rows_of(v); p.out = rows_of(out);
+  p.past = whole_lines(out, d->head_dim);
   p.lse = lse;
   p.part = static_cast<float*>(ws);
   if (p.c < 0.0f) {                     // so that a row's largest logit is that of its largest product
@@ -1369,6 +1380,7 @@ extern "C" svdq_status svdq_cross_attention_backward(const svdq_cross_desc* d, c
   CrossParams p = params_of(d, t, q->heads, k->heads);
   p.q = rows_of(q); p.k = rows_of(k); p.v = rows_of(v); p.out = rows_of(out); p.g = rows_of(g);
   p.dq = rows_of(dq); p.dk = rows_of(dk); p.dv = rows_of(dv);
+  p.past = whole_lines(dq, d->head_dim);
   p.lse = const_cast<float*>(lse);
   p.delta = static_cast<float*>(ws);
   p.part = p.delta + delta;

@@ -112,3 +112,22 @@ def test_no_row_of_a_request(keys):
     base.check_forward(c, out, lse)
     base.check_backward(c, out, lse, *grads)
     assert bool((grads[1][:keys] == 0).all()) and bool((grads[2][:keys] == 0).all())
+
+
+@pytest.mark.parametrize("keys", [77, 300])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("offset,gap", [(8, 0), (32, 0), (64, 0), (0, 16), (0, 32)])
+def test_results_at_any_place(offset, gap, d, keys):
+    """Rows that are whole lines are stored in another way than rows that are not: the same values, and nothing beside them."""
+    torch, image = base._torch()
+    c = base.Case([150, 40], [keys, keys], 4, 2, d, "bf16")
+    out, lse, grads = _both(c)
+    n = 4 * d + 128 + gap
+    wide = [torch.full((190, n), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    o, dq = (t[:, offset:offset + 4 * d].view(190, 4, d) for t in wide)
+    image.cross_attention(c.q, c.k, c.v, out=o, **c.where)
+    image.cross_attention_backward(c.g, c.q, c.k, c.v, out, lse, dq=dq, **c.where)
+    assert torch.equal(o, out) and torch.equal(dq, grads[0])
+    for t in (o, dq):
+        t.fill_(3.0)
+    assert all(bool((t == 3).all()) for t in wide)
