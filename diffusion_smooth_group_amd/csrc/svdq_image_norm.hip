@@ -26,6 +26,7 @@ struct NormParams {
   float *dw, *db;
   int64_t xs, xp, gs, gp, ys, yp;
   int64_t pixels, chunk;    // pixels of a chunk
+  int32_t each, last_each, last_over;   // and of a row of a chunk, a row of the last one, rows of that with one more
   int32_t samples, channels, groups, per;   // per = channels / groups
   int32_t cv, rows;         // 8-channel pieces of a pixel that a workgroup takes; pixels in flight in it
   int32_t block;            // groups a workgroup takes (k_norm_whole)
@@ -250,52 +251,52 @@ __global__ __launch_bounds__(1024) void k_norm_whole(NormParams p) {
 // rstd wrong by 5 to 30 %.  With s and q the sums of d = x - mean and d^2 over a run and
 // n pixels after it, mean += s / n and the square deviations grow by q - s s / n.
 // Threads, channels of a group and chunks are joined by their means, square
-// deviations about the joined mean.  Means are held less one value of the chunk's
-// own.  Memory bounds both launches: 1 x 512 x 512 x 128 takes 19 us (3.5 TB/s; 16.5
-// about the chunk's first pixel) and k_norm_apply, which reads the map again, 23 (5.8
-// TB/s).
-constexpr int RUN = 32;
+// deviations about the joined mean.  Memory bounds both launches: 1 x 512 x 512 x 128
+// takes 18 us (3.7 TB/s; 16.5 about the first pixel) and k_norm_apply, which reads the
+// map again, 24 (5.6 TB/s).
+constexpr int RUN = 32, AHEAD = 4;      // pixels of a run, and of those read at once
+
+// sum over `lanes` neighbouring lanes, a power of two
+__device__ __forceinline__ float lanes_sum(float x, int lanes) {
+  for (int m = 1; m < lanes; m *= 2) x += __shfl_xor(x, m);
+  return x;
+}
 
 template <int DT>
 __global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
   extern __shared__ float red[];        // [2][channels][rows]
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, waves = (int(blockDim.x) + 63) >> 6;
+  const int tid = int(threadIdx.x), lane = tid & 63;
   const int sample = int(blockIdx.x) / p.chunks, chunk = int(blockIdx.x) % p.chunks;
-  const int64_t from = int64_t(chunk) * p.chunk;
-  const int n = int(min(p.pixels - from, p.chunk));
   const int row = tid / p.cv, piece = tid % p.cv;
-  const bool on = row < p.rows;
-  const uint16_t* base = p.x + int64_t(sample) * p.xs + from * p.xp;
-  const int64_t k_at[3] = {int64_t(n / 4) * p.xp, int64_t(n / 2) * p.xp, (int64_t(n) * 3 / 4) * p.xp};
-  // pixels of row r of the chunk: every p.rows-th one
-  const int each = n / p.rows, over = n % p.rows;
-  float m[8] = {}, dev[8] = {}, f[8];
-  if (on && row < n) {
-    const uint16_t* x = base + 8 * piece;
-    float k[8], k1[8], k2[8];
-    unpack8<DT>(*reinterpret_cast<const u32x4*>(x + k_at[0]), k);
-    unpack8<DT>(*reinterpret_cast<const u32x4*>(x + k_at[1]), k1);
-    unpack8<DT>(*reinterpret_cast<const u32x4*>(x + k_at[2]), k2);
+  const bool on = row < p.rows, last = chunk + 1 == p.chunks;
+  // pixels of row r of the chunk: every p.rows-th one, one more in the first `over` rows
+  const int each = last ? p.last_each : p.each, over = last ? p.last_over : 0, n = each * p.rows + over;
+  auto pixels = [&](int r) { return each + (r < over ? 1 : 0); };
+  float m[8] = {}, dev[8] = {};
+  if (on) {
+    const uint16_t* x = p.x + int64_t(sample) * p.xs + (int64_t(chunk) * p.chunk + row) * p.xp + 8 * piece;
     const int64_t step = int64_t(p.rows) * p.xp;
-    x += int64_t(row) * p.xp;
-    unpack8<DT>(*reinterpret_cast<const u32x4*>(x), m);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      k[e] = middle(k[e], k1[e], k2[e]);
-      m[e] -= k[e];
-    }
-    const int mine = each + (row < over ? 1 : 0);
+    const int mine = pixels(row);
+    float k[8] = {}, f[8];              // the first pixel, which the mean is held from
     for (int done = 0; done < mine; done += RUN) {
       const int run = min(RUN, mine - done);
       float s[8] = {}, q[8] = {};
-#pragma unroll 4
-      for (int i = 0; i < run; ++i, x += step) {
-        unpack8<DT>(*reinterpret_cast<const u32x4*>(x), f);
+      for (int i = 0; i < run; i += AHEAD, x += AHEAD * step) {
+        u32x4 v[AHEAD];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = (f[e] - k[e]) - m[e];
-          s[e] += d;
-          q[e] = __builtin_fmaf(d, d, q[e]);
+        for (int j = 0; j < AHEAD; ++j)
+          if (i + j < run) v[j] = *reinterpret_cast<const u32x4*>(x + j * step);
+        if (done + i == 0) unpack8<DT>(v[0], k);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          if (i + j >= run) continue;
+          unpack8<DT>(v[j], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float d = (f[e] - k[e]) - m[e];
+            s[e] += d;
+            q[e] = __builtin_fmaf(d, d, q[e]);
+          }
         }
       }
       const float inv = 1.0f / float(done + run);
@@ -306,8 +307,10 @@ __global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
         dev[e] += not_negative(__builtin_fmaf(-s[e], by, q[e]));
       }
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[e] += k[e];
   }
-  // channels: a row's mean counts by its pixels
+  // channels: a row's mean counts by its pixels (rows of none hold zeros)
   const int ld = p.rows | 1, size = p.channels * ld;
   leave8(red, ld, m, piece, row, on);
   leave8(red + size, ld, dev, piece, row, on);
@@ -315,49 +318,51 @@ __global__ __launch_bounds__(1024) void k_norm_stats(NormParams p) {
   const float inv = 1.0f / float(n);
   const int lanes = sum_lanes(p.rows);
   for (int c = tid / lanes; c < p.channels; c += int(blockDim.x) / lanes) {
-    const int first = lane & (lanes - 1);
-    const float k = middle(h2f<DT>(base[k_at[0] + c]), h2f<DT>(base[k_at[1] + c]), h2f<DT>(base[k_at[2] + c]));
-    auto pixels = [&](int r) { return float(each + (r < over ? 1 : 0)); };
+    const int from = lane & (lanes - 1);
+    const float m0 = red[c * ld];       // row 0's: there is always one
     float t = 0.0f, u = 0.0f, d = 0.0f;
 #pragma unroll 4
-    for (int r = first; r < p.rows; r += lanes) t = __builtin_fmaf(pixels(r), red[c * ld + r], t);
-    for (int i = 1; i < lanes; i *= 2) t += __shfl_xor(t, i);
-    const float mean = t * inv;
-#pragma unroll 4
-    for (int r = first; r < p.rows; r += lanes) {
-      const float e = red[c * ld + r] - mean;
-      u = __builtin_fmaf(pixels(r) * e, e, u);
+    for (int r = from; r < p.rows; r += lanes) {
+      t = __builtin_fmaf(float(pixels(r)), red[c * ld + r] - m0, t);
       d += red[size + c * ld + r];
     }
-    for (int i = 1; i < lanes; i *= 2) {
-      u += __shfl_xor(u, i);
-      d += __shfl_xor(d, i);
+    const float mean = lanes_sum(t, lanes) * inv;
+#pragma unroll 4
+    for (int r = from; r < p.rows; r += lanes) {
+      const float e = (red[c * ld + r] - m0) - mean;
+      u = __builtin_fmaf(float(pixels(r)) * e, e, u);
     }
-    if (first != 0) continue;
+    u = lanes_sum(u + d, lanes);
+    if (from != 0) continue;
     // in the places of the channel's own first row: nobody else reads these
-    red[c * ld] = k + mean;
-    red[size + c * ld] = u + d;
+    red[c * ld] = m0 + mean;
+    red[size + c * ld] = u;
   }
   __syncthreads();
-  for (int g = wave; g < p.groups; g += waves) {
+  // groups: as many lanes as a power of two from their channels on, so that groups of
+  // few are summed side by side
+  int wide = 8;
+  while (wide < p.per && wide < 64) wide *= 2;
+  for (int g = tid / wide; g < p.groups; g += int(blockDim.x) / wide) {
+    const int from = lane & (wide - 1);
     const float* m0 = red + g * p.per * ld;
     const float* d0 = m0 + size;
     const float k0 = m0[0];
     float t = 0.0f, u = 0.0f, d = 0.0f;
-    for (int c = lane; c < p.per; c += 64) t += m0[c * ld] - k0;
-    t = wave_sum(t) / float(p.per);
-    for (int c = lane; c < p.per; c += 64) {
-      const float e = (m0[c * ld] - k0) - t;
-      u = __builtin_fmaf(e, e, u);
+    for (int c = from; c < p.per; c += wide) {
+      t += m0[c * ld] - k0;
       d += d0[c * ld];
     }
-    u = wave_sum(u);
-    d = wave_sum(d);
-    if (lane == 0) {
-      float* out = p.part + (int64_t(blockIdx.x) * p.groups + g) * 2;
-      out[0] = k0 + t;
-      out[1] = __builtin_fmaf(float(n), u, d);
+    t = lanes_sum(t, wide) / float(p.per);
+    for (int c = from; c < p.per; c += wide) {
+      const float e = (m0[c * ld] - k0) - t;
+      u = __builtin_fmaf(e, e, u);
     }
+    u = lanes_sum(__builtin_fmaf(float(n), u, d), wide);
+    if (from != 0) continue;
+    float* out = p.part + (int64_t(blockIdx.x) * p.groups + g) * 2;
+    out[0] = k0 + t;
+    out[1] = u;
   }
 }
 
@@ -803,6 +808,8 @@ NormParams params_of(const svdq_norm_desc* d, const NormCut& t) {
   p.b = static_cast<const uint16_t*>(d->bias);
   p.pixels = d->pixels; p.chunk = t.chunk;
   p.samples = int32_t(d->samples); p.channels = d->channels; p.groups = d->groups; p.per = d->channels / d->groups;
+  const int64_t tail = d->pixels - int64_t(t.chunks - 1) * t.chunk;
+  p.each = int32_t(t.chunk / t.rows); p.last_each = int32_t(tail / t.rows); p.last_over = int32_t(tail % t.rows);
   p.cv = t.cv; p.rows = t.rows; p.block = t.block; p.chunks = t.chunks; p.act = d->act; p.eps = d->eps;
   return p;
 }
