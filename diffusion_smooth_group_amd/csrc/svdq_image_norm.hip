@@ -148,8 +148,8 @@ __device__ __forceinline__ float2 channel_sums(const float* red, int size, int l
 // ------------------------------------------------------------ one launch
 // A workgroup has `block` groups of a sample: reads them once into registers
 // (NV pieces of 16 bytes a thread), mean first and square deviations after it,
-// writes them once.  1 x 8 x 8 x 1280: 5.9 us, latency (loads, two sums with a barrier
-// each, stores), under the call's 8.5 on the host.
+// writes them once.  1 x 8 x 8 x 1280: 6.0 us, latency (loads, two sums with a barrier
+// each, stores), under the call's 9.2 on the host.
 template <int DT, int ACT, int NV>
 __global__ __launch_bounds__(1024) void k_norm_whole(NormParams p) {
   extern __shared__ float red[];

@@ -87,7 +87,8 @@ typedef struct {
   int32_t head_dim;         /* multiple of 8, 8 to 128 */
   int32_t dtype;            /* svdq_dtype of all operands */
   int32_t max_q, max_k;     /* bounds on a request's rows and states; what is past them is
-                               not computed or seen */
+                               not computed or seen.  requests x q_heads x max_q is below 2^30,
+                               max_k at most 2^30 (both no more than tokens and states) */
   float scale;              /* of the logits, commonly 1 / sqrt(D); finite */
   const int32_t *q_start;   /* [requests + 1], rising: request r has rows q_start[r] .. q_start[r + 1];
                                NULL: max_q rows each, tokens = requests max_q */
@@ -111,7 +112,12 @@ svdq_status svdq_cross_attention(const svdq_cross_desc* desc, const svdq_heads* 
 /* Gradient from g (with respect to out), the inputs, and out and lse of the
  * forward call.  With p = exp(scale q k^T - lse), delta = g . out:
  *   dv = sum p g, ds = p (g . v - delta), dq = scale sum ds k, dk = scale sum ds q
- * (dk, dv: over rows and the query heads of a key head).  States that the mask
+ * (dk, dv: over rows and the query heads of a key head).  Where min(max_k, states)
+ * is 128 or less, delta = sum p (g . v) instead, which is the same for the forward
+ * call's out, and out is not read; above that the rounding of out enters delta,
+ * which counts against dq the more the more states share a row's weight (bf16,
+ * relative to 64 bits: 2.4e-3 up to some thousand states, 2.9e-3 over 7346 of
+ * random logits, where the result's own rounding is 1.7e-3).  States that the mask
  * hides get zeros, rows and states of no request or past the bounds are left
  * as they were.  The probabilities and ds are rounded to 16 bits for their
  * products (f16: ds under a power of two of its row's or state's own, so that
