@@ -251,9 +251,9 @@ __global__ __launch_bounds__(1024) void k_norm_whole(NormParams p) {
 // rstd wrong by 5 to 30 %.  With s and q the sums of d = x - mean and d^2 over a run and
 // n pixels after it, mean += s / n and the square deviations grow by q - s s / n.
 // Threads, channels of a group and chunks are joined by their means, square
-// deviations about the joined mean.  Memory bounds both launches: 1 x 512 x 512 x 128
-// takes 18 us (3.7 TB/s; 16.5 about the first pixel) and k_norm_apply, which reads the
-// map again, 24 (5.6 TB/s).
+// deviations about the joined mean.  1 x 512 x 512 x 128 takes 18 us (3.7 TB/s from
+// memory; 16.5 about the first pixel) and k_norm_apply 24: it moves 134 MB at 5.6 TB/s,
+// above a copy's 4.9, since a map of up to 256 MB still lies in the memory-side cache.
 constexpr int RUN = 32, AHEAD = 4;      // pixels of a run, and of those read at once
 
 // sum over `lanes` neighbouring lanes, a power of two
